@@ -547,6 +547,115 @@ vp_status vp_decode_steps_rows(const vp_model* model, int steps, int rows, const
                                int32_t* argmax, int32_t* n_commit, int32_t* committed, void* ws, size_t ws_bytes,
                                int* status, void* stream);
 
+/* ------------------------------------------------------------------ a served attention layer
+ *
+ * The calls below run the attention layers of the same models outside the verify pass: prompts, and
+ * single-token decode of many sequences, with the weights of a block-quantised FP8 checkpoint and a
+ * KV cache in pages.  One layer of a step chains them:
+ *   vp_add_rmsnorm_fp8 -> vp_linear_fp8_block (q, k, v) -> vp_paged_append -> vp_paged_attention ->
+ *   vp_quant_fp8 -> vp_linear_fp8_block (o).
+ * All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph. */
+
+/* Element type of an activation matrix. */
+enum { VP_BF16 = 0, VP_F32 = 1 };
+
+/* Block-scaled e4m3 activations.  Per row m and group b of 128 columns (the last one shorter when
+ * K % 128 != 0):
+ *   scales[m][b] = max(max_k |x[m][k]| / 448, 2^-126),   q[m][k] = e4m3(x[m][k] / scales[m][b]),
+ * to nearest even, saturated at 448; a NaN or infinity in a group makes the group's scale NaN or
+ * infinite, and the elements that have no value NaN.  x: bf16 or fp32 (x_type VP_BF16 / VP_F32),
+ * row stride ld_x elements; q: e4m3 bytes [M][K]; scales: fp32 [M][ceil(K / 128)].  1 <= M <= 2^24,
+ * K % 16 == 0, 16 <= K <= 65536, ld_x >= K and rows 16-byte aligned (VP_ERR_SHAPE, VP_ERR_ALIGNMENT).
+ * One launch, no workspace; the output must not overlap x. */
+vp_status vp_quant_fp8(const void* x, int x_type, int64_t ld_x, int M, int K, void* q, float* scales, void* stream);
+
+/* Residual addition, RMSNorm and the quantisation above in one pass over the rows:
+ *   h = bf16(x + residual)   (the sum in fp32; bf16(x) when residual is NULL),
+ *   y = h / sqrt(mean_k h^2 + eps) * weight   (weight 1 when NULL; not rounded),
+ *   q, scales = the block quantisation of y.
+ * The mean is taken over the rounded h, the residual stream that the next block reads.  It does not
+ * overflow or vanish where h^2 leaves fp32's range.  x: bf16 or fp32, row stride ld_x; residual: bf16
+ * [M][K] or NULL; weight: fp32 [K] or NULL; h: bf16 [M][K] or NULL (not written), may be `residual`
+ * itself or x (bf16 with ld_x == K) for an update in place; q, scales as above.  eps finite, > 0.
+ * 1 <= M <= 2^24, K % 16 == 0, 16 <= K <= 16384.  One launch, no workspace. */
+vp_status vp_add_rmsnorm_fp8(const void* x, int x_type, int64_t ld_x, const void* residual, const float* weight,
+                             float eps, int M, int K, void* h, void* q, float* scales, void* stream);
+
+/* Linear layer of a block-quantised FP8 checkpoint on block-quantised activations:
+ *   y[m][n] = sum_b x_scales[m][b] * w_scales[n / 128][b] * sum_{k in block b} e4m3(xq[m][k]) * e4m3(w[n][k]),
+ * the inner sums (128 products) on the tensor core with fp32 accumulation, the outer one in fp32.
+ * w_packed: the repacked weights (vp_pack_fp8_block, from [N][K] e4m3 bytes; 128 x 128 tiles, padded
+ * with zeros); w_scales: fp32 [ceil(N / 128)][ceil(K / 128)]; xq: e4m3 bytes [M][K]; x_scales: fp32
+ * [M][ceil(K / 128)]; y: bf16 (rounded once) or fp32 [M][N] (y_type).  Any M from 1 to 2^20; N % 16
+ * == 0, K % 16 == 0, K <= 65536, N <= 2^20, N * K < 2^40.  Work is split along K among CTAs where there
+ * are few output tiles, and joined in a fixed order: bit-identical from run to run.  One launch.
+ * Workspace: vp_linear_fp8_block_workspace_bytes(M, N, K), 256-byte aligned, zero-filled once; the
+ * status word reads VP_ERR_TIMEOUT when a bounded wait gave up (y is then not valid). */
+size_t vp_packed_bytes_fp8_block(int N, int K); /* 0 if N or K is unsupported */
+vp_status vp_pack_fp8_block(const void* w, int N, int K, void* packed, size_t packed_bytes, void* stream);
+size_t vp_linear_fp8_block_workspace_bytes(int M, int N, int K); /* 0 if the shape is unsupported */
+vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const void* xq, const float* x_scales,
+                              void* y, int y_type, int M, int N, int K, void* ws, size_t ws_bytes, void* stream);
+
+/* A key-value cache in pages: position p of sequence s lies in page pages[s][p / page_size], slot
+ * p % page_size.  k, v: bf16 [n_pages][Hkv][page_size][D], 16-byte aligned; pages: device int32
+ * [S][max_pages].  page_size 16, 32, 64 or 128; D 64, 128 or 256; 1 <= Hkv <= 1024;
+ * n_pages * Hkv * page_size < 2^31 and max_pages * page_size < 2^31.  The struct itself is host memory, read during
+ * the call. */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* pages;
+  int n_pages, page_size, max_pages, Hkv, D;
+} vp_paged_cache;
+
+/* Rotary embedding: the pair j of a head is rotated by position * inv_freq[j] (inv_freq: HOST array
+ * [rot_dim / 2] of fp64, finite, read during the call; angles are formed and reduced in fp64).  Pair
+ * j is elements (2j, 2j + 1) when interleaved is nonzero, else (j, j + rot_dim / 2); elements from
+ * rot_dim on pass through.  rot_dim % 16 == 0, 0 <= rot_dim <= D. */
+typedef struct {
+  const double* inv_freq;
+  int rot_dim, interleaved;
+} vp_rope;
+
+/* New rows into a paged cache, with the attention layer's Q/K norm and rotary embedding on the way.
+ * Row r of sequence s is its new position ctx[s] + i, i = r - row_start[s] (row_start: device int32
+ * [S + 1], nondecreasing, or NULL: one row per sequence, M == S):
+ *   q_out[r][h] = rope(norm(q[r][h])),  key slot = rope(norm(k[r][h])),  value slot = v[r][h],
+ * norm(x) = x / sqrt(mean x^2 + eps) * weight per head when q_norm / k_norm (fp32 [D]) is not NULL;
+ * fp32 in between, rounded once to bf16.  q: bf16 rows of Hq heads, row stride ld_q elements, or NULL
+ * (keys and values alone); k, v: rows of Hkv heads, strides ld_k, ld_v (the three may be parts of one
+ * fused projection); q_out: bf16 [M][Hq][D], may be q itself when ld_q == Hq D.  Rows outside
+ * row_start[0] .. row_start[S] - 1 (padding) are left as they were.  kv_len (device int32 [S] or
+ * NULL; not ctx itself) receives ctx[s] + its number of rows: the next call's ctx, and what
+ * vp_paged_attention takes.  A row whose position is negative or beyond the page table, or whose page
+ * is outside 0 .. n_pages - 1, appends nothing and sets *status (device int or NULL) to
+ * VP_ERR_SHAPE; its q_out row is zero.  row_start[0] < 0 or row_start[S] > M sets it too.  Two rows that name the same slot race: their order is
+ * undefined.  rope NULL: no rotation.  1 <= M <= 2^24, 1 <= S <= 65536, 1 <= Hq <= 4096; strides and
+ * pointers 16-byte aligned (ctx, row_start, kv_len, pages, status, the norms 4-byte).  One launch. */
+vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                          const void* v, int64_t ld_v, const float* q_norm, const float* k_norm, float eps,
+                          const vp_rope* rope, const int32_t* row_start, const int32_t* ctx, int S, int M, int Hq,
+                          void* q_out, int32_t* kv_len, int* status, void* stream);
+
+/* Attention of one new token per sequence over the paged cache (the new key and value appended):
+ *   out[s][h] = sum_t softmax_t(scale * q[s][h] . k_t) v_t over t < kv_len[s], kv head h / (Hq / Hkv),
+ * times sigmoid(gate[s][h]) elementwise when gate is not NULL, rounded once to bf16; lse[s][h] =
+ * log sum_t exp(scale * q . k_t) (fp32 [S][Hq] or NULL), by which partial results can be joined.
+ * q, gate, out: bf16 [S][Hq][D]; kv_len: device int32 [S].  A sequence with kv_len 0 gives zeros and
+ * lse -inf.  kv_len[s] < 0 or above max_pages * page_size does the same and sets the workspace's status
+ * word to VP_ERR_SHAPE; so does a page outside 0 .. n_pages - 1 among the sequence's pages, whose
+ * positions are left out.  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect.
+ * Hq % Hkv == 0, Hq / Hkv <= 16, scale finite; 1 <= S <= 8192, S * Hkv <= 65536.  The cached positions
+ * of all sequences are cut into equal shares, one per CTA, whatever the lengths (they are read on the
+ * device only); partial results are joined in a fixed order: bit-identical from run to run.  P V runs
+ * with the probabilities split in two bf16 parts (about 2^-17 relative).  One launch.  Workspace:
+ * vp_paged_attention_workspace_bytes(S, Hq, Hkv, D), 256-byte aligned, zero-filled once. */
+size_t vp_paged_attention_workspace_bytes(int S, int Hq, int Hkv, int D); /* 0 if unsupported */
+vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const int32_t* kv_len, int S, int Hq,
+                             float scale, const void* gate, void* out, float* lse, void* ws, size_t ws_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,7 @@ VP_OK, VP_ERR_INVALID_ARG, VP_ERR_SHAPE, VP_ERR_ALIGNMENT, VP_ERR_WORKSPACE, VP_
     VP_ERR_UNSUPPORTED = range(8)
 VP_OP_NVFP4, VP_OP_FP8, VP_OP_HEAD, VP_OP_ARGMAX, VP_OP_Q4, VP_OP_SAMPLE, VP_OP_ATTN = range(7)
 VP_LAYER_GDN, VP_LAYER_ATTN = 0, 1
+VP_BF16, VP_F32 = 0, 1
 
 # Every symbol include/verify.h declares.
 EXPORTS = [
@@ -31,6 +32,9 @@ EXPORTS = [
     "vp_argmax_accept_rows", "vp_verify_pass_rows", "vp_lookup_drafts_rows", "vp_commit_append_rows",
     "vp_decode_steps_rows",
     "vp_model_set_cores", "vp_pass_cores_workspace_bytes", "vp_verify_pass_cores", "vp_pass_cores_launch_count", "vp_commit_cores",
+    "vp_quant_fp8", "vp_add_rmsnorm_fp8", "vp_packed_bytes_fp8_block", "vp_pack_fp8_block",
+    "vp_linear_fp8_block_workspace_bytes", "vp_linear_fp8_block", "vp_paged_append",
+    "vp_paged_attention_workspace_bytes", "vp_paged_attention",
 ]
 
 
@@ -64,6 +68,26 @@ class vp_core_desc(ctypes.Structure):
 class vp_core_geom(ctypes.Structure):
     _fields_ = [("n_qk", ctypes.c_int), ("n_v", ctypes.c_int), ("d", ctypes.c_int), ("Hq", ctypes.c_int),
                 ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("cap", ctypes.c_int)]
+
+
+class vp_paged_cache(ctypes.Structure):
+    """The paged cache's descriptor; it keeps the tensors it was made from alive."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
+
+    def __init__(self, k, v, pages, n_pages: int, page_size: int, max_pages: int, Hkv: int, D: int):
+        super().__init__(_ptr(k), _ptr(v), _ptr(pages), n_pages, page_size, max_pages, Hkv, D)
+        self._keep = (k, v, pages)
+
+
+class vp_rope(ctypes.Structure):
+    """Rotary embedding: inv_freq is a host sequence of rot_dim / 2 floats (copied)."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+    def __init__(self, inv_freq, interleaved: bool):
+        vals = [float(f) for f in inv_freq]
+        self._arr = (ctypes.c_double * max(1, len(vals)))(*vals)
+        super().__init__(ctypes.cast(self._arr, ctypes.c_void_p), 2 * len(vals), int(bool(interleaved)))
 
 
 class vp_head_desc(ctypes.Structure):
@@ -122,6 +146,16 @@ def _load():
         "vp_verify_pass_cores": (I, [P, P, I, P, I, P, P, P, P, P, P, P, S, P]),
         "vp_commit_cores": (I, [P, I, P, I, P, S, P]),
         "vp_pass_cores_launch_count": (I, [P]),
+        "vp_quant_fp8": (I, [P, I, ctypes.c_int64, I, I, P, P, P]),
+        "vp_add_rmsnorm_fp8": (I, [P, I, ctypes.c_int64, P, P, F, I, I, P, P, P, P]),
+        "vp_packed_bytes_fp8_block": (S, [I, I]),
+        "vp_pack_fp8_block": (I, [P, I, I, P, S, P]),
+        "vp_linear_fp8_block_workspace_bytes": (S, [I, I, I]),
+        "vp_linear_fp8_block": (I, [P, P, P, P, P, I, I, I, I, P, S, P]),
+        "vp_paged_append": (I, [ctypes.POINTER(vp_paged_cache), P, ctypes.c_int64, P, ctypes.c_int64, P,
+                                ctypes.c_int64, P, P, F, ctypes.POINTER(vp_rope), P, P, I, I, I, P, P, P, P]),
+        "vp_paged_attention_workspace_bytes": (S, [I, I, I, I]),
+        "vp_paged_attention": (I, [ctypes.POINTER(vp_paged_cache), P, P, I, I, F, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -438,3 +472,55 @@ def vp_trace_read(M: int, dst) -> int:
     n = ctypes.c_uint(0)
     _check("vp_trace_read", _L.vp_trace_read(M, dst.ctypes.data, dst.nbytes, ctypes.byref(n)))
     return n.value
+
+
+def vp_quant_fp8(x, x_type: int, ld_x: int, M: int, K: int, q, scales, stream=None):
+    _check("vp_quant_fp8", _L.vp_quant_fp8(_ptr(x), x_type, ld_x, M, K, _ptr(q), _ptr(scales), _stream(stream)))
+
+
+def vp_add_rmsnorm_fp8(x, x_type: int, ld_x: int, residual, weight, eps: float, M: int, K: int, h, q, scales,
+                       stream=None):
+    _check("vp_add_rmsnorm_fp8",
+           _L.vp_add_rmsnorm_fp8(_ptr(x), x_type, ld_x, _ptr(residual), _ptr(weight), eps, M, K, _ptr(h), _ptr(q),
+                                 _ptr(scales), _stream(stream)))
+
+
+def vp_packed_bytes_fp8_block(N: int, K: int) -> int:
+    return _L.vp_packed_bytes_fp8_block(N, K)
+
+
+def vp_pack_fp8_block(w, N: int, K: int, packed, stream=None, packed_bytes=None):
+    pb = packed_bytes if packed_bytes is not None else _nbytes(packed)
+    _check("vp_pack_fp8_block", _L.vp_pack_fp8_block(_ptr(w), N, K, _ptr(packed), pb, _stream(stream)))
+
+
+def vp_linear_fp8_block_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _L.vp_linear_fp8_block_workspace_bytes(M, N, K)
+
+
+def vp_linear_fp8_block(w_packed, w_scales, xq, x_scales, y, y_type: int, M: int, N: int, K: int, ws, stream=None,
+                        ws_bytes=None):
+    wb = ws_bytes if ws_bytes is not None else _nbytes(ws)
+    _check("vp_linear_fp8_block",
+           _L.vp_linear_fp8_block(_ptr(w_packed), _ptr(w_scales), _ptr(xq), _ptr(x_scales), _ptr(y), y_type, M, N, K,
+                                  _ptr(ws), wb, _stream(stream)))
+
+
+def vp_paged_append(cache: vp_paged_cache, q, ld_q: int, k, ld_k: int, v, ld_v: int, q_norm, k_norm, eps: float,
+                    rope, row_start, ctx, S: int, M: int, Hq: int, q_out, kv_len=None, status=None, stream=None):
+    _check("vp_paged_append",
+           _L.vp_paged_append(ctypes.byref(cache), _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(q_norm),
+                              _ptr(k_norm), eps, ctypes.byref(rope) if rope is not None else None, _ptr(row_start),
+                              _ptr(ctx), S, M, Hq, _ptr(q_out), _ptr(kv_len), _ptr(status), _stream(stream)))
+
+
+def vp_paged_attention_workspace_bytes(S: int, Hq: int, Hkv: int, D: int) -> int:
+    return _L.vp_paged_attention_workspace_bytes(S, Hq, Hkv, D)
+
+
+def vp_paged_attention(cache: vp_paged_cache, q, kv_len, S: int, Hq: int, scale: float, gate, out, lse, ws,
+                       stream=None, ws_bytes=None):
+    wb = ws_bytes if ws_bytes is not None else _nbytes(ws)
+    _check("vp_paged_attention",
+           _L.vp_paged_attention(ctypes.byref(cache), _ptr(q), _ptr(kv_len), S, Hq, scale, _ptr(gate), _ptr(out),
+                                 _ptr(lse), _ptr(ws), wb, _stream(stream)))

@@ -758,6 +758,7 @@ struct vp_model {
 };
 
 namespace vp {
+vp_status device_sm_count(int* sms) { return device_sms(sms); }
 int model_hidden(const vp_model* model) { return model ? model->hidden : 0; }
 }  // namespace vp
 

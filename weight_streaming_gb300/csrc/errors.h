@@ -9,5 +9,7 @@ namespace vp {
 
 vp_status cuda_fail(cudaError_t e);
 int last_cuda_error();
+// SM count of the current device (at most kMaxGrid); VP_ERR_UNSUPPORTED unless it is sm_103 (api.cu).
+vp_status device_sm_count(int* sms);
 
 }  // namespace vp

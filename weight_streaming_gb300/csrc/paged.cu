@@ -1,0 +1,254 @@
+// New rows into a paged KV cache with the attention layer's Q/K norm and rotary embedding on the way
+// (vp_paged_append).
+//
+// Mathematics: per head, y = x / sqrt(mean x^2 + eps) * w (optional), then the pairs of the first rot_dim
+// elements turn by the angle pos * f_j.  Only the angle modulo one turn matters, and pos is an integer:
+// the host gives f_j / 2 pi modulo 1 as a 64-bit binary fraction F_j, and pos * F_j wraps around 2^64
+// by itself to the fraction of a turn -- exact but for F_j's own rounding (2^-54 of a turn per
+// position: 3e-8 of a turn at 2^29 positions), with one integer product and no fp64.
+//
+// D / 8 lanes hold one head (16 bytes each); the group's sum of squares and a half-split pair's other
+// element come by shuffles.  A block serves one row and a group of heads; its sines and cosines are
+// formed once, in shared memory.  The bytes bound it for prompts (each read and written once), the
+// latency of one load, the reduction and one store for single tokens.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "errors.h"
+#include "paged.h"
+#include "verify.h"
+
+namespace vp {
+
+namespace {
+
+constexpr int kThreadsP = 256;
+constexpr int kMaxPairs = 128;
+
+struct AppendArgs {
+  const uint16_t *q, *k, *v;
+  long long ld_q, ld_k, ld_v;
+  const float *q_norm, *k_norm;
+  float eps;
+  int rot, interleaved;
+  const int32_t *row_start, *ctx, *pages;
+  int S, M, Hq, Hkv, n_pages, log_page, max_pages, heads_per_block;
+  uint16_t *k_cache, *v_cache, *q_out;
+  int32_t* kv_len;
+  int* status;
+  unsigned long long turn[kMaxPairs];  // f_j / 2 pi mod 1, in units of 2^-64
+};
+
+__device__ __forceinline__ void unpack8(uint4 a, float (&v)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(w[e] << 16);
+    v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The sequence whose rows hold row r (the last s with row_start[s] <= r), or -1 for a padding row.
+__device__ __forceinline__ int find_seq(const int32_t* start, int S, int r) {
+  if (r < start[0] || r >= start[S]) return -1;
+  int lo = 0, hi = S;  // start[lo] <= r; the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= r) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kL = D / 8;                    // lanes per head
+  constexpr int kGroups = kThreadsP / kL;      // heads at a time
+  __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
+  const int r = blockIdx.x, tid = threadIdx.x;
+  // the lengths after this call, by the first blocks
+  if (a.kv_len && blockIdx.y == 0) {
+    for (long long s = (long long)r * kThreadsP + tid; s < a.S; s += (long long)gridDim.x * kThreadsP) {
+      const long long n = a.row_start ? (long long)a.row_start[s + 1] - a.row_start[s] : 1;
+      a.kv_len[s] = (int32_t)min((long long)a.ctx[s] + n, 0x7FFFFFFFLL);
+    }
+  }
+  if (a.row_start && r == 0 && blockIdx.y == 0 && tid == 0 && a.status && (a.row_start[0] < 0 || a.row_start[a.S] > a.M))
+    atomicExch(a.status, (int)VP_ERR_SHAPE);  // rows that this call does not have
+  const int s = a.row_start ? find_seq(a.row_start, a.S, r) : r;
+  if (s < 0) return;
+  const long long pos = (long long)a.ctx[s] + (a.row_start ? r - a.row_start[s] : 0);
+  int page = -1;
+  if (pos >= 0 && (pos >> a.log_page) < a.max_pages) page = a.pages[(size_t)s * a.max_pages + (pos >> a.log_page)];
+  const bool ok = page >= 0 && page < a.n_pages;
+  if (!ok && tid == 0 && blockIdx.y == 0 && a.status) atomicExch(a.status, (int)VP_ERR_SHAPE);
+  const int half = a.rot >> 1;
+  for (int j = tid; j < half; j += kThreadsP) {
+    const unsigned long long f = (unsigned long long)pos * a.turn[j];
+    // the nearest signed fraction of a turn, in half turns
+    sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s_sin[j], &s_cos[j]);
+  }
+  __syncthreads();
+  const int lane = tid & (kL - 1), heads = (a.q ? a.Hq : 0) + 2 * a.Hkv, nq = a.q ? a.Hq : 0;
+  const uint32_t mask = kL == 32 ? 0xFFFFFFFFu : ((1u << (kL & 31)) - 1) << ((threadIdx.x & 31) & ~(kL - 1));
+  const int end = min(heads, (int)(blockIdx.y + 1) * a.heads_per_block);
+  for (int hh = blockIdx.y * a.heads_per_block + tid / kL; hh < end; hh += kGroups) {
+    const bool isq = hh < nq, isk = !isq && hh < nq + a.Hkv;
+    if (!ok && !isq) continue;
+    const int g = hh - nq - (isk ? 0 : a.Hkv);  // key or value head
+    const uint16_t* src = isq ? a.q + (size_t)r * a.ld_q + hh * D
+                              : isk ? a.k + (size_t)r * a.ld_k + g * D : a.v + (size_t)r * a.ld_v + g * D;
+    const size_t slot = ((((size_t)(ok ? page : 0) * a.Hkv + g) << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
+    uint16_t* dst = isq ? a.q_out + ((size_t)r * a.Hq + hh) * D : (isk ? a.k_cache : a.v_cache) + slot;
+    uint4 raw = *reinterpret_cast<const uint4*>(src + 8 * lane);
+    if (!isq && !isk) {
+      *reinterpret_cast<uint4*>(dst + 8 * lane) = raw;
+      continue;
+    }
+    float x[8];
+    unpack8(raw, x);
+    const float* w = isq ? a.q_norm : a.k_norm;
+    if (w) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+      for (int o = kL / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+      float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
+      if (ss >= 1e-30f && ss <= 3.0e38f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * __ldg(w + 8 * lane + e);
+      } else {  // squares outside fp32's range (or a zero or NaN head): fp64
+        double sd = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sd += (double)x[e] * (double)x[e];
+#pragma unroll
+        for (int o = kL / 2; o; o >>= 1) sd += __shfl_xor_sync(mask, sd, o);
+        const double id = 1.0 / sqrt(sd / (double)D + (double)a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)((double)x[e] * id * (double)__ldg(w + 8 * lane + e));
+      }
+    }
+    if (a.interleaved) {
+      if (8 * lane < a.rot) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float c = s_cos[4 * lane + e / 2], sn = s_sin[4 * lane + e / 2], x0 = x[e], x1 = x[e + 1];
+          x[e] = fmaf(x0, c, -(x1 * sn));
+          x[e + 1] = fmaf(x0, sn, x1 * c);
+        }
+      }
+    } else if (half) {
+      const int hl = half / 8;  // lanes per half
+      const bool lo = lane < hl, in = lane < 2 * hl;
+      const int other = in ? (lo ? lane + hl : lane - hl) : lane;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = __shfl_sync(mask, x[e], other, kL);
+        if (in) {
+          const int j = (lo ? lane : other) * 8 + e;
+          const float c = s_cos[j], sn = s_sin[j];
+          x[e] = lo ? fmaf(x[e], c, -(y * sn)) : fmaf(y, sn, x[e] * c);
+        }
+      }
+    }
+    uint4 out = pack8(x);
+    if (!ok) out = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(dst + 8 * lane) = out;
+  }
+}
+
+bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+}  // namespace
+
+vp_status check_cache(const vp_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->pages) return VP_ERR_INVALID_ARG;
+  const int P = c->page_size;
+  if ((c->D != 64 && c->D != 128 && c->D != 256) || (P != 16 && P != 32 && P != 64 && P != 128) || c->Hkv < 1 ||
+      c->Hkv > 1024 || c->n_pages < 1 || c->max_pages < 1 || (long long)c->n_pages * c->Hkv * P >= (1LL << 31) ||
+      (long long)c->max_pages * P >= (1LL << 31))
+    return VP_ERR_SHAPE;
+  if (!al(c->k, 16) || !al(c->v, 16) || !al(c->pages, 4)) return VP_ERR_ALIGNMENT;
+  return VP_OK;
+}
+
+}  // namespace vp
+
+using namespace vp;
+
+extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld_q, const void* k,
+                                     int64_t ld_k, const void* v, int64_t ld_v, const float* q_norm,
+                                     const float* k_norm, float eps, const vp_rope* rope, const int32_t* row_start,
+                                     const int32_t* ctx, int S, int M, int Hq, void* q_out, int32_t* kv_len,
+                                     int* status, void* stream) {
+  vp_status st = check_cache(cache);
+  if (st != VP_OK) return st;
+  if (!k || !v || !ctx || (q && !q_out) || kv_len == ctx) return VP_ERR_INVALID_ARG;
+  if ((q_norm || k_norm) && !(eps > 0.0f && std::isfinite(eps))) return VP_ERR_INVALID_ARG;
+  const vp_paged_cache& c = *cache;
+  if (M < 1 || M > (1 << 24) || S < 1 || S > 65536 || (!row_start && M != S)) return VP_ERR_SHAPE;
+  const long long kd = (long long)c.Hkv * c.D, qd = (long long)Hq * c.D;
+  if (ld_k < kd || ld_v < kd || ld_k > (1LL << 40) || ld_v > (1LL << 40)) return VP_ERR_SHAPE;
+  if (q && (Hq < 1 || Hq > 4096 || ld_q < qd || ld_q > (1LL << 40))) return VP_ERR_SHAPE;
+  if (q && q_out == q && ld_q != qd) return VP_ERR_INVALID_ARG;
+  if (!al(k, 16) || !al(v, 16) || ld_k % 8 || ld_v % 8 || (q && (!al(q, 16) || ld_q % 8 || !al(q_out, 16))) ||
+      (q_norm && !al(q_norm, 4)) || (k_norm && !al(k_norm, 4)) || (row_start && !al(row_start, 4)) || !al(ctx, 4) ||
+      (kv_len && !al(kv_len, 4)) || (status && !al(status, 4)))
+    return VP_ERR_ALIGNMENT;
+  AppendArgs a;
+  a.rot = a.interleaved = 0;
+  if (rope && rope->rot_dim) {
+    if (!rope->inv_freq) return VP_ERR_INVALID_ARG;
+    if (rope->rot_dim < 0 || rope->rot_dim % 16 || rope->rot_dim > c.D) return VP_ERR_SHAPE;
+    a.rot = rope->rot_dim;
+    a.interleaved = rope->interleaved != 0;
+    for (int j = 0; j < a.rot / 2; ++j) {
+      const double f = rope->inv_freq[j] / 6.283185307179586476925;
+      if (!std::isfinite(f)) return VP_ERR_INVALID_ARG;
+      const double t = f - std::floor(f);  // [0, 1]: 1 wraps to 0
+      // the top 32 bits and the rest, each exact: 2^64 itself does not fit the integer
+      const double top = std::floor(t * 4294967296.0), low = (t * 4294967296.0 - top) * 4294967296.0;
+      a.turn[j] = ((unsigned long long)top << 32) + (unsigned long long)low;
+    }
+  }
+  int sms = 0;
+  if ((st = device_sm_count(&sms)) != VP_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.ld_q = ld_q, a.ld_k = ld_k, a.ld_v = ld_v;
+  a.q_norm = q_norm, a.k_norm = k_norm, a.eps = eps;
+  a.row_start = row_start, a.ctx = ctx, a.pages = c.pages;
+  a.S = S, a.M = M, a.Hq = Hq, a.Hkv = c.Hkv, a.n_pages = c.n_pages, a.max_pages = c.max_pages;
+  a.log_page = 4;
+  while ((1 << a.log_page) < c.page_size) ++a.log_page;
+  a.k_cache = static_cast<uint16_t*>(c.k);
+  a.v_cache = static_cast<uint16_t*>(c.v);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.kv_len = kv_len, a.status = status;
+  const int heads = (q ? Hq : 0) + 2 * c.Hkv, at_once = kThreadsP / (c.D / 8);
+  a.heads_per_block = (heads + at_once - 1) / at_once * at_once;
+  const dim3 grid((unsigned)M, (unsigned)((heads + a.heads_per_block - 1) / a.heads_per_block));
+  cudaStream_t s = (cudaStream_t)stream;
+  if (c.D == 64)
+    append_kernel<64><<<grid, kThreadsP, 0, s>>>(a);
+  else if (c.D == 128)
+    append_kernel<128><<<grid, kThreadsP, 0, s>>>(a);
+  else
+    append_kernel<256><<<grid, kThreadsP, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? VP_OK : cuda_fail(e);
+}
