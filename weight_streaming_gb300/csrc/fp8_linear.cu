@@ -3,12 +3,32 @@
 //
 // Mathematics: y[m][n] = sum_b xs[m][b] ws[n / 128][b] (sum_{k in b} xq[m][k] w[n][k]).  The products are
 // exact in fp32 (e4m3 has 4 significant bits); the scales differ from block to block, so each inner
-// sum of 128 products leaves the accumulator, is scaled and added to an fp32 register.
-// First form: CUDA cores, a 64 x 64 output tile per CTA, 4 x 4 outputs per thread.
+// sum of 128 products leaves the tensor core's accumulator, is scaled and added to an fp32 register.
+//
+// Design: one persistent CTA per SM; a producer warp, an MMA warp and eight epilogue warps.
+//  * Operands: one stage of the shared-memory ring is one 128-wide K block: the tokens by a tiled TMA
+//    load (128-byte swizzle; rows past M and columns past K read zero), the weights by one bulk copy
+//    of 16 KB per 128 rows (packed in the swizzled order).
+//  * tcgen05.mma kind::f8f6f4, 128 lanes x kBC columns, four K = 32 steps per block, into one of
+//    512 / kBC tensor-memory buffers (each block starts from zero); the epilogue warps read the buffer
+//    (tcgen05.ld), scale and accumulate in registers (fma.f32x2) while the next block's MMAs run.
+//  * Tokens on the lanes for M > 64 (the factor xs ws is one scalar per thread and block), weights on
+//    the lanes for M <= 64 (16, 32 or 64 token columns; the factors come by shuffles): a small batch
+//    then pads to 16 columns instead of 128 lanes, and the weight stream is what it waits for.
+//  * Work: whole rounds of output tiles first; the remaining tiles' K blocks form one line that is cut
+//    into equal runs, one per CTA (a few token rows split every tile along K that way).  A tile with
+//    several contributors goes through fp32 partials in the workspace: the last CTA to arrive (a
+//    counter, nobody waits) adds them in K order, so results do not depend on the arrival order.
+//
+// Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, drains its copies and MMAs and frees
+// its tensor memory.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "errors.h"
@@ -21,65 +41,436 @@ namespace vp {
 
 namespace {
 
-__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&v)[4]) {
-  uint32_t lo, hi;
-  e4m3x4_to_f16x2x2(w, lo, hi);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+constexpr int kLinThreads = 320;  // warp 0 copies, warp 1 MMAs, warps 2..9 epilogue
+constexpr int kLinGrid = 152;     // CTAs at most: one per SM
+constexpr int kEpiThreads = 256;
+constexpr int kSmemRing = 216 * 1024;
+constexpr int kMaxStages = 12;
+
+struct LinArgs {
+  const uint8_t* w;
+  const float *ws, *xs;
+  void* y;
+  int f32, M, N, KB;
+  int tiles, tile_m, tile_n;  // output tiles: in all, along the tokens, along the weight rows
+  int dp_rounds, sk_tiles;    // whole rounds per CTA; tiles cut along K (after the first dp_rounds * grid)
+  unsigned* counters;         // [sk_tiles][8 epilogue warps]
+  float* partials;            // [grid][2][kBC][128]
+  int* status;
+};
+
+template <int kBC>
+struct LinCfg {
+  static constexpr int kStage = 16384 + kBC * 128;
+  static constexpr int kStages = kSmemRing / kStage < kMaxStages ? kSmemRing / kStage : kMaxStages;
+  static constexpr int kBufs = 512 / kBC < 8 ? 512 / kBC : 8;
+  static constexpr int kCols = kBC * kBufs;   // tensor-memory columns (a power of two >= 128)
+  static constexpr int kSmem = kStages * kStage + 1024;
+};
+
+struct Item {
+  int tile, kb0, kb1, sk;  // sk: index among the tiles cut along K, or -1
+};
+// The i-th piece of work of CTA c, or false: its whole tiles, then its run of K blocks of the rest.
+struct Sched {
+  int c, G, KB, i, dp, base;
+  int u, u1;
+  __device__ Sched(const LinArgs& a) : c(blockIdx.x), G(gridDim.x), KB(a.KB), i(0), dp(a.dp_rounds) {
+    base = dp * G;
+    const long long U = (long long)a.sk_tiles * KB;
+    u = (int)(c * U / G);
+    u1 = (int)((c + 1) * U / G);
+  }
+  __device__ bool next(Item& it) {
+    if (i < dp) {
+      it.tile = i++ * G + c;
+      it.kb0 = 0;
+      it.kb1 = KB;
+      it.sk = -1;
+      return true;
+    }
+    if (u >= u1) return false;
+    it.sk = u / KB;
+    it.kb0 = u - it.sk * KB;
+    it.kb1 = min(KB, it.kb0 + u1 - u);
+    it.tile = base + it.sk;
+    u += it.kb1 - it.kb0;
+    return true;
+  }
+};
+
+// Tile order: groups of 8 token tiles, weight tiles across, so that the CTAs of one round share rows
+// of both operands in L2.
+__device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& mt, int& nt) {
+  constexpr int kGroup = 8;
+  const int per = kGroup * a.tile_n, g = t / per, r = t - g * per, gm = min(kGroup, a.tile_m - g * kGroup);
+  nt = r / gm;
+  mt = g * kGroup + r - nt * gm;
 }
 
-__global__ void __launch_bounds__(256) linear_simple(const uint8_t* __restrict__ w, const float* __restrict__ ws,
-                                                     const uint8_t* __restrict__ xq, const float* __restrict__ xs,
-                                                     void* __restrict__ y, int f32, int M, int N, int K) {
-  __shared__ float sx[32][65], sw[32][65];  // [k][row]
-  const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64, tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int KB = qblocks(K);
-  float acc[4][4] = {};
-  for (int kb = 0; kb < KB; ++kb) {
-    float part[4][4] = {};
-    for (int k0 = 0; k0 < kQBlock; k0 += 32) {
-      for (int i = tid; i < 512; i += 256) {  // 64 rows x 8 words of each operand
-        const int r = i >> 3, c = i & 7, k = kb * kQBlock + k0 + 4 * c;
-        float v[4];
-        uint32_t word = 0;
-        if (m0 + r < M && k < K) word = *reinterpret_cast<const uint32_t*>(xq + (size_t)(m0 + r) * K + k);
-        e4m3x4_to_f32(word, v);
-        for (int e = 0; e < 4; ++e) sx[4 * c + e][r] = v[e];
-        const int n = n0 + r;
-        word = 0;
-        if (n < N)
-          word = *reinterpret_cast<const uint32_t*>(w + ((size_t)(n >> 7) * KB + kb) * kQTileBytes +
-                                                    qtile_offset(n & 127, (k0 >> 4) + (c >> 2)) + 4 * (c & 3));
-        e4m3x4_to_f32(word, v);
-        for (int e = 0; e < 4; ++e) sw[4 * c + e][r] = v[e];
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sx[k][ty + 16 * i], sw[k][tx + 16 * j], part[i][j]);
-      __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (m < M && n < N) acc[i][j] = fmaf(part[i][j], xs[(size_t)m * KB + kb] * ws[(size_t)(n >> 7) * KB + kb], acc[i][j]);
-      }
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// K-major operand with the 128-byte swizzle: 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// Arrives on `bar` when every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
+}
+// kN consecutive 32-bit columns of the warp's lane, waited for (in one statement: no use of the registers
+// can move in front of the wait).
+template <int kN>
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* r) {
+  if constexpr (kN == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t)
+        : "memory");
+  } else if constexpr (kN == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        " tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t));
+  } else {
+    static_assert(kN == 8, "");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 " tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= M || n >= N) continue;
-      if (f32)
-        static_cast<float*>(y)[(size_t)m * N + n] = acc[i][j];
-      else
-        static_cast<__nv_bfloat16*>(y)[(size_t)m * N + n] = __float2bfloat16_rn(acc[i][j]);
+}
+// (acc.x, acc.y) += (lo, hi) * s, elementwise.
+__device__ __forceinline__ void fma2(unsigned long long& acc, uint32_t lo, uint32_t hi, unsigned long long s) {
+  asm("{ .reg .b64 t; mov.b64 t, {%1, %2}; fma.rn.f32x2 %0, t, %3, %0; }" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
+}
+__device__ __forceinline__ unsigned long long pack2(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+// kBC: columns of a tile (token columns when kSwap, else weight rows).
+template <int kBC, bool kSwap>
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ CUtensorMap xmap) {
+  using C = LinCfg<kBC>;
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[8], tempty[8], drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], kEpiThreads / 32);
+    }
+    mbar_init(&drain, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(&s_tmem, C::kCols);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *(volatile uint32_t*)&s_tmem;
+
+  // A bounded wait; false when it ran out here or elsewhere in the CTA.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    for (uint32_t i = 0; i < kMbarPolls; ++i) {
+      if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
+      if (*(volatile int*)&s_abort) return false;
+    }
+    *(volatile int*)&s_abort = 1;
+    atomicExch(a.status, (int)VP_ERR_TIMEOUT);
+    return false;
+  };
+
+  Sched sched(a);
+  Item it;
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0;
+      bool ok = true;
+      const uint64_t pol = l2_evict_first_policy();
+      while (ok && sched.next(it)) {
+        int mt, nt;
+        tile_at(a, it.tile, mt, nt);
+        // weight tiles of this output tile: one, or up to kBC / 128
+        const int nb = kSwap ? nt : nt * (kBC / 128), nbs = kSwap ? 1 : min(kBC / 128, qblocks(a.N) - nb);
+        const int rows = kSwap ? kBC : 128;
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+          const int s = n % C::kStages;
+          if (!(ok = wait(&empty[s], ((n / C::kStages) & 1) ^ 1))) break;
+          const uint32_t st = ring + s * C::kStage, bar = smem_addr(&full[s]);
+          // lanes' operand first (16 KB), columns' operand behind it
+          const uint32_t dst_w = kSwap ? st : st + 16384, dst_x = kSwap ? st + 16384 : st;
+          mbar_arrive_expect_tx(&full[s], rows * 128 + nbs * kQTileBytes);
+          tma_load_2d(dst_x, &xmap, kb * kQBlock, mt * rows, bar);
+          for (int i = 0; i < nbs; ++i) {
+            const uint8_t* src = a.w + ((size_t)(nb + i) * a.KB + kb) * kQTileBytes;
+            if (a.tile_m == 1)  // each weight byte is read once
+              bulk_g2s(dst_w + i * kQTileBytes, src, kQTileBytes, bar, pol);
+            else
+              bulk_load(dst_w + i * kQTileBytes, src, kQTileBytes, bar);
+          }
+        }
+      }
+      if (!ok)  // the copies in flight land before the CTA's shared memory goes
+        for (int s = 0; s < min(n, C::kStages); ++s) {
+          const int last = (n - 1 - s) / C::kStages;
+          mbar_wait_bounded(&full[s], last & 1);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int n = 0;
+      bool ok = true;
+      while (ok && sched.next(it)) {
+        int mt, nt;
+        tile_at(a, it.tile, mt, nt);
+        const int cols = kSwap ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
+        const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (128u >> 4) << 24;  // e4m3 x e4m3 -> fp32
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+          const int s = n % C::kStages, b = n % C::kBufs;
+          if (!(ok = wait(&tempty[b], ((n / C::kBufs) & 1) ^ 1))) break;
+          if (!(ok = wait(&full[s], (n / C::kStages) & 1))) break;
+          tmem_fence_after();
+          const uint64_t da = smem_desc(ring + s * C::kStage), db = smem_desc(ring + s * C::kStage + 16384);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 32 bytes along K inside the swizzle atom
+            mma_f8(tmem + b * kBC, da + 2 * k, db + 2 * k, idesc, k > 0);
+          mma_commit(&empty[s]);
+          mma_commit(&tfull[b]);
+        }
+      }
+      if (!ok) {
+        mma_commit(&drain);
+        mbar_wait_bounded(&drain, 0);
+      }
+    }
+  } else {
+    constexpr int kW = kBC / 2;                   // columns per warp
+    constexpr int kCh = kW < 32 ? kW : kW == 128 ? 16 : 32;  // columns per load (128 sums leave 168 - 128 registers)
+    const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane, c0 = half * kW;
+    const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + c0;
+    int n = 0;
+    bool ok = true;
+    while (ok && sched.next(it)) {
+      int mt, nt;
+      tile_at(a, it.tile, mt, nt);
+      // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there)
+      const int m = kSwap ? mt * kBC + c0 + lane : mt * 128 + row;
+      const int nb = kSwap ? nt : nt * (kBC / 128) + (kBC == 256 ? half : 0);
+      const bool live = m < a.M && (!kSwap || lane < kW), wlive = nb < qblocks(a.N);
+      const float* px = a.xs + (size_t)(live ? m : 0) * a.KB;
+      const float* pw = a.ws + (size_t)(wlive ? nb : 0) * a.KB;
+      unsigned long long acc[kW / 2];
+#pragma unroll
+      for (int j = 0; j < kW / 2; ++j) acc[j] = 0;
+      float f_next = live && wlive ? __ldg(px + it.kb0) * __ldg(pw + it.kb0) : 0.0f;
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+        const int b = n % C::kBufs;
+        const float f = f_next;
+        if (kb + 1 < it.kb1 && live && wlive) f_next = __ldg(px + kb + 1) * __ldg(pw + kb + 1);
+        ok = __all_sync(0xFFFFFFFFu, wait(&tfull[b], (n / C::kBufs) & 1));
+        if (!ok) break;
+        tmem_fence_after();
+#pragma unroll
+        for (int ch = 0; ch < kW; ch += kCh) {
+          uint32_t r[kCh];
+          tmem_ld<kCh>(tm + b * kBC + ch, r);
+          if (ch + kCh == kW) {  // the buffer is read: the next MMAs may have it
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < kCh; j += 2) {
+            const unsigned long long s = kSwap ? pack2(__shfl_sync(0xFFFFFFFFu, f, ch + j), __shfl_sync(0xFFFFFFFFu, f, ch + j + 1))
+                                               : pack2(f, f);
+            fma2(acc[(ch + j) / 2], r[j], r[j + 1], s);
+          }
+        }
+      }
+      if (!ok) break;
+      if (it.kb0 > 0 || it.kb1 < a.KB) {
+        // a part of the tile's K blocks: leave it, and let the last contributor add them up
+        const int G = gridDim.x;
+        const long long U = (long long)a.sk_tiles * a.KB, u0 = (long long)it.sk * a.KB;
+        const int first = (int)(((u0 + 1) * G - 1) / U), last = (int)(((u0 + a.KB) * G - 1) / U);
+        float* mine = a.partials + ((size_t)blockIdx.x * 2 + (it.kb0 == 0)) * kBC * 128;
+#pragma unroll
+        for (int j = 0; j < kW / 2; ++j) {
+          const float2 v = unpack2(acc[j]);
+          __stcg(mine + (c0 + 2 * j) * 128 + row, v.x);
+          __stcg(mine + (c0 + 2 * j + 1) * 128 + row, v.y);
+        }
+        __threadfence();
+        __syncwarp();
+        // each warp joins its own part of the tile (8 counters per tile): no CTA-wide wait
+        unsigned old = 0;
+        if (lane == 0) old = atom_add_acq_rel_gpu(a.counters + it.sk * 8 + warp - 2, 1);
+        const bool join = __shfl_sync(0xFFFFFFFFu, old, 0) == (unsigned)(last - first);
+        if (!join) continue;
+        if (lane == 0) a.counters[it.sk * 8 + warp - 2] = 0;  // every contributor has arrived
+        __threadfence();
+#pragma unroll
+        for (int j = 0; j < kW / 2; ++j) acc[j] = 0;
+        for (int c = first; c <= last; ++c) {
+          const float* p = a.partials + ((size_t)c * 2 + (c == first)) * kBC * 128 + row;
+#pragma unroll
+          for (int j = 0; j < kW / 2; ++j) {
+            const float2 v = unpack2(acc[j]);
+            acc[j] = pack2(v.x + __ldcg(p + (c0 + 2 * j) * 128), v.y + __ldcg(p + (c0 + 2 * j + 1) * 128));
+          }
+        }
+      }
+      if (kSwap) {
+        const int nn = nt * 128 + row;
+        if (nn < a.N) {
+#pragma unroll
+          for (int j = 0; j < kW / 2; ++j) {
+            const float2 v = unpack2(acc[j]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int mm = mt * kBC + c0 + 2 * j + e;
+              if (mm >= a.M) continue;
+              const size_t at = (size_t)mm * a.N + nn;
+              if (a.f32)
+                static_cast<float*>(a.y)[at] = e ? v.y : v.x;
+              else
+                static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(e ? v.y : v.x);
+            }
+          }
+        }
+      } else if (m < a.M) {
+        const int n0 = nt * kBC + c0;
+#pragma unroll
+        for (int j = 0; j < kW; j += 8) {
+          if (n0 + j >= a.N) continue;
+          float2 v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = unpack2(acc[j / 2 + e]);
+          const size_t at = (size_t)m * a.N + n0 + j;
+          if (a.f32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
+            o[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            o[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 p = __floats2bfloat162_rn(v[e].x, v[e].y);
+              w[e] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kCols);
 }
 
 bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 constexpr int kMaxMq = 1 << 20;
+
+// The tile form of a shape.
+struct LinPlan {
+  int bc;
+  bool swap;
+  int tile_m, tile_n, tiles;
+  size_t counters, partials, total;
+};
+
+LinPlan lin_plan(int M, int N) {
+  LinPlan p;
+  p.swap = M <= 64;
+  p.bc = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  p.tile_m = p.swap ? 1 : (M + 127) / 128;
+  p.tile_n = p.swap ? qblocks(N) : (N + p.bc - 1) / p.bc;
+  p.tiles = p.tile_m * p.tile_n;
+  p.counters = 256;
+  p.partials = align_up(p.counters + sizeof(unsigned) * kLinGrid * (kEpiThreads / 32), 256);
+  p.total = p.partials + sizeof(float) * 2 * kLinGrid * (size_t)p.bc * 128;
+  return p;
+}
+
+// The driver's tensor-map encoder (looked up once; host only).
+vp_status encode_fn(PFN_cuTensorMapEncodeTiled_v12000* fn) {
+  static std::atomic<void*> cached{nullptr};
+  void* p = cached.load();
+  if (!p) {
+    cudaDriverEntryPointQueryResult res;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (res != cudaDriverEntryPointSuccess || !p) return VP_ERR_UNSUPPORTED;
+    cached.store(p);
+  }
+  *fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  return VP_OK;
+}
+
+template <int kBC, bool kSwap>
+cudaError_t launch_linear(const LinArgs& a, const CUtensorMap& map, int grid, cudaStream_t s) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev].load()) {
+    e = cudaFuncSetAttribute(linear_kernel<kBC, kSwap>, cudaFuncAttributeMaxDynamicSharedMemorySize, LinCfg<kBC>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev].store(true);
+  }
+  linear_kernel<kBC, kSwap><<<grid, kLinThreads, LinCfg<kBC>::kSmem, s>>>(a, map);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -91,7 +482,7 @@ extern "C" {
 
 size_t vp_linear_fp8_block_workspace_bytes(int M, int N, int K) {
   if (M < 1 || M > kMaxMq || !q_shape_ok(N, K)) return 0;
-  return 256;
+  return lin_plan(M, N).total;
 }
 
 vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const void* xq, const float* x_scales,
@@ -104,12 +495,43 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
     return VP_ERR_ALIGNMENT;
   if (ws_bytes < need) return VP_ERR_WORKSPACE;
   int sms = 0;
-  const vp_status st = device_sm_count(&sms);
+  vp_status st = device_sm_count(&sms);
   if (st != VP_OK) return st;
-  linear_simple<<<dim3((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64)), 256, 0, (cudaStream_t)stream>>>(
-      static_cast<const uint8_t*>(w_packed), w_scales, static_cast<const uint8_t*>(xq), x_scales, y, y_type == VP_F32,
-      M, N, K);
-  const cudaError_t e = cudaGetLastError();
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  if ((st = encode_fn(&encode)) != VP_OK) return st;
+  const LinPlan p = lin_plan(M, N);
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {kQBlock, (cuuint32_t)(p.swap ? p.bc : 128)}, step[2] = {1, 1};
+  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(xq), dims, strides, box, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return VP_ERR_UNSUPPORTED;
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  LinArgs a;
+  a.w = static_cast<const uint8_t*>(w_packed);
+  a.ws = w_scales;
+  a.xs = x_scales;
+  a.y = y;
+  a.f32 = y_type == VP_F32;
+  a.M = M, a.N = N, a.KB = qblocks(K);
+  a.tiles = p.tiles, a.tile_m = p.tile_m, a.tile_n = p.tile_n;
+  int grid = std::min(sms, kLinGrid);
+  a.dp_rounds = p.tiles / grid;
+  a.sk_tiles = p.tiles - a.dp_rounds * grid;
+  if (a.dp_rounds == 0) grid = (int)std::min<long long>(grid, (long long)p.tiles * a.KB);
+  a.counters = reinterpret_cast<unsigned*>(b + p.counters);
+  a.partials = reinterpret_cast<float*>(b + p.partials);
+  a.status = reinterpret_cast<int*>(b);
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  switch (p.bc) {
+    case 16: e = launch_linear<16, true>(a, map, grid, s); break;
+    case 32: e = launch_linear<32, true>(a, map, grid, s); break;
+    case 64: e = launch_linear<64, true>(a, map, grid, s); break;
+    case 128: e = launch_linear<128, false>(a, map, grid, s); break;
+    default: e = launch_linear<256, false>(a, map, grid, s); break;
+  }
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
 
