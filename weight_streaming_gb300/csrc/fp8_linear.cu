@@ -11,7 +11,7 @@
 //    of 16 KB per 128 rows (packed in the swizzled order).
 //  * tcgen05.mma kind::f8f6f4, 128 lanes x kBC columns, four K = 32 steps per block, into one of
 //    512 / kBC tensor-memory buffers (each block starts from zero); the epilogue warps read the buffer
-//    (tcgen05.ld), scale and accumulate in registers (fma.f32x2) while the next block's MMAs run.
+//    (tcgen05.ld), scale and accumulate in registers while the next block's MMAs run.
 //  * Tokens on the lanes for M > 64 (the factor xs ws is one scalar per thread and block), weights on
 //    the lanes for M <= 64 (16, 32 or 64 token columns; the factors come by shuffles): a small batch
 //    then pads to 16 columns instead of 128 lanes, and the weight stream is what it waits for.
@@ -41,7 +41,7 @@ namespace vp {
 
 namespace {
 
-constexpr int kLinThreads = 320;  // warp 0 copies, warp 1 MMAs, warps 2..9 epilogue
+constexpr int kLinThreads = 384;  // warp 0 copies, warp 1 MMAs, warps 2 and 3 idle, warps 4..11 epilogue
 constexpr int kLinGrid = 152;     // CTAs at most: one per SM
 constexpr int kEpiThreads = 256;
 constexpr int kSmemRing = 216 * 1024;
@@ -140,14 +140,14 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
 }
-// kN consecutive 32-bit columns of the warp's lane, waited for (in one statement: no use of the registers
-// can move in front of the wait).
+// kN consecutive 32-bit columns of the warp's lane: the load, and the wait for it, which takes the
+// registers as operands so that no use of them can move in front of it.
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* r) {
   if constexpr (kN == 32) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
@@ -156,35 +156,37 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t* r) {
         : "memory");
   } else if constexpr (kN == 16) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        " tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(t));
   } else {
     static_assert(kN == 8, "");
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 " tcgen05.wait::ld.sync.aligned;"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(t)
                  : "memory");
   }
 }
-// (acc.x, acc.y) += (lo, hi) * s, elementwise.
-__device__ __forceinline__ void fma2(unsigned long long& acc, uint32_t lo, uint32_t hi, unsigned long long s) {
-  asm("{ .reg .b64 t; mov.b64 t, {%1, %2}; fma.rn.f32x2 %0, t, %3, %0; }" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
+template <int kN>
+__device__ __forceinline__ void tmem_wait(uint32_t* r) {
+  if constexpr (kN == 32) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+  } else if constexpr (kN == 16) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+  }
 }
-__device__ __forceinline__ unsigned long long pack2(float x, float y) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(unsigned long long v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-
 // kBC: columns of a tile (token columns when kSwap, else weight rows).
 template <int kBC, bool kSwap>
 __global__ void __launch_bounds__(kLinThreads, 1)
@@ -226,10 +228,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     return false;
   };
 
-  Sched sched(a);
-  Item it;
-  if (warp == 0) {
-    if (lane == 0) {
+  // Registers: launched at 168 a thread; the four warps that only issue keep 40, the epilogue's eight get
+  // 232 (4 x 40 + 8 x 232 = 12 x 168).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    Sched sched(a);
+    Item it;
+    if (warp == 0 && lane == 0) {
       int n = 0;
       bool ok = true;
       const uint64_t pol = l2_evict_first_policy();
@@ -262,8 +267,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           mbar_wait_bounded(&full[s], last & 1);
         }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    if (warp == 1 && lane == 0) {
       int n = 0;
       bool ok = true;
       while (ok && sched.next(it)) {
@@ -290,9 +294,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    Sched sched(a);
+    Item it;
     constexpr int kW = kBC / 2;                   // columns per warp
-    constexpr int kCh = kW < 32 ? kW : kW == 128 ? 16 : 32;  // columns per load (128 sums leave 168 - 128 registers)
-    const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane, c0 = half * kW;
+    constexpr int kCh = kW < 32 ? kW : 32;        // columns per tensor-memory load
+    const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane, c0 = half * kW;
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + c0;
     int n = 0;
     bool ok = true;
@@ -305,31 +312,41 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const bool live = m < a.M && (!kSwap || lane < kW), wlive = nb < qblocks(a.N);
       const float* px = a.xs + (size_t)(live ? m : 0) * a.KB;
       const float* pw = a.ws + (size_t)(wlive ? nb : 0) * a.KB;
-      unsigned long long acc[kW / 2];
+      float acc[kW];
 #pragma unroll
-      for (int j = 0; j < kW / 2; ++j) acc[j] = 0;
-      float f_next = live && wlive ? __ldg(px + it.kb0) * __ldg(pw + it.kb0) : 0.0f;
+      for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
+      // the next block's factors are on their way while this one is waited for
+      float fx = 0.0f, fw = 0.0f;
+      if (live) fx = __ldg(px + it.kb0);
+      if (wlive) fw = __ldg(pw + it.kb0);
       for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
         const int b = n % C::kBufs;
-        const float f = f_next;
-        if (kb + 1 < it.kb1 && live && wlive) f_next = __ldg(px + kb + 1) * __ldg(pw + kb + 1);
+        const float f = fx * fw;
+        if (kb + 1 < it.kb1) {
+          if (live) fx = __ldg(px + kb + 1);
+          if (wlive) fw = __ldg(pw + kb + 1);
+        }
         ok = __all_sync(0xFFFFFFFFu, wait(&tfull[b], (n / C::kBufs) & 1));
         if (!ok) break;
         tmem_fence_after();
+        // chunk by chunk; the next chunk's load is in flight while this one is accumulated
+        constexpr int kNCh = kW / kCh;
+        uint32_t r[2][kCh];
+        tmem_ld<kCh>(tm + b * kBC, r[0]);
 #pragma unroll
-        for (int ch = 0; ch < kW; ch += kCh) {
-          uint32_t r[kCh];
-          tmem_ld<kCh>(tm + b * kBC + ch, r);
-          if (ch + kCh == kW) {  // the buffer is read: the next MMAs may have it
+        for (int i = 0; i < kNCh; ++i) {
+          tmem_wait<kCh>(r[i & 1]);
+          if (i + 1 < kNCh) {
+            tmem_ld<kCh>(tm + b * kBC + (i + 1) * kCh, r[(i + 1) & 1]);
+          } else {  // the buffer is read: the next MMAs may have it
             tmem_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[b]);
           }
 #pragma unroll
-          for (int j = 0; j < kCh; j += 2) {
-            const unsigned long long s = kSwap ? pack2(__shfl_sync(0xFFFFFFFFu, f, ch + j), __shfl_sync(0xFFFFFFFFu, f, ch + j + 1))
-                                               : pack2(f, f);
-            fma2(acc[(ch + j) / 2], r[j], r[j + 1], s);
+          for (int j = 0; j < kCh; ++j) {
+            const int col = i * kCh + j;
+            acc[col] = fmaf(__uint_as_float(r[i & 1][j]), kSwap ? __shfl_sync(0xFFFFFFFFu, f, col) : f, acc[col]);
           }
         }
       }
@@ -341,47 +358,36 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int first = (int)(((u0 + 1) * G - 1) / U), last = (int)(((u0 + a.KB) * G - 1) / U);
         float* mine = a.partials + ((size_t)blockIdx.x * 2 + (it.kb0 == 0)) * kBC * 128;
 #pragma unroll
-        for (int j = 0; j < kW / 2; ++j) {
-          const float2 v = unpack2(acc[j]);
-          __stcg(mine + (c0 + 2 * j) * 128 + row, v.x);
-          __stcg(mine + (c0 + 2 * j + 1) * 128 + row, v.y);
-        }
+        for (int j = 0; j < kW; ++j) __stcg(mine + (c0 + j) * 128 + row, acc[j]);
         __threadfence();
         __syncwarp();
         // each warp joins its own part of the tile (8 counters per tile): no CTA-wide wait
         unsigned old = 0;
-        if (lane == 0) old = atom_add_acq_rel_gpu(a.counters + it.sk * 8 + warp - 2, 1);
+        if (lane == 0) old = atom_add_acq_rel_gpu(a.counters + it.sk * 8 + warp - 4, 1);
         const bool join = __shfl_sync(0xFFFFFFFFu, old, 0) == (unsigned)(last - first);
         if (!join) continue;
-        if (lane == 0) a.counters[it.sk * 8 + warp - 2] = 0;  // every contributor has arrived
+        if (lane == 0) a.counters[it.sk * 8 + warp - 4] = 0;  // every contributor has arrived
         __threadfence();
 #pragma unroll
-        for (int j = 0; j < kW / 2; ++j) acc[j] = 0;
+        for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
         for (int c = first; c <= last; ++c) {
           const float* p = a.partials + ((size_t)c * 2 + (c == first)) * kBC * 128 + row;
 #pragma unroll
-          for (int j = 0; j < kW / 2; ++j) {
-            const float2 v = unpack2(acc[j]);
-            acc[j] = pack2(v.x + __ldcg(p + (c0 + 2 * j) * 128), v.y + __ldcg(p + (c0 + 2 * j + 1) * 128));
-          }
+          for (int j = 0; j < kW; ++j) acc[j] += __ldcg(p + (c0 + j) * 128);
         }
       }
       if (kSwap) {
         const int nn = nt * 128 + row;
         if (nn < a.N) {
 #pragma unroll
-          for (int j = 0; j < kW / 2; ++j) {
-            const float2 v = unpack2(acc[j]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int mm = mt * kBC + c0 + 2 * j + e;
-              if (mm >= a.M) continue;
-              const size_t at = (size_t)mm * a.N + nn;
-              if (a.f32)
-                static_cast<float*>(a.y)[at] = e ? v.y : v.x;
-              else
-                static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(e ? v.y : v.x);
-            }
+          for (int j = 0; j < kW; ++j) {
+            const int mm = mt * kBC + c0 + j;
+            if (mm >= a.M) continue;
+            const size_t at = (size_t)mm * a.N + nn;
+            if (a.f32)
+              static_cast<float*>(a.y)[at] = acc[j];
+            else
+              static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(acc[j]);
           }
         }
       } else if (m < a.M) {
@@ -389,19 +395,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
         for (int j = 0; j < kW; j += 8) {
           if (n0 + j >= a.N) continue;
-          float2 v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = unpack2(acc[j / 2 + e]);
           const size_t at = (size_t)m * a.N + n0 + j;
           if (a.f32) {
             float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.y) + at);
-            o[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-            o[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+            o[0] = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+            o[1] = make_float4(acc[j + 4], acc[j + 5], acc[j + 6], acc[j + 7]);
           } else {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 p = __floats2bfloat162_rn(v[e].x, v[e].y);
+              const __nv_bfloat162 p = __floats2bfloat162_rn(acc[j + 2 * e], acc[j + 2 * e + 1]);
               w[e] = *reinterpret_cast<const uint32_t*>(&p);
             }
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
