@@ -5,7 +5,9 @@
 // exact in fp32 (e4m3 has 4 significant bits); the scales differ from block to block, so each inner
 // sum of 128 products leaves the tensor core's accumulator, is scaled and added to an fp32 register.
 //
-// Design: one persistent CTA per SM; a producer warp, an MMA warp and eight epilogue warps.
+// Design: one persistent CTA per SM; a producer warp, an MMA warp and eight epilogue warps.  Above 128
+// tokens two CTAs form a pair (cta_group::2) on a tile of 256 tokens x 256 weight rows: each loads its
+// 128 tokens and half of the weights, 32 KB a K block in place of 48 KB.
 //  * Operands: one stage of the shared-memory ring is one 128-wide K block: the tokens by a tiled TMA
 //    load (128-byte swizzle; rows past M and columns past K read zero), the weights by one bulk copy
 //    of 16 KB per 128 rows (packed in the swizzled order).
@@ -54,18 +56,20 @@ struct LinArgs {
   int f32, M, N, KB;
   int tiles, tile_m, tile_n;  // output tiles: in all, along the tokens, along the weight rows
   int dp_rounds, sk_tiles;    // whole rounds per CTA; tiles cut along K (after the first dp_rounds * grid)
-  unsigned* counters;         // [sk_tiles][8 epilogue warps]
+  int sk_ctas;                // CTAs (pairs) that these are cut among: each has at least one K block
+  unsigned* counters;         // [sk_tiles][2 CTAs of a pair][8 epilogue warps]
   float* partials;            // [grid][2][kBC][128]
   int* status;
 };
 
-template <int kBC>
+template <int kBC, bool kPair>
 struct LinCfg {
-  static constexpr int kStage = 16384 + kBC * 128;
-  static constexpr int kStages = kSmemRing / kStage < kMaxStages ? kSmemRing / kStage : kMaxStages;
+  static constexpr int kStage = 16384 + (kPair ? kBC / 2 : kBC) * 128;  // a pair's CTAs hold half of the columns each
+  static constexpr int kStages = kPair ? 5 : kSmemRing / kStage < kMaxStages ? kSmemRing / kStage : kMaxStages;
+  static constexpr int kOut = kPair ? 8 * 8192 : 0;  // output staging: 8 KB per epilogue warp
   static constexpr int kBufs = 512 / kBC < 8 ? 512 / kBC : 8;
   static constexpr int kCols = kBC * kBufs;   // tensor-memory columns (a power of two >= 128)
-  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kSmem = kStages * kStage + kOut + 1024;
 };
 
 struct Item {
@@ -75,11 +79,16 @@ struct Item {
 struct Sched {
   int c, G, KB, i, dp, base;
   int u, u1;
-  __device__ Sched(const LinArgs& a) : c(blockIdx.x), G(gridDim.x), KB(a.KB), i(0), dp(a.dp_rounds) {
+  // pair: the CTAs 2 c and 2 c + 1 work on the same tiles
+  __device__ Sched(const LinArgs& a, int pair)
+      : c(blockIdx.x >> pair), G(gridDim.x >> pair), KB(a.KB), i(0), dp(a.dp_rounds) {
     base = dp * G;
     const long long U = (long long)a.sk_tiles * KB;
-    u = (int)(c * U / G);
-    u1 = (int)((c + 1) * U / G);
+    u = u1 = 0;
+    if (c < a.sk_ctas) {
+      u = (int)(c * U / a.sk_ctas);
+      u1 = (int)((c + 1) * U / a.sk_ctas);
+    }
   }
   __device__ bool next(Item& it) {
     if (i < dp) {
@@ -125,17 +134,94 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
+template <bool kPair>
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// Arrives on `bar` (in both CTAs of a pair, at the same offset) when every MMA issued so far by this thread
+// has completed.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void lin_tmem_alloc(uint32_t* dst, uint32_t cols) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, cols);
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void lin_tmem_dealloc(uint32_t t, uint32_t cols) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
+  else
+    tmem_dealloc(t, cols);
+}
+// Pair forms: loads into this CTA's shared memory that complete on a barrier of the pair's first CTA, the
+// address of that CTA's copy of a variable, an arrival there, and the pair's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// Arrives on `bar` when every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+               "r"(y), "r"(src)
                : "memory");
+}
+__device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
@@ -187,17 +273,21 @@ __device__ __forceinline__ void tmem_wait(uint32_t* r) {
                  : "memory");
   }
 }
-// kBC: columns of a tile (token columns when kSwap, else weight rows).
-template <int kBC, bool kSwap>
+// kBC: columns of a tile (token columns when kSwap, else weight rows).  kPair: two CTAs (a cluster) work
+// on one tile of 256 tokens x 256 weight rows, 128 tokens' sums in each one's tensor memory; the first
+// CTA's MMA warp issues for both.
+template <int kBC, bool kSwap, bool kPair>
 __global__ void __launch_bounds__(kLinThreads, 1)
-    linear_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ CUtensorMap xmap) {
-  using C = LinCfg<kBC>;
+    linear_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ CUtensorMap xmap,
+                  const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap ymap) {
+  using C = LinCfg<kBC, kPair>;
   extern __shared__ uint8_t dyn[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], tfull[8], tempty[8], drain;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -205,15 +295,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], kEpiThreads / 32);
+      mbar_init(&tempty[b], (kPair ? 2 : 1) * kEpiThreads / 32);
     }
     mbar_init(&drain, 1);
     s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&s_tmem, C::kCols);
+  if (warp == 1) lin_tmem_alloc<kPair>(&s_tmem, C::kCols);
   tmem_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();  // the other CTA's barriers exist
   tmem_fence_after();
   const uint32_t tmem = *(volatile uint32_t*)&s_tmem;
 
@@ -232,70 +323,89 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // 232 (4 x 40 + 8 x 232 = 12 x 168).
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    Sched sched(a);
+    Sched sched(a, kPair);
     Item it;
-    if (warp == 0 && lane == 0) {
+    // Whole warps run the two issuing loops, one elected lane issues: the operands stay warp-uniform.
+    if (warp == 0) {
       int n = 0;
       bool ok = true;
       const uint64_t pol = l2_evict_first_policy();
       while (ok && sched.next(it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
-        // weight tiles of this output tile: one, or up to kBC / 128
-        const int nb = kSwap ? nt : nt * (kBC / 128), nbs = kSwap ? 1 : min(kBC / 128, qblocks(a.N) - nb);
-        const int rows = kSwap ? kBC : 128;
+        // weight tiles of this output tile: one, or up to kBC / 128 (a pair's CTAs take one each; past the
+        // last row block the last one again, whose products are not stored)
+        const int nbs = kSwap || kPair ? 1 : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128));
+        const int nb = kSwap ? nt : kPair ? min(2 * nt + rank, qblocks(a.N) - 1) : nt * (kBC / 128);
+        const int rows = kSwap ? kBC : 128, m0 = kPair ? mt * 256 + rank * 128 : mt * rows;
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
           const int s = n % C::kStages;
-          if (!(ok = wait(&empty[s], ((n / C::kStages) & 1) ^ 1))) break;
-          const uint32_t st = ring + s * C::kStage, bar = smem_addr(&full[s]);
-          // lanes' operand first (16 KB), columns' operand behind it
-          const uint32_t dst_w = kSwap ? st : st + 16384, dst_x = kSwap ? st + 16384 : st;
-          mbar_arrive_expect_tx(&full[s], rows * 128 + nbs * kQTileBytes);
-          tma_load_2d(dst_x, &xmap, kb * kQBlock, mt * rows, bar);
-          for (int i = 0; i < nbs; ++i) {
-            const uint8_t* src = a.w + ((size_t)(nb + i) * a.KB + kb) * kQTileBytes;
-            if (a.tile_m == 1)  // each weight byte is read once
-              bulk_g2s(dst_w + i * kQTileBytes, src, kQTileBytes, bar, pol);
-            else
-              bulk_load(dst_w + i * kQTileBytes, src, kQTileBytes, bar);
+          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], ((n / C::kStages) & 1) ^ 1)))) break;
+          if (elect_one()) {
+            const uint32_t st = ring + s * C::kStage;
+            // lanes' operand first (16 KB), columns' operand behind it
+            const uint32_t dst_w = kSwap ? st : st + 16384, dst_x = kSwap ? st + 16384 : st;
+            if constexpr (kPair) {
+              const uint32_t bar = leader_addr(smem_addr(&full[s]));
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);  // both CTAs' copies
+              tma_load_2d_pair(dst_x, &xmap, kb * kQBlock, m0, bar);
+              tma_load_3d_pair(dst_w, &wmap, 0, 0, nb * a.KB + kb, bar);
+            } else {
+              const uint32_t bar = smem_addr(&full[s]);
+              mbar_arrive_expect_tx(&full[s], rows * 128 + nbs * kQTileBytes);
+              tma_load_2d(dst_x, &xmap, kb * kQBlock, m0, bar);
+              for (int i = 0; i < nbs; ++i) {
+                const uint8_t* src = a.w + ((size_t)(nb + i) * a.KB + kb) * kQTileBytes;
+                if (a.tile_m == 1)  // each weight byte is read once
+                  bulk_g2s(dst_w + i * kQTileBytes, src, kQTileBytes, bar, pol);
+                else
+                  bulk_load(dst_w + i * kQTileBytes, src, kQTileBytes, bar);
+              }
+            }
           }
+          __syncwarp();
         }
       }
-      if (!ok)  // the copies in flight land before the CTA's shared memory goes
+      if (!ok && rank == 0)  // the copies in flight land before the shared memory goes
         for (int s = 0; s < min(n, C::kStages); ++s) {
           const int last = (n - 1 - s) / C::kStages;
           mbar_wait_bounded(&full[s], last & 1);
         }
     }
-    if (warp == 1 && lane == 0) {
+    if (warp == 1 && rank == 0) {
       int n = 0;
       bool ok = true;
       while (ok && sched.next(it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
-        const int cols = kSwap ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
-        const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (128u >> 4) << 24;  // e4m3 x e4m3 -> fp32
+        const int cols = kSwap || kPair ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
+        // e4m3 x e4m3 -> fp32, 128 rows (a pair's two CTAs: 256)
+        const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (kPair ? 16u : 8u) << 24;
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
           const int s = n % C::kStages, b = n % C::kBufs;
-          if (!(ok = wait(&tempty[b], ((n / C::kBufs) & 1) ^ 1))) break;
-          if (!(ok = wait(&full[s], (n / C::kStages) & 1))) break;
-          tmem_fence_after();
           const uint64_t da = smem_desc(ring + s * C::kStage), db = smem_desc(ring + s * C::kStage + 16384);
+          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&full[s], (n / C::kStages) & 1)))) break;
+          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&tempty[b], ((n / C::kBufs) & 1) ^ 1)))) break;
+          tmem_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 32 bytes along K inside the swizzle atom
-            mma_f8(tmem + b * kBC, da + 2 * k, db + 2 * k, idesc, k > 0);
-          mma_commit(&empty[s]);
-          mma_commit(&tfull[b]);
+            for (int k = 0; k < 4; ++k)  // 32 bytes along K inside the swizzle atom
+              mma_f8<kPair>(tmem + b * kBC, da + 2 * k, db + 2 * k, idesc, k > 0);
+            mma_commit<kPair>(&tfull[b]);
+            mma_commit<kPair>(&empty[s]);
+          }
+          __syncwarp();
         }
       }
       if (!ok) {
-        mma_commit(&drain);
+        if (elect_one()) mma_commit<kPair>(&drain);
+        __syncwarp();
         mbar_wait_bounded(&drain, 0);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    Sched sched(a);
+    Sched sched(a, kPair);
     Item it;
     constexpr int kW = kBC / 2;                   // columns per warp
     constexpr int kCh = kW < 32 ? kW : 32;        // columns per tensor-memory load
@@ -307,7 +417,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int mt, nt;
       tile_at(a, it.tile, mt, nt);
       // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there)
-      const int m = kSwap ? mt * kBC + c0 + lane : mt * 128 + row;
+      const int m = kSwap ? mt * kBC + c0 + lane : kPair ? mt * 256 + rank * 128 + row : mt * 128 + row;
       const int nb = kSwap ? nt : nt * (kBC / 128) + (kBC == 256 ? half : 0);
       const bool live = m < a.M && (!kSwap || lane < kW), wlive = nb < qblocks(a.N);
       const float* px = a.xs + (size_t)(live ? m : 0) * a.KB;
@@ -341,7 +451,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           } else {  // the buffer is read: the next MMAs may have it
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[b]);
+            if (lane == 0) {
+              if (kPair)
+                mbar_arrive_cluster(leader_addr(smem_addr(&tempty[b])));
+              else
+                mbar_arrive(&tempty[b]);
+            }
           }
 #pragma unroll
           for (int j = 0; j < kCh; ++j) {
@@ -353,7 +468,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       if (!ok) break;
       if (it.kb0 > 0 || it.kb1 < a.KB) {
         // a part of the tile's K blocks: leave it, and let the last contributor add them up
-        const int G = gridDim.x;
+        const int G = a.sk_ctas;
         const long long U = (long long)a.sk_tiles * a.KB, u0 = (long long)it.sk * a.KB;
         const int first = (int)(((u0 + 1) * G - 1) / U), last = (int)(((u0 + a.KB) * G - 1) / U);
         float* mine = a.partials + ((size_t)blockIdx.x * 2 + (it.kb0 == 0)) * kBC * 128;
@@ -363,15 +478,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         __syncwarp();
         // each warp joins its own part of the tile (8 counters per tile): no CTA-wide wait
         unsigned old = 0;
-        if (lane == 0) old = atom_add_acq_rel_gpu(a.counters + it.sk * 8 + warp - 4, 1);
+        if (lane == 0) old = atom_add_acq_rel_gpu(a.counters + (it.sk * 2 + rank) * 8 + warp - 4, 1);
         const bool join = __shfl_sync(0xFFFFFFFFu, old, 0) == (unsigned)(last - first);
         if (!join) continue;
-        if (lane == 0) a.counters[it.sk * 8 + warp - 4] = 0;  // every contributor has arrived
+        if (lane == 0) a.counters[(it.sk * 2 + rank) * 8 + warp - 4] = 0;  // every contributor has arrived
         __threadfence();
 #pragma unroll
         for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
         for (int c = first; c <= last; ++c) {
-          const float* p = a.partials + ((size_t)c * 2 + (c == first)) * kBC * 128 + row;
+          const int cta = kPair ? 2 * c + rank : c;
+          const float* p = a.partials + ((size_t)cta * 2 + (c == first)) * kBC * 128 + row;
 #pragma unroll
           for (int j = 0; j < kW; ++j) acc[j] += __ldcg(p + (c0 + j) * 128);
         }
@@ -389,6 +505,61 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             else
               static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(acc[j]);
           }
+        }
+      } else if (kPair) {
+        // through shared memory (128-byte swizzled rows) to asynchronous tile stores, which cut off at M and N
+        const uint32_t stage = ring + C::kStages * C::kStage + (warp - 4) * 8192;
+        const int y0 = mt * 256 + rank * 128 + quad * 32;
+        const uint32_t swz = (uint32_t)(lane & 7);
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging's last stores have read it
+        __syncwarp();
+        if (a.f32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {  // boxes of 32 columns
+            const uint32_t box = stage + (q & 1) * 4096, r = box + lane * 128;
+            if (q == 2) {
+              asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              sts128(r + ((c ^ swz) << 4), make_uint4(__float_as_uint(acc[32 * q + 4 * c]), __float_as_uint(acc[32 * q + 4 * c + 1]),
+                                                      __float_as_uint(acc[32 * q + 4 * c + 2]), __float_as_uint(acc[32 * q + 4 * c + 3])));
+            fence_proxy_async_smem();
+            __syncwarp();
+            const int x = nt * 256 + half * 128 + q * 32;
+            if (elect_one()) {
+              if (y0 < a.M && x < a.N) tma_store_2d(&ymap, x, y0, box);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            __syncwarp();
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {  // boxes of 64 columns
+            const uint32_t box = stage + q * 4096, r = box + lane * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(acc[64 * q + 8 * c + 2 * e], acc[64 * q + 8 * c + 2 * e + 1]);
+                w[e] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+              sts128(r + ((c ^ swz) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int x = nt * 256 + half * 128 + q * 64;
+              if (y0 < a.M && x < a.N) tma_store_2d(&ymap, x, y0, stage + q * 4096);
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          __syncwarp();
         }
       } else if (m < a.M) {
         const int n0 = nt * kBC + c0;
@@ -413,11 +584,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
     }
   }
+  if (kPair) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the thread's output stores are done
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();  // nobody reads or signals this CTA's shared memory any more
   tmem_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::kCols);
+  if (warp == 1) lin_tmem_dealloc<kPair>(tmem, C::kCols);
 }
 
 bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -427,7 +600,7 @@ constexpr int kMaxMq = 1 << 20;
 // The tile form of a shape.
 struct LinPlan {
   int bc;
-  bool swap;
+  bool swap, pair;
   int tile_m, tile_n, tiles;
   size_t counters, partials, total;
 };
@@ -435,12 +608,13 @@ struct LinPlan {
 LinPlan lin_plan(int M, int N) {
   LinPlan p;
   p.swap = M <= 64;
+  p.pair = M > 128;
   p.bc = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  p.tile_m = p.swap ? 1 : (M + 127) / 128;
+  p.tile_m = p.swap ? 1 : p.pair ? (M + 255) / 256 : 1;
   p.tile_n = p.swap ? qblocks(N) : (N + p.bc - 1) / p.bc;
   p.tiles = p.tile_m * p.tile_n;
   p.counters = 256;
-  p.partials = align_up(p.counters + sizeof(unsigned) * kLinGrid * (kEpiThreads / 32), 256);
+  p.partials = align_up(p.counters + sizeof(unsigned) * kLinGrid * 2 * (kEpiThreads / 32), 256);
   p.total = p.partials + sizeof(float) * 2 * kLinGrid * (size_t)p.bc * 128;
   return p;
 }
@@ -460,19 +634,31 @@ vp_status encode_fn(PFN_cuTensorMapEncodeTiled_v12000* fn) {
   return VP_OK;
 }
 
-template <int kBC, bool kSwap>
-cudaError_t launch_linear(const LinArgs& a, const CUtensorMap& map, int grid, cudaStream_t s) {
+template <int kBC, bool kSwap, bool kPair>
+cudaError_t launch_linear(const LinArgs& a, const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& ymap,
+                          int grid, cudaStream_t s) {
+  constexpr int kSmem = LinCfg<kBC, kPair>::kSmem;
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !done[dev].load()) {
-    e = cudaFuncSetAttribute(linear_kernel<kBC, kSwap>, cudaFuncAttributeMaxDynamicSharedMemorySize, LinCfg<kBC>::kSmem);
+    e = cudaFuncSetAttribute(linear_kernel<kBC, kSwap, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(true);
   }
-  linear_kernel<kBC, kSwap><<<grid, kLinThreads, LinCfg<kBC>::kSmem, s>>>(a, map);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kPair ? 2 : 1;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<kBC, kSwap, kPair>, a, xmap, wmap, ymap);
 }
 
 }  // namespace
@@ -503,13 +689,33 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   if ((st = encode_fn(&encode)) != VP_OK) return st;
   const LinPlan p = lin_plan(M, N);
-  CUtensorMap map;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)K};
-  const cuuint32_t box[2] = {kQBlock, (cuuint32_t)(p.swap ? p.bc : 128)}, step[2] = {1, 1};
-  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(xq), dims, strides, box, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return VP_ERR_UNSUPPORTED;
+  CUtensorMap xmap, wmap, ymap;
+  {
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)M}, strides[1] = {(cuuint64_t)K};
+    const cuuint32_t box[2] = {kQBlock, (cuuint32_t)(p.swap ? p.bc : 128)}, step[2] = {1, 1};
+    if (encode(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(xq), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return VP_ERR_UNSUPPORTED;
+  }
+  if (p.pair) {  // one packed tile per box (already in the swizzled order)
+    const cuuint64_t dims[3] = {kQBlock, kQBlock, (cuuint64_t)qblocks(N) * qblocks(K)};
+    const cuuint64_t strides[2] = {kQBlock, kQTileBytes};
+    const cuuint32_t box[3] = {kQBlock, kQBlock, 1}, step[3] = {1, 1, 1};
+    if (encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w_packed), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return VP_ERR_UNSUPPORTED;
+    const bool f32 = y_type == VP_F32;  // boxes of 128 bytes x 32 rows
+    const cuuint64_t ydims[2] = {(cuuint64_t)N, (cuuint64_t)M}, ystrides[1] = {(cuuint64_t)N * (f32 ? 4 : 2)};
+    const cuuint32_t ybox[2] = {f32 ? 32u : 64u, 32u}, ystep[2] = {1, 1};
+    if (encode(&ymap, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, ydims, ystrides, ybox,
+               ystep, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return VP_ERR_UNSUPPORTED;
+  } else {
+    wmap = ymap = xmap;
+  }
   uint8_t* b = static_cast<uint8_t*>(ws);
   LinArgs a;
   a.w = static_cast<const uint8_t*>(w_packed);
@@ -519,21 +725,23 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   a.f32 = y_type == VP_F32;
   a.M = M, a.N = N, a.KB = qblocks(K);
   a.tiles = p.tiles, a.tile_m = p.tile_m, a.tile_n = p.tile_n;
-  int grid = std::min(sms, kLinGrid);
+  int grid = std::min(sms, kLinGrid) / (p.pair ? 2 : 1);  // CTAs, or pairs
   a.dp_rounds = p.tiles / grid;
   a.sk_tiles = p.tiles - a.dp_rounds * grid;
-  if (a.dp_rounds == 0) grid = (int)std::min<long long>(grid, (long long)p.tiles * a.KB);
+  a.sk_ctas = (int)std::min<long long>(grid, (long long)a.sk_tiles * a.KB);
+  if (a.dp_rounds == 0) grid = a.sk_ctas;
+  if (p.pair) grid *= 2;
   a.counters = reinterpret_cast<unsigned*>(b + p.counters);
   a.partials = reinterpret_cast<float*>(b + p.partials);
   a.status = reinterpret_cast<int*>(b);
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   switch (p.bc) {
-    case 16: e = launch_linear<16, true>(a, map, grid, s); break;
-    case 32: e = launch_linear<32, true>(a, map, grid, s); break;
-    case 64: e = launch_linear<64, true>(a, map, grid, s); break;
-    case 128: e = launch_linear<128, false>(a, map, grid, s); break;
-    default: e = launch_linear<256, false>(a, map, grid, s); break;
+    case 16: e = launch_linear<16, true, false>(a, xmap, wmap, ymap, grid, s); break;
+    case 32: e = launch_linear<32, true, false>(a, xmap, wmap, ymap, grid, s); break;
+    case 64: e = launch_linear<64, true, false>(a, xmap, wmap, ymap, grid, s); break;
+    case 128: e = launch_linear<128, false, false>(a, xmap, wmap, ymap, grid, s); break;
+    default: e = launch_linear<256, false, true>(a, xmap, wmap, ymap, grid, s); break;
   }
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
