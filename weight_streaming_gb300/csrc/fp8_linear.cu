@@ -54,6 +54,7 @@ struct LinArgs {
   const float *ws, *xs;
   void* y;
   int f32, M, N, KB;
+  int vec_x, vec_w;           // the scales' rows can be read 16 bytes at a time
   int tiles, tile_m, tile_n;  // output tiles: in all, along the tokens, along the weight rows
   int dp_rounds, sk_tiles;    // whole rounds per CTA; tiles cut along K (after the first dp_rounds * grid)
   int sk_ctas;                // CTAs (pairs) that these are cut among: each has at least one K block
@@ -209,6 +210,47 @@ __device__ __forceinline__ uint32_t leader_addr(uint32_t a) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// The rest of a bounded wait of a converged warp.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int* abort, int* status) {
+  for (uint32_t i = 0; i < kMbarPolls; ++i) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(20000u)
+                 : "memory");
+    if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
+    if (__any_sync(0xFFFFFFFFu, *(volatile int*)abort)) return false;
+  }
+  *(volatile int*)abort = 1;
+  atomicExch(status, (int)VP_ERR_TIMEOUT);
+  return false;
+}
+// acc += x * f, in its place among the volatile loads.
+__device__ __forceinline__ void fma_here(float& acc, uint32_t x, float f) {
+  asm volatile("fma.rn.f32 %0, %1, %2, %0;" : "+f"(acc) : "f"(__uint_as_float(x)), "f"(f));
+}
+// p[k .. k + 3] as far as it lies before n (k a multiple of 4; vec: p + k is 16-byte aligned and n too).
+__device__ __forceinline__ float4 load4(const float* p, int k, int n, int vec) {
+  if (vec) return __ldg(reinterpret_cast<const float4*>(p + k));
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  v.x = __ldg(p + k);
+  if (k + 1 < n) v.y = __ldg(p + k + 1);
+  if (k + 2 < n) v.z = __ldg(p + k + 2);
+  if (k + 3 < n) v.w = __ldg(p + k + 3);
+  return v;
+}
+__device__ __forceinline__ float pick4(const float4& v, int k) {
+  const float lo = k & 1 ? v.y : v.x, hi = k & 1 ? v.w : v.z;
+  return k & 2 ? hi : lo;
+}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -223,8 +265,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar) : "memory");
 }
 // kN consecutive 32-bit columns of the warp's lane: the load, and the wait for it, which takes the
 // registers as operands so that no use of them can move in front of it.
@@ -308,15 +350,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = *(volatile uint32_t*)&s_tmem;
 
-  // A bounded wait; false when it ran out here or elsewhere in the CTA.
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    for (uint32_t i = 0; i < kMbarPolls; ++i) {
-      if (mbar_try_wait_hint(bar, parity, 20000u)) return true;
-      if (*(volatile int*)&s_abort) return false;
-    }
-    *(volatile int*)&s_abort = 1;
-    atomicExch(a.status, (int)VP_ERR_TIMEOUT);
-    return false;
+  // A bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
+    return wait_slow(bar, parity, &s_abort, a.status);
   };
 
   // Registers: launched at 168 a thread; the four warps that only issue keep 40, the epilogue's eight get
@@ -327,7 +364,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     Item it;
     // Whole warps run the two issuing loops, one elected lane issues: the operands stay warp-uniform.
     if (warp == 0) {
-      int n = 0;
+      int n = 0, s = 0;
+      uint32_t par = 1;  // of the empty barriers: the first round passes
       bool ok = true;
       const uint64_t pol = l2_evict_first_policy();
       while (ok && sched.next(it)) {
@@ -339,8 +377,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int nb = kSwap ? nt : kPair ? min(2 * nt + rank, qblocks(a.N) - 1) : nt * (kBC / 128);
         const int rows = kSwap ? kBC : 128, m0 = kPair ? mt * 256 + rank * 128 : mt * rows;
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-          const int s = n % C::kStages;
-          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&empty[s], ((n / C::kStages) & 1) ^ 1)))) break;
+          if (!(ok = wait(smem_addr(&empty[s]), par))) break;
           if (elect_one()) {
             const uint32_t st = ring + s * C::kStage;
             // lanes' operand first (16 KB), columns' operand behind it
@@ -364,6 +401,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
           }
           __syncwarp();
+          if (++s == C::kStages) s = 0, par ^= 1;
         }
       }
       if (!ok && rank == 0)  // the copies in flight land before the shared memory goes
@@ -373,7 +411,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
     }
     if (warp == 1 && rank == 0) {
-      int n = 0;
+      int s = 0, b = 0;
+      uint32_t par = 0, tpar = 1;
       bool ok = true;
       while (ok && sched.next(it)) {
         int mt, nt;
@@ -381,11 +420,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int cols = kSwap || kPair ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
         // e4m3 x e4m3 -> fp32, 128 rows (a pair's two CTAs: 256)
         const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (kPair ? 16u : 8u) << 24;
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-          const int s = n % C::kStages, b = n % C::kBufs;
-          const uint64_t da = smem_desc(ring + s * C::kStage), db = smem_desc(ring + s * C::kStage + 16384);
-          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&full[s], (n / C::kStages) & 1)))) break;
-          if (!(ok = __all_sync(0xFFFFFFFFu, wait(&tempty[b], ((n / C::kBufs) & 1) ^ 1)))) break;
+        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+          const uint64_t da = smem_desc(ring) + (uint64_t)(s * (C::kStage >> 4)), db = da + (16384 >> 4);
+          if (!(ok = wait(smem_addr(&full[s]), par))) break;
+          if (!(ok = wait(smem_addr(&tempty[b]), tpar))) break;
           tmem_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -395,6 +433,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mma_commit<kPair>(&empty[s]);
           }
           __syncwarp();
+          if (++s == C::kStages) s = 0, par ^= 1;
+          if (++b == C::kBufs) b = 0, tpar ^= 1;
         }
       }
       if (!ok) {
@@ -411,59 +451,60 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     constexpr int kCh = kW < 32 ? kW : 32;        // columns per tensor-memory load
     const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane, c0 = half * kW;
     const uint32_t tm = tmem + ((uint32_t)(quad * 32) << 16) + c0;
-    int n = 0;
+    const uint32_t tfull0 = smem_addr(tfull), tempty0 = kPair ? leader_addr(smem_addr(tempty)) : smem_addr(tempty);
+    int b = 0;
+    uint32_t par = 0;
     bool ok = true;
     while (ok && sched.next(it)) {
       int mt, nt;
       tile_at(a, it.tile, mt, nt);
-      // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there)
+      // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there); what is
+      // past the last row or column is computed with another's factor and not stored
       const int m = kSwap ? mt * kBC + c0 + lane : kPair ? mt * 256 + rank * 128 + row : mt * 128 + row;
       const int nb = kSwap ? nt : nt * (kBC / 128) + (kBC == 256 ? half : 0);
-      const bool live = m < a.M && (!kSwap || lane < kW), wlive = nb < qblocks(a.N);
-      const float* px = a.xs + (size_t)(live ? m : 0) * a.KB;
-      const float* pw = a.ws + (size_t)(wlive ? nb : 0) * a.KB;
+      const float* px = a.xs + (size_t)min(m, a.M - 1) * a.KB;
+      const float* pw = a.ws + (size_t)min(nb, qblocks(a.N) - 1) * a.KB;
       float acc[kW];
 #pragma unroll
       for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-      // the next block's factors are on their way while this one is waited for
-      float fx = 0.0f, fw = 0.0f;
-      if (live) fx = __ldg(px + it.kb0);
-      if (wlive) fw = __ldg(pw + it.kb0);
-      for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
-        const int b = n % C::kBufs;
-        const float f = fx * fw;
-        if (kb + 1 < it.kb1) {
-          if (live) fx = __ldg(px + kb + 1);
-          if (wlive) fw = __ldg(pw + kb + 1);
-        }
-        ok = __all_sync(0xFFFFFFFFu, wait(&tfull[b], (n / C::kBufs) & 1));
-        if (!ok) break;
+      // Factors of four blocks at a time: each of a warp's 32 rows is a cache line of its own, so a load per
+      // block would keep the load unit busy for 256 cycles of the block's 512.
+      float4 fx = load4(px, it.kb0 & ~3, a.KB, a.vec_x), fw = load4(pw, it.kb0 & ~3, a.KB, a.vec_w);
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
+        if (!(ok = wait(tfull0 + 8 * b, par))) break;
         tmem_fence_after();
+        const uint32_t tb = tm + b * kBC;
         // chunk by chunk; the next chunk's load is in flight while this one is accumulated
         constexpr int kNCh = kW / kCh;
         uint32_t r[2][kCh];
-        tmem_ld<kCh>(tm + b * kBC, r[0]);
+        tmem_ld<kCh>(tb, r[0]);
+        const float f = pick4(fx, kb) * pick4(fw, kb);
+        if ((kb & 3) == 3 && kb + 1 < it.kb1) {
+          fx = load4(px, kb + 1, a.KB, a.vec_x);
+          fw = load4(pw, kb + 1, a.KB, a.vec_w);
+        }
 #pragma unroll
         for (int i = 0; i < kNCh; ++i) {
           tmem_wait<kCh>(r[i & 1]);
           if (i + 1 < kNCh) {
-            tmem_ld<kCh>(tm + b * kBC + (i + 1) * kCh, r[(i + 1) & 1]);
+            tmem_ld<kCh>(tb + (i + 1) * kCh, r[(i + 1) & 1]);
           } else {  // the buffer is read: the next MMAs may have it
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) {
+            if (elect_one()) {
               if (kPair)
-                mbar_arrive_cluster(leader_addr(smem_addr(&tempty[b])));
+                mbar_arrive_cluster(tempty0 + 8 * b);
               else
-                mbar_arrive(&tempty[b]);
+                mbar_arrive(tempty0 + 8 * b);
             }
           }
 #pragma unroll
           for (int j = 0; j < kCh; ++j) {
             const int col = i * kCh + j;
-            acc[col] = fmaf(__uint_as_float(r[i & 1][j]), kSwap ? __shfl_sync(0xFFFFFFFFu, f, col) : f, acc[col]);
+            fma_here(acc[col], r[i & 1][j], kSwap ? __shfl_sync(0xFFFFFFFFu, f, col) : f);
           }
         }
+        if (++b == C::kBufs) b = 0, par ^= 1;
       }
       if (!ok) break;
       if (it.kb0 > 0 || it.kb1 < a.KB) {
@@ -724,6 +765,8 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   a.y = y;
   a.f32 = y_type == VP_F32;
   a.M = M, a.N = N, a.KB = qblocks(K);
+  a.vec_x = a.KB % 4 == 0 && al(x_scales, 16);
+  a.vec_w = a.KB % 4 == 0 && al(w_scales, 16);
   a.tiles = p.tiles, a.tile_m = p.tile_m, a.tile_n = p.tile_n;
   int grid = std::min(sms, kLinGrid) / (p.pair ? 2 : 1);  // CTAs, or pairs
   a.dp_rounds = p.tiles / grid;
