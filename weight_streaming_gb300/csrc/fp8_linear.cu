@@ -455,21 +455,34 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int b = 0;
     uint32_t par = 0;
     bool ok = true;
-    while (ok && sched.next(it)) {
-      int mt, nt;
-      tile_at(a, it.tile, mt, nt);
+    // Factors of four blocks at a time: each of a warp's 32 rows is a cache line of its own, so a load per
+    // block would keep the load unit busy for 256 cycles of the block's 512.  The next tile's first
+    // factors are loaded before this tile's output is stored.
+    const float *px, *pw;
+    float4 fx, fw;
+    int mt, nt, next_mt = 0, next_nt = 0;
+    Item next;
+    auto fetch = [&]() -> bool {
+      if (!sched.next(next)) return false;
+      tile_at(a, next.tile, next_mt, next_nt);
       // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there); what is
       // past the last row or column is computed with another's factor and not stored
-      const int m = kSwap ? mt * kBC + c0 + lane : kPair ? mt * 256 + rank * 128 + row : mt * 128 + row;
-      const int nb = kSwap ? nt : nt * (kBC / 128) + (kBC == 256 ? half : 0);
-      const float* px = a.xs + (size_t)min(m, a.M - 1) * a.KB;
-      const float* pw = a.ws + (size_t)min(nb, qblocks(a.N) - 1) * a.KB;
+      const int m = kSwap ? next_mt * kBC + c0 + lane : kPair ? next_mt * 256 + rank * 128 + row : next_mt * 128 + row;
+      const int nb = kSwap ? next_nt : next_nt * (kBC / 128) + (kBC == 256 ? half : 0);
+      px = a.xs + (size_t)min(m, a.M - 1) * a.KB;
+      pw = a.ws + (size_t)min(nb, qblocks(a.N) - 1) * a.KB;
+      fx = load4(px, next.kb0 & ~3, a.KB, a.vec_x);
+      fw = load4(pw, next.kb0 & ~3, a.KB, a.vec_w);
+      return true;
+    };
+    bool more = fetch();
+    while (more) {
+      it = next;
+      mt = next_mt;
+      nt = next_nt;
       float acc[kW];
 #pragma unroll
       for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-      // Factors of four blocks at a time: each of a warp's 32 rows is a cache line of its own, so a load per
-      // block would keep the load unit busy for 256 cycles of the block's 512.
-      float4 fx = load4(px, it.kb0 & ~3, a.KB, a.vec_x), fw = load4(pw, it.kb0 & ~3, a.KB, a.vec_w);
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
         if (!(ok = wait(tfull0 + 8 * b, par))) break;
         tmem_fence_after();
@@ -507,6 +520,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (++b == C::kBufs) b = 0, par ^= 1;
       }
       if (!ok) break;
+      more = fetch();
+      const int m = kPair ? mt * 256 + rank * 128 + row : mt * 128 + row;  // tokens on the lanes
       if (it.kb0 > 0 || it.kb1 < a.KB) {
         // a part of the tile's K blocks: leave it, and let the last contributor add them up
         const int G = a.sk_ctas;
