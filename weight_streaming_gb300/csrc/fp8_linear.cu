@@ -17,10 +17,10 @@
 //  * Tokens on the lanes for M > 64 (the factor xs ws is one scalar per thread and block), weights on
 //    the lanes for M <= 64 (16, 32 or 64 token columns; the factors come by shuffles): a small batch
 //    then pads to 16 columns instead of 128 lanes, and the weight stream is what it waits for.
-//  * Work: whole rounds of output tiles first; the remaining tiles' K blocks form one line that is cut
-//    into equal runs, one per CTA (a few token rows split every tile along K that way).  A tile with
-//    several contributors goes through fp32 partials in the workspace: the last CTA to arrive (a
-//    counter, nobody waits) adds them in K order, so results do not depend on the arrival order.
+//  * Work: whole rounds of output tiles first; each remaining tile is cut along K into as many parts as
+//    there are CTAs for it (at most 16).  Parts go through fp32 partials in the workspace: the last CTA
+//    to arrive (a counter, nobody waits) adds them in K order, so results do not depend on the
+//    arrival order.
 //
 // Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, drains its copies and MMAs and frees
 // its tensor memory.
@@ -48,6 +48,7 @@ constexpr int kLinGrid = 152;     // CTAs at most: one per SM
 constexpr int kEpiThreads = 256;
 constexpr int kSmemRing = 216 * 1024;
 constexpr int kMaxStages = 12;
+constexpr int kMaxSplit = 16;     // parts along K: each costs the last one a read of its sums
 
 struct LinArgs {
   const uint8_t* w;
@@ -56,10 +57,10 @@ struct LinArgs {
   int f32, M, N, KB;
   int vec_x, vec_w;           // the scales' rows can be read 16 bytes at a time
   int tiles, tile_m, tile_n;  // output tiles: in all, along the tokens, along the weight rows
-  int dp_rounds, sk_tiles;    // whole rounds per CTA; tiles cut along K (after the first dp_rounds * grid)
-  int sk_ctas;                // CTAs (pairs) that these are cut among: each has at least one K block
-  unsigned* counters;         // [sk_tiles][2 CTAs of a pair][8 epilogue warps]
-  float* partials;            // [grid][2][kBC][128]
+  int dp_rounds, cut_tiles;   // whole tiles per CTA (pair); the tiles after them, each cut into
+  int split;                  // this many parts along K, one per CTA (pair)
+  unsigned* counters;         // [cut_tiles][2 CTAs of a pair][8 epilogue warps]
+  float* partials;            // [grid][kBC][128]
   int* status;
 };
 
@@ -74,37 +75,26 @@ struct LinCfg {
 };
 
 struct Item {
-  int tile, kb0, kb1, sk;  // sk: index among the tiles cut along K, or -1
+  int tile, kb0, kb1;
 };
-// The i-th piece of work of CTA c, or false: its whole tiles, then its run of K blocks of the rest.
+// The pieces of work of CTA (pair) c in turn: its whole tiles, then one part of a tile that is cut along K.
 struct Sched {
-  int c, G, KB, i, dp, base;
-  int u, u1;
+  int c, G, i;
   // pair: the CTAs 2 c and 2 c + 1 work on the same tiles
-  __device__ Sched(const LinArgs& a, int pair)
-      : c(blockIdx.x >> pair), G(gridDim.x >> pair), KB(a.KB), i(0), dp(a.dp_rounds) {
-    base = dp * G;
-    const long long U = (long long)a.sk_tiles * KB;
-    u = u1 = 0;
-    if (c < a.sk_ctas) {
-      u = (int)(c * U / a.sk_ctas);
-      u1 = (int)((c + 1) * U / a.sk_ctas);
-    }
-  }
-  __device__ bool next(Item& it) {
-    if (i < dp) {
+  __device__ explicit Sched(int pair) : c(blockIdx.x >> pair), G(gridDim.x >> pair), i(0) {}
+  __device__ bool next(const LinArgs& a, Item& it) {
+    if (i < a.dp_rounds) {
       it.tile = i++ * G + c;
       it.kb0 = 0;
-      it.kb1 = KB;
-      it.sk = -1;
+      it.kb1 = a.KB;
       return true;
     }
-    if (u >= u1) return false;
-    it.sk = u / KB;
-    it.kb0 = u - it.sk * KB;
-    it.kb1 = min(KB, it.kb0 + u1 - u);
-    it.tile = base + it.sk;
-    u += it.kb1 - it.kb0;
+    if (i > a.dp_rounds || c >= a.cut_tiles * a.split) return false;
+    ++i;
+    const int t = c / a.split, part = c - t * a.split;
+    it.tile = a.dp_rounds * G + t;
+    it.kb0 = part * a.KB / a.split;
+    it.kb1 = (part + 1) * a.KB / a.split;
     return true;
   }
 };
@@ -360,7 +350,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   // 232 (4 x 40 + 8 x 232 = 12 x 168).
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    Sched sched(a, kPair);
+    Sched sched(kPair);
     Item it;
     // Whole warps run the two issuing loops, one elected lane issues: the operands stay warp-uniform.
     if (warp == 0) {
@@ -368,7 +358,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       uint32_t par = 1;  // of the empty barriers: the first round passes
       bool ok = true;
       const uint64_t pol = l2_evict_first_policy();
-      while (ok && sched.next(it)) {
+      while (ok && sched.next(a, it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
         // weight tiles of this output tile: one, or up to kBC / 128 (a pair's CTAs take one each; past the
@@ -414,7 +404,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int s = 0, b = 0;
       uint32_t par = 0, tpar = 1;
       bool ok = true;
-      while (ok && sched.next(it)) {
+      while (ok && sched.next(a, it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
         const int cols = kSwap || kPair ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
@@ -445,7 +435,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    Sched sched(a, kPair);
+    Sched sched(kPair);
     Item it;
     constexpr int kW = kBC / 2;                   // columns per warp
     constexpr int kCh = kW < 32 ? kW : 32;        // columns per tensor-memory load
@@ -463,7 +453,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     int mt, nt, next_mt = 0, next_nt = 0;
     Item next;
     auto fetch = [&]() -> bool {
-      if (!sched.next(next)) return false;
+      if (!sched.next(a, next)) return false;
       tile_at(a, next.tile, next_mt, next_nt);
       // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there); what is
       // past the last row or column is computed with another's factor and not stored
@@ -475,79 +465,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       fw = load4(pw, next.kb0 & ~3, a.KB, a.vec_w);
       return true;
     };
-    bool more = fetch();
-    while (more) {
-      it = next;
-      mt = next_mt;
-      nt = next_nt;
-      float acc[kW];
-#pragma unroll
-      for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-      for (int kb = it.kb0; kb < it.kb1; ++kb) {
-        if (!(ok = wait(tfull0 + 8 * b, par))) break;
-        tmem_fence_after();
-        const uint32_t tb = tm + b * kBC;
-        // chunk by chunk; the next chunk's load is in flight while this one is accumulated
-        constexpr int kNCh = kW / kCh;
-        uint32_t r[2][kCh];
-        tmem_ld<kCh>(tb, r[0]);
-        const float f = pick4(fx, kb) * pick4(fw, kb);
-        if ((kb & 3) == 3 && kb + 1 < it.kb1) {
-          fx = load4(px, kb + 1, a.KB, a.vec_x);
-          fw = load4(pw, kb + 1, a.KB, a.vec_w);
-        }
-#pragma unroll
-        for (int i = 0; i < kNCh; ++i) {
-          tmem_wait<kCh>(r[i & 1]);
-          if (i + 1 < kNCh) {
-            tmem_ld<kCh>(tb + (i + 1) * kCh, r[(i + 1) & 1]);
-          } else {  // the buffer is read: the next MMAs may have it
-            tmem_fence_before();
-            __syncwarp();
-            if (elect_one()) {
-              if (kPair)
-                mbar_arrive_cluster(tempty0 + 8 * b);
-              else
-                mbar_arrive(tempty0 + 8 * b);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kCh; ++j) {
-            const int col = i * kCh + j;
-            fma_here(acc[col], r[i & 1][j], kSwap ? __shfl_sync(0xFFFFFFFFu, f, col) : f);
-          }
-        }
-        if (++b == C::kBufs) b = 0, par ^= 1;
-      }
-      if (!ok) break;
-      more = fetch();
+    // Writes the warp's part of tile (mt, nt).
+    auto store = [&](const float (&acc)[kW], int mt, int nt) {
       const int m = kPair ? mt * 256 + rank * 128 + row : mt * 128 + row;  // tokens on the lanes
-      if (it.kb0 > 0 || it.kb1 < a.KB) {
-        // a part of the tile's K blocks: leave it, and let the last contributor add them up
-        const int G = a.sk_ctas;
-        const long long U = (long long)a.sk_tiles * a.KB, u0 = (long long)it.sk * a.KB;
-        const int first = (int)(((u0 + 1) * G - 1) / U), last = (int)(((u0 + a.KB) * G - 1) / U);
-        float* mine = a.partials + ((size_t)blockIdx.x * 2 + (it.kb0 == 0)) * kBC * 128;
-#pragma unroll
-        for (int j = 0; j < kW; ++j) __stcg(mine + (c0 + j) * 128 + row, acc[j]);
-        __threadfence();
-        __syncwarp();
-        // each warp joins its own part of the tile (8 counters per tile): no CTA-wide wait
-        unsigned old = 0;
-        if (lane == 0) old = atom_add_acq_rel_gpu(a.counters + (it.sk * 2 + rank) * 8 + warp - 4, 1);
-        const bool join = __shfl_sync(0xFFFFFFFFu, old, 0) == (unsigned)(last - first);
-        if (!join) continue;
-        if (lane == 0) a.counters[(it.sk * 2 + rank) * 8 + warp - 4] = 0;  // every contributor has arrived
-        __threadfence();
-#pragma unroll
-        for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-        for (int c = first; c <= last; ++c) {
-          const int cta = kPair ? 2 * c + rank : c;
-          const float* p = a.partials + ((size_t)cta * 2 + (c == first)) * kBC * 128 + row;
-#pragma unroll
-          for (int j = 0; j < kW; ++j) acc[j] += __ldcg(p + (c0 + j) * 128);
-        }
-      }
       if (kSwap) {
         const int nn = nt * 128 + row;
         if (nn < a.N) {
@@ -638,6 +558,78 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
       }
+    };
+    bool more = fetch();
+    while (more) {
+      it = next;
+      mt = next_mt;
+      nt = next_nt;
+      float acc[kW];
+#pragma unroll
+      for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
+      for (int kb = it.kb0; kb < it.kb1; ++kb) {
+        if (!(ok = wait(tfull0 + 8 * b, par))) break;
+        tmem_fence_after();
+        const uint32_t tb = tm + b * kBC;
+        // chunk by chunk; the next chunk's load is in flight while this one is accumulated
+        constexpr int kNCh = kW / kCh;
+        uint32_t r[2][kCh];
+        tmem_ld<kCh>(tb, r[0]);
+        const float f = pick4(fx, kb) * pick4(fw, kb);
+        if ((kb & 3) == 3 && kb + 1 < it.kb1) {
+          fx = load4(px, kb + 1, a.KB, a.vec_x);
+          fw = load4(pw, kb + 1, a.KB, a.vec_w);
+        }
+#pragma unroll
+        for (int i = 0; i < kNCh; ++i) {
+          tmem_wait<kCh>(r[i & 1]);
+          if (i + 1 < kNCh) {
+            tmem_ld<kCh>(tb + (i + 1) * kCh, r[(i + 1) & 1]);
+          } else {  // the buffer is read: the next MMAs may have it
+            tmem_fence_before();
+            __syncwarp();
+            if (elect_one()) {
+              if (kPair)
+                mbar_arrive_cluster(tempty0 + 8 * b);
+              else
+                mbar_arrive(tempty0 + 8 * b);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kCh; ++j) {
+            const int col = i * kCh + j;
+            fma_here(acc[col], r[i & 1][j], kSwap ? __shfl_sync(0xFFFFFFFFu, f, col) : f);
+          }
+        }
+        if (++b == C::kBufs) b = 0, par ^= 1;
+      }
+      if (!ok) break;
+      more = fetch();
+      if (it.kb1 - it.kb0 < a.KB) {
+        // A part of the tile's K blocks: left in the workspace, and the last contributor adds them up.  Each
+        // warp joins its own part of the tile (8 counters per tile and CTA): no CTA-wide wait.
+        const size_t slot = (size_t)kBC * 128;
+        float* mine = a.partials + blockIdx.x * slot + c0 * 128 + row;
+#pragma unroll
+        for (int j = 0; j < kW; ++j) __stcg(mine + j * 128, acc[j]);
+        __threadfence();
+        __syncwarp();
+        const int t = sched.c / a.split;
+        unsigned old = 0, *counter = a.counters + (t * 2 + rank) * 8 + warp - 4;
+        if (lane == 0) old = atom_add_acq_rel_gpu(counter, 1);
+        if (__shfl_sync(0xFFFFFFFFu, old, 0) != (unsigned)(a.split - 1)) continue;
+        if (lane == 0) *counter = 0;  // every contributor has arrived
+        __threadfence();
+#pragma unroll
+        for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
+        for (int e = 0; e < a.split; ++e) {  // in K order
+          const int c = t * a.split + e;
+          const float* p = a.partials + (kPair ? 2 * c + rank : c) * slot + c0 * 128 + row;
+#pragma unroll
+          for (int j = 0; j < kW; ++j) acc[j] += __ldcg(p + j * 128);
+        }
+      }
+      store(acc, mt, nt);
     }
   }
   if (kPair) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the thread's output stores are done
@@ -671,7 +663,7 @@ LinPlan lin_plan(int M, int N) {
   p.tiles = p.tile_m * p.tile_n;
   p.counters = 256;
   p.partials = align_up(p.counters + sizeof(unsigned) * kLinGrid * 2 * (kEpiThreads / 32), 256);
-  p.total = p.partials + sizeof(float) * 2 * kLinGrid * (size_t)p.bc * 128;
+  p.total = p.partials + sizeof(float) * kLinGrid * (size_t)p.bc * 128;
   return p;
 }
 
@@ -785,9 +777,9 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   a.tiles = p.tiles, a.tile_m = p.tile_m, a.tile_n = p.tile_n;
   int grid = std::min(sms, kLinGrid) / (p.pair ? 2 : 1);  // CTAs, or pairs
   a.dp_rounds = p.tiles / grid;
-  a.sk_tiles = p.tiles - a.dp_rounds * grid;
-  a.sk_ctas = (int)std::min<long long>(grid, (long long)a.sk_tiles * a.KB);
-  if (a.dp_rounds == 0) grid = a.sk_ctas;
+  a.cut_tiles = p.tiles - a.dp_rounds * grid;
+  a.split = a.cut_tiles ? std::max(1, std::min({grid / a.cut_tiles, a.KB, kMaxSplit})) : 1;
+  if (a.dp_rounds == 0) grid = a.cut_tiles * a.split;
   if (p.pair) grid *= 2;
   a.counters = reinterpret_cast<unsigned*>(b + p.counters);
   a.partials = reinterpret_cast<float*>(b + p.partials);
