@@ -66,11 +66,15 @@ struct LinArgs {
 
 template <int kBC, bool kPair>
 struct LinCfg {
-  static constexpr int kStage = 16384 + (kPair ? kBC / 2 : kBC) * 128;  // a pair's CTAs hold half of the columns each
+  // K blocks per stage, barrier and tensor-memory buffer: waits, commits and loop cost the MMA warp about 650
+  // cycles a block when they are taken for each, more than a block of a narrow tile takes to arrive.
+  static constexpr int kG = kBC == 16 ? 4 : kBC <= 64 ? 2 : 1;
+  static constexpr int kBlock = 16384 + (kPair ? kBC / 2 : kBC) * 128;  // a pair's CTAs hold half of the columns each
+  static constexpr int kStage = kG * kBlock;
   static constexpr int kStages = kPair ? 5 : kSmemRing / kStage < kMaxStages ? kSmemRing / kStage : kMaxStages;
   static constexpr int kOut = kPair ? 8 * 8192 : 0;  // output staging: 8 KB per epilogue warp
-  static constexpr int kBufs = 512 / kBC < 8 ? 512 / kBC : 8;
-  static constexpr int kCols = kBC * kBufs;   // tensor-memory columns (a power of two >= 128)
+  static constexpr int kBufs = 512 / (kBC * kG) < 8 ? 512 / (kBC * kG) : 8;
+  static constexpr int kCols = kBC * kG * kBufs;  // tensor-memory columns (512)
   static constexpr int kSmem = kStages * kStage + kOut + 1024;
 };
 
@@ -357,7 +361,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int n = 0, s = 0;
       uint32_t par = 1;  // of the empty barriers: the first round passes
       bool ok = true;
-      const uint64_t pol = l2_evict_first_policy();
       while (ok && sched.next(a, it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
@@ -366,27 +369,31 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int nbs = kSwap || kPair ? 1 : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128));
         const int nb = kSwap ? nt : kPair ? min(2 * nt + rank, qblocks(a.N) - 1) : nt * (kBC / 128);
         const int rows = kSwap ? kBC : 128, m0 = kPair ? mt * 256 + rank * 128 : mt * rows;
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++n) {
+        for (int kb0 = it.kb0; kb0 < it.kb1; kb0 += C::kG, ++n) {
           if (!(ok = wait(smem_addr(&empty[s]), par))) break;
           if (elect_one()) {
-            const uint32_t st = ring + s * C::kStage;
-            // lanes' operand first (16 KB), columns' operand behind it
-            const uint32_t dst_w = kSwap ? st : st + 16384, dst_x = kSwap ? st + 16384 : st;
+            const int cnt = min(C::kG, it.kb1 - kb0);
             if constexpr (kPair) {
-              const uint32_t bar = leader_addr(smem_addr(&full[s]));
               if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);  // both CTAs' copies
-              tma_load_2d_pair(dst_x, &xmap, kb * kQBlock, m0, bar);
-              tma_load_3d_pair(dst_w, &wmap, 0, 0, nb * a.KB + kb, bar);
             } else {
-              const uint32_t bar = smem_addr(&full[s]);
-              mbar_arrive_expect_tx(&full[s], rows * 128 + nbs * kQTileBytes);
-              tma_load_2d(dst_x, &xmap, kb * kQBlock, m0, bar);
-              for (int i = 0; i < nbs; ++i) {
-                const uint8_t* src = a.w + ((size_t)(nb + i) * a.KB + kb) * kQTileBytes;
-                if (a.tile_m == 1)  // each weight byte is read once
-                  bulk_g2s(dst_w + i * kQTileBytes, src, kQTileBytes, bar, pol);
-                else
-                  bulk_load(dst_w + i * kQTileBytes, src, kQTileBytes, bar);
+              mbar_arrive_expect_tx(&full[s], cnt * (rows * 128 + nbs * kQTileBytes));
+            }
+#pragma unroll
+            for (int g = 0; g < C::kG; ++g) {
+              if (g >= cnt) break;
+              const int kb = kb0 + g;
+              const uint32_t st = ring + s * C::kStage + g * C::kBlock;
+              // lanes' operand first (16 KB), columns' operand behind it
+              const uint32_t dst_w = kSwap ? st : st + 16384, dst_x = kSwap ? st + 16384 : st;
+              if constexpr (kPair) {
+                const uint32_t bar = leader_addr(smem_addr(&full[s]));
+                tma_load_2d_pair(dst_x, &xmap, kb * kQBlock, m0, bar);
+                tma_load_3d_pair(dst_w, &wmap, 0, 0, nb * a.KB + kb, bar);
+              } else {
+                const uint32_t bar = smem_addr(&full[s]);
+                tma_load_2d(dst_x, &xmap, kb * kQBlock, m0, bar);
+                for (int i = 0; i < nbs; ++i)
+                  bulk_load(dst_w + i * kQTileBytes, a.w + ((size_t)(nb + i) * a.KB + kb) * kQTileBytes, kQTileBytes, bar);
               }
             }
           }
@@ -410,15 +417,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int cols = kSwap || kPair ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
         // e4m3 x e4m3 -> fp32, 128 rows (a pair's two CTAs: 256)
         const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (kPair ? 16u : 8u) << 24;
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
+        for (int kb0 = it.kb0; kb0 < it.kb1; kb0 += C::kG) {
+          const int cnt = min(C::kG, it.kb1 - kb0);
           const uint64_t da = smem_desc(ring) + (uint64_t)(s * (C::kStage >> 4)), db = da + (16384 >> 4);
           if (!(ok = wait(smem_addr(&full[s]), par))) break;
           if (!(ok = wait(smem_addr(&tempty[b]), tpar))) break;
           tmem_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)  // 32 bytes along K inside the swizzle atom
-              mma_f8<kPair>(tmem + b * kBC, da + 2 * k, db + 2 * k, idesc, k > 0);
+            for (int g = 0; g < C::kG; ++g) {
+              if (g >= cnt) break;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // 32 bytes along K inside the swizzle atom
+                mma_f8<kPair>(tmem + (b * C::kG + g) * kBC, da + g * (C::kBlock >> 4) + 2 * k,
+                              db + g * (C::kBlock >> 4) + 2 * k, idesc, k > 0);
+            }
             mma_commit<kPair>(&tfull[b]);
             mma_commit<kPair>(&empty[s]);
           }
@@ -449,7 +462,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // block would keep the load unit busy for 256 cycles of the block's 512.  The next tile's first
     // factors are loaded before this tile's output is stored.
     const float *px, *pw;
-    float4 fx, fw;
+    float4 fx, fw, fx1, fw1;
     int mt, nt, next_mt = 0, next_nt = 0;
     Item next;
     auto fetch = [&]() -> bool {
@@ -463,6 +476,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       pw = a.ws + (size_t)min(nb, qblocks(a.N) - 1) * a.KB;
       fx = load4(px, next.kb0 & ~3, a.KB, a.vec_x);
       fw = load4(pw, next.kb0 & ~3, a.KB, a.vec_w);
+      if (kSwap && (next.kb0 & ~3) + 4 < next.kb1) {
+        fx1 = load4(px, (next.kb0 & ~3) + 4, a.KB, a.vec_x);
+        fw1 = load4(pw, (next.kb0 & ~3) + 4, a.KB, a.vec_w);
+      }
       return true;
     };
     // Writes the warp's part of tile (mt, nt).
@@ -567,10 +584,39 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       float acc[kW];
 #pragma unroll
       for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-      for (int kb = it.kb0; kb < it.kb1; ++kb) {
+      for (int kb = it.kb0; kb < it.kb1; kb += C::kG) {
         if (!(ok = wait(tfull0 + 8 * b, par))) break;
         tmem_fence_after();
-        const uint32_t tb = tm + b * kBC;
+        const uint32_t tb = tm + b * C::kG * kBC;
+        if constexpr (kSwap) {  // a few columns per block: all blocks' loads, then their sums
+          uint32_t r[C::kG][kW];
+#pragma unroll
+          for (int g = 0; g < C::kG; ++g)
+            if (kb + g < it.kb1) tmem_ld<kW>(tb + g * kBC, r[g]);
+#pragma unroll
+          for (int g = 0; g < C::kG; ++g) tmem_wait<kW>(r[g]);
+          tmem_fence_before();
+          __syncwarp();
+          if (elect_one()) mbar_arrive(tempty0 + 8 * b);
+#pragma unroll
+          for (int g = 0; g < C::kG; ++g) {
+            if (kb + g >= it.kb1) break;
+            const float f = pick4(fx, kb + g) * pick4(fw, kb + g);
+            if (((kb + g) & 3) == 3) {  // the next four factors are here already
+              fx = fx1;
+              fw = fw1;
+              if (kb + g + 5 < it.kb1) {
+                fx1 = load4(px, kb + g + 5, a.KB, a.vec_x);
+                fw1 = load4(pw, kb + g + 5, a.KB, a.vec_w);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < kW; ++j)
+              acc[j] = fmaf(__uint_as_float(r[g][j]), __shfl_sync(0xFFFFFFFFu, f, j), acc[j]);
+          }
+          if (++b == C::kBufs) b = 0, par ^= 1;
+          continue;
+        }
         // chunk by chunk; the next chunk's load is in flight while this one is accumulated
         constexpr int kNCh = kW / kCh;
         uint32_t r[2][kCh];
@@ -598,7 +644,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (int j = 0; j < kCh; ++j) {
             const int col = i * kCh + j;
-            fma_here(acc[col], r[i & 1][j], kSwap ? __shfl_sync(0xFFFFFFFFu, f, col) : f);
+            fma_here(acc[col], r[i & 1][j], f);
           }
         }
         if (++b == C::kBufs) b = 0, par ^= 1;
