@@ -24,10 +24,8 @@
 //
 // Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, drains its copies and MMAs and frees
 // its tensor memory.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
@@ -37,6 +35,7 @@
 #include "fp8_block.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "tma.h"
 #include "verify.h"
 
 namespace vp {
@@ -713,21 +712,6 @@ LinPlan lin_plan(int M, int N) {
   return p;
 }
 
-// The driver's tensor-map encoder (looked up once; host only).
-vp_status encode_fn(PFN_cuTensorMapEncodeTiled_v12000* fn) {
-  static std::atomic<void*> cached{nullptr};
-  void* p = cached.load();
-  if (!p) {
-    cudaDriverEntryPointQueryResult res;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &res);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (res != cudaDriverEntryPointSuccess || !p) return VP_ERR_UNSUPPORTED;
-    cached.store(p);
-  }
-  *fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  return VP_OK;
-}
-
 template <int kBC, bool kSwap, bool kPair>
 cudaError_t launch_linear(const LinArgs& a, const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& ymap,
                           int grid, cudaStream_t s) {
@@ -781,7 +765,7 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   vp_status st = device_sm_count(&sms);
   if (st != VP_OK) return st;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
-  if ((st = encode_fn(&encode)) != VP_OK) return st;
+  if ((st = tensor_map_encoder(&encode)) != VP_OK) return st;
   const LinPlan p = lin_plan(M, N);
   CUtensorMap xmap, wmap, ymap;
   {

@@ -2,79 +2,554 @@
 //
 // Mathematics: t_i = scale q . k_i; one pass keeps m = max t, l = sum e^(t - m), o = sum e^(t - m) v, and
 // two partial results join as m = max(m1, m2), l = l1 e^(m1 - m) + l2 e^(m2 - m) (o alike).
-// First form: one CTA per (q head, sequence); its warps take every fourth position.
+//
+// What bounds it: every cached key and value is read once for the G = Hq / Hkv query heads that share it
+// (G flops per byte at most), so the bytes do; everything else hides behind the copies.
+//  * The cached positions of all (sequence, key-value head)s form one line of pieces of 8 KB of keys and
+//    8 KB of values (16, 32 or 64 positions at D = 256, 128, 64).  It is cut into equal runs, one per
+//    CTA (one CTA per SM), whatever the lengths, which are read on the device: each CTA sums them up and
+//    finds its first piece.
+//  * A producer warp walks the run, looks the pages up and issues the TMA loads (box = the piece's rows
+//    of one page, 128-byte swizzle) into a ring of 16 KB stages; five warps (four above 8 heads) take the pieces in
+//    turn, each with its own running maximum, sum and output in registers: no synchronisation between
+//    them until the (sequence, head) ends, where they are joined through shared memory.
+//  * The tensor core's 16 rows hold up to 16 query heads.  P is split in two bf16 parts, hi + lo (about
+//    2^-17 relative): with G <= 8 heads the parts are the tile's upper and lower 8 rows of one MMA, and
+//    their sums are added at the end; above, two MMAs.
+//  * A (sequence, head) that crosses CTAs goes through fp32 partials in the workspace (two per CTA at
+//    most: its first and its last one), announced after the CTA's last copy (a GPU-scope fence waits
+//    for the copies in flight); the last contributor joins them in order.
+// Waits are bounded: a warp whose wait ran out reports VP_ERR_TIMEOUT and goes on without waiting, so the
+// CTA ends.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 #include "errors.h"
 #include "internal.h"
 #include "paged.h"
+#include "ptx.cuh"
+#include "tma.h"
 #include "verify.h"
 
 namespace vp {
 
 namespace {
 
+constexpr int kPaGrid = 152;                  // CTAs at most: one per SM
+constexpr int kPieceBytes = 8192;             // of keys, and of values
+constexpr int kMinPieces = 8;                 // pieces per CTA at least
+
 struct PagedArgs {
-  const uint16_t *q, *k, *v, *gate;
+  const uint16_t *q, *gate;
   uint16_t* out;
   float* lse;
   const int32_t *kv_len, *pages;
-  int S, Hq, Hkv, n_pages, log_page, max_pages;
-  float scale;
+  int S, Hq, Hkv, G, n_pages, log_page, max_pages, log_box;
+  float scale2;        // scale * log2(e)
+  unsigned* counters;  // [S][Hkv]
+  float* part_o;       // [grid][2][16][D]
+  float* part_ml;      // [grid][2][16][2]: maximum (log2 units), sum
   int* status;
 };
 
+__device__ __forceinline__ void ldsm_x4(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two fp32 values as bf16 pairs: hi = bf16(x) (a in the low half), lo = bf16(x - hi).
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                            uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
+}
+template <int kThreads>
+__device__ __forceinline__ void named_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+__device__ __forceinline__ float bfv(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+
+// The usable length of sequence s (0 when it is out of range).
+__device__ __forceinline__ int seq_len(const PagedArgs& a, int s) {
+  const int n = __ldg(a.kv_len + s);
+  return n < 0 || n > ((long long)a.max_pages << a.log_page) ? 0 : n;
+}
+
+// Four output values of row r of a (sequence, head group) from the joined sums; M in log2 units.
 template <int D>
-__global__ void __launch_bounds__(128) attend_simple(const PagedArgs a) {
-  constexpr int kE = D / 32;
-  __shared__ float so[4][D], sm[4], sl[4];
-  const int h = blockIdx.x, s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = h / (a.Hq / a.Hkv);
-  int n = a.kv_len[s];
-  if (n < 0 || n > (a.max_pages << a.log_page)) {
-    if (threadIdx.x == 0) atomicExch(a.status, (int)VP_ERR_SHAPE);
-    n = 0;
+__device__ __forceinline__ void finish(const PagedArgs& a, size_t qrow, int r, int d, float4 y, float M, float L) {
+  const size_t at = qrow + (size_t)r * D + d;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  float v[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+  if (a.gate) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] /= 1.0f + expf(-bfv(a.gate[at + e]));
   }
-  auto bf = [](uint16_t x) { return __uint_as_float((uint32_t)x << 16); };
-  const size_t row = ((size_t)s * a.Hq + h) * D;
-  float q[kE], o[kE], m = -INFINITY, l = 0.0f;
-  for (int e = 0; e < kE; ++e) q[e] = bf(a.q[row + lane + 32 * e]), o[e] = 0.0f;
-  for (int p = warp; p < n; p += 4) {
-    const int page = a.pages[(size_t)s * a.max_pages + (p >> a.log_page)];
-    if (page < 0 || page >= a.n_pages) {
-      if (lane == 0) atomicExch(a.status, (int)VP_ERR_SHAPE);
-      continue;
+  const __nv_bfloat162 p0 = __floats2bfloat162_rn(v[0], v[1]), p1 = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(a.out + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
+  if (a.lse && d == 0) a.lse[qrow / D + r] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+template <int D, bool kWide>
+struct PaCfg {
+  static constexpr int kRows = kPieceBytes / (2 * D);      // positions per piece
+  // Consumer warps, two stages each: a warp takes every kWarps-th piece, so it alone waits on its stages'
+  // barriers and sees each of their phases (copies of other warps' stages may land in any order).
+  static constexpr int kWarps = kWide ? 4 : 5;
+  static constexpr int kStages = 2 * kWarps;
+  static constexpr int kThreads = (kWarps + 1) * 32, kConsumers = kWarps * 32;
+  static constexpr int kM = kWide ? 16 : 8;                // query rows kept
+  static constexpr int kLd = D + 8;                        // padded row of the join buffer
+  static constexpr int kJoin = kWarps * kM * kLd * 4 > 16 * kPaGrid * 4 ? kWarps * kM * kLd * 4 : 16 * kPaGrid * 4;
+  static constexpr int kSmem = 1024 + kStages * 2 * kPieceBytes + kJoin;
+  static_assert(kSmem <= 225 * 1024, "shared memory of one CTA");
+};
+
+// A run of pieces of one (sequence, head): [p0, p1) of its np; u = the line's index of its piece 0.
+struct Segment {
+  int s, h, p0, p1, np, len;
+  long long u;
+};
+struct Walk {
+  long long u, u1;       // next piece and end of the run
+  int s, h, p, np, len;  // the piece's sequence, head and number; the sequence's pieces and length
+  template <int kRows>
+  __device__ bool next(const PagedArgs& a, Segment& g) {
+    if (u >= u1) return false;
+    while (p >= np) {  // the next head, or the next sequence that has positions
+      p = 0;
+      if (np > 0 && ++h < a.Hkv) continue;
+      h = 0;
+      do {
+        if (++s >= a.S) return false;
+        len = seq_len(a, s);
+        np = (len + kRows - 1) / kRows;
+      } while (np == 0);
     }
-    const size_t at = ((((size_t)page * a.Hkv + g) << a.log_page) + (p & ((1 << a.log_page) - 1))) * D;
-    float t = 0.0f;
-    for (int e = 0; e < kE; ++e) t = fmaf(q[e], bf(a.k[at + lane + 32 * e]), t);
-    for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
-    t *= a.scale;
-    const float mn = fmaxf(m, t);
-    const float c = m == -INFINITY ? 0.0f : expf(m - mn), w = t == -INFINITY ? 0.0f : expf(t - mn);
-    m = mn;
-    l = l * c + w;
-    for (int e = 0; e < kE; ++e) o[e] = o[e] * c + w * bf(a.v[at + lane + 32 * e]);
+    g.s = s;
+    g.h = h;
+    g.p0 = p;
+    g.p1 = (int)min((long long)np, p + u1 - u);
+    g.np = np;
+    g.len = len;
+    g.u = u - p;
+    u += g.p1 - p;
+    p = g.p1;
+    return true;
   }
-  for (int e = 0; e < kE; ++e) so[warp][lane + 32 * e] = o[e];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
+};
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
+    paged_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
+  using C = PaCfg<D, kWide>;
+  constexpr int kR = C::kRows, kM = C::kM, kLd = C::kLd;
+  constexpr int kPaWarps = C::kWarps, kPaThreads = C::kThreads, kPaConsumers = C::kConsumers;
+  extern __shared__ uint8_t dyn[];
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ int s_bad[C::kStages];          // boxes of the stage whose page is out of range (bit per box)
+  __shared__ long long s_scan[kPaThreads / 32];
+  __shared__ int s_first[3], s_abort, s_last[2];
+  __shared__ float s_ml[kPaWarps][kM][2], s_row[16][2];
+  const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
+  float* join = reinterpret_cast<float*>(dyn + (ring - smem_addr(dyn)) + C::kStages * 2 * kPieceBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  // Sequences without positions: zeros, and the status of those out of range.
+  for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+    if (seq_len(a, s) > 0) continue;
+    if (tid == 0 && __ldg(a.kv_len + s) != 0) atomicExch(a.status, (int)VP_ERR_SHAPE);
+    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s * a.Hq * D);
+    for (int i = tid; i < a.Hq * D / 8; i += kPaThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kPaThreads) a.lse[(size_t)s * a.Hq + i] = -INFINITY;
+  }
+  // The line: pieces before each thread's share of the sequences, and in all.
+  const int per = (a.S + kPaThreads - 1) / kPaThreads, sa = min(a.S, tid * per), sb = min(a.S, sa + per);
+  long long mine = 0;
+  for (int s = sa; s < sb; ++s) mine += (seq_len(a, s) + kR - 1) / kR;
+  long long pre = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xFFFFFFFFu, pre, o);
+    if (lane >= o) pre += v;
+  }
+  if (lane == 31) s_scan[warp] = pre;
   __syncthreads();
-  float M = -INFINITY, L = 0.0f;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sm[w]);
-  float c[4];
-  for (int w = 0; w < 4; ++w) L += sl[w] * (c[w] = sm[w] == -INFINITY ? 0.0f : expf(sm[w] - M));
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float y = 0.0f;
-    for (int w = 0; w < 4; ++w) y += so[w][d] * c[w];
-    y = L == 0.0f ? 0.0f : y / L;
-    if (a.gate) y /= 1.0f + expf(-bf(a.gate[row + d]));
-    a.out[row + d] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kPaThreads / 32; ++w) {
+    if (w < warp) pre += s_scan[w];
+    total += s_scan[w];
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[(size_t)s * a.Hq + h] = L == 0.0f ? -INFINITY : M + logf(L);
+  pre -= mine;  // exclusive
+  const long long U = total * a.Hkv;
+  const int ctas = (int)min((long long)gridDim.x, (U + kMinPieces - 1) / kMinPieces), c = blockIdx.x;
+  if (c >= ctas) return;
+  const long long u0 = c * U / ctas, u1 = (c + 1) * U / ctas;
+  if (u0 >= pre * a.Hkv && u0 < (pre + mine) * a.Hkv) {
+    long long at = pre * a.Hkv;
+    for (int s = sa;; ++s) {
+      const int np = (seq_len(a, s) + kR - 1) / kR;
+      if (u0 < at + (long long)np * a.Hkv) {
+        s_first[0] = s;
+        s_first[1] = (int)((u0 - at) / np);
+        s_first[2] = (int)((u0 - at) % np);
+        break;
+      }
+      at += (long long)np * a.Hkv;
+    }
+  }
+  __syncthreads();
+  Walk walk;
+  walk.u = u0;
+  walk.u1 = u1;
+  walk.s = s_first[0];
+  walk.h = s_first[1];
+  walk.p = s_first[2];
+  walk.len = seq_len(a, walk.s);
+  walk.np = (walk.len + kR - 1) / kR;
+  Segment g;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // a converged warp
+    for (uint32_t i = 0; i < kMbarPolls; ++i) {
+      if (*(volatile int*)&s_abort) return false;
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait_hint(bar, parity, 20000u))) return true;
+    }
+    *(volatile int*)&s_abort = 1;
+    atomicExch(a.status, (int)VP_ERR_TIMEOUT);
+    return false;
+  };
+
+  if (warp == kPaWarps) {
+    // ------------------------------------------------------------ producer
+    const uint64_t pol = l2_evict_first_policy();
+    const int box = 1 << a.log_box, boxes = kR >> a.log_box;
+    int n = 0, ws = -1, w0 = 0, window = 0;  // 32 page ids of sequence ws from page w0 on, one per lane
+    bool ok = true;
+    while (ok && walk.template next<kR>(a, g)) {
+      const int used = ((g.len - 1) >> a.log_page) + 1;
+      for (int p = g.p0; p < g.p1; ++p, ++n) {
+        const int st = n % C::kStages;
+        const int first = (p * kR) >> a.log_page, last = min(p * kR + kR, g.len) - 1;
+        if (g.s != ws || first < w0 || (last >> a.log_page) >= w0 + 32) {
+          ws = g.s;
+          w0 = first;
+          window = w0 + lane < used ? __ldg(a.pages + (size_t)g.s * a.max_pages + w0 + lane) : -1;
+        }
+        int pg[4], bad = 0, good = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int pos = p * kR + (j << a.log_box);
+          pg[j] = -1;
+          if (j >= boxes || pos > last) continue;
+          pg[j] = __shfl_sync(0xFFFFFFFFu, window, (pos >> a.log_page) - w0);
+          if (pg[j] < 0 || pg[j] >= a.n_pages) {
+            pg[j] = -1;
+            bad |= 1 << j;
+          } else {
+            ++good;
+          }
+        }
+        if (!(ok = wait(&empty[st], ((n / C::kStages) & 1) ^ 1))) break;
+        if (lane == 0) {
+          s_bad[st] = bad;
+          if (bad) atomicExch(a.status, (int)VP_ERR_SHAPE);
+          const uint32_t bar = smem_addr(&full[st]), dst = ring + st * 2 * kPieceBytes;
+          mbar_arrive_expect_tx(&full[st], good * (4 * D << a.log_box));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (pg[j] < 0) continue;
+            const int pos = p * kR + (j << a.log_box);
+            const int row = ((pg[j] * a.Hkv + g.h) << a.log_page) + (pos & ((1 << a.log_page) - 1));
+            tma_load_3d(dst + j * box * 2 * D, &kmap, 0, row, 0, bar, pol);
+            tma_load_3d(dst + kPieceBytes + j * box * 2 * D, &vmap, 0, row, 0, bar, pol);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok)  // the copies in flight land before the shared memory goes
+      for (int i = 0; i < min(n, C::kStages); ++i) mbar_wait_bounded(&full[i], ((n - 1 - i) / C::kStages) & 1);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int gq = lane >> 2, cq = lane & 3;
+  int n = 0;                       // pieces of the run so far
+  int pend_s[2] = {-1, -1}, pend_h[2] = {0, 0};
+  int pend_first[2] = {0, 0}, pend_last[2] = {0, 0};
+  const int sub = 128 << a.log_box;  // bytes between a box's 64-column groups
+  while (walk.template next<kR>(a, g)) {
+    const size_t qrow = ((size_t)g.s * a.Hq + (size_t)g.h * a.G) * D;
+    // Q fragments: rows gq (and gq + 8) of the group's heads; rows past G are zero
+    uint32_t qf[D / 16][kWide ? 4 : 2];
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+#pragma unroll
+      for (int e = 0; e < (kWide ? 4 : 2); ++e) {
+        const int r = kWide ? gq + 8 * (e & 1) : gq, d = 16 * ks + 2 * cq + 8 * (kWide ? e >> 1 : e);
+        qf[ks][e] = r < a.G ? __ldg(reinterpret_cast<const uint32_t*>(a.q + qrow + (size_t)r * D + d)) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    constexpr int kH = kWide ? 2 : 1;  // row groups with maxima of their own
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int p = g.p0; p < g.p1; ++p, ++n) {
+      if (n % kPaWarps != warp) continue;
+      const int st = n % C::kStages;
+      if (!wait(&full[st], (n / C::kStages) & 1)) continue;
+      const uint32_t kb = ring + st * 2 * kPieceBytes, vb = kb + kPieceBytes;
+      const int valid = g.len - p * kR, bad = *(volatile int*)&s_bad[st];
+      const bool masked = valid < kR || bad;
+      auto seen = [&](int key) { return key < valid && !((bad >> (key >> a.log_box)) & 1); };
+      if (masked) {
+        // values of positions that take no part: zeros (0 * NaN would not vanish)
+        for (int i = lane; i < kR * (D / 8); i += 32) {
+          const int r = i / (D / 8), ch = i % (D / 8);
+          if (!seen(r))
+            sts128(vb + (r >> a.log_box) * (2 * D << a.log_box) + (ch >> 3) * sub + (r & ((1 << a.log_box) - 1)) * 128 + ((ch & 7) << 4),
+                   make_uint4(0, 0, 0, 0));
+        }
+        __syncwarp();
+      }
+      // S = Q K^T: 16 positions (two n-tiles) at a time
+      float s[kR / 8][4];
+#pragma unroll
+      for (int i = 0; i < kR / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kR / 16; ++t) {
+        const int r = 16 * t + ((lane >> 4) << 3) + (lane & 7);
+        const uint32_t row = kb + (r >> a.log_box) * (2 * D << a.log_box) + (r & ((1 << a.log_box) - 1)) * 128;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int ch = 2 * ks + ((lane >> 3) & 1);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4(row + (ch >> 3) * sub + (((ch & 7) ^ (lane & 7)) << 4), b0, b1, b2, b3);
+          if constexpr (kWide) {
+            mma_bf16(s[2 * t], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b0, b1);
+            mma_bf16(s[2 * t + 1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], b2, b3);
+          } else {
+            mma_bf16(s[2 * t], qf[ks][0], 0u, qf[ks][1], 0u, b0, b1);
+            mma_bf16(s[2 * t + 1], qf[ks][0], 0u, qf[ks][1], 0u, b2, b3);
+          }
+        }
+      }
+      // online softmax (log2 units)
+      float mx[2] = {m[0], m[1]};
+#pragma unroll
+      for (int i = 0; i < kR / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2 * kH; ++e) {
+          float v = s[i][e] * a.scale2;
+          if (masked && !seen(8 * i + 2 * cq + (e & 1))) v = -INFINITY;
+          s[i][e] = v;
+          mx[e >> 1] = fmaxf(mx[e >> 1], v);
+        }
+      bool grow = false;
+      float alpha[2] = {1.0f, 1.0f};
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xFFFFFFFFu, mx[h], 2));
+        if (mx[h] > m[h]) {
+          alpha[h] = exp2f(m[h] - mx[h]);
+          grow = true;
+        }
+        m[h] = mx[h];
+        l[h] *= alpha[h];
+      }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= alpha[0];
+          o[i][1] *= alpha[0];
+          o[i][2] *= alpha[kWide ? 1 : 0];
+          o[i][3] *= alpha[kWide ? 1 : 0];
+        }
+      }
+      const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+      uint32_t hi[kR / 8][kH], lo[kR / 8][kH];
+#pragma unroll
+      for (int i = 0; i < kR / 8; ++i)
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const float mm = h ? m1 : m0, x = exp2f(s[i][2 * h] - mm), y = exp2f(s[i][2 * h + 1] - mm);
+          l[h] += x + y;
+          split_bf16(x, y, hi[i][h], lo[i][h]);
+        }
+      // O += P V
+#pragma unroll
+      for (int t = 0; t < kR / 16; ++t) {
+        const int r = 16 * t + (lane & 15);
+        const uint32_t row = vb + (r >> a.log_box) * (2 * D << a.log_box) + (r & ((1 << a.log_box) - 1)) * 128;
+#pragma unroll
+        for (int np = 0; np < D / 16; ++np) {
+          const int ch = 2 * np + (lane >> 4);
+          uint32_t b0, b1, b2, b3;
+          ldsm_x4_t(row + (ch >> 3) * sub + (((ch & 7) ^ (lane & 7)) << 4), b0, b1, b2, b3);
+          if constexpr (kWide) {
+            mma_bf16(o[2 * np], hi[2 * t][0], hi[2 * t][1], hi[2 * t + 1][0], hi[2 * t + 1][1], b0, b1);
+            mma_bf16(o[2 * np], lo[2 * t][0], lo[2 * t][1], lo[2 * t + 1][0], lo[2 * t + 1][1], b0, b1);
+            mma_bf16(o[2 * np + 1], hi[2 * t][0], hi[2 * t][1], hi[2 * t + 1][0], hi[2 * t + 1][1], b2, b3);
+            mma_bf16(o[2 * np + 1], lo[2 * t][0], lo[2 * t][1], lo[2 * t + 1][0], lo[2 * t + 1][1], b2, b3);
+          } else {  // rows 0..7: hi, rows 8..15: lo
+            mma_bf16(o[2 * np], hi[2 * t][0], lo[2 * t][0], hi[2 * t + 1][0], lo[2 * t + 1][0], b0, b1);
+            mma_bf16(o[2 * np + 1], hi[2 * t][0], lo[2 * t][0], hi[2 * t + 1][0], lo[2 * t + 1][0], b2, b3);
+          }
+        }
+      }
+      if (masked) fence_proxy_async_smem();  // the zeros, before the stage's next copy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    // ---- the warps' results of this (sequence, head)
+#pragma unroll
+    for (int h = 0; h < kH; ++h) {
+      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
+      if (cq == 0) {
+        s_ml[warp][gq + 8 * h][0] = m[h];
+        s_ml[warp][gq + 8 * h][1] = l[h];
+      }
+    }
+    float* jw = join + (size_t)warp * kM * kLd;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const int d = 8 * i + 2 * cq;
+      if constexpr (kWide) {
+        *reinterpret_cast<float2*>(jw + gq * kLd + d) = make_float2(o[i][0], o[i][1]);
+        *reinterpret_cast<float2*>(jw + (gq + 8) * kLd + d) = make_float2(o[i][2], o[i][3]);
+      } else {
+        *reinterpret_cast<float2*>(jw + gq * kLd + d) = make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]);
+      }
+    }
+    named_sync<kPaConsumers>();
+    const bool whole = g.p0 == 0 && g.p1 == g.np;
+    const int slot = g.p0 == 0 ? 1 : 0;
+    for (int i = tid; i < a.G * (D / 4); i += kPaConsumers) {
+      const int r = i / (D / 4), d = 4 * (i % (D / 4));
+      float M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, s_ml[w][r][0]);
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) {
+        const float mw = s_ml[w][r][0], f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
+        const float4 v = *reinterpret_cast<const float4*>(join + ((size_t)w * kM + r) * kLd + d);
+        L += f * s_ml[w][r][1];
+        y.x += f * v.x;
+        y.y += f * v.y;
+        y.z += f * v.z;
+        y.w += f * v.w;
+      }
+      if (whole) {
+        finish<D>(a, qrow, r, d, y, M, L);
+      } else {
+        const size_t ps = (size_t)c * 2 + slot;
+        __stcg(reinterpret_cast<float4*>(a.part_o + (ps * 16 + r) * D + d), y);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + (ps * 16 + r) * 2), make_float2(M, L));
+      }
+    }
+    if (!whole) {
+      pend_s[slot] = g.s;
+      pend_h[slot] = g.h;
+      // the CTAs that own the (sequence, head)'s first and last piece
+      pend_first[slot] = (int)(((g.u + 1) * ctas - 1) / U);
+      pend_last[slot] = (int)(((g.u + g.np) * ctas - 1) / U);
+    }
+    named_sync<kPaConsumers>();  // the join buffer is free
+  }
+  // -------------------------------------------------------------- results shared with other CTAs
+  if (pend_s[0] < 0 && pend_s[1] < 0) return;
+  __threadfence();
+  named_sync<kPaConsumers>();
+  if (tid < 2 && pend_s[tid] >= 0) {
+    unsigned* cnt = a.counters + (size_t)pend_s[tid] * a.Hkv + pend_h[tid];
+    const unsigned old = atom_add_acq_rel_gpu(cnt, 1);
+    s_last[tid] = old == (unsigned)(pend_last[tid] - pend_first[tid]);
+    if (s_last[tid]) *cnt = 0;  // every contributor has arrived
+  }
+  named_sync<kPaConsumers>();
+  float(*s_w)[kPaGrid] = reinterpret_cast<float(*)[kPaGrid]>(join);  // weights of the parts per row
+  for (int e = 0; e < 2; ++e) {
+    if (pend_s[e] < 0 || !*(volatile int*)&s_last[e]) continue;
+    __threadfence();
+    const int first = pend_first[e], cnt = pend_last[e] - first + 1;
+    // weights of the parts, a warp per row; then the weighted sums in order
+    for (int r = warp; r < a.G; r += kPaWarps) {
+      float M = -INFINITY, L = 0.0f;
+      for (int i = lane; i < cnt; i += 32) M = fmaxf(M, __ldcg(a.part_ml + (((size_t)(first + i) * 2 + (i == 0)) * 16 + r) * 2));
+#pragma unroll
+      for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+      for (int i = lane; i < cnt; i += 32) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (((size_t)(first + i) * 2 + (i == 0)) * 16 + r) * 2));
+        const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
+        s_w[r][i] = f;
+        L += f * ml.y;
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
+      if (lane == 0) s_row[r][0] = M, s_row[r][1] = L;
+    }
+    named_sync<kPaConsumers>();
+    const size_t qrow = ((size_t)pend_s[e] * a.Hq + (size_t)pend_h[e] * a.G) * D;
+    for (int i = tid; i < a.G * (D / 4); i += kPaConsumers) {
+      const int r = i / (D / 4), d = 4 * (i % (D / 4));
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+      for (int x = 0; x < cnt; ++x) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (((size_t)(first + x) * 2 + (x == 0)) * 16 + r) * D + d));
+        const float f = s_w[r][x];
+        y.x += f * v.x;
+        y.y += f * v.y;
+        y.z += f * v.z;
+        y.w += f * v.w;
+      }
+      finish<D>(a, qrow, r, d, y, s_row[r][0], s_row[r][1]);
+    }
+    named_sync<kPaConsumers>();
+  }
 }
 
 bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -82,6 +557,34 @@ bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool attend_shape_ok(int S, int Hq, int Hkv, int D) {
   return S >= 1 && S <= 8192 && Hkv >= 1 && Hkv <= 1024 && (long long)S * Hkv <= 65536 && Hq >= Hkv && Hq % Hkv == 0 &&
          Hq / Hkv <= 16 && (D == 64 || D == 128 || D == 256);
+}
+
+struct PagedWs {
+  size_t counters, part_o, part_ml, total;
+};
+PagedWs paged_ws(int S, int Hkv, int D) {
+  PagedWs w;
+  w.counters = 256;
+  w.part_o = align_up(w.counters + sizeof(unsigned) * (size_t)S * Hkv, 256);
+  w.part_ml = w.part_o + sizeof(float) * kPaGrid * 2 * 16 * (size_t)D;
+  w.total = w.part_ml + sizeof(float) * kPaGrid * 2 * 16 * 2;
+  return w;
+}
+
+template <int D, bool kWide>
+cudaError_t launch_paged(const PagedArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  constexpr int kSmem = PaCfg<D, kWide>::kSmem;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !done[dev].load()) {
+    e = cudaFuncSetAttribute(paged_kernel<D, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) done[dev].store(true);
+  }
+  paged_kernel<D, kWide><<<grid, (PaCfg<D, kWide>::kThreads), kSmem, s>>>(a, kmap, vmap);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -94,7 +597,7 @@ extern "C" {
 
 size_t vp_paged_attention_workspace_bytes(int S, int Hq, int Hkv, int D) {
   if (!attend_shape_ok(S, Hq, Hkv, D)) return 0;
-  return 256;
+  return paged_ws(S, Hkv, D).total;
 }
 
 vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const int32_t* kv_len, int S, int Hq,
@@ -110,28 +613,48 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
   if (ws_bytes < vp_paged_attention_workspace_bytes(S, Hq, c.Hkv, c.D)) return VP_ERR_WORKSPACE;
   int sms = 0;
   if ((st = device_sm_count(&sms)) != VP_OK) return st;
+  PFN_cuTensorMapEncodeTiled_v12000 encode;
+  if ((st = tensor_map_encoder(&encode)) != VP_OK) return st;
+  const PagedWs w = paged_ws(S, c.Hkv, c.D);
+  uint8_t* b = static_cast<uint8_t*>(ws);
   PagedArgs a;
   a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(c.k);
-  a.v = static_cast<const uint16_t*>(c.v);
   a.gate = static_cast<const uint16_t*>(gate);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.kv_len = kv_len, a.pages = c.pages;
-  a.S = S, a.Hq = Hq, a.Hkv = c.Hkv, a.n_pages = c.n_pages, a.max_pages = c.max_pages;
+  a.S = S, a.Hq = Hq, a.Hkv = c.Hkv, a.G = Hq / c.Hkv, a.n_pages = c.n_pages, a.max_pages = c.max_pages;
   a.log_page = 4;
   while ((1 << a.log_page) < c.page_size) ++a.log_page;
-  a.scale = scale;
-  a.status = static_cast<int*>(ws);
-  const dim3 grid((unsigned)Hq, (unsigned)S);
+  const int rows = kPieceBytes / (2 * c.D);
+  a.log_box = 4;
+  while ((1 << a.log_box) < std::min(rows, c.page_size)) ++a.log_box;
+  a.scale2 = scale * 1.4426950408889634f;
+  a.counters = reinterpret_cast<unsigned*>(b + w.counters);
+  a.part_o = reinterpret_cast<float*>(b + w.part_o);
+  a.part_ml = reinterpret_cast<float*>(b + w.part_ml);
+  a.status = reinterpret_cast<int*>(b);
+  // keys and values as [D / 64][rows of all pages and heads][64]: a box is the piece's rows, all columns
+  CUtensorMap maps[2];
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t dims[3] = {64, (cuuint64_t)c.n_pages * c.Hkv * c.page_size, (cuuint64_t)c.D / 64};
+    const cuuint64_t strides[2] = {(cuuint64_t)c.D * 2, 128};
+    const cuuint32_t box[3] = {64, 1u << a.log_box, (cuuint32_t)c.D / 64}, step[3] = {1, 1, 1};
+    if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i ? c.v : c.k, dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return VP_ERR_UNSUPPORTED;
+  }
+  const int grid = std::min(sms, kPaGrid);
   cudaStream_t s = (cudaStream_t)stream;
+  const bool wide = a.G > 8;
+  cudaError_t e;
   if (c.D == 64)
-    attend_simple<64><<<grid, 128, 0, s>>>(a);
+    e = wide ? launch_paged<64, true>(a, maps[0], maps[1], grid, s) : launch_paged<64, false>(a, maps[0], maps[1], grid, s);
   else if (c.D == 128)
-    attend_simple<128><<<grid, 128, 0, s>>>(a);
+    e = wide ? launch_paged<128, true>(a, maps[0], maps[1], grid, s) : launch_paged<128, false>(a, maps[0], maps[1], grid, s);
   else
-    attend_simple<256><<<grid, 128, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
+    e = wide ? launch_paged<256, true>(a, maps[0], maps[1], grid, s) : launch_paged<256, false>(a, maps[0], maps[1], grid, s);
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
 
