@@ -90,6 +90,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
       : "memory");
 }
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -251,8 +257,8 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // a converged warp
     for (uint32_t i = 0; i < kMbarPolls; ++i) {
-      if (*(volatile int*)&s_abort) return false;
       if (__all_sync(0xFFFFFFFFu, mbar_try_wait_hint(bar, parity, 20000u))) return true;
+      if (__any_sync(0xFFFFFFFFu, *(volatile int*)&s_abort)) return false;
     }
     *(volatile int*)&s_abort = 1;
     atomicExch(a.status, (int)VP_ERR_TIMEOUT);
@@ -261,50 +267,53 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
 
   if (warp == kPaWarps) {
     // ------------------------------------------------------------ producer
+    // 32 pieces at a time: each lane looks up the pages of one, then they are issued in turn.
     const uint64_t pol = l2_evict_first_policy();
-    const int box = 1 << a.log_box, boxes = kR >> a.log_box;
-    int n = 0, ws = -1, w0 = 0, window = 0;  // 32 page ids of sequence ws from page w0 on, one per lane
+    const int boxes = kR >> a.log_box, box_bytes = 2 * D << a.log_box, slots = (1 << a.log_page) - 1;
+    constexpr int kMaxBoxes = kR / 16;
+    int n = 0, st = 0;
+    uint32_t par = 1;  // the first round of empty stages passes
     bool ok = true;
     while (ok && walk.template next<kR>(a, g)) {
-      const int used = ((g.len - 1) >> a.log_page) + 1;
-      for (int p = g.p0; p < g.p1; ++p, ++n) {
-        const int st = n % C::kStages;
-        const int first = (p * kR) >> a.log_page, last = min(p * kR + kR, g.len) - 1;
-        if (g.s != ws || first < w0 || (last >> a.log_page) >= w0 + 32) {
-          ws = g.s;
-          w0 = first;
-          window = w0 + lane < used ? __ldg(a.pages + (size_t)g.s * a.max_pages + w0 + lane) : -1;
-        }
-        int pg[4], bad = 0, good = 0;
+      const int32_t* table = a.pages + (size_t)g.s * a.max_pages;
+      for (int base = g.p0; ok && base < g.p1; base += 32) {
+        int rows[kMaxBoxes], bad = 0, good = 0;
+        const int p = base + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kMaxBoxes; ++j) {
           const int pos = p * kR + (j << a.log_box);
-          pg[j] = -1;
-          if (j >= boxes || pos > last) continue;
-          pg[j] = __shfl_sync(0xFFFFFFFFu, window, (pos >> a.log_page) - w0);
-          if (pg[j] < 0 || pg[j] >= a.n_pages) {
-            pg[j] = -1;
-            bad |= 1 << j;
-          } else {
+          rows[j] = -1;
+          if (j >= boxes || p >= g.p1 || pos >= g.len) continue;
+          const int pg = __ldg(table + (pos >> a.log_page));
+          if (pg >= 0 && pg < a.n_pages) {
+            rows[j] = ((pg * a.Hkv + g.h) << a.log_page) + (pos & slots);
             ++good;
+          } else {
+            bad |= 1 << j;
           }
         }
-        if (!(ok = wait(&empty[st], ((n / C::kStages) & 1) ^ 1))) break;
-        if (lane == 0) {
-          s_bad[st] = bad;
-          if (bad) atomicExch(a.status, (int)VP_ERR_SHAPE);
-          const uint32_t bar = smem_addr(&full[st]), dst = ring + st * 2 * kPieceBytes;
-          mbar_arrive_expect_tx(&full[st], good * (4 * D << a.log_box));
+        if (bad) atomicExch(a.status, (int)VP_ERR_SHAPE);
+        const int cnt = min(32, g.p1 - base);
+        for (int i = 0; i < cnt; ++i, ++n) {
+          int row[kMaxBoxes];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (pg[j] < 0) continue;
-            const int pos = p * kR + (j << a.log_box);
-            const int row = ((pg[j] * a.Hkv + g.h) << a.log_page) + (pos & ((1 << a.log_page) - 1));
-            tma_load_3d(dst + j * box * 2 * D, &kmap, 0, row, 0, bar, pol);
-            tma_load_3d(dst + kPieceBytes + j * box * 2 * D, &vmap, 0, row, 0, bar, pol);
+          for (int j = 0; j < kMaxBoxes; ++j) row[j] = __shfl_sync(0xFFFFFFFFu, rows[j], i);
+          const int bd = __shfl_sync(0xFFFFFFFFu, bad, i), gd = __shfl_sync(0xFFFFFFFFu, good, i);
+          if (!(ok = wait(&empty[st], par))) break;
+          if (elect_one()) {
+            s_bad[st] = bd;
+            const uint32_t bar = smem_addr(&full[st]), dst = ring + st * 2 * kPieceBytes;
+            mbar_arrive_expect_tx(&full[st], gd * 2 * box_bytes);
+#pragma unroll
+            for (int j = 0; j < kMaxBoxes; ++j) {
+              if (row[j] < 0) continue;
+              tma_load_3d(dst + j * box_bytes, &kmap, 0, row[j], 0, bar, pol);
+              tma_load_3d(dst + kPieceBytes + j * box_bytes, &vmap, 0, row[j], 0, bar, pol);
+            }
           }
+          __syncwarp();
+          if (++st == C::kStages) st = 0, par ^= 1;
         }
-        __syncwarp();
       }
     }
     if (!ok)  // the copies in flight land before the shared memory goes
@@ -314,7 +323,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
 
   // -------------------------------------------------------------- consumers
   const int gq = lane >> 2, cq = lane & 3;
-  int n = 0;                       // pieces of the run so far
+  int n = 0;                       // the run's pieces before the segment
+  int st = warp;                   // the warp's next stage (warp or warp + kWarps), and its phase
+  uint32_t par = 0;
   int pend_s[2] = {-1, -1}, pend_h[2] = {0, 0};
   int pend_first[2] = {0, 0}, pend_last[2] = {0, 0};
   const int sub = 128 << a.log_box;  // bytes between a box's 64-column groups
@@ -335,12 +346,17 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     constexpr int kH = kWide ? 2 : 1;  // row groups with maxima of their own
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    for (int p = g.p0; p < g.p1; ++p, ++n) {
-      if (n % kPaWarps != warp) continue;
-      const int st = n % C::kStages;
-      if (!wait(&full[st], (n / C::kStages) & 1)) continue;
-      const uint32_t kb = ring + st * 2 * kPieceBytes, vb = kb + kPieceBytes;
-      const int valid = g.len - p * kR, bad = *(volatile int*)&s_bad[st];
+    // the segment's first piece of this warp: the run's pieces go round the warps
+    const int skip = (warp - n % kPaWarps + kPaWarps) % kPaWarps;
+    n += g.p1 - g.p0;
+    for (int p = g.p0 + skip; p < g.p1; p += kPaWarps) {
+      const bool ok = wait(&full[st], par);
+      const int at = st;
+      st += kPaWarps;
+      if (st >= C::kStages) st = warp, par ^= 1;
+      if (!ok) continue;
+      const uint32_t kb = ring + at * 2 * kPieceBytes, vb = kb + kPieceBytes;
+      const int valid = g.len - p * kR, bad = *(volatile int*)&s_bad[at];
       const bool masked = valid < kR || bad;
       auto seen = [&](int key) { return key < valid && !((bad >> (key >> a.log_box)) & 1); };
       if (masked) {
@@ -441,7 +457,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       }
       if (masked) fence_proxy_async_smem();  // the zeros, before the stage's next copy
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive(&empty[at]);
     }
     // ---- the warps' results of this (sequence, head)
 #pragma unroll
