@@ -90,6 +90,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(pol)
       : "memory");
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -113,17 +118,23 @@ __device__ __forceinline__ int seq_len(const PagedArgs& a, int s) {
 
 // Four output values of row r of a (sequence, head group) from the joined sums; M in log2 units.
 template <int D>
-__device__ __forceinline__ void finish(const PagedArgs& a, size_t qrow, int r, int d, float4 y, float M, float L) {
+__device__ __forceinline__ void finish(const PagedArgs& a, size_t qrow, int r, int d, float4 y, float M, float L, uint2 gate) {
   const size_t at = qrow + (size_t)r * D + d;
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   float v[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
   if (a.gate) {
+    const float g[4] = {bfv(gate.x & 0xFFFF), bfv(gate.x >> 16), bfv(gate.y & 0xFFFF), bfv(gate.y >> 16)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] /= 1.0f + expf(-bfv(a.gate[at + e]));
+    for (int e = 0; e < 4; ++e) v[e] /= 1.0f + expf(-g[e]);
   }
   const __nv_bfloat162 p0 = __floats2bfloat162_rn(v[0], v[1]), p1 = __floats2bfloat162_rn(v[2], v[3]);
   *reinterpret_cast<uint2*>(a.out + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
   if (a.lse && d == 0) a.lse[qrow / D + r] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// a / b in 32 bits where that holds a (a 64-bit division is a call of some hundred instructions).
+__device__ __forceinline__ long long div64(long long a, int b) {
+  return a >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
 template <int D, bool kWide>
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   constexpr int kR = C::kRows, kM = C::kM, kLd = C::kLd;
   constexpr int kPaWarps = C::kWarps, kPaThreads = C::kThreads, kPaConsumers = C::kConsumers;
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages];
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], s_join;
   __shared__ int s_bad[C::kStages];          // boxes of the stage whose page is out of range (bit per box)
   __shared__ long long s_scan[kPaThreads / 32];
   __shared__ int s_first[3], s_abort, s_last[2];
@@ -196,6 +207,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
+    mbar_init(&s_join, 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -230,15 +242,16 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   const long long U = total * a.Hkv;
   const int ctas = (int)min((long long)gridDim.x, (U + kMinPieces - 1) / kMinPieces), c = blockIdx.x;
   if (c >= ctas) return;
-  const long long u0 = c * U / ctas, u1 = (c + 1) * U / ctas;
+  const long long u0 = div64(c * U, ctas), u1 = div64((c + 1) * U, ctas);
   if (u0 >= pre * a.Hkv && u0 < (pre + mine) * a.Hkv) {
     long long at = pre * a.Hkv;
     for (int s = sa;; ++s) {
       const int np = (seq_len(a, s) + kR - 1) / kR;
       if (u0 < at + (long long)np * a.Hkv) {
         s_first[0] = s;
-        s_first[1] = (int)((u0 - at) / np);
-        s_first[2] = (int)((u0 - at) % np);
+        const int h = (int)div64(u0 - at, np);
+        s_first[1] = h;
+        s_first[2] = (int)(u0 - at - (long long)h * np);
         break;
       }
       at += (long long)np * a.Hkv;
@@ -500,7 +513,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
         y.w += f * v.w;
       }
       if (whole) {
-        finish<D>(a, qrow, r, d, y, M, L);
+        uint2 gate = make_uint2(0, 0);
+        if (a.gate) gate = __ldg(reinterpret_cast<const uint2*>(a.gate + qrow + (size_t)r * D + d));
+        finish<D>(a, qrow, r, d, y, M, L, gate);
       } else {
         const size_t ps = (size_t)c * 2 + slot;
         __stcg(reinterpret_cast<float4*>(a.part_o + (ps * 16 + r) * D + d), y);
@@ -511,8 +526,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       pend_s[slot] = g.s;
       pend_h[slot] = g.h;
       // the CTAs that own the (sequence, head)'s first and last piece
-      pend_first[slot] = (int)(((g.u + 1) * ctas - 1) / U);
-      pend_last[slot] = (int)(((g.u + g.np) * ctas - 1) / U);
+      const long long a0 = (g.u + 1) * ctas - 1, a1 = (g.u + g.np) * ctas - 1;
+      pend_first[slot] = U >> 31 ? (int)(a0 / U) : (int)div64(a0, (int)U);
+      pend_last[slot] = U >> 31 ? (int)(a1 / U) : (int)div64(a1, (int)U);
     }
     named_sync<kPaConsumers>();  // the join buffer is free
   }
@@ -527,42 +543,95 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     if (s_last[tid]) *cnt = 0;  // every contributor has arrived
   }
   named_sync<kPaConsumers>();
-  float(*s_w)[kPaGrid] = reinterpret_cast<float(*)[kPaGrid]>(join);  // weights of the parts per row
+  // The last contributor's copies land in the ring, which is free: every part's maxima and sums (one copy, at
+  // the ring's end) and the parts' outputs, as many at a time as fit, a copy per lane of the first warp.
+  constexpr int kItems = (kM * (D / 4) + kPaConsumers - 1) / kPaConsumers;  // float4 sums per thread
+  constexpr int kMlBytes = 256 * kPaGrid, kRing = C::kStages * 2 * kPieceBytes - kMlBytes;
+  const uint8_t* ring_p = dyn + (ring - smem_addr(dyn));
+  const float* ml = reinterpret_cast<const float*>(ring_p + kRing);      // [2 part - 1][16][2]
+  float(*s_w)[kPaGrid] = reinterpret_cast<float(*)[kPaGrid]>(join);      // [row][part]: the parts' weights
+  const int part_bytes = a.G * D * 4, room = kRing / part_bytes;
+  uint32_t jpar = 0;
+#pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     if (pend_s[e] < 0 || !*(volatile int*)&s_last[e]) continue;
-    __threadfence();
     const int first = pend_first[e], cnt = pend_last[e] - first + 1;
-    // weights of the parts, a warp per row; then the weighted sums in order
-    for (int r = warp; r < a.G; r += kPaWarps) {
-      float M = -INFINITY, L = 0.0f;
-      for (int i = lane; i < cnt; i += 32) M = fmaxf(M, __ldcg(a.part_ml + (((size_t)(first + i) * 2 + (i == 0)) * 16 + r) * 2));
+    const size_t qrow = ((size_t)pend_s[e] * a.Hq + (size_t)pend_h[e] * a.G) * D;
+    // part x lies in its CTA's end slot when it is the first, else in the start slot
+    auto fetch = [&](int x0, int n, bool with_ml) {  // the first warp: parts x0 .. x0 + n - 1, and every part's maxima
+      const uint32_t bar = smem_addr(&s_join), ml_bytes = (2 * cnt - 1) * 128;
+      asm volatile("fence.proxy.async;" ::: "memory");  // the other CTAs' stores, before these copies read them
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&s_join, n * part_bytes + (with_ml ? ml_bytes : 0));
+        if (with_ml) bulk_load(ring + kRing, a.part_ml + ((size_t)first * 2 + 1) * 32, ml_bytes, bar);
+      }
+      __syncwarp();
+      for (int x = x0 + lane; x < x0 + n; x += 32)
+        bulk_load(ring + (x - x0) * part_bytes, a.part_o + ((size_t)(first + x) * 2 + (x == 0)) * (16 * D), part_bytes, bar);
+    };
+    if (warp == 0) fetch(0, min(room, cnt), true);
+    // the gate, while the parts are on their way
+    uint2 gate[kItems];
 #pragma unroll
-      for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
-      for (int i = lane; i < cnt; i += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (((size_t)(first + i) * 2 + (i == 0)) * 16 + r) * 2));
-        const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - M);
-        s_w[r][i] = f;
-        L += f * ml.y;
+    for (int k = 0; k < kItems; ++k) {
+      const int i = tid + k * kPaConsumers;
+      gate[k] = make_uint2(0, 0);
+      if (a.gate && i < a.G * (D / 4))
+        gate[k] = __ldg(reinterpret_cast<const uint2*>(a.gate + qrow + (size_t)(i / (D / 4)) * D + 4 * (i % (D / 4))));
+    }
+    wait(&s_join, jpar);
+    jpar ^= 1;
+    for (int r = warp; r < a.G; r += kPaWarps) {  // weights of the parts, a warp per row
+      float M = -INFINITY, L = 0.0f;
+      // part 0 lies first, part x >= 1 at index 2 x - 1 (the slots in between are other tiles')
+      for (int x = lane; x < cnt; x += 32) M = fmaxf(M, ml[max(2 * x - 1, 0) * 32 + 2 * r]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+      for (int x = lane; x < cnt; x += 32) {
+        const float* p = ml + max(2 * x - 1, 0) * 32 + 2 * r;
+        const float f = p[0] == -INFINITY ? 0.0f : exp2f(p[0] - M);
+        s_w[r][x] = f;
+        L += f * p[1];
       }
 #pragma unroll
-      for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
+      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
       if (lane == 0) s_row[r][0] = M, s_row[r][1] = L;
     }
     named_sync<kPaConsumers>();
-    const size_t qrow = ((size_t)pend_s[e] * a.Hq + (size_t)pend_h[e] * a.G) * D;
-    for (int i = tid; i < a.G * (D / 4); i += kPaConsumers) {
-      const int r = i / (D / 4), d = 4 * (i % (D / 4));
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int x = 0; x < cnt; ++x) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (((size_t)(first + x) * 2 + (x == 0)) * 16 + r) * D + d));
-        const float f = s_w[r][x];
-        y.x += f * v.x;
-        y.y += f * v.y;
-        y.z += f * v.z;
-        y.w += f * v.w;
+    float4 y[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int x0 = 0; x0 < cnt; x0 += room) {
+      const int n = min(room, cnt - x0);
+      if (x0) {
+        named_sync<kPaConsumers>();  // the ring is read
+        if (warp == 0) fetch(x0, n, false);
+        wait(&s_join, jpar);
+        jpar ^= 1;
       }
-      finish<D>(a, qrow, r, d, y, s_row[r][0], s_row[r][1]);
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int i = tid + k * kPaConsumers;
+        if (i >= a.G * (D / 4)) break;
+        const float* w = s_w[i / (D / 4)] + x0;
+        const uint8_t* src = ring_p + 16 * i;
+#pragma unroll 8
+        for (int x = 0; x < n; ++x) {  // in order
+          const float f = w[x];
+          const float4 v = *reinterpret_cast<const float4*>(src + x * part_bytes);
+          y[k].x += f * v.x;
+          y[k].y += f * v.y;
+          y[k].z += f * v.z;
+          y[k].w += f * v.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int i = tid + k * kPaConsumers;
+      if (i >= a.G * (D / 4)) break;
+      const int r = i / (D / 4);
+      finish<D>(a, qrow, r, 4 * (i % (D / 4)), y[k], s_row[r][0], s_row[r][1], gate[k]);
     }
     named_sync<kPaConsumers>();
   }
