@@ -26,6 +26,12 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float& a, float& b) {
   a = __uint_as_float(w << 16);
   b = __uint_as_float(w & 0xFFFF0000u);
 }
+__device__ __forceinline__ void unpack8(uint4 a, float (&v)[8]) {
+  unpack_bf16x2(a.x, v[0], v[1]);
+  unpack_bf16x2(a.y, v[2], v[3]);
+  unpack_bf16x2(a.z, v[4], v[5]);
+  unpack_bf16x2(a.w, v[6], v[7]);
+}
 // Eight consecutive values of a row of x (16-byte aligned).
 template <bool kF32>
 __device__ __forceinline__ void load8(const void* x, size_t at, float (&v)[8]) {
@@ -34,11 +40,7 @@ __device__ __forceinline__ void load8(const void* x, size_t at, float (&v)[8]) {
     const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4));
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
-    unpack_bf16x2(a.x, v[0], v[1]);
-    unpack_bf16x2(a.y, v[2], v[3]);
-    unpack_bf16x2(a.z, v[4], v[5]);
-    unpack_bf16x2(a.w, v[6], v[7]);
+    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at)), v);
   }
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -80,76 +82,111 @@ __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, 
   }
 }
 
-// One CTA per row, kC chunks of 8 values per thread in registers (one pass over the data).
+__device__ __noinline__ float scale64(float v, double s, float w) { return (float)((double)v * s * (double)w); }
+__device__ __noinline__ double square64(float v) { return (double)v * (double)v; }
+
+// One CTA per row, kC chunks of 8 values per thread, held in registers as the bf16 pairs that the residual
+// stream is rounded to: one pass over the data, every load issued before the first use.  Many rows: four
+// chunks per thread, so that an SM holds several rows' CTAs and 100 KB and more of loads in flight while
+// others reduce; few rows: one chunk per thread, the shortest path through a row.
 template <bool kF32, int kC>
 __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld, const uint16_t* residual,
-                                                    const float* __restrict__ weight, float eps, int K, uint16_t* h,
-                                                    uint8_t* __restrict__ q, float* __restrict__ scales) {
+                                                    const float* __restrict__ weight, int vec, float eps, int K,
+                                                    uint16_t* h, uint8_t* __restrict__ q, float* __restrict__ scales) {
   __shared__ float red[32];
   __shared__ double redd[32];
-  const int m = blockIdx.x, tid = threadIdx.x, T = blockDim.x, KB = qblocks(K);
-  float v[kC][8];
+  const int m = blockIdx.x, tid = threadIdx.x, T = blockDim.x, KB = qblocks(K), warps = T >> 5;
+  uint4 a[kC], b[kF32 ? kC : 1], r[kC];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    const int k = (tid + i * T) * 8;
+    a[i] = r[i] = make_uint4(0, 0, 0, 0);
+    if (kF32) b[i] = make_uint4(0, 0, 0, 0);
+    if (k >= K) continue;
+    const uint4* px = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + ((size_t)m * ld + k) * (kF32 ? 4 : 2));
+    a[i] = px[0];
+    if (kF32) b[i] = px[1];
+    if (residual) r[i] = *reinterpret_cast<const uint4*>(residual + (size_t)m * K + k);
+  }
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
     const int k = (tid + i * T) * 8;
+    float v[8];
+    if (kF32) {
+      const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-    if (k >= K) continue;
-    load8<kF32>(x, (size_t)m * ld + k, v[i]);
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+      unpack8(a[i], v);
+    }
     if (residual) {
-      float r[8];
-      load8<false>(residual, (size_t)m * K + k, r);
+      float t[8];
+      unpack8(r[i], t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] += r[e];
+      for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v[i][2 * e], v[i][2 * e + 1]);  // the residual stream is bf16
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);  // the residual stream is bf16
       w[e] = *reinterpret_cast<const uint32_t*>(&p);
-      unpack_bf16x2(w[e], v[i][2 * e], v[i][2 * e + 1]);
     }
-    if (h) *reinterpret_cast<uint4*>(h + (size_t)m * K + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    a[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (h && k < K) *reinterpret_cast<uint4*>(h + (size_t)m * K + k) = a[i];
+    unpack8(a[i], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+    for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
   if ((tid & 31) == 0) red[tid >> 5] = ss;
   __syncthreads();
   ss = 0.0f;
-  for (int w = 0; w < (T + 31) / 32; ++w) ss += red[w];
-  float inv = 1.0f / sqrtf(ss / (float)K + eps);
-  double invd = 0.0;
+  for (int w = 0; w < warps; ++w) ss += red[w];
+  const float inv = 1.0f / sqrtf(ss / (float)K + eps);
   const bool wide = !(ss >= 1e-30f && ss <= 3.0e38f);  // squares outside fp32 (or a zero or NaN row): fp64
+  double invd = 0.0;
   if (wide) {
     double sd = 0.0;
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
+    for (int i = 0; i < kC; ++i) {
+      float v[8];
+      unpack8(a[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sd += (double)v[i][e] * (double)v[i][e];
+      for (int e = 0; e < 8; ++e) sd += square64(v[e]);
+    }
     for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xFFFFFFFFu, sd, o);
     if ((tid & 31) == 0) redd[tid >> 5] = sd;
     __syncthreads();
     sd = 0.0;
-    for (int w = 0; w < (T + 31) / 32; ++w) sd += redd[w];
+    for (int w = 0; w < warps; ++w) sd += redd[w];
     invd = 1.0 / sqrt(sd / (double)K + (double)eps);
   }
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
     const int k = (tid + i * T) * 8;
     if ((k & ~127) >= K) continue;  // uniform over the half warp
-    float y[8], wt[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+    float v[8], wt[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+    unpack8(a[i], v);
     if (weight && k < K) {
+      if (vec) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(weight + k)), d = __ldg(reinterpret_cast<const float4*>(weight + k + 4));
+        wt[0] = c.x, wt[1] = c.y, wt[2] = c.z, wt[3] = c.w, wt[4] = d.x, wt[5] = d.y, wt[6] = d.z, wt[7] = d.w;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wt[e] = __ldg(weight + k + e);
+        for (int e = 0; e < 8; ++e) wt[e] = __ldg(weight + k + e);
+      }
     }
+    if (wide) {  // calls: as a choice between two results the slow fp64 products would be formed for every row
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      y[e] = wide ? (float)((double)v[i][e] * invd * (double)wt[e]) : v[i][e] * inv * wt[e];
+      for (int e = 0; e < 8; ++e) v[e] = scale64(v[e], invd, wt[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * wt[e];
+    }
     uint2 c;
-    const float s = quant_group(y, c);
+    const float s = quant_group(v, c);
     if (k < K) *reinterpret_cast<uint2*>(q + (size_t)m * K + k) = c;
     if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
   }
@@ -231,13 +268,15 @@ vp_status vp_add_rmsnorm_fp8(const void* x, int x_type, int64_t ld_x, const void
   int sms = 0;
   if ((st = device_sm_count(&sms)) != VP_OK) return st;
   const int chunks = K / 8;
-  const int threads = std::min(1024, (chunks + 31) / 32 * 32);
-  const bool two = chunks > threads;
-  auto* kern = x_type == VP_F32 ? (two ? norm_kernel<true, 2> : norm_kernel<true, 1>)
-                                : (two ? norm_kernel<false, 2> : norm_kernel<false, 1>);
-  kern<<<(unsigned)M, threads, 0, (cudaStream_t)stream>>>(x, ld_x, static_cast<const uint16_t*>(residual), weight, eps,
-                                                          K, static_cast<uint16_t*>(h), static_cast<uint8_t*>(q),
-                                                          scales);
+  const int per = M >= 2 * sms ? 4 : chunks > 1024 ? 2 : 1;
+  const int threads = (chunks + 32 * per - 1) / (32 * per) * 32;
+  const bool wide = x_type == VP_F32;
+  auto* kern = per == 4 ? (wide ? norm_kernel<true, 4> : norm_kernel<false, 4>)
+                        : per == 2 ? (wide ? norm_kernel<true, 2> : norm_kernel<false, 2>)
+                                   : (wide ? norm_kernel<true, 1> : norm_kernel<false, 1>);
+  kern<<<(unsigned)M, threads, 0, (cudaStream_t)stream>>>(x, ld_x, static_cast<const uint16_t*>(residual), weight,
+                                                          al(weight, 16), eps, K, static_cast<uint16_t*>(h),
+                                                          static_cast<uint8_t*>(q), scales);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
