@@ -64,21 +64,33 @@ __device__ __forceinline__ float quant_group(const float (&v)[8], uint2& codes) 
   return s;
 }
 
-// One half warp per (row, group).  Bounded by the bytes: 2 or 4 read and about 1 written per value.
-template <bool kF32>
+// A half warp takes kU (row, group) pairs in a row, all loads first.  Bounded by the bytes: 2 or 4 read and
+// about 1 written per value.
+template <bool kF32, int kU>
 __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, long long ld, int M, int K,
                                                     uint8_t* __restrict__ q, float* __restrict__ scales) {
   const int KB = qblocks(K), lane = threadIdx.x & 15;
-  const long long n = (long long)M * KB, step = (long long)gridDim.x * 16;
-  for (long long u = (long long)blockIdx.x * 16 + (threadIdx.x >> 4); u < n; u += step) {
-    const int m = (int)(u / KB), b = (int)(u - (long long)m * KB), k = b * kQBlock + lane * 8;
-    const bool ok = k < K;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (ok) load8<kF32>(x, (size_t)m * ld + k, v);
+  const long long n = (long long)M * KB, u0 = ((long long)blockIdx.x * 16 + (threadIdx.x >> 4)) * kU;
+  if (u0 >= n) return;
+  int m = n >> 32 ? (int)(u0 / KB) : (int)((uint32_t)u0 / (uint32_t)KB), b = (int)(u0 - (long long)m * KB);
+  float v[kU][8];
+  size_t at[kU];
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
+    const int k = b * kQBlock + lane * 8;
+    at[i] = m < M && k < K ? (size_t)m * K + k : ~(size_t)0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+    if (at[i] != ~(size_t)0) load8<kF32>(x, (size_t)m * ld + k, v[i]);
+    if (++b == KB) b = 0, ++m;
+  }
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
+    if (u0 + i >= n) break;
     uint2 c;
-    const float s = quant_group(v, c);
-    if (ok) *reinterpret_cast<uint2*>(q + (size_t)m * K + k) = c;
-    if (lane == 0) scales[u] = s;
+    const float s = quant_group(v[i], c);
+    if (at[i] != ~(size_t)0) *reinterpret_cast<uint2*>(q + at[i]) = c;
+    if (lane == 0) scales[u0 + i] = s;
   }
 }
 
@@ -251,9 +263,11 @@ vp_status vp_quant_fp8(const void* x, int x_type, int64_t ld_x, int M, int K, vo
   int sms = 0;
   if ((st = device_sm_count(&sms)) != VP_OK) return st;
   const long long n = (long long)M * qblocks(K);
-  const unsigned grid = (unsigned)std::min<long long>((n + 15) / 16, 64LL * sms);
-  auto* kern = x_type == VP_F32 ? quant_kernel<true> : quant_kernel<false>;
-  kern<<<grid, 256, 0, (cudaStream_t)stream>>>(x, ld_x, M, K, static_cast<uint8_t*>(q), scales);
+  const bool wide = x_type == VP_F32, many = n >= 512LL * sms;  // enough pairs to fill the SMs four at a time
+  const long long per = many ? 64 : 16, blocks = (n + per - 1) / per;
+  auto* kern = many ? (wide ? quant_kernel<true, 4> : quant_kernel<false, 4>)
+                    : (wide ? quant_kernel<true, 1> : quant_kernel<false, 1>);
+  kern<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(x, ld_x, M, K, static_cast<uint8_t*>(q), scales);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
