@@ -7,10 +7,10 @@
 // by itself to the fraction of a turn -- exact but for F_j's own rounding (2^-54 of a turn per
 // position: 3e-8 of a turn at 2^29 positions), with one integer product and no fp64.
 //
-// D / 8 lanes hold one head (16 bytes each); the group's sum of squares and a half-split pair's other
-// element come by shuffles.  A block serves one row and a group of heads; its sines and cosines are
-// formed once, in shared memory.  The bytes bound it for prompts (each read and written once), the
-// latency of one load, the reduction and one store for single tokens.
+// D / 8 lanes hold one head, each both elements of its four pairs; the sum of squares comes by shuffles.  A
+// block serves one row and a group of heads; its sines and cosines are formed once.  The bytes bound it for
+// prompts (each read and written once), the latency of one load, the reduction and one store for single
+// tokens.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,7 +36,7 @@ struct AppendArgs {
   float eps;
   int rot, interleaved;
   const int32_t *row_start, *ctx, *pages;
-  int S, M, Hq, Hkv, n_pages, log_page, max_pages, heads_per_block;
+  int S, M, Hq, Hkv, n_pages, log_page, max_pages;
   uint16_t *k_cache, *v_cache, *q_out;
   int32_t* kv_len;
   int* status;
@@ -72,12 +72,65 @@ __device__ __forceinline__ int find_seq(const int32_t* start, int S, int r) {
   return lo;
 }
 
-template <int D>
+__device__ __noinline__ double square64(float v) { return (double)v * (double)v; }
+__device__ __noinline__ float scale64(float v, double s, float w) { return (float)((double)v * s * (double)w); }
+
+// One head over its root mean square, times the weights at w0 (first four values) and w1; kL lanes hold 8 values each.
+template <int kL>
+__device__ __forceinline__ void norm_head(float (&x)[8], const float* w0, const float* w1, float eps, uint32_t mask) {
+  float ss = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+  for (int o = kL / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+  if (ss >= 1e-30f && ss <= 3.0e38f) {
+    const float inv = 1.0f / sqrtf(ss / (float)(8 * kL) + eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * __ldg(e < 4 ? w0 + e : w1 + e - 4);
+  } else {  // squares outside fp32's range (or a zero or NaN head): fp64, in calls so that no other head pays for it
+    double sd = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sd += square64(x[e]);
+#pragma unroll
+    for (int o = kL / 2; o; o >>= 1) sd += __shfl_xor_sync(mask, sd, o);
+    const double id = 1.0 / sqrt(sd / (double)(8 * kL) + (double)eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = scale64(x[e], id, __ldg(e < 4 ? w0 + e : w1 + e - 4));
+  }
+}
+__device__ __forceinline__ void turn(float& x0, float& x1, float c, float s) {
+  const float a = x0, b = x1;
+  x0 = fmaf(a, c, -(b * s));
+  x1 = fmaf(a, s, b * c);
+}
+
+// kB: heads per group of lanes.  Every load of the block's heads is issued first: they depend on nothing
+// that the row's position has to be looked up for.
+template <int D, int kB>
 __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kL = D / 8;                    // lanes per head
   constexpr int kGroups = kThreadsP / kL;      // heads at a time
-  __shared__ float s_cos[kMaxPairs], s_sin[kMaxPairs];
+  __shared__ __align__(16) float s_cos[kMaxPairs], s_sin[kMaxPairs];
   const int r = blockIdx.x, tid = threadIdx.x;
+  const int lane = tid & (kL - 1), nq = a.q ? a.Hq : 0, heads = nq + 2 * a.Hkv;
+  const int h0 = blockIdx.y * kB * kGroups + tid / kL;
+  // A lane's eight values: two runs of four.  Half-split pairs: elements 4 l .. and half + 4 l .. for the lanes of
+  // the rotated part, so that both elements of a pair are the lane's own; else eight in a row.
+  const int half = a.rot >> 1, rl = half >> 2;  // rl: lanes of the rotated part (both pairings)
+  const bool turns = lane < rl, split = turns && !a.interleaved;
+  const int off0 = split ? 4 * lane : 8 * lane, off1 = split ? half + 4 * lane : 8 * lane + 4;
+  uint4 raw[kB];
+#pragma unroll
+  for (int i = 0; i < kB; ++i) {
+    const int hh = h0 + i * kGroups;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (hh >= heads) continue;
+    const uint16_t* src = hh < nq ? a.q + (size_t)r * a.ld_q + hh * D
+                                  : hh < nq + a.Hkv ? a.k + (size_t)r * a.ld_k + (hh - nq) * D
+                                                    : a.v + (size_t)r * a.ld_v + (hh - nq - a.Hkv) * D;
+    const uint2 u = *reinterpret_cast<const uint2*>(src + off0), v = *reinterpret_cast<const uint2*>(src + off1);
+    raw[i] = make_uint4(u.x, u.y, v.x, v.y);
+  }
   // the lengths after this call, by the first blocks
   if (a.kv_len && blockIdx.y == 0) {
     for (long long s = (long long)r * kThreadsP + tid; s < a.S; s += (long long)gridDim.x * kThreadsP) {
@@ -87,86 +140,65 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
   }
   if (a.row_start && r == 0 && blockIdx.y == 0 && tid == 0 && a.status && (a.row_start[0] < 0 || a.row_start[a.S] > a.M))
     atomicExch(a.status, (int)VP_ERR_SHAPE);  // rows that this call does not have
-  const int s = a.row_start ? find_seq(a.row_start, a.S, r) : r;
+  int s = r;
+  if (a.row_start) {
+    if (a.S <= 2 * kThreadsP) {  // the number of sequences that start at or before the row: two loads for all
+      s = -1 + __syncthreads_count(tid < a.S && a.row_start[tid] <= r);
+      if (a.S > kThreadsP) s += __syncthreads_count(tid + kThreadsP < a.S && a.row_start[tid + kThreadsP] <= r);
+      if (s >= 0 && r >= a.row_start[a.S]) s = -1;
+    } else {
+      s = find_seq(a.row_start, a.S, r);
+    }
+  }
   if (s < 0) return;
   const long long pos = (long long)a.ctx[s] + (a.row_start ? r - a.row_start[s] : 0);
   int page = -1;
   if (pos >= 0 && (pos >> a.log_page) < a.max_pages) page = a.pages[(size_t)s * a.max_pages + (pos >> a.log_page)];
-  const bool ok = page >= 0 && page < a.n_pages;
-  if (!ok && tid == 0 && blockIdx.y == 0 && a.status) atomicExch(a.status, (int)VP_ERR_SHAPE);
-  const int half = a.rot >> 1;
   for (int j = tid; j < half; j += kThreadsP) {
     const unsigned long long f = (unsigned long long)pos * a.turn[j];
     // the nearest signed fraction of a turn, in half turns
     sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s_sin[j], &s_cos[j]);
   }
+  const bool ok = page >= 0 && page < a.n_pages;
+  if (!ok && tid == 0 && blockIdx.y == 0 && a.status) atomicExch(a.status, (int)VP_ERR_SHAPE);
   __syncthreads();
-  const int lane = tid & (kL - 1), heads = (a.q ? a.Hq : 0) + 2 * a.Hkv, nq = a.q ? a.Hq : 0;
-  const uint32_t mask = kL == 32 ? 0xFFFFFFFFu : ((1u << (kL & 31)) - 1) << ((threadIdx.x & 31) & ~(kL - 1));
-  const int end = min(heads, (int)(blockIdx.y + 1) * a.heads_per_block);
-  for (int hh = blockIdx.y * a.heads_per_block + tid / kL; hh < end; hh += kGroups) {
+  float4 cs = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (turns) {  // of pairs 4 lane .. 4 lane + 3, the same for every head
+    cs = *reinterpret_cast<const float4*>(s_cos + 4 * lane);
+    sn = *reinterpret_cast<const float4*>(s_sin + 4 * lane);
+  }
+  const uint32_t mask = kL == 32 ? 0xFFFFFFFFu : ((1u << (kL & 31)) - 1) << ((tid & 31) & ~(kL - 1));
+#pragma unroll
+  for (int i = 0; i < kB; ++i) {
+    const int hh = h0 + i * kGroups;
+    if (hh >= heads) break;
     const bool isq = hh < nq, isk = !isq && hh < nq + a.Hkv;
-    if (!ok && !isq) continue;
+    if (!ok && !isq) break;                     // nor any later one
     const int g = hh - nq - (isk ? 0 : a.Hkv);  // key or value head
-    const uint16_t* src = isq ? a.q + (size_t)r * a.ld_q + hh * D
-                              : isk ? a.k + (size_t)r * a.ld_k + g * D : a.v + (size_t)r * a.ld_v + g * D;
     const size_t slot = ((((size_t)(ok ? page : 0) * a.Hkv + g) << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
     uint16_t* dst = isq ? a.q_out + ((size_t)r * a.Hq + hh) * D : (isk ? a.k_cache : a.v_cache) + slot;
-    uint4 raw = *reinterpret_cast<const uint4*>(src + 8 * lane);
-    if (!isq && !isk) {
-      *reinterpret_cast<uint4*>(dst + 8 * lane) = raw;
-      continue;
-    }
-    float x[8];
-    unpack8(raw, x);
-    const float* w = isq ? a.q_norm : a.k_norm;
-    if (w) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = kL / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-      float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
-      if (ss >= 1e-30f && ss <= 3.0e38f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * __ldg(w + 8 * lane + e);
-      } else {  // squares outside fp32's range (or a zero or NaN head): fp64
-        double sd = 0.0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sd += (double)x[e] * (double)x[e];
-#pragma unroll
-        for (int o = kL / 2; o; o >>= 1) sd += __shfl_xor_sync(mask, sd, o);
-        const double id = 1.0 / sqrt(sd / (double)D + (double)a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (float)((double)x[e] * id * (double)__ldg(w + 8 * lane + e));
+    uint4 out = raw[i];
+    const float* w = isq ? a.q_norm : isk ? a.k_norm : nullptr;
+    if ((isq || isk) && (w || turns)) {
+      float x[8];
+      unpack8(raw[i], x);
+      if (w) norm_head<kL>(x, w + off0, w + off1, a.eps, mask);
+      if (split) {
+        turn(x[0], x[4], cs.x, sn.x);
+        turn(x[1], x[5], cs.y, sn.y);
+        turn(x[2], x[6], cs.z, sn.z);
+        turn(x[3], x[7], cs.w, sn.w);
+      } else if (turns) {
+        turn(x[0], x[1], cs.x, sn.x);
+        turn(x[2], x[3], cs.y, sn.y);
+        turn(x[4], x[5], cs.z, sn.z);
+        turn(x[6], x[7], cs.w, sn.w);
       }
+      out = pack8(x);
     }
-    if (a.interleaved) {
-      if (8 * lane < a.rot) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float c = s_cos[4 * lane + e / 2], sn = s_sin[4 * lane + e / 2], x0 = x[e], x1 = x[e + 1];
-          x[e] = fmaf(x0, c, -(x1 * sn));
-          x[e + 1] = fmaf(x0, sn, x1 * c);
-        }
-      }
-    } else if (half) {
-      const int hl = half / 8;  // lanes per half
-      const bool lo = lane < hl, in = lane < 2 * hl;
-      const int other = in ? (lo ? lane + hl : lane - hl) : lane;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = __shfl_sync(mask, x[e], other, kL);
-        if (in) {
-          const int j = (lo ? lane : other) * 8 + e;
-          const float c = s_cos[j], sn = s_sin[j];
-          x[e] = lo ? fmaf(x[e], c, -(y * sn)) : fmaf(y, sn, x[e] * c);
-        }
-      }
-    }
-    uint4 out = pack8(x);
     if (!ok) out = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(dst + 8 * lane) = out;
+    *reinterpret_cast<uint2*>(dst + off0) = make_uint2(out.x, out.y);
+    *reinterpret_cast<uint2*>(dst + off1) = make_uint2(out.z, out.w);
   }
 }
 
@@ -240,15 +272,14 @@ extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q,
   a.q_out = static_cast<uint16_t*>(q_out);
   a.kv_len = kv_len, a.status = status;
   const int heads = (q ? Hq : 0) + 2 * c.Hkv, at_once = kThreadsP / (c.D / 8);
-  a.heads_per_block = (heads + at_once - 1) / at_once * at_once;
-  const dim3 grid((unsigned)M, (unsigned)((heads + a.heads_per_block - 1) / a.heads_per_block));
-  cudaStream_t s = (cudaStream_t)stream;
-  if (c.D == 64)
-    append_kernel<64><<<grid, kThreadsP, 0, s>>>(a);
-  else if (c.D == 128)
-    append_kernel<128><<<grid, kThreadsP, 0, s>>>(a);
-  else
-    append_kernel<256><<<grid, kThreadsP, 0, s>>>(a);
+  // Few rows: one head per group of lanes (more blocks, the shortest path through each); many: four.
+  const bool many = (long long)M * heads >= 16LL * sms * at_once;
+  const int per = (many ? 4 : 1) * at_once;
+  const dim3 grid((unsigned)M, (unsigned)((heads + per - 1) / per));
+  auto* kern = c.D == 64 ? (many ? append_kernel<64, 4> : append_kernel<64, 1>)
+                         : c.D == 128 ? (many ? append_kernel<128, 4> : append_kernel<128, 1>)
+                                      : (many ? append_kernel<256, 4> : append_kernel<256, 1>);
+  kern<<<grid, kThreadsP, 0, (cudaStream_t)stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
