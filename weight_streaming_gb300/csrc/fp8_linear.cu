@@ -57,7 +57,8 @@ struct LinArgs {
   int vec_x, vec_w;           // the scales' rows can be read 16 bytes at a time
   int tiles, tile_m, tile_n;  // output tiles: in all, along the tokens, along the weight rows
   int dp_rounds, cut_tiles;   // whole tiles per CTA (pair); the tiles after them, each cut into
-  int split;                  // this many parts along K, one per CTA (pair)
+  int split;                  // this many parts along K, one per CTA (pair), at multiples of
+  int unit, units;            // this many K blocks; ceil(KB / unit)
   unsigned* counters;         // [cut_tiles][2 CTAs of a pair][8 epilogue warps]
   float* partials;            // [grid][kBC][128]
   int* status;
@@ -96,8 +97,8 @@ struct Sched {
     ++i;
     const int t = c / a.split, part = c - t * a.split;
     it.tile = a.dp_rounds * G + t;
-    it.kb0 = part * a.KB / a.split;
-    it.kb1 = (part + 1) * a.KB / a.split;
+    it.kb0 = part * a.units / a.split * a.unit;
+    it.kb1 = min(a.KB, (part + 1) * a.units / a.split * a.unit);
     return true;
   }
 };
@@ -461,7 +462,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     // block would keep the load unit busy for 256 cycles of the block's 512.  The next tile's first
     // factors are loaded before this tile's output is stored.
     const float *px, *pw;
-    float4 fx, fw, fx1, fw1;
+    float4 fx, fw;          // tokens on the lanes: the current four blocks'
+    float4 ax[4], aw[4];    // weights on the lanes: the next sixteen blocks'
     int mt, nt, next_mt = 0, next_nt = 0;
     Item next;
     auto fetch = [&]() -> bool {
@@ -473,11 +475,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int nb = kSwap ? next_nt : next_nt * (kBC / 128) + (kBC == 256 ? half : 0);
       px = a.xs + (size_t)min(m, a.M - 1) * a.KB;
       pw = a.ws + (size_t)min(nb, qblocks(a.N) - 1) * a.KB;
-      fx = load4(px, next.kb0 & ~3, a.KB, a.vec_x);
-      fw = load4(pw, next.kb0 & ~3, a.KB, a.vec_w);
-      if (kSwap && (next.kb0 & ~3) + 4 < next.kb1) {
-        fx1 = load4(px, (next.kb0 & ~3) + 4, a.KB, a.vec_x);
-        fw1 = load4(pw, (next.kb0 & ~3) + 4, a.KB, a.vec_w);
+      if constexpr (kSwap) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          if (next.kb0 + 4 * d < next.kb1) {
+            ax[d] = load4(px, next.kb0 + 4 * d, a.KB, a.vec_x);
+            aw[d] = load4(pw, next.kb0 + 4 * d, a.KB, a.vec_w);
+          }
+      } else {
+        fx = load4(px, next.kb0 & ~3, a.KB, a.vec_x);
+        fw = load4(pw, next.kb0 & ~3, a.KB, a.vec_w);
       }
       return true;
     };
@@ -583,39 +590,49 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       float acc[kW];
 #pragma unroll
       for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-      for (int kb = it.kb0; kb < it.kb1; kb += C::kG) {
+      if constexpr (kSwap) {
+        // A few columns per block.  The factors come 16 blocks ahead (four blocks per load, four loads in
+        // registers): behind the weight stream a miss takes microseconds.
+        for (int kb4 = it.kb0; ok && kb4 < it.kb1; kb4 += 16) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+#pragma unroll
+            for (int h = 0; h < 4; h += C::kG) {  // one buffer of kG blocks
+              const int kb = kb4 + 4 * d + h;
+              if (!ok || kb >= it.kb1) break;
+              if (!(ok = wait(tfull0 + 8 * b, par))) break;
+              tmem_fence_after();
+              const uint32_t tb = tm + b * C::kG * kBC;
+              uint32_t r[C::kG][kW];
+#pragma unroll
+              for (int g = 0; g < C::kG; ++g)
+                if (kb + g < it.kb1) tmem_ld<kW>(tb + g * kBC, r[g]);
+#pragma unroll
+              for (int g = 0; g < C::kG; ++g) tmem_wait<kW>(r[g]);
+              tmem_fence_before();
+              __syncwarp();
+              if (elect_one()) mbar_arrive(tempty0 + 8 * b);
+#pragma unroll
+              for (int g = 0; g < C::kG; ++g) {
+                if (kb + g >= it.kb1) break;
+                const float f = pick4(ax[d], h + g) * pick4(aw[d], h + g);
+#pragma unroll
+                for (int j = 0; j < kW; ++j)
+                  acc[j] = fmaf(__uint_as_float(r[g][j]), __shfl_sync(0xFFFFFFFFu, f, j), acc[j]);
+              }
+              if (++b == C::kBufs) b = 0, par ^= 1;
+            }
+            if (kb4 + 4 * d + 16 < it.kb1) {
+              ax[d] = load4(px, kb4 + 4 * d + 16, a.KB, a.vec_x);
+              aw[d] = load4(pw, kb4 + 4 * d + 16, a.KB, a.vec_w);
+            }
+          }
+        }
+      }
+      for (int kb = it.kb0; !kSwap && kb < it.kb1; ++kb) {
         if (!(ok = wait(tfull0 + 8 * b, par))) break;
         tmem_fence_after();
-        const uint32_t tb = tm + b * C::kG * kBC;
-        if constexpr (kSwap) {  // a few columns per block: all blocks' loads, then their sums
-          uint32_t r[C::kG][kW];
-#pragma unroll
-          for (int g = 0; g < C::kG; ++g)
-            if (kb + g < it.kb1) tmem_ld<kW>(tb + g * kBC, r[g]);
-#pragma unroll
-          for (int g = 0; g < C::kG; ++g) tmem_wait<kW>(r[g]);
-          tmem_fence_before();
-          __syncwarp();
-          if (elect_one()) mbar_arrive(tempty0 + 8 * b);
-#pragma unroll
-          for (int g = 0; g < C::kG; ++g) {
-            if (kb + g >= it.kb1) break;
-            const float f = pick4(fx, kb + g) * pick4(fw, kb + g);
-            if (((kb + g) & 3) == 3) {  // the next four factors are here already
-              fx = fx1;
-              fw = fw1;
-              if (kb + g + 5 < it.kb1) {
-                fx1 = load4(px, kb + g + 5, a.KB, a.vec_x);
-                fw1 = load4(pw, kb + g + 5, a.KB, a.vec_w);
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < kW; ++j)
-              acc[j] = fmaf(__uint_as_float(r[g][j]), __shfl_sync(0xFFFFFFFFu, f, j), acc[j]);
-          }
-          if (++b == C::kBufs) b = 0, par ^= 1;
-          continue;
-        }
+        const uint32_t tb = tm + b * kBC;
         // chunk by chunk; the next chunk's load is in flight while this one is accumulated
         constexpr int kNCh = kW / kCh;
         uint32_t r[2][kCh];
@@ -808,7 +825,9 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   int grid = std::min(sms, kLinGrid) / (p.pair ? 2 : 1);  // CTAs, or pairs
   a.dp_rounds = p.tiles / grid;
   a.cut_tiles = p.tiles - a.dp_rounds * grid;
-  a.split = a.cut_tiles ? std::max(1, std::min({grid / a.cut_tiles, a.KB, kMaxSplit})) : 1;
+  a.unit = p.swap ? 4 : 1;
+  a.units = (a.KB + a.unit - 1) / a.unit;
+  a.split = a.cut_tiles ? std::max(1, std::min({grid / a.cut_tiles, a.units, kMaxSplit})) : 1;
   if (a.dp_rounds == 0) grid = a.cut_tiles * a.split;
   if (p.pair) grid *= 2;
   a.counters = reinterpret_cast<unsigned*>(b + p.counters);
