@@ -43,7 +43,7 @@ namespace {
 constexpr int kPaGrid = 152;                  // CTAs at most: one per SM
 constexpr int kPieceBytes = 8192;             // of keys, and of values
 constexpr int kMinPieces = 8;                 // pieces per CTA at least
-constexpr int kJoinCost = 48;                 // joining parts of a (sequence, head) costs as much as these many pieces
+constexpr int kJoinCost = 18;                 // joining parts of a (sequence, head) costs as much as these many pieces
 
 struct PagedArgs {
   const uint16_t *q, *gate;
@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   __shared__ int s_bad[C::kStages];          // boxes of the stage whose page is out of range (bit per box)
   __shared__ long long s_scan[kPaThreads / 32];
   __shared__ int s_most[kPaThreads / 32];
-  __shared__ int s_first[3], s_abort, s_last[2];
-  __shared__ float s_ml[kPaWarps][kM][2], s_row[16][2];
+  __shared__ int s_first[6], s_abort, s_last[2];
+  __shared__ float s_ml[kPaWarps][kM][2], s_row[16];
   const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
   float* join = reinterpret_cast<float*>(dyn + (ring - smem_addr(dyn)) + C::kStages * 2 * kPieceBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -251,32 +251,75 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   pre -= mine;  // exclusive
   const long long U = total * a.Hkv;
   // Short sequences are not cut: a CTA takes those that start in its run.  The longest one then adds to the run
-  // (or is the run, where there are fewer (sequence, head)s than CTAs), and nothing has to be joined.  Four
-  // sequences of up to 700 positions, 4 x 256 heads: 21 us cut, 14 us whole.
+  // (or is the run, where there are fewer (sequence, head)s than CTAs), and nothing has to be joined.  64
+  // sequences of 100 to 300 positions, 8 x 128 heads: 25 us cut, 20 us whole.
   const long long run = max((U + gridDim.x - 1) / gridDim.x, (long long)kMinPieces);
   const bool whole = most + (a.S * a.Hkv > (int)gridDim.x ? run : 0) <= run + kJoinCost;
-  const int ctas = whole ? (int)min((long long)gridDim.x, U) : (int)min((long long)gridDim.x, (U + kMinPieces - 1) / kMinPieces);
   const int c = blockIdx.x;
-  if (c >= ctas) return;
-  const long long u0 = div64(c * U, ctas), u1 = div64((c + 1) * U, ctas);
-  if (u0 >= pre * a.Hkv && u0 < (pre + mine) * a.Hkv) {
-    long long at = pre * a.Hkv;
-    for (int s = sa;; ++s) {
-      const int np = (seq_len(a, s) + kR - 1) / kR;
-      if (u0 < at + (long long)np * a.Hkv) {
-        s_first[0] = s;
-        const int h = (int)div64(u0 - at, np);
-        s_first[1] = h;
-        s_first[2] = (int)(u0 - at - (long long)h * np);
-        break;
-      }
-      at += (long long)np * a.Hkv;
-    }
-  }
-  __syncthreads();
+  // Few (sequence, head)s: each is cut by itself into equal parts of at most `part` pieces, one per CTA.  A run of
+  // the line would end one and start another, two results to join in turn; the parts are longer than the
+  // runs, but not by more than that costs.  One sequence of 2,000 positions: 21 us in runs, 13 us in parts.
+  const int heads = a.S * a.Hkv;
+  const long long part = heads < (int)gridDim.x ? max((U + gridDim.x - heads - 1) / (gridDim.x - heads), (long long)kMinPieces) : 0;
+  const bool even = !whole && heads < (int)gridDim.x && part - run <= kJoinCost;
+  int ctas;
   Walk walk;
-  walk.u = u0;
-  walk.u1 = u1;
+  if (even) {
+    const int L = (int)part;
+    int parts = 0;  // of the thread's sequence (fewer sequences than threads here)
+    if (tid < a.S) parts = ((seq_len(a, tid) + kR - 1) / kR + L - 1) / L;
+    int before = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+      if (lane >= o) before += v;
+    }
+    __syncthreads();  // s_most is read
+    if (lane == 31) s_most[warp] = before;
+    __syncthreads();
+    ctas = 0;
+#pragma unroll
+    for (int w = 0; w < kPaThreads / 32; ++w) {
+      if (w < warp) before += s_most[w];
+      ctas += s_most[w];
+    }
+    ctas *= a.Hkv;
+    if (c >= ctas) return;
+    const int at = (before - parts) * a.Hkv;
+    if (c >= at && c < before * a.Hkv) {
+      const int np = (seq_len(a, tid) + kR - 1) / kR, h = (c - at) / parts, x = c - at - h * parts;
+      s_first[0] = tid;
+      s_first[1] = h;
+      s_first[2] = (int)((long long)x * np / parts);
+      s_first[3] = (int)((long long)(x + 1) * np / parts);
+      s_first[4] = c - x;
+      s_first[5] = c - x + parts - 1;
+    }
+    __syncthreads();
+    walk.u = 0;
+    walk.u1 = s_first[3] - s_first[2];
+  } else {
+    ctas = whole ? (int)min((long long)gridDim.x, U) : (int)min((long long)gridDim.x, (U + kMinPieces - 1) / kMinPieces);
+    if (c >= ctas) return;
+    const long long u0 = div64(c * U, ctas), u1 = div64((c + 1) * U, ctas);
+    if (u0 >= pre * a.Hkv && u0 < (pre + mine) * a.Hkv) {
+      long long at = pre * a.Hkv;
+      for (int s = sa;; ++s) {
+        const int np = (seq_len(a, s) + kR - 1) / kR;
+        if (u0 < at + (long long)np * a.Hkv) {
+          s_first[0] = s;
+          const int h = (int)div64(u0 - at, np);
+          s_first[1] = h;
+          s_first[2] = (int)(u0 - at - (long long)h * np);
+          break;
+        }
+        at += (long long)np * a.Hkv;
+      }
+    }
+    __syncthreads();
+    walk.u = u0;
+    walk.u1 = u1;
+  }
   walk.s = s_first[0];
   walk.h = s_first[1];
   walk.p = s_first[2];
@@ -547,9 +590,14 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       pend_s[slot] = g.s;
       pend_h[slot] = g.h;
       // the CTAs that own the (sequence, head)'s first and last piece
-      const long long a0 = (g.u + 1) * ctas - 1, a1 = (g.u + g.np) * ctas - 1;
-      pend_first[slot] = U >> 31 ? (int)(a0 / U) : (int)div64(a0, (int)U);
-      pend_last[slot] = U >> 31 ? (int)(a1 / U) : (int)div64(a1, (int)U);
+      if (even) {
+        pend_first[slot] = s_first[4];
+        pend_last[slot] = s_first[5];
+      } else {
+        const long long a0 = (g.u + 1) * ctas - 1, a1 = (g.u + g.np) * ctas - 1;
+        pend_first[slot] = U >> 31 ? (int)(a0 / U) : (int)div64(a0, (int)U);
+        pend_last[slot] = U >> 31 ? (int)(a1 / U) : (int)div64(a1, (int)U);
+      }
     }
     named_sync<kPaConsumers>();  // the join buffer is free
   }
@@ -602,26 +650,21 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     }
     wait(&s_join, jpar);
     jpar ^= 1;
-    for (int r = warp; r < a.G; r += kPaWarps) {  // weights of the parts, a warp per row
-      float M = -INFINITY, L = 0.0f;
-      // part 0 lies first, part x >= 1 at index 2 x - 1 (the slots in between are other tiles')
-      for (int x = lane; x < cnt; x += 32) M = fmaxf(M, ml[max(2 * x - 1, 0) * 32 + 2 * r]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-      for (int x = lane; x < cnt; x += 32) {
-        const float* p = ml + max(2 * x - 1, 0) * 32 + 2 * r;
-        const float f = p[0] == -INFINITY ? 0.0f : exp2f(p[0] - M);
-        s_w[r][x] = f;
-        L += f * p[1];
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
-      if (lane == 0) s_row[r][0] = M, s_row[r][1] = L;
+    // part 0's maxima and sums lie first, part x's at index 2 x - 1 (the slots in between are other tiles')
+    for (int i = tid; i < a.G * cnt; i += kPaConsumers) {
+      const int r = i / cnt, x = i - r * cnt;
+      float M = -INFINITY;
+#pragma unroll 8
+      for (int z = 0; z < cnt; ++z) M = fmaxf(M, ml[max(2 * z - 1, 0) * 32 + 2 * r]);
+      const float m = ml[max(2 * x - 1, 0) * 32 + 2 * r];
+      s_w[r][x] = m == -INFINITY ? 0.0f : exp2f(m - M);
+      if (x == 0) s_row[r] = M;
     }
     named_sync<kPaConsumers>();
     float4 y[kItems];
+    float L[kItems];
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < kItems; ++k) y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), L[k] = 0.0f;
     for (int x0 = 0; x0 < cnt; x0 += room) {
       const int n = min(room, cnt - x0);
       if (x0) {
@@ -634,11 +677,13 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       for (int k = 0; k < kItems; ++k) {
         const int i = tid + k * kPaConsumers;
         if (i >= a.G * (D / 4)) break;
-        const float* w = s_w[i / (D / 4)] + x0;
+        const int r = i / (D / 4);
+        const float* w = s_w[r] + x0;
         const uint8_t* src = ring_p + 16 * i;
 #pragma unroll 8
         for (int x = 0; x < n; ++x) {  // in order
           const float f = w[x];
+          L[k] += f * ml[max(2 * (x0 + x) - 1, 0) * 32 + 2 * r + 1];
           const float4 v = *reinterpret_cast<const float4*>(src + x * part_bytes);
           y[k].x += f * v.x;
           y[k].y += f * v.y;
@@ -652,7 +697,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       const int i = tid + k * kPaConsumers;
       if (i >= a.G * (D / 4)) break;
       const int r = i / (D / 4);
-      finish<D>(a, qrow, r, 4 * (i % (D / 4)), y[k], s_row[r][0], s_row[r][1], gate[k]);
+      finish<D>(a, qrow, r, 4 * (i % (D / 4)), y[k], s_row[r], L[k], gate[k]);
     }
     named_sync<kPaConsumers>();
   }
