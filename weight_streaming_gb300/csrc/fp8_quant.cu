@@ -2,10 +2,10 @@
 // (vp_quant_fp8), and the residual addition + RMSNorm with a quantised output (vp_add_rmsnorm_fp8).
 //
 // Mathematics: a group of 128 values shares s = max(max|x| / 448, 2^-126), so that |x / s| <= 448 up to
-// one rounding, and q = e4m3(x * (1 / s)): the reciprocal is one fp32 rounding away from the quotient,
-// which moves a value across a border of e4m3 (steps of 2^-3 relative) for about 1 in 2^19 values.
-// e4m3's half step is 2^-4 of the value: the 8 bits the tensor core multiplies.  The maximum is taken
-// on the magnitude's bits as integers, where NaN is above infinity: both reach the scale.
+// one rounding, and q = e4m3(x * (1 / s)): the reciprocal is below two fp32 roundings away from the
+// quotient, which moves a value across a border of e4m3 (steps of 2^-3 relative) for about 1 in 2^18
+// values.  e4m3's half step is 2^-4 of the value: the 8 bits the tensor core multiplies.  NaN and
+// infinities reach the scale.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -32,64 +32,116 @@ __device__ __forceinline__ void unpack8(uint4 a, float (&v)[8]) {
   unpack_bf16x2(a.z, v[4], v[5]);
   unpack_bf16x2(a.w, v[6], v[7]);
 }
-// Eight consecutive values of a row of x (16-byte aligned).
-template <bool kF32>
-__device__ __forceinline__ void load8(const void* x, size_t at, float (&v)[8]) {
-  if (kF32) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(x) + at));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(x) + at + 4));
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at)), v);
-  }
-}
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// s = max(m / 448, 2^-126) and r = 1 / s.  The quotient is m times the constant's reciprocal with its
+// remainder added back (exact in an fma, so the result is the rounded quotient), the reciprocal one
+// Newton step on the hardware's approximation (below 2 u): about 10 instructions in place of two
+// divisions' 40, in a kernel that issues as much as it loads.
+__device__ __forceinline__ void scale_of(float m, float& s, float& r) {
+  constexpr float kInv = 1.0f / kE4m3Max;
+  const float q = m * kInv;
+  s = fmaf(fmaf(-q, kE4m3Max, m), kInv, q);
+  s = fmaxf(s, 1.17549435e-38f);           // 2^-126: its reciprocal is finite
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = fmaf(r, fmaf(-s, r, 1.0f), r);
+  if (!(m <= 3.402823466e38f)) s = m, r = m == m ? 0.0f : m;  // an infinity: finite values over it are 0; NaN
+}
+// This lane's eight codes of values times r.
+__device__ __forceinline__ uint2 codes_of(const float (&v)[8], float r) {
+  return make_uint2(e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+}
 // The half warp's 16 x 8 values are one group: its scale (returned to every lane) and this lane's codes.
 __device__ __forceinline__ float quant_group(const float (&v)[8], uint2& codes) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);  // the other half warp may be past the row's end
-  uint32_t m = 0;
+  float m = fabsf(v[0]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(v[e]));
 #pragma unroll
-  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(half, m, o));
-  float s = __uint_as_float(m) / kE4m3Max;
-  if (s < 1.17549435e-38f) s = 1.17549435e-38f;  // 2^-126: its reciprocal is finite (NaN stays)
-  const float r = 1.0f / s;
-  codes.x = e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r);
-  codes.y = e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r);
+  for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(half, m, o));
+  float s, r;
+  scale_of(m, s, r);
+  codes = codes_of(v, r);
+  return s;
+}
+// The same of eight bf16 values as loaded: the maximum is taken on the magnitudes' bits, two at a time (as
+// integers NaN is above infinity).
+__device__ __forceinline__ float quant_group(uint4 w, uint2& codes) {
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16), abs = 0x7FFF7FFFu;
+  uint32_t m2 = max_u16x2(max_u16x2(w.x & abs, w.y & abs), max_u16x2(w.z & abs, w.w & abs));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) m2 = max_u16x2(m2, __shfl_xor_sync(half, m2, o));
+  float s, r, v[8];
+  scale_of(__uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u)), s, r);
+  unpack8(w, v);
+  codes = codes_of(v, r);
   return s;
 }
 
-// A half warp takes kU (row, group) pairs in a row, all loads first.  Bounded by the bytes: 2 or 4 read and
-// about 1 written per value.
-template <bool kF32, int kU>
+// A half warp takes kU (row, group) pairs in a row, all loads first.  Bounded by the bytes (2 or 4 read and
+// about 1 written per value) once the instructions are few.  kFlat: whole groups in a dense matrix, so the
+// pairs are consecutive in memory and need no row arithmetic.
+template <bool kF32, int kU, bool kFlat>
 __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, long long ld, int M, int K,
                                                     uint8_t* __restrict__ q, float* __restrict__ scales) {
   const int KB = qblocks(K), lane = threadIdx.x & 15;
   const long long n = (long long)M * KB, u0 = ((long long)blockIdx.x * 16 + (threadIdx.x >> 4)) * kU;
   if (u0 >= n) return;
-  int m = n >> 32 ? (int)(u0 / KB) : (int)((uint32_t)u0 / (uint32_t)KB), b = (int)(u0 - (long long)m * KB);
-  float v[kU][8];
-  size_t at[kU];
+  int m = 0, b = 0;
+  if (!kFlat) {
+    m = n >> 32 ? (int)(u0 / KB) : (int)((uint32_t)u0 / (uint32_t)KB);
+    b = (int)(u0 - (long long)m * KB);
+  }
+  uint4 w[kU][kF32 ? 2 : 1];
+  size_t at[kU];  // of the codes; ~0: nothing there
 #pragma unroll
   for (int i = 0; i < kU; ++i) {
     const int k = b * kQBlock + lane * 8;
-    at[i] = m < M && k < K ? (size_t)m * K + k : ~(size_t)0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-    if (at[i] != ~(size_t)0) load8<kF32>(x, (size_t)m * ld + k, v[i]);
-    if (++b == KB) b = 0, ++m;
+    bool ok;
+    size_t src;
+    if (kFlat) {
+      ok = u0 + i < n;
+      src = (size_t)u0 * kQBlock + lane * 8 + i * kQBlock;
+      at[i] = src;
+    } else {
+      ok = m < M && k < K;
+      src = (size_t)m * ld + k;
+      at[i] = ok ? (size_t)m * K + k : ~(size_t)0;
+      if (++b == KB) b = 0, ++m;
+    }
+    w[i][0] = w[i][kF32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
+    if (!ok) continue;
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + src * (kF32 ? 4 : 2));
+    w[i][0] = __ldg(p);
+    if (kF32) w[i][kF32 ? 1 : 0] = __ldg(p + 1);
   }
 #pragma unroll
   for (int i = 0; i < kU; ++i) {
     if (u0 + i >= n) break;
     uint2 c;
-    const float s = quant_group(v[i], c);
-    if (at[i] != ~(size_t)0) *reinterpret_cast<uint2*>(q + at[i]) = c;
+    float s;
+    if constexpr (kF32) {
+      const uint4 a = w[i][0], d = w[i][1];
+      const float v[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                          __uint_as_float(d.x), __uint_as_float(d.y), __uint_as_float(d.z), __uint_as_float(d.w)};
+      s = quant_group(v, c);
+    } else {
+      s = quant_group(w[i][0], c);
+    }
+    if (kFlat || at[i] != ~(size_t)0) *reinterpret_cast<uint2*>(q + at[i]) = c;
     if (lane == 0) scales[u0 + i] = s;
   }
 }
@@ -265,8 +317,10 @@ vp_status vp_quant_fp8(const void* x, int x_type, int64_t ld_x, int M, int K, vo
   const long long n = (long long)M * qblocks(K);
   const bool wide = x_type == VP_F32, many = n >= 512LL * sms;  // enough pairs to fill the SMs four at a time
   const long long per = many ? 64 : 16, blocks = (n + per - 1) / per;
-  auto* kern = many ? (wide ? quant_kernel<true, 4> : quant_kernel<false, 4>)
-                    : (wide ? quant_kernel<true, 1> : quant_kernel<false, 1>);
+  const bool flat = ld_x == K && K % kQBlock == 0;
+  auto* kern = !many ? (wide ? quant_kernel<true, 1, false> : quant_kernel<false, 1, false>)
+               : flat ? (wide ? quant_kernel<true, 4, true> : quant_kernel<false, 4, true>)
+                      : (wide ? quant_kernel<true, 4, false> : quant_kernel<false, 4, false>);
   kern<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(x, ld_x, M, K, static_cast<uint8_t*>(q), scales);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
