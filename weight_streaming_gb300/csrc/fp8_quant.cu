@@ -159,23 +159,25 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
                                                     uint16_t* h, uint8_t* __restrict__ q, float* __restrict__ scales) {
   __shared__ float red[32];
   __shared__ double redd[32];
-  const int m = blockIdx.x, tid = threadIdx.x, T = blockDim.x, KB = qblocks(K), warps = T >> 5;
+  const int m = blockIdx.x, tid = threadIdx.x, step = blockDim.x * 8, KB = qblocks(K), warps = blockDim.x >> 5;
+  const int k0 = tid * 8;  // the thread's first chunk; the others follow at `step`
+  const uint8_t* px = static_cast<const uint8_t*>(x) + ((size_t)m * ld + k0) * (kF32 ? 4 : 2);
+  const size_t row = (size_t)m * K + k0;
   uint4 a[kC], b[kF32 ? kC : 1], r[kC];
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    const int k = (tid + i * T) * 8;
     a[i] = r[i] = make_uint4(0, 0, 0, 0);
     if (kF32) b[i] = make_uint4(0, 0, 0, 0);
-    if (k >= K) continue;
-    const uint4* px = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + ((size_t)m * ld + k) * (kF32 ? 4 : 2));
-    a[i] = px[0];
-    if (kF32) b[i] = px[1];
-    if (residual) r[i] = *reinterpret_cast<const uint4*>(residual + (size_t)m * K + k);
+    if (k0 + i * step >= K) continue;
+    const uint4* p = reinterpret_cast<const uint4*>(px + i * step * (kF32 ? 4 : 2));
+    a[i] = p[0];
+    if (kF32) b[i] = p[1];
+    if (residual) r[i] = *reinterpret_cast<const uint4*>(residual + row + i * step);
   }
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    const int k = (tid + i * T) * 8;
+    const int k = k0 + i * step;
     float v[8];
     if (kF32) {
       const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
       w[e] = *reinterpret_cast<const uint32_t*>(&p);
     }
     a[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (h && k < K) *reinterpret_cast<uint4*>(h + (size_t)m * K + k) = a[i];
+    if (h && k < K) *reinterpret_cast<uint4*>(h + row + i * step) = a[i];
     unpack8(a[i], v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
@@ -208,50 +210,60 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
   __syncthreads();
   ss = 0.0f;
   for (int w = 0; w < warps; ++w) ss += red[w];
-  const float inv = 1.0f / sqrtf(ss / (float)K + eps);
-  const bool wide = !(ss >= 1e-30f && ss <= 3.0e38f);  // squares outside fp32 (or a zero or NaN row): fp64
-  double invd = 0.0;
-  if (wide) {
-    double sd = 0.0;
+  const float* pw = weight + k0;
+  if (ss >= 1e-30f && ss <= 3.0e38f) {
+    const float inv = 1.0f / sqrtf(ss / (float)K + eps);
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
+      const int k = k0 + i * step;
+      if ((k & ~127) >= K) break;  // uniform over the half warp
       float v[8];
       unpack8(a[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sd += square64(v[e]);
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
+      if (weight && k < K) {
+        if (vec) {
+          const float4 c = __ldg(reinterpret_cast<const float4*>(pw + i * step)), d = __ldg(reinterpret_cast<const float4*>(pw + i * step) + 1);
+          v[0] *= c.x, v[1] *= c.y, v[2] *= c.z, v[3] *= c.w, v[4] *= d.x, v[5] *= d.y, v[6] *= d.z, v[7] *= d.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= __ldg(pw + i * step + e);
+        }
+      }
+      uint2 c;
+      const float s = quant_group(v, c);
+      if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
+      if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
     }
-    for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xFFFFFFFFu, sd, o);
-    if ((tid & 31) == 0) redd[tid >> 5] = sd;
-    __syncthreads();
-    sd = 0.0;
-    for (int w = 0; w < warps; ++w) sd += redd[w];
-    invd = 1.0 / sqrt(sd / (double)K + (double)eps);
+    return;
   }
+  // Squares outside fp32 (or a zero or NaN row): fp64, in calls apart from the loop above, which would carry
+  // their slow products and registers otherwise.
+  double sd = 0.0;
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    const int k = (tid + i * T) * 8;
-    if ((k & ~127) >= K) continue;  // uniform over the half warp
-    float v[8], wt[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+    float v[8];
     unpack8(a[i], v);
-    if (weight && k < K) {
-      if (vec) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(weight + k)), d = __ldg(reinterpret_cast<const float4*>(weight + k + 4));
-        wt[0] = c.x, wt[1] = c.y, wt[2] = c.z, wt[3] = c.w, wt[4] = d.x, wt[5] = d.y, wt[6] = d.z, wt[7] = d.w;
-      } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wt[e] = __ldg(weight + k + e);
-      }
-    }
-    if (wide) {  // calls: as a choice between two results the slow fp64 products would be formed for every row
+    for (int e = 0; e < 8; ++e) sd += square64(v[e]);
+  }
+  for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xFFFFFFFFu, sd, o);
+  if ((tid & 31) == 0) redd[tid >> 5] = sd;
+  __syncthreads();
+  sd = 0.0;
+  for (int w = 0; w < warps; ++w) sd += redd[w];
+  const double invd = 1.0 / sqrt(sd / (double)K + (double)eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = scale64(v[e], invd, wt[e]);
-    } else {
+  for (int i = 0; i < kC; ++i) {
+    const int k = k0 + i * step;
+    if ((k & ~127) >= K) break;
+    float v[8];
+    unpack8(a[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * inv * wt[e];
-    }
+    for (int e = 0; e < 8; ++e) v[e] = scale64(v[e], invd, weight && k < K ? __ldg(pw + i * step + e) : 1.0f);
     uint2 c;
     const float s = quant_group(v, c);
-    if (k < K) *reinterpret_cast<uint2*>(q + (size_t)m * K + k) = c;
+    if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
     if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
   }
 }
