@@ -26,7 +26,7 @@ namespace vp {
 
 namespace {
 
-constexpr int kThreadsP = 256;
+constexpr int kThreadsP = 128;
 constexpr int kMaxPairs = 128;
 
 struct AppendArgs {
@@ -119,15 +119,17 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
   const int half = a.rot >> 1, rl = half >> 2;  // rl: lanes of the rotated part (both pairings)
   const bool turns = lane < rl, split = turns && !a.interleaved;
   const int off0 = split ? 4 * lane : 8 * lane, off1 = split ? half + 4 * lane : 8 * lane + 4;
+  // the row's arrays, each as if its heads had the numbers that they have here (q, then k, then v)
+  const uint16_t* q_row = a.q + (size_t)r * a.ld_q;
+  const uint16_t* k_row = a.k + (ptrdiff_t)r * a.ld_k - nq * D;
+  const uint16_t* v_row = a.v + (ptrdiff_t)r * a.ld_v - (nq + a.Hkv) * D;
   uint4 raw[kB];
 #pragma unroll
   for (int i = 0; i < kB; ++i) {
     const int hh = h0 + i * kGroups;
     raw[i] = make_uint4(0, 0, 0, 0);
     if (hh >= heads) continue;
-    const uint16_t* src = hh < nq ? a.q + (size_t)r * a.ld_q + hh * D
-                                  : hh < nq + a.Hkv ? a.k + (size_t)r * a.ld_k + (hh - nq) * D
-                                                    : a.v + (size_t)r * a.ld_v + (hh - nq - a.Hkv) * D;
+    const uint16_t* src = (hh < nq ? q_row : hh < nq + a.Hkv ? k_row : v_row) + hh * D;
     const uint2 u = *reinterpret_cast<const uint2*>(src + off0), v = *reinterpret_cast<const uint2*>(src + off1);
     raw[i] = make_uint4(u.x, u.y, v.x, v.y);
   }
@@ -167,6 +169,11 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     cs = *reinterpret_cast<const float4*>(s_cos + 4 * lane);
     sn = *reinterpret_cast<const float4*>(s_sin + 4 * lane);
   }
+  const int head_step = D << a.log_page;  // from one head's slot to the next one's in a page
+  const ptrdiff_t slot = (((ptrdiff_t)(ok ? page : 0) * a.Hkv << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
+  uint16_t* q_dst = a.q_out + (size_t)r * a.Hq * D;
+  uint16_t* k_dst = a.k_cache + (slot - (ptrdiff_t)nq * head_step);
+  uint16_t* v_dst = a.v_cache + (slot - (ptrdiff_t)(nq + a.Hkv) * head_step);
   const uint32_t mask = kL == 32 ? 0xFFFFFFFFu : ((1u << (kL & 31)) - 1) << ((tid & 31) & ~(kL - 1));
 #pragma unroll
   for (int i = 0; i < kB; ++i) {
@@ -174,9 +181,7 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     if (hh >= heads) break;
     const bool isq = hh < nq, isk = !isq && hh < nq + a.Hkv;
     if (!ok && !isq) break;                     // nor any later one
-    const int g = hh - nq - (isk ? 0 : a.Hkv);  // key or value head
-    const size_t slot = ((((size_t)(ok ? page : 0) * a.Hkv + g) << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
-    uint16_t* dst = isq ? a.q_out + ((size_t)r * a.Hq + hh) * D : (isk ? a.k_cache : a.v_cache) + slot;
+    uint16_t* dst = isq ? q_dst + hh * D : (isk ? k_dst : v_dst) + (ptrdiff_t)hh * head_step;
     uint4 out = raw[i];
     const float* w = isq ? a.q_norm : isk ? a.k_norm : nullptr;
     if ((isq || isk) && (w || turns)) {
@@ -272,14 +277,19 @@ extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q,
   a.q_out = static_cast<uint16_t*>(q_out);
   a.kv_len = kv_len, a.status = status;
   const int heads = (q ? Hq : 0) + 2 * c.Hkv, at_once = kThreadsP / (c.D / 8);
-  // Few rows: one head per group of lanes (more blocks, the shortest path through each); many: four.
-  const bool many = (long long)M * heads >= 16LL * sms * at_once;
-  const int per = (many ? 4 : 1) * at_once;
-  const dim3 grid((unsigned)M, (unsigned)((heads + per - 1) / per));
-  auto* kern = c.D == 64 ? (many ? append_kernel<64, 4> : append_kernel<64, 1>)
-                         : c.D == 128 ? (many ? append_kernel<128, 4> : append_kernel<128, 1>)
-                                      : (many ? append_kernel<256, 4> : append_kernel<256, 1>);
-  kern<<<grid, kThreadsP, 0, (cudaStream_t)stream>>>(a);
+  // Few rows: one head per group of lanes (more blocks, the shortest path through each).  Many: a row's heads
+  // over the fewest blocks of at most six per group, evenly (every block looks the row's position up; 6001
+  // rows of 48 heads: 45, 32, 30 us at 2 x 256, 3 x 128 and 6 x 128 heads x threads).
+  const int turns = (heads + at_once - 1) / at_once;
+  const bool many = (long long)M * turns >= 16LL * sms;
+  const int blocks = many ? (turns + 5) / 6 : turns, per = (turns + blocks - 1) / blocks;
+  using Kernel = void (*)(const AppendArgs);
+  static const Kernel kernels[3][6] = {
+      {append_kernel<64, 1>, append_kernel<64, 2>, append_kernel<64, 3>, append_kernel<64, 4>, append_kernel<64, 5>, append_kernel<64, 6>},
+      {append_kernel<128, 1>, append_kernel<128, 2>, append_kernel<128, 3>, append_kernel<128, 4>, append_kernel<128, 5>, append_kernel<128, 6>},
+      {append_kernel<256, 1>, append_kernel<256, 2>, append_kernel<256, 3>, append_kernel<256, 4>, append_kernel<256, 5>, append_kernel<256, 6>}};
+  const Kernel kern = kernels[c.D == 64 ? 0 : c.D == 128 ? 1 : 2][per - 1];
+  kern<<<dim3((unsigned)M, (unsigned)blocks), kThreadsP, 0, (cudaStream_t)stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
