@@ -554,7 +554,11 @@ vp_status vp_decode_steps_rows(const vp_model* model, int steps, int rows, const
  * KV cache in pages.  One layer of a step chains them:
  *   vp_add_rmsnorm_fp8 -> vp_linear_fp8_block (q, k, v) -> vp_paged_append -> vp_paged_attention ->
  *   vp_quant_fp8 -> vp_linear_fp8_block (o).
- * All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph. */
+ * All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph.  Outputs
+ * must not overlap inputs except where a call says so.  One workspace, zero-filled once, serves
+ * vp_linear_fp8_block and vp_paged_attention calls of any shapes in turn on one stream (of the
+ * largest of their sizes); a workspace that another section's call has used is zero-filled again
+ * first (vp_workspace_init). */
 
 /* Element type of an activation matrix. */
 enum { VP_BF16 = 0, VP_F32 = 1 };
@@ -566,7 +570,7 @@ enum { VP_BF16 = 0, VP_F32 = 1 };
  * infinite, and the elements that have no value NaN.  x: bf16 or fp32 (x_type VP_BF16 / VP_F32),
  * row stride ld_x elements; q: e4m3 bytes [M][K]; scales: fp32 [M][ceil(K / 128)].  1 <= M <= 2^24,
  * K % 16 == 0, 16 <= K <= 65536, ld_x >= K and rows 16-byte aligned (VP_ERR_SHAPE, VP_ERR_ALIGNMENT).
- * One launch, no workspace; the output must not overlap x. */
+ * One launch, no workspace. */
 vp_status vp_quant_fp8(const void* x, int x_type, int64_t ld_x, int M, int K, void* q, float* scales, void* stream);
 
 /* Residual addition, RMSNorm and the quantisation above in one pass over the rows:

@@ -604,6 +604,100 @@ def test_attention_shared_workspace_streams_and_graph(V):
     check_attend(V, p, q_rot, [606, 11, 339], D ** -0.5, what="after replays")
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,P,lens", [
+    (256, 8, 1, 128, [40000]),             # one head over every CTA: its parts come in several rounds
+    (64, 16, 1, 16, [70001]),              # the same above 8 heads
+    (128, 16, 2, 32, [9000, 3, 0, 5000]),  # long and short ones together
+    (128, 64, 8, 16, [1500] * 12),         # more (sequence, head)s than half the CTAs: runs over their borders
+    (64, 24, 24, 64, [900, 1, 64, 333, 2000, 0, 77]),
+])
+def test_attention_every_way_of_cutting(V, D, Hq, Hkv, P, lens):
+    rng = np.random.default_rng(len(lens) + D)
+    S = len(lens)
+    p = Paged(V, 31, S, -(-max(lens) // P), P, Hkv, D)
+    q, gate = bf16(rng, (S, Hq, D), 1.5), bf16(rng, (S, Hq, D), 2.0)
+    a, lse = check_attend(V, p, q, lens, D ** -0.5, gate, what=f"{S} x {max(lens)}")
+    b, lse_b = attend(V, p, q, lens, D ** -0.5, gate)
+    assert torch.equal(a, b) and torch.equal(lse, lse_b)
+
+
+def test_one_workspace_for_calls_of_every_shape(V):
+    """A workspace of the largest size serves attention and linear calls of any shapes in turn, without a
+    reset: the counters of one call are never another one's data."""
+    rng = np.random.default_rng(33)
+    calls = []
+    for S, Hq, Hkv, D, P, top in ((1000, 4, 2, 64, 16, 70), (1, 8, 1, 256, 64, 9000), (300, 12, 4, 128, 32, 500),
+                                  (4, 24, 4, 256, 64, 700)):
+        p = Paged(V, S, S, -(-top // P), P, Hkv, D)
+        lens = rng.integers(0, top + 1, S)
+        lens[0] = top
+        q = bf16(rng, (S, Hq, D), 1.5)
+        calls.append((V.vp_paged_attention_workspace_bytes(S, Hq, Hkv, D),
+                      lambda ws, p=p, q=q, lens=lens, D=D: attend(V, p, q, lens, D ** -0.5, ws=ws)[0]))
+    for M, N, K in ((8, 2560, 4096), (300, 1040, 2064), (100, 640, 640)):
+        c = dev_case(linear_case(M, M, N, K))
+        calls.append((V.vp_linear_fp8_block_workspace_bytes(M, N, K), lambda ws, c=c: linear(V, *c, True, wsp=ws)))
+    alone = [f(workspace(n)) for n, f in calls]
+    ws = workspace(max(n for n, _ in calls))
+    for _ in range(2):
+        for (_, f), want in zip(calls, alone):
+            assert torch.equal(f(ws), want)
+    for i in (6, 2, 5, 0, 4, 3, 1):
+        assert torch.equal(calls[i][1](ws), alone[i])
+
+
+def test_calls_on_two_streams_at_once(V):
+    """Independent calls overlap: a linear of each kind beside attention, each with its own workspace."""
+    rng = np.random.default_rng(34)
+    p = Paged(V, 35, 40, 16, 64, 4, 256)
+    q, lens = bf16(rng, (40, 24, 256), 1.5), i32([1000] * 40)
+    want_o, _ = attend(V, p, q, [1000] * 40, 0.0625)
+    shapes = [(8, 5120, 4096), (100, 2560, 4096), (1500, 2560, 2048)]
+    cases = [dev_case(linear_case(1, *s)) for s in shapes]
+    want = [linear(V, *c, True) for c in cases]
+    packs, ys, lws = [], [], []
+    for c, (M, N, K) in zip(cases, shapes):
+        packs.append(torch.empty(V.vp_packed_bytes_fp8_block(N, K), dtype=torch.uint8, device="cuda"))
+        V.vp_pack_fp8_block(c[2], N, K, packs[-1])
+        ys.append(torch.empty((M, N), device="cuda"))
+        lws.append(workspace(V.vp_linear_fp8_block_workspace_bytes(M, N, K)))
+    out = torch.empty_like(q)
+    aws = workspace(V.vp_paged_attention_workspace_bytes(40, 24, 4, 256))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    desc = p.desc()
+    for _ in range(10):
+        V.vp_paged_attention(desc, q, lens, 40, 24, 0.0625, None, out, None, aws, stream=s1)
+        for pk, c, y, w, (M, N, K) in zip(packs, cases, ys, lws, shapes):
+            V.vp_linear_fp8_block(pk, c[3], c[0], c[1], y, V.VP_F32, M, N, K, w, stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want_o) and all(torch.equal(a, b) for a, b in zip(ys, want))
+    assert V.vp_read_status(aws) == V.VP_OK and all(V.vp_read_status(w) == V.VP_OK for w in lws)
+
+
+@pytest.mark.parametrize("S", [100, 128, 129, 256, 257, 700])
+def test_append_finds_the_sequence_of_every_row(V, S):
+    """Row offsets with empty sequences and padding at both ends, over each way of looking a row up."""
+    rng = np.random.default_rng(S)
+    rows = rng.integers(0, 4, S)
+    ctx = rng.integers(0, 30, S)
+    start = 3 + np.concatenate([[0], np.cumsum(rows)])
+    T = int(rows.sum())
+    M, Hkv, D, P = T + 8, 2, 64, 16
+    p = Paged(V, S, S, 3, P, Hkv, D)
+    k, v = bf16(rng, (M, Hkv, D)), bf16(rng, (M, Hkv, D))
+    want_k, want_v = p.k.clone(), p.v.clone()
+    seq = np.repeat(np.arange(S), rows)
+    pos = np.repeat(ctx, rows) + np.concatenate([np.arange(n) for n in rows])
+    pg, sl = torch.from_numpy(p.table[seq, pos // P]).cuda().long(), torch.from_numpy(pos % P).cuda()
+    want_k[pg, :, sl], want_v[pg, :, sl] = k[3:3 + T], v[3:3 + T]
+    kv_len, status = i32([0] * S), i32([0])
+    V.vp_paged_append(p.desc(), None, 0, k, Hkv * D, v, Hkv * D, None, None, 0.0, None, i32(start), i32(ctx), S, M, 0, None,
+                      kv_len, status)
+    assert torch.equal(p.k, want_k) and torch.equal(p.v, want_v)
+    assert kv_len.tolist() == (ctx + rows).tolist() and int(status) == 0
+
+
 # ------------------------------------------------------------------ together
 def test_layer_of_a_served_step(V):
     """One attention layer as it is used: a prompt of two sequences, then two single-token steps.  Every

@@ -35,6 +35,7 @@
 #include "fp8_block.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "serve_ws.h"
 #include "tma.h"
 #include "verify.h"
 
@@ -712,7 +713,7 @@ struct LinPlan {
   int bc;
   bool swap, pair;
   int tile_m, tile_n, tiles;
-  size_t counters, partials, total;
+  size_t total;  // workspace bytes
 };
 
 LinPlan lin_plan(int M, int N) {
@@ -723,9 +724,8 @@ LinPlan lin_plan(int M, int N) {
   p.tile_m = p.swap ? 1 : p.pair ? (M + 255) / 256 : 1;
   p.tile_n = p.swap ? qblocks(N) : (N + p.bc - 1) / p.bc;
   p.tiles = p.tile_m * p.tile_n;
-  p.counters = 256;
-  p.partials = align_up(p.counters + sizeof(unsigned) * kLinGrid * 2 * (kEpiThreads / 32), 256);
-  p.total = p.partials + sizeof(float) * kLinGrid * (size_t)p.bc * 128;
+  static_assert(kLinGrid * 2 * (kEpiThreads / 32) <= kServeMaxCounters, "counters");
+  p.total = kServeData + sizeof(float) * kLinGrid * (size_t)p.bc * 128;
   return p;
 }
 
@@ -845,8 +845,8 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   a.split = a.cut_tiles ? lin_split(p.bc, a.KB, std::min({grid / a.cut_tiles, a.units, kMaxSplit})) : 1;
   if (a.dp_rounds == 0) grid = a.cut_tiles * a.split;
   if (p.pair) grid *= 2;
-  a.counters = reinterpret_cast<unsigned*>(b + p.counters);
-  a.partials = reinterpret_cast<float*>(b + p.partials);
+  a.counters = reinterpret_cast<unsigned*>(b + kServeCounters);
+  a.partials = reinterpret_cast<float*>(b + kServeData);
   a.status = reinterpret_cast<int*>(b);
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;

@@ -33,6 +33,7 @@
 #include "internal.h"
 #include "paged.h"
 #include "ptx.cuh"
+#include "serve_ws.h"
 #include "tma.h"
 #include "verify.h"
 
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     s_abort = 0;
     fence_mbar_init();
   }
+  if (tid < 6) s_first[tid] = 0;
   // Sequences without positions: zeros, and the status of those out of range.
   for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
     if (seq_len(a, s) > 0) continue;
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     const long long u0 = div64(c * U, ctas), u1 = div64((c + 1) * U, ctas);
     if (u0 >= pre * a.Hkv && u0 < (pre + mine) * a.Hkv) {
       long long at = pre * a.Hkv;
-      for (int s = sa;; ++s) {
+      for (int s = sa; s < sb; ++s) {
         const int np = (seq_len(a, s) + kR - 1) / kR;
         if (u0 < at + (long long)np * a.Hkv) {
           s_first[0] = s;
@@ -598,6 +600,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
         pend_first[slot] = U >> 31 ? (int)(a0 / U) : (int)div64(a0, (int)U);
         pend_last[slot] = U >> 31 ? (int)(a1 / U) : (int)div64(a1, (int)U);
       }
+      // in range whatever is written to kv_len meanwhile
+      pend_first[slot] = max(0, min(pend_first[slot], ctas - 1));
+      pend_last[slot] = max(pend_first[slot], min(pend_last[slot], ctas - 1));
     }
     named_sync<kPaConsumers>();  // the join buffer is free
   }
@@ -706,17 +711,16 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
 bool al(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 bool attend_shape_ok(int S, int Hq, int Hkv, int D) {
-  return S >= 1 && S <= 8192 && Hkv >= 1 && Hkv <= 1024 && (long long)S * Hkv <= 65536 && Hq >= Hkv && Hq % Hkv == 0 &&
+  return S >= 1 && S <= 8192 && Hkv >= 1 && Hkv <= 1024 && (size_t)S * Hkv <= kServeMaxCounters && Hq >= Hkv && Hq % Hkv == 0 &&
          Hq / Hkv <= 16 && (D == 64 || D == 128 || D == 256);
 }
 
 struct PagedWs {
-  size_t counters, part_o, part_ml, total;
+  size_t part_o, part_ml, total;
 };
-PagedWs paged_ws(int S, int Hkv, int D) {
+PagedWs paged_ws(int D) {  // the counters, one per (sequence, head), lie at kServeCounters
   PagedWs w;
-  w.counters = 256;
-  w.part_o = align_up(w.counters + sizeof(unsigned) * (size_t)S * Hkv, 256);
+  w.part_o = kServeData;
   w.part_ml = w.part_o + sizeof(float) * kPaGrid * 2 * 16 * (size_t)D;
   w.total = w.part_ml + sizeof(float) * kPaGrid * 2 * 16 * 2;
   return w;
@@ -748,7 +752,7 @@ extern "C" {
 
 size_t vp_paged_attention_workspace_bytes(int S, int Hq, int Hkv, int D) {
   if (!attend_shape_ok(S, Hq, Hkv, D)) return 0;
-  return paged_ws(S, Hkv, D).total;
+  return paged_ws(D).total;
 }
 
 vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const int32_t* kv_len, int S, int Hq,
@@ -766,7 +770,7 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
   if ((st = device_sm_count(&sms)) != VP_OK) return st;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   if ((st = tensor_map_encoder(&encode)) != VP_OK) return st;
-  const PagedWs w = paged_ws(S, c.Hkv, c.D);
+  const PagedWs w = paged_ws(c.D);
   uint8_t* b = static_cast<uint8_t*>(ws);
   PagedArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -781,7 +785,7 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
   a.log_box = 4;
   while ((1 << a.log_box) < std::min(rows, c.page_size)) ++a.log_box;
   a.scale2 = scale * 1.4426950408889634f;
-  a.counters = reinterpret_cast<unsigned*>(b + w.counters);
+  a.counters = reinterpret_cast<unsigned*>(b + kServeCounters);
   a.part_o = reinterpret_cast<float*>(b + w.part_o);
   a.part_ml = reinterpret_cast<float*>(b + w.part_ml);
   a.status = reinterpret_cast<int*>(b);
