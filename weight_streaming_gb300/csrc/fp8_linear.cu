@@ -18,9 +18,10 @@
 //    the lanes for M <= 64 (16, 32 or 64 token columns; the factors come by shuffles): a small batch
 //    then pads to 16 columns instead of 128 lanes, and the weight stream is what it waits for.
 //  * Work: whole rounds of output tiles first; each remaining tile is cut along K into as many parts as
-//    there are CTAs for it (at most 16).  Parts go through fp32 partials in the workspace: the last CTA
-//    to arrive (a counter, nobody waits) adds them in K order, so results do not depend on the
-//    arrival order.
+//    there are CTAs for it (at most 16).  Where few narrow tiles are all of the work, a tile's parts are
+//    a cluster and join through shared memory; else they go through fp32 partials in the workspace,
+//    which the last CTA to arrive (a counter, nobody waits) adds.  In K order both times, so results
+//    do not depend on the arrival order.
 //
 // Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, drains its copies and MMAs and frees
 // its tensor memory.
@@ -48,6 +49,7 @@ constexpr int kLinGrid = 152;     // CTAs at most: one per SM
 constexpr int kEpiThreads = 256;
 constexpr int kSmemRing = 216 * 1024;
 constexpr int kMaxStages = 12;
+constexpr int kMaxCluster = 8;    // CTAs of a cluster that joins parts
 constexpr int kMaxSplit = 16;     // parts along K: each costs the last one a read of its sums
 
 struct LinArgs {
@@ -60,6 +62,7 @@ struct LinArgs {
   int dp_rounds, cut_tiles;   // whole tiles per CTA (pair); the tiles after them, each cut into
   int split;                  // this many parts along K, one per CTA (pair), at multiples of
   int unit, units;            // this many K blocks; ceil(KB / unit)
+  int cluster;                // > 1: the parts of a tile are the CTAs of a cluster and join in shared memory
   unsigned* counters;         // [cut_tiles][2 CTAs of a pair][8 epilogue warps]
   float* partials;            // [grid][kBC][128]
   int* status;
@@ -257,6 +260,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
   return r;
 }
+// A float of the cluster's CTA `rank`, at this CTA's shared address.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, int rank) {
+  uint32_t r;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+  return v;
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -340,8 +351,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   if (warp == 1) lin_tmem_alloc<kPair>(&s_tmem, C::kCols);
   tmem_fence_before();
-  __syncthreads();
-  if (kPair) cluster_sync();  // the other CTA's barriers exist
+  if constexpr (kPair) {
+    __syncthreads();
+    cluster_sync();  // the other CTA's barriers exist
+  } else {           // the copying warp made the barriers and needs nothing else: it starts at once
+    __syncwarp();
+    if (warp == 0)
+      asm volatile("bar.arrive 2, %0;" ::"n"(kLinThreads) : "memory");
+    else
+      asm volatile("bar.sync 2, %0;" ::"n"(kLinThreads) : "memory");
+  }
   tmem_fence_after();
   const uint32_t tmem = *(volatile uint32_t*)&s_tmem;
 
@@ -668,6 +687,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       if (!ok) break;
       more = fetch();
+      if (kSwap && a.cluster > 1) {  // a part: left in the ring, which is free, for the cluster (below)
+#pragma unroll
+        for (int j = 0; j < kW; ++j)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(ring + ((c0 + j) * 128 + row) * 4), "f"(acc[j]) : "memory");
+        continue;
+      }
       if (it.kb1 - it.kb0 < a.KB) {
         // A part of the tile's K blocks: left in the workspace, and the last contributor adds them up.  Each
         // warp joins its own part of the tile (8 counters per tile and CTA): no CTA-wide wait.
@@ -697,9 +722,39 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
   if (kPair) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the thread's output stores are done
   __syncwarp();
+  if constexpr (kSwap && kBC <= 32) {
+    if (a.cluster > 1) {
+      cluster_sync();  // every part lies in its CTA's shared memory
+      if (warp >= 4) {  // each CTA adds every cluster-th token's sums, in K order
+        Sched sched(0);
+        Item it;
+        int mt, nt;
+        sched.next(a, it);
+        tile_at(a, it.tile, mt, nt);
+        const int c0 = ((warp - 4) >> 2) * (kBC / 2), row = (warp & 3) * 32 + lane, nn = nt * 128 + row;
+        for (int j = (int)cluster_rank(); j < kBC / 2; j += a.cluster) {
+          const int mm = mt * kBC + c0 + j;
+          if (mm >= a.M) break;
+          const uint32_t at = ring + ((c0 + j) * 128 + row) * 4;
+          float y = 0.0f;
+#pragma unroll
+          for (int e = 0; e < kMaxCluster; ++e) {
+            if (e >= a.cluster) break;
+            y += ld_cluster(at, e);
+          }
+          if (nn >= a.N) continue;
+          if (a.f32)
+            static_cast<float*>(a.y)[(size_t)mm * a.N + nn] = y;
+          else
+            static_cast<__nv_bfloat16*>(a.y)[(size_t)mm * a.N + nn] = __float2bfloat16_rn(y);
+        }
+      }
+      __syncwarp();
+    }
+  }
   tmem_fence_before();
   __syncthreads();
-  if (kPair) cluster_sync();  // nobody reads or signals this CTA's shared memory any more
+  if (kPair || (kSwap && a.cluster > 1)) cluster_sync();  // nobody reads or signals this CTA's shared memory any more
   tmem_fence_after();
   if (warp == 1) lin_tmem_dealloc<kPair>(tmem, C::kCols);
 }
@@ -744,18 +799,24 @@ int lin_split(int bc, int KB, int most) {
   return best;
 }
 
+// Narrow tiles that are all cut join in clusters where every cluster is resident at once (clusters of 7 leave
+// SMs of most GPCs idle, for one).  5120 x 17408, 3 parts: 8 tokens 19.6 us through the workspace, 18.3 in
+// clusters; 32 tokens 21.0 and 20.7; 64 tokens 22.8 and 23.7 (32 KB a part), so those keep the workspace.
 template <int kBC, bool kSwap, bool kPair>
-cudaError_t launch_linear(const LinArgs& a, const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& ymap,
+cudaError_t launch_linear(LinArgs& a, const CUtensorMap& xmap, const CUtensorMap& wmap, const CUtensorMap& ymap,
                           int grid, cudaStream_t s) {
   constexpr int kSmem = LinCfg<kBC, kPair>::kSmem;
+  auto* kern = linear_kernel<kBC, kSwap, kPair>;
   static std::atomic<bool> done[64];
+  static std::atomic<int> resident[64][kMaxCluster + 1];  // clusters of a size, plus one; 0: not asked yet
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !done[dev].load()) {
-    e = cudaFuncSetAttribute(linear_kernel<kBC, kSwap, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const bool known = dev >= 0 && dev < 64;
+  if (!known || !done[dev].load()) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) done[dev].store(true);
+    if (known) done[dev].store(true);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -768,7 +829,24 @@ cudaError_t launch_linear(const LinArgs& a, const CUtensorMap& xmap, const CUten
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<kBC, kSwap, kPair>, a, xmap, wmap, ymap);
+  a.cluster = 1;
+  if (kSwap && kBC <= 32 && known && a.dp_rounds == 0 && a.split > 1 && a.split <= kMaxCluster) {
+    int n = resident[dev][a.split].load();
+    if (n == 0) {
+      at.val.clusterDim.x = (unsigned)a.split;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+      }
+      resident[dev][a.split].store(++n);
+      at.val.clusterDim.x = 1;
+    }
+    if (a.cut_tiles <= n - 1) {
+      a.cluster = a.split;
+      at.val.clusterDim.x = (unsigned)a.split;
+    }
+  }
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const LinArgs>(a), xmap, wmap, ymap);
 }
 
 }  // namespace
