@@ -164,6 +164,52 @@ def test_add_rmsnorm_range(V):
     assert np.isnan(v[6]).all() and np.isnan(s[6]).all()
 
 
+E4M3 = ref.e4m3_value(np.arange(127))  # rising
+
+
+def nearest_codes(y, K):
+    """e4m3 magnitudes (codes without sign) of y * 448 / max of every group, one rounding, ties to even; and how far
+    each is from the border between two codes, relative to it."""
+    t = np.abs(y)
+    for b in range(0, K, 128):
+        t[:, b:b + 128] = t[:, b:b + 128] * 448.0 / t[:, b:b + 128].max(axis=1, keepdims=True)
+    hi = np.clip(np.searchsorted(E4M3, t), 1, 126)
+    border = (E4M3[hi - 1] + E4M3[hi]) / 2
+    up = np.where(t == border, hi % 2 == 0, t > border)
+    return (hi - 1 + up).astype(np.uint8), np.abs(t / border - 1), border
+
+
+@pytest.mark.parametrize("M,K", [(3, 1040), (700, 1408)])
+def test_quant_of_bf16_rounds_once(V, M, K):
+    """Products of eight bits hit e4m3's ties; the fp64 quotient is exact there."""
+    rng = np.random.default_rng(M)
+    x = bf16(rng, (M, K))
+    q = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    s = torch.empty((M, -(-K // 128)), dtype=torch.float32, device="cuda")
+    V.vp_quant_fp8(x, V.VP_BF16, K, M, K, q, s)
+    want, _, border = nearest_codes(f64(x), K)
+    got = q.cpu().numpy() & 127
+    normal = border > 2.0 ** -6  # below, a tie is met in no more than 24 bits of the product
+    assert np.array_equal(got[normal], want[normal])
+    assert np.abs(got.astype(int) - want).max() <= 1
+
+
+@pytest.mark.parametrize("M,K", [(4, 16384), (9, 2064), (700, 2064)])
+@pytest.mark.parametrize("weight", ["random", "ones", "tenths"])
+def test_add_rmsnorm_codes_round_once(V, M, K, weight):
+    """The codes are those of the fp64 quotient but for ties (within 2^-36 of a border, which a weight of 24 bits
+    times a value of 8 over another such product only meets by being one)."""
+    rng = np.random.default_rng(M + K)
+    x, r = bf16(rng, (M, K)), bf16(rng, (M, K))
+    w = f32({"random": rng.uniform(-2, 2, K), "ones": np.ones(K), "tenths": np.full(K, 0.1)}[weight])
+    _, q, _ = run_norm(V, x, r, w, 1e-6, K)
+    _, y = ref.add_rmsnorm(f64(x), bits16(r), f64(w), 1e-6)
+    want, off, border = nearest_codes(y, K)
+    sure = (off > 2.0 ** -36) & (border > 2.0 ** -6)
+    assert np.array_equal((q & 127)[sure], want[sure])
+    assert np.abs((q & 127).astype(int) - want).max() <= 1
+
+
 # ------------------------------------------------------------------ block-scaled linear
 def codes(rng, shape):
     """Random finite e4m3 bytes, small magnitudes as likely as large ones."""

@@ -2,11 +2,10 @@
 // (vp_quant_fp8), and the residual addition + RMSNorm with a quantised output (vp_add_rmsnorm_fp8).
 //
 // Mathematics: a group of 128 values shares s = max(max|x| / 448, 2^-126), so that |x / s| <= 448 up to
-// one rounding, and q = e4m3(x * (448 / max|x|)): two fp32 roundings before e4m3's own.  They move a value
-// across a border of e4m3 (steps of 2^-3 relative) for about 1 in 2^18 values of full precision, and decide
-// the exact ties of bf16 values (giving each quotient its remainder back, so that ties stay ties, cost 5 %
-// of the time and changed 1 code in 10^4).  e4m3's half step is 2^-4 of the value: the 8 bits the tensor
-// core multiplies.  NaN and infinities reach the scale.
+// one rounding, and q = e4m3(x * 448 / max|x|).  Of bf16 values, and after a norm, the codes are those of the
+// exact quotient (e4m3's half step, 2^-4 of the value, is the only rounding); of fp32 values three fp32 roundings
+// come before, which move about 1 value in 2^18 across a border between two codes.  Infinities and NaN reach
+// the scale of their group, and nothing else.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -48,54 +47,73 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// s = max(m / 448, 2^-126) and r = 448 / m (1 / s before its rounding; 2^126 at the floor).  The quotient s is m
-// times the constant's reciprocal with its remainder added back (exact in an fma, so the result is the
-// rounded quotient); r is the hardware's approximation of 1 / s with one Newton step towards 448 / m: about
-// 12 instructions in place of two divisions' 40, in a kernel that issues as much as it loads.
-__device__ __forceinline__ void scale_of(float m, float& s, float& r) {
-  constexpr float kInv = 1.0f / kE4m3Max, kTiny = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
-  const float q = m * kInv;
-  s = fmaf(fmaf(-q, kE4m3Max, m), kInv, q);
-  s = fmaxf(s, kTiny);
+constexpr float kScaleFloor = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
+// Of a group whose values are f times those at hand, with the maximum m at hand:
+// s = max(m f / 448, 2^-126), and the factor r = 448 / m of the values at hand (f 2^126 at the floor).  The
+// quotient is the dividend times the constant's reciprocal with its remainder added back (exact in an fma, so
+// the result is the rounded quotient); r is the hardware's approximation with one Newton step towards
+// 448 / m: about 12 instructions in place of two divisions' 40, in a kernel that issues as much as it loads.
+__device__ __forceinline__ void scale_of(float m, float f, float& s, float& r) {
+  constexpr float kInv = 1.0f / kE4m3Max, kTiny = kScaleFloor;
+  const float mf = m * f, q = mf * kInv;
+  s = fmaf(fmaf(-q, kE4m3Max, mf), kInv, q);
   float r0;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(s));
-  r = m > kTiny * kE4m3Max ? fmaf(fmaf(-r0, m, kE4m3Max) * kInv, r0, r0) : r0;
-  if (!(m <= 3.402823466e38f)) s = m, r = m == m ? 0.0f : m;  // an infinity: finite values over it are 0; NaN
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(fmaxf(m * kInv, kTiny)));
+  r = fmaf(fmaf(-r0, m, kE4m3Max) * kInv, r0, r0);
+  if (!(s > kTiny)) {  // NaN is put right below
+    s = kTiny;
+    r = f * 8.50705917e37f;  // 2^126
+  }
+  if (!(mf <= 3.402823466e38f)) s = mf, r = mf == mf ? 0.0f : mf;  // an infinity: finite values over it are 0; NaN
 }
 // This lane's eight codes of values times r.
 __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float r) {
   return make_uint2(e4m3x4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), e4m3x4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
 }
-// The half warp's 16 x 8 values are one group: its scale (returned to every lane) and this lane's codes.
-__device__ __forceinline__ float quant_group(const float (&v)[8], uint2& codes) {
+// The largest magnitude of the half warp's 16 x 8 values (one group).
+__device__ __forceinline__ float group_max(const float (&v)[8]) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);  // the other half warp may be past the row's end
   float m = fabsf(v[0]);
 #pragma unroll
   for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(v[e]));
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(half, m, o));
+  return m;
+}
+// The group's scale (returned to every lane) and this lane's codes.
+__device__ __forceinline__ float quant_group(const float (&v)[8], uint2& codes) {
   float s, r;
-  scale_of(m, s, r);
+  scale_of(group_max(v), 1.0f, s, r);
   codes = codes_of(v, r);
   return s;
 }
-// The same of eight bf16 values as loaded: the maximum is taken on the magnitudes' bits, two at a time (as
+// The same of eight bf16 values (times f) as loaded: the maximum is taken on the magnitudes' bits, two at a time (as
 // integers NaN is above infinity).
-__device__ __forceinline__ float quant_group(uint4 w, uint2& codes) {
+__device__ __forceinline__ float quant_group(uint4 w, float f, uint2& codes) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16), abs = 0x7FFF7FFFu;
   uint32_t m2 = max_u16x2(max_u16x2(w.x & abs, w.y & abs), max_u16x2(w.z & abs, w.w & abs));
 #pragma unroll
   for (int o = 8; o; o >>= 1) m2 = max_u16x2(m2, __shfl_xor_sync(half, m2, o));
   float s, r, v[8];
-  scale_of(__uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u)), s, r);
+  const float m = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
+  scale_of(m, f, s, r);
   unpack8(w, v);
-  codes = codes_of(v, r);
+  // Values of 8 bits hit e4m3's ties: x 448 / m is k 2^j with an odd k below 32, or 2^-13 and more away from it.
+  // So r a little larger (its error and the product's are below 2^-22) and the product cut to 16 bits give the
+  // tie itself, and leave every other value on its side: the codes are those of the exact quotient.
+  const uint32_t keep = s > kScaleFloor ? 0xFFFFFF00u : ~0u;  // at the floor r is f over a power of two
+  r = s > kScaleFloor ? r * (1.0f + 4.76837158e-7f) : r;      // 2^-21
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(__float_as_uint(v[e] * r) & keep);
+  codes = codes_of(v, 1.0f);
   return s;
 }
 
-// A half warp takes kU (row, group) pairs in a row, all loads first.  Bounded by the bytes (2 or 4 read and
-// about 1 written per value) once the instructions are few.  kFlat: whole groups in a dense matrix, so the
-// pairs are consecutive in memory and need no row arithmetic.
+// A half warp takes kU (row, group) pairs in a row, all loads first.  kFlat: whole groups in a dense matrix, so
+// the pairs are consecutive in memory and need no row arithmetic.  2051 rows of 17408 in bf16 (108 MB): 23 us
+// from memory (4.7 TB/s, of 6.8 that a copy reaches), 21 us when L2 holds a part.  One pair each: 29 us.  It
+// issues for much of the time: maximum, product, cut and conversion of every value are what is left.
+// 4 rows of 6144: 4.2 us, a launch.
 template <bool kF32, int kU, bool kFlat>
 __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, long long ld, int M, int K,
                                                     uint8_t* __restrict__ q, float* __restrict__ scales) {
@@ -141,7 +159,7 @@ __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, 
                           __uint_as_float(d.x), __uint_as_float(d.y), __uint_as_float(d.z), __uint_as_float(d.w)};
       s = quant_group(v, c);
     } else {
-      s = quant_group(w[i][0], c);
+      s = quant_group(w[i][0], 1.0f, c);
     }
     if (kFlat || at[i] != ~(size_t)0) *reinterpret_cast<uint2*>(q + at[i]) = c;
     if (lane == 0) scales[u0 + i] = s;
@@ -151,10 +169,47 @@ __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, 
 __device__ __noinline__ float scale64(float v, double s, float w) { return (float)((double)v * s * (double)w); }
 __device__ __noinline__ double square64(float v) { return (double)v * (double)v; }
 
+// The codes of a group of values h p w (eight per lane, weights at w; 0 past the row) in pairs of floats, for
+// the groups that fp32 does not decide: y = hi + lo and the maximum m + ml are exact, and t = hi 448 / m takes
+// back its remainder 448 y - t (m + ml) (both over 512, so that nothing overflows).  What is left of that after
+// its rounding makes t odd, so that e4m3's is the only rounding.
+__device__ __noinline__ uint2 codes_pair(uint4 a, float p, const float* w, bool valid) {
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  float hi[8], lo[8], ml = 0.0f;
+  unpack8(a, hi);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = hi[e] * p, g = valid ? __ldg(w + e) : 0.0f;
+    hi[e] = x * g;
+    lo[e] = fmaf(x, g, -hi[e]);
+  }
+  float m = group_max(hi);
+  const float r = kE4m3Max / m;
+  ml = -m;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (fabsf(hi[e]) == m) ml = fmaxf(ml, copysignf(1.0f, hi[e]) * lo[e]);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) ml = fmaxf(ml, __shfl_xor_sync(half, ml, o));
+  m *= 0.001953125f, ml *= 0.001953125f;  // 1 / 512
+  const float c = r * 1.142857143f;  // 512 / 448
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = hi[e] * r, x = hi[e] * 0.875f, y = t * m;
+    const float rest = (x - y) + (fmaf(hi[e], 0.875f, -x) - fmaf(t, m, -y) + fmaf(lo[e], 0.875f, -t * ml));
+    const float u = fmaf(rest, c, t), d = fmaf(rest, c, t - u);
+    const int up = d == 0.0f || (__float_as_int(u) & 1) ? 0 : (d > 0.0f) == (u > 0.0f) ? 1 : -1;
+    hi[e] = u == 0.0f ? u : __int_as_float(__float_as_int(u) + up);
+  }
+  return codes_of(hi, 1.0f);
+}
+
 // One CTA per row, kC chunks of 8 values per thread, held in registers as the bf16 pairs that the residual
 // stream is rounded to: one pass over the data, every load issued before the first use.  Many rows: four
 // chunks per thread, so that an SM holds several rows' CTAs and 100 KB and more of loads in flight while
-// others reduce; few rows: one chunk per thread, the shortest path through a row.
+// others reduce; few rows: one chunk per thread, the shortest path through a row.  4099 rows of 5120 in bf16
+// with a residual (148 MB): 33 us, 4.5 TB/s of 6.8 (codes left to fp32's three roundings: 31 us; one chunk per
+// thread: more than 40 us), 8 rows: 4.9 us, 1.4 more if one of them has an open group; 4.3 us is a launch.
 template <bool kF32, int kC>
 __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld, const uint16_t* residual,
                                                     const float* __restrict__ weight, int vec, float eps, int K,
@@ -215,15 +270,30 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
   const float* pw = weight + k0;
   if (ss >= 1e-30f && ss <= 3.0e38f) {
     const float inv = 1.0f / sqrtf(ss / (float)K + eps);
+    if (!weight) {  // the row's factor cancels from the codes and enters the scales only
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const int k = k0 + i * step;
+        if ((k & ~127) >= K) break;  // uniform over the half warp
+        uint2 c;
+        const float s = quant_group(a[i], inv, c);
+        if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
+        if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
+      }
+      return;
+    }
+    // inv = p f with p a power of two: the values are scaled by p (exactly); f cancels from the codes.
+    const float p = __uint_as_float(__float_as_uint(inv) & 0x7F800000u), f = inv / p;
+    unsigned open = 0;  // chunks of the thread that fp32 leaves open
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int k = k0 + i * step;
-      if ((k & ~127) >= K) break;  // uniform over the half warp
+      if ((k & ~127) >= K) break;
       float v[8];
       unpack8(a[i], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= inv;
-      if (weight && k < K) {
+      for (int e = 0; e < 8; ++e) v[e] *= p;
+      if (k < K) {
         if (vec) {
           const float4 c = __ldg(reinterpret_cast<const float4*>(pw + i * step)), d = __ldg(reinterpret_cast<const float4*>(pw + i * step) + 1);
           v[0] *= c.x, v[1] *= c.y, v[2] *= c.z, v[3] *= c.w, v[4] *= d.x, v[5] *= d.y, v[6] *= d.z, v[7] *= d.w;
@@ -232,10 +302,31 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
           for (int e = 0; e < 8; ++e) v[e] *= __ldg(pw + i * step + e);
         }
       }
-      uint2 c;
-      const float s = quant_group(v, c);
+      float s, r;
+      scale_of(group_max(v), f, s, r);
+      // Products within 5 steps of fp32 of a border of e4m3's (its normal ones, where the lower 20 bits begin):
+      // three fp32 roundings leave those open.
+      unsigned near = ~0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] *= r;
+        near = min(near, (__float_as_uint(v[e]) << 12) - (0x7FFFBu << 12));
+      }
+      const uint2 c = codes_of(v, 1.0f);
+      if (near <= 10u << 12 && s >= 2.4e-38f && s <= 3.0e38f) open |= 1u << i;
       if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
       if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
+    }
+    open = __reduce_or_sync(0xFFFFFFFFu, open);
+    if (open) {  // 1 group in 900, apart from the loop above, which keeps its registers that way
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        const int k = k0 + i * step;
+        if ((k & ~127) >= K) break;
+        if (!(open >> i & 1)) continue;
+        const uint2 c = codes_pair(a[i], p, pw + i * step, k < K);
+        if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
+      }
     }
     return;
   }
