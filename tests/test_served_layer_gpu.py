@@ -194,6 +194,26 @@ def test_quant_of_bf16_rounds_once(V, M, K):
     assert np.abs(got.astype(int) - want).max() <= 1
 
 
+@pytest.mark.parametrize("M", [5, 400])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_add_rmsnorm_weights_of_every_size(V, M, wide, in_place):
+    """Groups whose products, or whose scales, leave the range that fp32 keeps exactly; a group of zero weights."""
+    rng = np.random.default_rng(M + wide)
+    K = 128 * 40
+    x = f32(rng.standard_normal((M, K))) if wide else bf16(rng, (M, K))
+    r = bf16(rng, (M, K))
+    w = rng.uniform(0.5, 2, K).reshape(40, 128) * 10.0 ** np.linspace(-37, 37, 40)[:, None]
+    w[7] = 0.0
+    w = f32(w.reshape(-1))
+    want_h, y = ref.add_rmsnorm(f64(x), bits16(r), f64(w), 1e-6)
+    h, q, s = run_norm(V, x, r, w, 1e-6, K, h=r if in_place else None)
+    if in_place:
+        assert np.array_equal(bits16(h), want_h)
+    assert_codes(q, s, y, 40 * U, "weights of every size")
+    assert not (q[:, 7 * 128:8 * 128] & 127).any()
+
+
 @pytest.mark.parametrize("M,K", [(4, 16384), (9, 2064), (700, 2064)])
 @pytest.mark.parametrize("weight", ["random", "ones", "tenths"])
 def test_add_rmsnorm_codes_round_once(V, M, K, weight):

@@ -42,6 +42,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -73,9 +78,9 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[8], float r) {
 // The largest magnitude of the half warp's 16 x 8 values (one group).
 __device__ __forceinline__ float group_max(const float (&v)[8]) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);  // the other half warp may be past the row's end
-  float m = fabsf(v[0]);
+  float m = max_nan(fabsf(v[0]), fabsf(v[1]));
 #pragma unroll
-  for (int e = 1; e < 8; ++e) m = max_nan(m, fabsf(v[e]));
+  for (int e = 2; e < 8; e += 2) m = max_nan(m, fabsf(v[e]), fabsf(v[e + 1]));
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(half, m, o));
   return m;
@@ -166,25 +171,22 @@ __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, 
   }
 }
 
-__device__ __noinline__ float scale64(float v, double s, float w) { return (float)((double)v * s * (double)w); }
-__device__ __noinline__ double square64(float v) { return (double)v * (double)v; }
-
-// The codes of a group of values h p w (eight per lane, weights at w; 0 past the row) in pairs of floats, for
+// The codes of a group of values h w (eight per lane, weights at w; 0 past the row) in pairs of floats, for
 // the groups that fp32 does not decide: y = hi + lo and the maximum m + ml are exact, and t = hi 448 / m takes
 // back its remainder 448 y - t (m + ml) (both over 512, so that nothing overflows).  What is left of that after
 // its rounding makes t odd, so that e4m3's is the only rounding.
-__device__ __noinline__ uint2 codes_pair(uint4 a, float p, const float* w, bool valid) {
+__device__ __forceinline__ uint2 codes_pair(uint4 a, const float* w, bool valid) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
   float hi[8], lo[8], ml = 0.0f;
   unpack8(a, hi);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float x = hi[e] * p, g = valid ? __ldg(w + e) : 0.0f;
+    const float x = hi[e], g = valid ? __ldg(w + e) : 0.0f;
     hi[e] = x * g;
     lo[e] = fmaf(x, g, -hi[e]);
   }
   float m = group_max(hi);
-  const float r = kE4m3Max / m;
+  const float r = m > 0.0f ? kE4m3Max / m : 0.0f;  // the other half warp's group may be the open one, and this one zero
   ml = -m;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
@@ -204,12 +206,112 @@ __device__ __noinline__ uint2 codes_pair(uint4 a, float p, const float* w, bool 
   return codes_of(hi, 1.0f);
 }
 
+// h: the sum, rounded to fp32, then to the residual stream's bf16.
+__device__ __forceinline__ uint4 residual_sum(float (&v)[8], uint4 r) {
+  float t[8];
+  unpack8(r, t);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * e] + t[2 * e], v[2 * e + 1] + t[2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A chunk of the residual stream again, from memory: h where it was written, else the inputs (which then still
+// stand).  What follows is rare, and kept apart so that the ordinary path holds no registers for it.
+template <bool kF32>
+__device__ __forceinline__ uint4 reload(const void* x, long long at_x, const uint16_t* residual, const uint16_t* h, size_t at) {
+  if (h) return *reinterpret_cast<const uint4*>(h + at);
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + at_x * (kF32 ? 4 : 2));
+  const uint4 b = p[0];
+  float v[8];
+  if (kF32) {
+    const uint4 c = p[1];
+    const uint32_t u[8] = {b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[e]);
+  } else {
+    unpack8(b, v);
+  }
+  return residual_sum(v, residual ? *reinterpret_cast<const uint4*>(residual + at) : make_uint4(0, 0, 0, 0));
+}
+// The group of this lane's chunk `a` with every product in fp64; w: the chunk's weights, or NULL.
+__device__ __noinline__ void group64(uint4 a, const float* w, double inv, bool valid, uint8_t* q, float* scale) {
+  float v[8];
+  uint2 c;
+  unpack8(a, v);
+  const bool some = ((a.x | a.y | a.z | a.w) & 0x7FFF7FFFu) != 0;
+  if (__any_sync(0xFFFFu << (threadIdx.x & 16), some) || !(fabs(inv) <= 1e300)) {
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {  // rotating, so that the loop stays one
+      const float y = (float)((double)v[0] * inv * (double)(valid && w ? __ldg(w + e) : 1.0f));
+#pragma unroll
+      for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
+      v[7] = y;
+    }
+  } else if (valid && w) {  // zeros (a padding row's): theirs, or a NaN weight's
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= __ldg(w + e);
+  }
+  const float s = quant_group(v, c);
+  if (valid) *reinterpret_cast<uint2*>(q) = c;
+  if ((threadIdx.x & 15) == 0) *scale = s;
+}
+// The chunk at column k of row m again: its codes from pairs of floats; all of it in fp64 where the products
+// or the scale leave fp32's range (`far`).
+template <bool kF32>
+__device__ __noinline__ void redo_chunk(const void* x, long long ld, const uint16_t* residual, const float* weight, int m,
+                                        int k, int K, const uint16_t* h, float inv, bool far, uint8_t* q, float* scale) {
+  const bool valid = k < K;
+  const size_t at = (size_t)m * K + k;
+  const uint4 a = valid ? reload<kF32>(x, m * ld + k, residual, h, at) : make_uint4(0, 0, 0, 0);
+  if (far) {
+    group64(a, weight + k, inv, valid, q + at, scale);
+  } else {
+    const uint2 c = codes_pair(a, weight + k, valid);
+    if (valid) *reinterpret_cast<uint2*>(q + at) = c;
+  }
+}
+// A row whose squares leave fp32's range (or a zero or NaN row): all of it in fp64.
+template <bool kF32>
+__device__ __noinline__ void redo_row(const void* x, long long ld, const uint16_t* residual, const float* weight, int m,
+                                      int K, const uint16_t* h, float eps, uint8_t* q, float* scales, double* red) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int k = threadIdx.x * 8; k < K; k += blockDim.x * 8) {
+    float v[8];
+    const uint4 a = reload<kF32>(x, m * ld + k, residual, h, (size_t)m * K + k);
+    if (((a.x | a.y | a.z | a.w) & 0x7FFF7FFFu) == 0) continue;
+    unpack8(a, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)v[e] * (double)v[e];
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += red[w];
+  const double inv = 1.0 / sqrt(sum / (double)K + (double)eps);
+#pragma unroll 1
+  for (int k = threadIdx.x * 8; (k & ~127) < K; k += blockDim.x * 8) {
+    const bool valid = k < K;
+    const size_t at = (size_t)m * K + k;
+    group64(valid ? reload<kF32>(x, m * ld + k, residual, h, at) : make_uint4(0, 0, 0, 0), weight ? weight + k : nullptr,
+            inv, valid, q + at, scales + (size_t)m * qblocks(K) + k / kQBlock);
+  }
+}
+
 // One CTA per row, kC chunks of 8 values per thread, held in registers as the bf16 pairs that the residual
 // stream is rounded to: one pass over the data, every load issued before the first use.  Many rows: four
 // chunks per thread, so that an SM holds several rows' CTAs and 100 KB and more of loads in flight while
 // others reduce; few rows: one chunk per thread, the shortest path through a row.  4099 rows of 5120 in bf16
-// with a residual (148 MB): 33 us, 4.5 TB/s of 6.8 (codes left to fp32's three roundings: 31 us; one chunk per
-// thread: more than 40 us), 8 rows: 4.9 us, 1.4 more if one of them has an open group; 4.3 us is a launch.
+// with a residual (148 MB): 31 us from memory, 4.7 TB/s of the 6.8 that a copy reaches (5.2 in a row of calls; fp32
+// input 5.9; without weights 6.2): the bf16 form issues for most of the time.  With the rare paths inline, over
+// chunks held in registers, 33 us; two chunks per thread 33 us; a resident grid that copies a row ahead into shared
+// memory 37 us (fewer warps to hide a row's reductions).  8 rows: 4.9 us, 1.4 more if one of them has an open
+// group; 4.2 us is a launch.
 template <bool kF32, int kC>
 __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld, const uint16_t* residual,
                                                     const float* __restrict__ weight, int vec, float eps, int K,
@@ -282,17 +384,14 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
       }
       return;
     }
-    // inv = p f with p a power of two: the values are scaled by p (exactly); f cancels from the codes.
-    const float p = __uint_as_float(__float_as_uint(inv) & 0x7F800000u), f = inv / p;
-    unsigned open = 0;  // chunks of the thread that fp32 leaves open
+    // The values at hand are h w: inv cancels from the codes.
+    unsigned open = 0, far = 0;  // chunks of the thread that fp32 leaves open, or whose products leave its range
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       const int k = k0 + i * step;
       if ((k & ~127) >= K) break;
       float v[8];
       unpack8(a[i], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= p;
       if (k < K) {
         if (vec) {
           const float4 c = __ldg(reinterpret_cast<const float4*>(pw + i * step)), d = __ldg(reinterpret_cast<const float4*>(pw + i * step) + 1);
@@ -303,62 +402,32 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
         }
       }
       float s, r;
-      scale_of(group_max(v), f, s, r);
+      const float most = group_max(v);
+      scale_of(most, inv, s, r);
       // Products within 5 steps of fp32 of a border of e4m3's (its normal ones, where the lower 20 bits begin):
       // three fp32 roundings leave those open.
       unsigned near = ~0u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] *= r;
-        near = min(near, (__float_as_uint(v[e]) << 12) - (0x7FFFBu << 12));
+      for (int e = 0; e < 8; e += 2) {
+        v[e] *= r, v[e + 1] *= r;
+        near = __vimin3_u32(near, (__float_as_uint(v[e]) << 12) - (0x7FFFBu << 12), (__float_as_uint(v[e + 1]) << 12) - (0x7FFFBu << 12));
       }
       const uint2 c = codes_of(v, 1.0f);
-      if (near <= 10u << 12 && s >= 2.4e-38f && s <= 3.0e38f) open |= 1u << i;
+      if (near <= 10u << 12) open |= 1u << i;
+      if (most != 0.0f && !(most >= 1e-25f && most <= 1e30f && s > 2.0f * kScaleFloor)) far |= 1u << i;  // NaN too
       if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
       if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
     }
-    open = __reduce_or_sync(0xFFFFFFFFu, open);
-    if (open) {  // 1 group in 900, apart from the loop above, which keeps its registers that way
-#pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        const int k = k0 + i * step;
-        if ((k & ~127) >= K) break;
-        if (!(open >> i & 1)) continue;
-        const uint2 c = codes_pair(a[i], p, pw + i * step, k < K);
-        if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
-      }
+    open = __reduce_or_sync(0xFFFFFFFFu, open | far);
+#pragma unroll 1
+    for (int i = 0; open >> i; ++i) {  // 1 group in 900
+      const int k = k0 + i * step;
+      if (!(open >> i & 1) || (k & ~127) >= K) continue;
+      redo_chunk<kF32>(x, ld, residual, weight, m, k, K, h, inv, far >> i & 1, q, scales + (size_t)m * KB + k / kQBlock);
     }
     return;
   }
-  // Squares outside fp32 (or a zero or NaN row): fp64, in calls apart from the loop above, which would carry
-  // their slow products and registers otherwise.
-  double sd = 0.0;
-#pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    float v[8];
-    unpack8(a[i], v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sd += square64(v[e]);
-  }
-  for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xFFFFFFFFu, sd, o);
-  if ((tid & 31) == 0) redd[tid >> 5] = sd;
-  __syncthreads();
-  sd = 0.0;
-  for (int w = 0; w < warps; ++w) sd += redd[w];
-  const double invd = 1.0 / sqrt(sd / (double)K + (double)eps);
-#pragma unroll
-  for (int i = 0; i < kC; ++i) {
-    const int k = k0 + i * step;
-    if ((k & ~127) >= K) break;
-    float v[8];
-    unpack8(a[i], v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = scale64(v[e], invd, weight && k < K ? __ldg(pw + i * step + e) : 1.0f);
-    uint2 c;
-    const float s = quant_group(v, c);
-    if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
-    if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
-  }
+  redo_row<kF32>(x, ld, residual, weight, m, K, h, eps, q, scales, redd);
 }
 
 __global__ void pack_block_kernel(const uint8_t* __restrict__ w, int N, int K, uint8_t* __restrict__ out) {
