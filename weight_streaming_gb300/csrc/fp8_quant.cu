@@ -47,9 +47,9 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // of the magnitudes, NaN if either is; signs mean nothing
   uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 constexpr float kScaleFloor = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
@@ -92,15 +92,14 @@ __device__ __forceinline__ float quant_group(const float (&v)[8], uint2& codes) 
   codes = codes_of(v, r);
   return s;
 }
-// The same of eight bf16 values (times f) as loaded: the maximum is taken on the magnitudes' bits, two at a time (as
-// integers NaN is above infinity).
+// The same of eight bf16 values (times f) as loaded: the maximum is taken two at a time.
 __device__ __forceinline__ float quant_group(uint4 w, float f, uint2& codes) {
-  const uint32_t half = 0xFFFFu << (threadIdx.x & 16), abs = 0x7FFF7FFFu;
-  uint32_t m2 = max_u16x2(max_u16x2(w.x & abs, w.y & abs), max_u16x2(w.z & abs, w.w & abs));
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  uint32_t m2 = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
 #pragma unroll
-  for (int o = 8; o; o >>= 1) m2 = max_u16x2(m2, __shfl_xor_sync(half, m2, o));
+  for (int o = 8; o; o >>= 1) m2 = max_bf16x2(m2, __shfl_xor_sync(half, m2, o));
   float s, r, v[8];
-  const float m = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
+  const float m = max_nan(fabsf(__uint_as_float(m2 << 16)), fabsf(__uint_as_float(m2 & 0xFFFF0000u)));
   scale_of(m, f, s, r);
   unpack8(w, v);
   // Values of 8 bits hit e4m3's ties: x 448 / m is k 2^j with an odd k below 32, or 2^-13 and more away from it.
@@ -115,9 +114,10 @@ __device__ __forceinline__ float quant_group(uint4 w, float f, uint2& codes) {
 }
 
 // A half warp takes kU (row, group) pairs in a row, all loads first.  kFlat: whole groups in a dense matrix, so
-// the pairs are consecutive in memory and need no row arithmetic.  2051 rows of 17408 in bf16 (108 MB): 23 us
-// from memory (4.7 TB/s, of 6.8 that a copy reaches), 21 us when L2 holds a part.  One pair each: 29 us.  It
-// issues for much of the time: maximum, product, cut and conversion of every value are what is left.
+// the pairs are consecutive in memory and need no row arithmetic.  2051 rows of 17408 in bf16 (108 MB): 21 us
+// from memory (5.2 TB/s, of 6.8 that a copy reaches), 19 us when L2 holds a part (23 and 21 with the maximum taken
+// over the magnitudes' bits as integers).  The integer pipe bounds it: product, cut and conversion of every value
+// are what is left.  One pair each: 29 us before the last steps.
 // 4 rows of 6144: 4.2 us, a launch.
 template <bool kF32, int kU, bool kFlat>
 __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, long long ld, int M, int K,
@@ -310,7 +310,8 @@ __device__ __noinline__ void redo_row(const void* x, long long ld, const uint16_
 // with a residual (148 MB): 31 us from memory, 4.7 TB/s of the 6.8 that a copy reaches (5.2 in a row of calls; fp32
 // input 5.9; without weights 6.2): the bf16 form issues for most of the time.  With the rare paths inline, over
 // chunks held in registers, 33 us; two chunks per thread 33 us; a resident grid that copies a row ahead into shared
-// memory 37 us (fewer warps to hide a row's reductions).  8 rows: 4.9 us, 1.4 more if one of them has an open
+// memory 37 us (fewer warps to hide a row's reductions).  Weights that are all one leave most groups open: 46 us
+// (NULL does not).  8 rows: 4.9 us, 1.4 more if one of them has an open
 // group; 4.2 us is a launch.
 template <bool kF32, int kC>
 __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld, const uint16_t* residual,
