@@ -25,8 +25,8 @@
 //
 // What bounds it, N x K: 8 tokens, 5120 x 17408 (89.5 MB of weights) take 20.8 us, 4.3 TB/s: the stream at about
 // 6.5 TB/s and 7 us of launch, first copies, last block and join.  200 tokens, 16384 x 5120: 26 us, 64 pairs
-// with a tile each.  4096 tokens, 17408 x 5120: 262 to 292 us, 2.5 to 2.8 PFLOP/s (cuBLAS' bf16 1.9): 62 % of the
-// tensor cycles.  A K block of a pair's tile is 512 cycles of MMAs and about 330 of reading and scaling its
+// with a tile each.  4096 tokens, 17408 x 5120: 258 us, 2.8 PFLOP/s (cuBLAS' bf16 1.9), 292 us once at the power limit: 62 % of
+// the tensor cycles.  A K block of a pair's tile is 512 cycles of MMAs and about 330 of reading and scaling its
 // sums; two tensor-memory buffers (all there is at 128 x 256 sums) leave 760 cycles a block of that chain.
 //
 // Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, drains its copies and MMAs and frees
