@@ -194,6 +194,41 @@ def test_quant_of_bf16_rounds_once(V, M, K):
     assert np.abs(got.astype(int) - want).max() <= 1
 
 
+@pytest.mark.parametrize("M,K,pad", [(700, 16384, 0), (1300, 8208, 8)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_quant_of_many_groups(V, M, K, pad, wide):
+    """Enough groups for several per half warp: whole ones in a dense matrix, and ragged rows with a stride."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn((M, K + pad), generator=g, device="cuda").to(torch.float32 if wide else torch.bfloat16)
+    q = torch.full((M + 1, K), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((M * -(-K // 128) + 1,), -1.0, device="cuda")
+    V.vp_quant_fp8(x, V.VP_F32 if wide else V.VP_BF16, K + pad, M, K, q, s)
+    torch.cuda.synchronize()
+    assert (q[M] == 0x55).all() and s[-1] == -1.0
+    assert_codes(q[:M].cpu().numpy(), f64(s[:-1]).reshape(M, -1), f64(x[:, :K]), 0.0, "many groups")
+
+
+@pytest.mark.parametrize("M", [3, 400])
+def test_add_rmsnorm_weights_without_a_value(V, M):
+    """A NaN or an infinity among the weights reaches its group's scale in every row, and no other group."""
+    rng = np.random.default_rng(M)
+    K = 1280
+    x, w = bf16(rng, (M, K)), rng.uniform(0.5, 2, K)
+    x[1, 128 * 4 + 3] = 0.0
+    w[128 * 4 + 3], w[128 * 9 + 5] = np.inf, np.nan
+    _, q, s = run_norm(V, x, None, f32(w), 1e-6, K)
+    with np.errstate(invalid="ignore"):
+        _, y = ref.add_rmsnorm(f64(x), None, f64(f32(w)), 1e-6)
+    ok = [b for b in range(10) if b not in (4, 9)]
+    cols = np.concatenate([np.arange(b * 128, b * 128 + 128) for b in ok])
+    assert_codes(q[:, cols], s[:, ok], y[:, cols], 40 * U, "weights without a value")
+    v = ref.e4m3_value(q)
+    assert np.isnan(s[:, 9]).all() and np.isnan(v[:, 128 * 9:]).all()
+    inf = np.isinf(s[:, 4])
+    assert inf.sum() == M - 1 and np.isnan(s[1, 4])  # 0 * inf
+    assert np.isnan(v[inf, 128 * 4 + 3]).all() and not v[inf, 128 * 4 + 4:128 * 5].any()
+
+
 @pytest.mark.parametrize("M", [5, 400])
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("in_place", [False, True])
