@@ -21,7 +21,7 @@
 //    for the copies in flight); the last contributor joins them in order.
 // Measured, from memory: 131,071 positions of 4 x 256 heads (537 MB) in 92 us, 5.9 TB/s with start and join (7.1
 // TB/s while it streams; a copy reaches 6.8 of reads and writes); 61 sequences of 300 to 9,000 positions, 8 x 128
-// heads (1.18 GB) in 182 us, 6.5 TB/s; 4 sequences of up to 700 positions in 14.5 us: launch, lengths, first
+// heads (1.18 GB) in 182 us, 6.5 TB/s; 4 sequences of up to 700 positions in 14.3 us: launch, lengths, first
 // copies, join.
 // Waits are bounded: a warp whose wait ran out reports VP_ERR_TIMEOUT and goes on without waiting, so the
 // CTA ends.
@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kPaGrid = 152;                  // CTAs at most: one per SM
 constexpr int kPieceBytes = 8192;             // of keys, and of values
-constexpr int kMinPieces = 8;                 // pieces per CTA at least
+constexpr int kMinPieces = 5;                 // pieces per CTA at least: one per warp (8: 4 sequences of 700 12.9 us, 5: 12.3)
 constexpr int kJoinCost = 18;                 // joining parts of a (sequence, head) costs as much as these many pieces
 
 struct PagedArgs {
@@ -131,7 +131,7 @@ __device__ __forceinline__ void finish(const PagedArgs& a, size_t qrow, int r, i
   if (a.gate) {
     const float g[4] = {bfv(gate.x & 0xFFFF), bfv(gate.x >> 16), bfv(gate.y & 0xFFFF), bfv(gate.y >> 16)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] /= 1.0f + expf(-g[e]);
+    for (int e = 0; e < 4; ++e) v[e] = __fdividef(v[e], 1.0f + expf(-g[e]));  // 2 ulp; 0 where the sum is above 2^126
   }
   const __nv_bfloat162 p0 = __floats2bfloat162_rn(v[0], v[1]), p1 = __floats2bfloat162_rn(v[2], v[3]);
   *reinterpret_cast<uint2*>(a.out + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
         qf[ks][e] = r < a.G ? __ldg(reinterpret_cast<const uint32_t*>(a.q + qrow + (size_t)r * D + d)) : 0u;
       }
     }
+    if (a.gate)  // used at the segment's end: on its way meanwhile (16 positions of one sequence: 7.3 -> 6.8 us)
+      for (int i = tid; i < a.G * D / 64; i += kPaConsumers)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.gate + qrow + 64 * i));
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
