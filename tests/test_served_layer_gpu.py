@@ -209,6 +209,30 @@ def test_quant_of_many_groups(V, M, K, pad, wide):
 
 
 @pytest.mark.parametrize("M", [3, 400])
+@pytest.mark.parametrize("weight", [False, True])
+@pytest.mark.parametrize("wide", [False, True])
+def test_add_rmsnorm_small_rows_with_zero_and_tiny_groups(V, M, weight, wide):
+    """The row's factor is large; a group is zero, or its scale is at the floor."""
+    rng = np.random.default_rng(M)
+    K = 1280
+    x = rng.standard_normal((M, K)) * np.array([1e-3, 1e-9, 1e-13])[np.arange(M) % 3][:, None]
+    x[:, 256:384] = 0.0
+    x[:, 640:768] = rng.standard_normal((M, 128)) * 1e-39
+    x[:, 1024:1152] = rng.standard_normal((M, 128)) * 1e-38
+    x[:, 1152:] = rng.standard_normal((M, 128)) * 1e-20
+    x = f32(x) if wide else f32(x).to(torch.bfloat16)
+    w = rng.uniform(0.5, 2, K)
+    w[1152:] *= 1e-30  # products that fp32 loses before the row's factor
+    w = f32(w) if weight else None
+    _, q, s = run_norm(V, x, None, w, 1e-30, K)
+    _, y = ref.add_rmsnorm(f64(x), None, f64(w) if weight else None, 1e-30)
+    assert (s[:, 2] == 2.0 ** -126).all() and not (q[:, 256:384] & 127).any()
+    if not weight:  # 5 * 1e-39 * 1e3 / 448 < 2^-126; a weight of 2 may exceed it
+        assert (s[0::3, 5] == 2.0 ** -126).all()
+    assert_codes(q, s, y, 40 * U, "small rows")
+
+
+@pytest.mark.parametrize("M", [3, 400])
 def test_add_rmsnorm_weights_without_a_value(V, M):
     """A NaN or an infinity among the weights reaches its group's scale in every row, and no other group."""
     rng = np.random.default_rng(M)

@@ -67,7 +67,7 @@ __device__ __forceinline__ void scale_of(float m, float f, float& s, float& r) {
   r = fmaf(fmaf(-r0, m, kE4m3Max) * kInv, r0, r0);
   if (!(s > kTiny)) {  // NaN is put right below
     s = kTiny;
-    r = f * 8.50705917e37f;  // 2^126
+    r = fminf(f * 8.50705917e37f, 3e38f);  // 2^126; finite, for zeros under a large f
   }
   if (!(mf <= 3.402823466e38f)) s = mf, r = mf == mf ? 0.0f : mf;  // an infinity: finite values over it are 0; NaN
 }
@@ -92,14 +92,15 @@ __device__ __forceinline__ float quant_group(const float (&v)[8], uint2& codes) 
   codes = codes_of(v, r);
   return s;
 }
-// The same of eight bf16 values (times f) as loaded: the maximum is taken two at a time.
-__device__ __forceinline__ float quant_group(uint4 w, float f, uint2& codes) {
+// The same of eight bf16 values (times f; m: the largest before that) as loaded: the maximum is taken two at a time.
+// Where f is not 1, m lies well inside fp32's range and the scale above the floor, or the result is not used.
+__device__ __forceinline__ float quant_group(uint4 w, float f, uint2& codes, float& m) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
   uint32_t m2 = max_bf16x2(max_bf16x2(w.x, w.y), max_bf16x2(w.z, w.w));
 #pragma unroll
   for (int o = 8; o; o >>= 1) m2 = max_bf16x2(m2, __shfl_xor_sync(half, m2, o));
   float s, r, v[8];
-  const float m = max_nan(fabsf(__uint_as_float(m2 << 16)), fabsf(__uint_as_float(m2 & 0xFFFF0000u)));
+  m = max_nan(fabsf(__uint_as_float(m2 << 16)), fabsf(__uint_as_float(m2 & 0xFFFF0000u)));
   scale_of(m, f, s, r);
   unpack8(w, v);
   // Values of 8 bits hit e4m3's ties: x 448 / m is k 2^j with an odd k below 32, or 2^-13 and more away from it.
@@ -164,7 +165,8 @@ __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, 
                           __uint_as_float(d.x), __uint_as_float(d.y), __uint_as_float(d.z), __uint_as_float(d.w)};
       s = quant_group(v, c);
     } else {
-      s = quant_group(w[i][0], 1.0f, c);
+      float m;
+      s = quant_group(w[i][0], 1.0f, c, m);
     }
     if (kFlat || at[i] != ~(size_t)0) *reinterpret_cast<uint2*>(q + at[i]) = c;
     if (lane == 0) scales[u0 + i] = s;
@@ -268,8 +270,8 @@ __device__ __noinline__ void redo_chunk(const void* x, long long ld, const uint1
   const size_t at = (size_t)m * K + k;
   const uint4 a = valid ? reload<kF32>(x, m * ld + k, residual, h, at) : make_uint4(0, 0, 0, 0);
   if (far) {
-    group64(a, weight + k, inv, valid, q + at, scale);
-  } else {
+    group64(a, weight ? weight + k : nullptr, inv, valid, q + at, scale);
+  } else if (weight) {  // without weights: the other half warp's group is the one
     const uint2 c = codes_pair(a, weight + k, valid);
     if (valid) *reinterpret_cast<uint2*>(q + at) = c;
   }
@@ -307,8 +309,8 @@ __device__ __noinline__ void redo_row(const void* x, long long ld, const uint16_
 // stream is rounded to: one pass over the data, every load issued before the first use.  Many rows: four
 // chunks per thread, so that an SM holds several rows' CTAs and 100 KB and more of loads in flight while
 // others reduce; few rows: one chunk per thread, the shortest path through a row.  4099 rows of 5120 in bf16
-// with a residual (148 MB): 31 us from memory, 4.7 TB/s of the 6.8 that a copy reaches (5.2 in a row of calls; fp32
-// input 5.9; without weights 6.2): the bf16 form issues for most of the time.  With the rare paths inline, over
+// with a residual (148 MB): 31 us from memory, 4.7 TB/s of the 6.8 that a copy reaches (5.1 in a row of calls; fp32
+// input 5.8; without weights 6.0): the bf16 form issues for most of the time.  With the rare paths inline, over
 // chunks held in registers, 33 us; two chunks per thread 33 us; a resident grid that copies a row ahead into shared
 // memory 37 us (fewer warps to hide a row's reductions).  Weights that are all one leave most groups open: 46 us
 // (NULL does not).  8 rows: 4.9 us, 1.4 more if one of them has an open
@@ -373,51 +375,56 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
   const float* pw = weight + k0;
   if (ss >= 1e-30f && ss <= 3.0e38f) {
     const float inv = 1.0f / sqrtf(ss / (float)K + eps);
-    if (!weight) {  // the row's factor cancels from the codes and enters the scales only
+    // The values at hand are h w: the row's factor cancels from the codes and enters the scales only.
+    unsigned open = 0, far = 0;  // chunks of the thread that fp32 leaves open, or that leave its range
+    auto outside = [&](float most, float s) {  // NaN too; a group of zeros is done
+      return most != 0.0f && !(most >= 1e-25f && most <= 1e30f && s > 2.0f * kScaleFloor);
+    };
+    if (!weight) {
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
         const int k = k0 + i * step;
         if ((k & ~127) >= K) break;  // uniform over the half warp
         uint2 c;
-        const float s = quant_group(a[i], inv, c);
+        float most;
+        const float s = quant_group(a[i], inv, c, most);
+        if (outside(most, s)) far |= 1u << i;
         if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
         if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
       }
-      return;
-    }
-    // The values at hand are h w: inv cancels from the codes.
-    unsigned open = 0, far = 0;  // chunks of the thread that fp32 leaves open, or whose products leave its range
+    } else {
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      const int k = k0 + i * step;
-      if ((k & ~127) >= K) break;
-      float v[8];
-      unpack8(a[i], v);
-      if (k < K) {
-        if (vec) {
-          const float4 c = __ldg(reinterpret_cast<const float4*>(pw + i * step)), d = __ldg(reinterpret_cast<const float4*>(pw + i * step) + 1);
-          v[0] *= c.x, v[1] *= c.y, v[2] *= c.z, v[3] *= c.w, v[4] *= d.x, v[5] *= d.y, v[6] *= d.z, v[7] *= d.w;
-        } else {
+      for (int i = 0; i < kC; ++i) {
+        const int k = k0 + i * step;
+        if ((k & ~127) >= K) break;
+        float v[8];
+        unpack8(a[i], v);
+        if (k < K) {
+          if (vec) {
+            const float4 c = __ldg(reinterpret_cast<const float4*>(pw + i * step)), d = __ldg(reinterpret_cast<const float4*>(pw + i * step) + 1);
+            v[0] *= c.x, v[1] *= c.y, v[2] *= c.z, v[3] *= c.w, v[4] *= d.x, v[5] *= d.y, v[6] *= d.z, v[7] *= d.w;
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= __ldg(pw + i * step + e);
+            for (int e = 0; e < 8; ++e) v[e] *= __ldg(pw + i * step + e);
+          }
         }
-      }
-      float s, r;
-      const float most = group_max(v);
-      scale_of(most, inv, s, r);
-      // Products within 5 steps of fp32 of a border of e4m3's (its normal ones, where the lower 20 bits begin):
-      // three fp32 roundings leave those open.
-      unsigned near = ~0u;
+        float s, r;
+        const float most = group_max(v);
+        scale_of(most, inv, s, r);
+        // Products within 5 steps of fp32 of a border of e4m3's (its normal ones, where the lower 20 bits begin):
+        // three fp32 roundings leave those open.
+        unsigned near = ~0u;
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        v[e] *= r, v[e + 1] *= r;
-        near = __vimin3_u32(near, (__float_as_uint(v[e]) << 12) - (0x7FFFBu << 12), (__float_as_uint(v[e + 1]) << 12) - (0x7FFFBu << 12));
+        for (int e = 0; e < 8; e += 2) {
+          v[e] *= r, v[e + 1] *= r;
+          near = __vimin3_u32(near, (__float_as_uint(v[e]) << 12) - (0x7FFFBu << 12), (__float_as_uint(v[e + 1]) << 12) - (0x7FFFBu << 12));
+        }
+        const uint2 c = codes_of(v, 1.0f);
+        if (near <= 10u << 12) open |= 1u << i;
+        if (most == 0.0f || outside(most, s)) far |= 1u << i;  // zero, or lost
+        if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
+        if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
       }
-      const uint2 c = codes_of(v, 1.0f);
-      if (near <= 10u << 12) open |= 1u << i;
-      if (most != 0.0f && !(most >= 1e-25f && most <= 1e30f && s > 2.0f * kScaleFloor)) far |= 1u << i;  // NaN too
-      if (k < K) *reinterpret_cast<uint2*>(q + row + i * step) = c;
-      if ((tid & 15) == 0) scales[(size_t)m * KB + k / kQBlock] = s;
     }
     open = __reduce_or_sync(0xFFFFFFFFu, open | far);
 #pragma unroll 1
