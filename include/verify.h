@@ -651,7 +651,7 @@ vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld
  * word to VP_ERR_SHAPE; so does a page outside 0 .. n_pages - 1 among the sequence's pages, whose
  * positions are left out.  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect;
  * before it, an infinite value makes its column NaN.
- * Hq % Hkv == 0, Hq / Hkv <= 16, scale finite; 1 <= S <= 8192, S * Hkv <= 65536.  The cached positions
+ * Hq % Hkv == 0, Hq / Hkv <= 16, scale finite and below 2^127; 1 <= S <= 8192, S * Hkv <= 65536.  The cached positions
  * are cut into shares of about equal length, one per CTA, whatever the lengths (they are read on the
  * device only); partial results are joined in a fixed order: bit-identical from run to run.  P V runs
  * with the probabilities split in two bf16 parts (about 2^-17 relative).  One launch.  Workspace:

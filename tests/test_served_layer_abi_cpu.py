@@ -141,6 +141,7 @@ def test_paged_attention_sizes_and_refusals(V):
     for name in ("c", "q", "len", "out", "ws"):
         assert call(**{name: None}) == V.VP_ERR_INVALID_ARG, name
     assert call(scale=float("nan")) == V.VP_ERR_INVALID_ARG and call(scale=float("inf")) == V.VP_ERR_INVALID_ARG
+    assert call(scale=3e38) == V.VP_ERR_INVALID_ARG  # times log2 e
     for bad in BAD_CACHES:
         assert call(c=ctypes.byref(cache(V, **bad))) == V.VP_ERR_SHAPE, bad
     for kw in (dict(S=0), dict(S=8193), dict(Hq=25), dict(Hq=68), dict(Hq=2)):

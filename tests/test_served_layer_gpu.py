@@ -232,6 +232,24 @@ def test_add_rmsnorm_small_rows_with_zero_and_tiny_groups(V, M, weight, wide):
     assert_codes(q, s, y, 40 * U, "small rows")
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("size", [1.0, 1e-22])
+def test_add_rmsnorm_same_bits_with_and_without_h(V, wide, size):
+    """Rare groups (ties under equal weights) and rows (squares outside fp32) are formed again from h or from the inputs."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((330, 1040)) * size
+    x[:, ::7] = -0.0
+    x = f32(x) if wide else f32(x).to(torch.bfloat16)
+    w = torch.ones(1040, device="cuda")
+    h, q, s = run_norm(V, x, None, w, 1e-30, 1040)
+    _, q2, s2 = run_norm(V, x, None, w, 1e-30, 1040, h=None)
+    assert np.array_equal(q, q2) and np.array_equal(s, s2)
+    if not wide:
+        x2 = x.clone()
+        _, q3, s3 = run_norm(V, x2, None, w, 1e-30, 1040, h=x2)
+        assert torch.equal(x2, h) and np.array_equal(q, q3) and np.array_equal(s, s3)
+
+
 @pytest.mark.parametrize("M", [3, 400])
 def test_add_rmsnorm_weights_without_a_value(V, M):
     """A NaN or an infinity among the weights reaches its group's scale in every row, and no other group."""

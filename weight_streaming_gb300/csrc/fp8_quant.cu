@@ -237,7 +237,8 @@ __device__ __forceinline__ uint4 reload(const void* x, long long at_x, const uin
   } else {
     unpack8(b, v);
   }
-  return residual_sum(v, residual ? *reinterpret_cast<const uint4*>(residual + at) : make_uint4(0, 0, 0, 0));
+  constexpr uint32_t kNone = 0x80008000u;  // -0: adding it leaves a zero's sign, too
+  return residual_sum(v, residual ? *reinterpret_cast<const uint4*>(residual + at) : make_uint4(kNone, kNone, kNone, kNone));
 }
 // The group of this lane's chunk `a` with every product in fp64; w: the chunk's weights, or NULL.
 __device__ __noinline__ void group64(uint4 a, const float* w, double inv, bool valid, uint8_t* q, float* scale) {

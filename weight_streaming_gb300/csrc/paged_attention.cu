@@ -45,6 +45,7 @@ namespace vp {
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPaGrid = 152;                  // CTAs at most: one per SM
 constexpr int kPieceBytes = 8192;             // of keys, and of values
 constexpr int kMinPieces = 5;                 // pieces per CTA at least: one per warp (8: 4 sequences of 700 12.9 us, 5: 12.3)
@@ -767,7 +768,7 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
                              void* stream) {
   vp_status st = check_cache(cache);
   if (st != VP_OK) return st;
-  if (!q || !kv_len || !out || !ws || !std::isfinite(scale)) return VP_ERR_INVALID_ARG;
+  if (!q || !kv_len || !out || !ws || !std::isfinite(scale * kLog2e)) return VP_ERR_INVALID_ARG;
   const vp_paged_cache& c = *cache;
   if (!attend_shape_ok(S, Hq, c.Hkv, c.D)) return VP_ERR_SHAPE;
   if (!al(q, 16) || !al(kv_len, 4) || (gate && !al(gate, 16)) || !al(out, 16) || (lse && !al(lse, 4)) || !al(ws, 256))
@@ -791,7 +792,7 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
   const int rows = kPieceBytes / (2 * c.D);
   a.log_box = 4;
   while ((1 << a.log_box) < std::min(rows, c.page_size)) ++a.log_box;
-  a.scale2 = scale * 1.4426950408889634f;
+  a.scale2 = scale * kLog2e;
   a.counters = reinterpret_cast<unsigned*>(b + kServeCounters);
   a.part_o = reinterpret_cast<float*>(b + w.part_o);
   a.part_ml = reinterpret_cast<float*>(b + w.part_ml);
