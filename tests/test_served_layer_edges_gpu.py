@@ -1,0 +1,108 @@
+"""GPU tests of the served attention layer's operators at their edges.  Tolerances as in test_served_layer_gpu.py,
+unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import workspace
+from oracle import served_layer as ref
+from test_served_layer_gpu import U, Paged, assert_within, bf16, f32, f64, freqs, i32, linear
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def V():
+    from weight_streaming_gb300 import _lib
+    return _lib
+
+
+# ------------------------------------------------------------------ kernels of large calls
+def append_cases():  # (D, Hq, Hkv, norm)
+    for D in (64, 128, 256):
+        for per in range(1, 7):
+            for norm in (False, True):
+                yield D, 128 * 8 // D * per - 3, 1, norm
+    yield 256, 20, 4, True    # seven turns: two blocks a row
+    yield 128, 32, 8, True
+    yield 64, 96, 24, False
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,norm", list(append_cases()))
+def test_append_of_many_rows(V, D, Hq, Hkv, norm):
+    """Prompts: several heads per group of lanes (one to six), ragged sequences, padding rows at both ends."""
+    rng = np.random.default_rng(D + Hq)
+    P, inter = (16, True) if Hq % 2 else (64, False)
+    rot = D if norm else D // 2
+    at_once = 1024 // D
+    turns = -(-(Hq + 2 * Hkv) // at_once)
+    T = 16 * 160 // turns + 7  # 16 rows per SM and turn: past the rule for many
+    cut = np.sort(rng.integers(0, T + 1, 3))
+    rows = np.diff(np.concatenate([[0], cut, [T]]))
+    rows = np.concatenate([rows[:2], [0], rows[2:]])
+    S, ctx = len(rows), np.array([0, P - 1, 3, 2 * P, 5])
+    M = T + 3
+    max_pages = int(-(-(ctx + rows).max() // P)) + 1
+    p = Paged(V, D + Hq, S, max_pages, P, Hkv, D)
+    ld = (Hq + 2 * Hkv) * D + 8
+    x = bf16(rng, (M, ld))
+    q, k, v = x[:, :Hq * D], x[:, Hq * D:(Hq + Hkv) * D], x[:, (Hq + Hkv) * D:(Hq + 2 * Hkv) * D]
+    qn, kn = (f32(rng.uniform(0.5, 1.5, D)) for _ in range(2)) if norm else (None, None)
+    want_k, want_v = p.k.clone(), p.v.clone()
+    q_out = torch.full((M, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    kv_len, status = i32([-9] * S), i32([0])
+    start = 2 + np.concatenate([[0], np.cumsum(rows)])
+    V.vp_paged_append(p.desc(), q, ld, k, ld, v, ld, qn, kn, 1e-6, V.vp_rope(freqs(rot), inter), i32(start), i32(ctx), S, M, Hq,
+                      q_out, kv_len, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and kv_len.tolist() == (ctx + rows).tolist()
+    assert bool((q_out[:2] == 7.0).all()) and bool((q_out[2 + T:] == 7.0).all())
+    seq = np.repeat(np.arange(S), rows)
+    pos = np.concatenate([c + np.arange(n) for c, n in zip(ctx, rows)])
+    pg, sl = torch.from_numpy(p.table[seq, pos // P]).cuda().long(), torch.from_numpy(pos % P).cuda()
+    got_k = p.k[pg, :, sl]
+    for name, src, w, H, got in (("q", q, qn, Hq, q_out[2:2 + T]), ("k", k, kn, Hkv, got_k)):
+        xin = f64(src[2:2 + T]).reshape(T, H, D)
+        want, mag = ref.norm_rope(xin, f64(w) if norm else None, 1e-6, pos, freqs(rot), inter)
+        assert_within(f64(got), want, 2.0 ** -8 * np.abs(want) + 32 * U * mag, f"append {name}")
+        if not norm:
+            assert np.array_equal(f64(got)[..., rot:], xin[..., rot:])
+    want_k[pg, :, sl], want_v[pg, :, sl] = got_k, v[2:2 + T].reshape(T, Hkv, D)
+    assert torch.equal(p.k, want_k) and torch.equal(p.v, want_v)  # the rows' slots alone have changed
+
+
+def linear_plain(xq, xs, wq, ws):
+    """The definition in fp64 on the device, 4,096 weight rows at a time -> (y, sum |x w|)."""
+    K = xq.shape[1]
+    spread = lambda s: s.double().repeat_interleave(128, 1)[:, :K]  # noqa: E731
+    x = xq.view(torch.float8_e4m3fn).double() * spread(xs)
+    ys, mags = [], []
+    for n in range(0, wq.shape[0], 4096):
+        w = wq[n:n + 4096]
+        w = w.view(torch.float8_e4m3fn).double() * spread(ws[n // 128:(n + 4096) // 128].repeat_interleave(128, 0)[:len(w)])
+        ys.append(x @ w.t())
+        mags.append(x.abs() @ w.abs().t())
+    return torch.cat(ys, 1), torch.cat(mags, 1)
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 19600, 5136), (24, 19600, 5136), (60, 19600, 5136), (100, 19600, 5136),
+                                   (16, 39040, 2064), (32, 39040, 2064), (64, 39040, 2064), (128, 39040, 2064),
+                                   (1024, 5120, 5120), (1000, 5136, 5136), (300, 20496, 528)])
+def test_linear_block_of_more_tiles_than_ctas(V, M, N, K):
+    """Whole rounds of output tiles, then a remainder: cut along K (and joined) for the longer K."""
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    code = lambda *s: torch.randint(0, 255, s, generator=g, device="cuda").to(torch.uint8)  # noqa: E731
+    xq, wq = code(M, K), code(N, K)
+    for t in (xq, wq):
+        t[(t & 127) == 127] = 0x30
+    kb, nb = -(-K // 128), -(-N // 128)
+    xs = (0.5 + torch.rand((M, kb), generator=g, device="cuda")) * 1e-2
+    ws = (0.5 + torch.rand((nb, kb), generator=g, device="cuda")) * 1e-3
+    want, mag = linear_plain(xq, xs, wq, ws)
+    bound = 2 * (130 + kb) * U * mag + 1e-30
+    wsp = workspace(V.vp_linear_fp8_block_workspace_bytes(M, N, K))
+    y32 = linear(V, xq, xs, wq, ws, True, wsp=wsp)
+    assert bool(((y32.double() - want).abs() <= bound).all())
+    y16 = linear(V, xq, xs, wq, ws, False, wsp=wsp)
+    assert bool(((y16.double() - want).abs() <= bound + 2.0 ** -8 * want.abs()).all())
+    assert torch.equal(linear(V, xq, xs, wq, ws, True, wsp=wsp), y32)
