@@ -558,7 +558,8 @@ vp_status vp_decode_steps_rows(const vp_model* model, int steps, int rows, const
  * must not overlap inputs except where a call says so.  One workspace, zero-filled once, serves
  * vp_linear_fp8_block and vp_paged_attention calls of any shapes in turn on one stream (of the
  * largest of their sizes); a workspace that another section's call has used, or whose status word
- * reads VP_ERR_TIMEOUT, is zero-filled again first (vp_workspace_init). */
+ * reads VP_ERR_TIMEOUT, is zero-filled again first (vp_workspace_init).  VP_ERR_SHAPE, which the calls
+ * below report on the device, never takes the place of a VP_ERR_TIMEOUT. */
 
 /* Element type of an activation matrix. */
 enum { VP_BF16 = 0, VP_F32 = 1 };

@@ -6,7 +6,7 @@ import torch
 
 from helpers import workspace
 from oracle import served_layer as ref
-from test_served_layer_gpu import U, Paged, assert_within, bf16, f32, f64, freqs, i32, linear
+from test_served_layer_gpu import U, Paged, assert_within, attend, bf16, f32, f64, freqs, i32, linear
 
 pytestmark = pytest.mark.gpu
 
@@ -15,6 +15,31 @@ pytestmark = pytest.mark.gpu
 def V():
     from weight_streaming_gb300 import _lib
     return _lib
+
+
+# ------------------------------------------------------------------ status
+def preset(ws, value):
+    ws[:4].view(torch.int32).fill_(value)
+    return ws
+
+
+@pytest.mark.parametrize("before,after", [("VP_OK", "VP_ERR_SHAPE"), ("VP_ERR_TIMEOUT", "VP_ERR_TIMEOUT")])
+def test_a_bad_length_or_page_does_not_hide_a_timeout(V, before, after):
+    """A timed-out call leaves counters behind, so its report must stand until the workspace is zero-filled."""
+    rng = np.random.default_rng(1)
+    P, D = 32, 128
+    p = Paged(V, 2, 3, 4, P, 2, D)
+    q = bf16(rng, (3, 4, D), 1.5)
+    n = V.vp_paged_attention_workspace_bytes(3, 4, 2, D)
+    attend(V, p, q, [100, -1, 20], D ** -0.5, ws=preset(workspace(n), getattr(V, before)), expect=getattr(V, after))
+    p.pages[2, 0] = p.n
+    attend(V, p, q, [100, 0, 20], D ** -0.5, ws=preset(workspace(n), getattr(V, before)), expect=getattr(V, after))
+    status = i32([getattr(V, before)])
+    k, v = bf16(rng, (3, 2, D)), bf16(rng, (3, 2, D))
+    for start in (None, i32([0, 1, 2, 9])):
+        V.vp_paged_append(p.desc(), None, 0, k, 2 * D, v, 2 * D, None, None, 0.0, None, start, i32([1, 1, -1]), 3, 3, 0, None,
+                          None, status)
+        assert int(status) == getattr(V, after)
 
 
 # ------------------------------------------------------------------ kernels of large calls

@@ -22,6 +22,7 @@
 
 #include "errors.h"
 #include "paged.h"
+#include "ptx.cuh"
 #include "verify.h"
 
 namespace vp {
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     }
   }
   if (a.row_start && r == 0 && blockIdx.y == 0 && tid == 0 && a.status && (a.row_start[0] < 0 || a.row_start[a.S] > a.M))
-    atomicExch(a.status, (int)VP_ERR_SHAPE);  // rows that this call does not have
+    report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);  // rows that this call does not have
   int s = r;
   if (a.row_start) {
     if (a.S <= 2 * kThreadsP) {  // the number of sequences that start at or before the row: two loads for all
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s_sin[j], &s_cos[j]);
   }
   const bool ok = page >= 0 && page < a.n_pages;
-  if (!ok && tid == 0 && blockIdx.y == 0 && a.status) atomicExch(a.status, (int)VP_ERR_SHAPE);
+  if (!ok && tid == 0 && blockIdx.y == 0 && a.status) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
   __syncthreads();
   float4 cs = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sn = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (turns) {  // of pairs 4 lane .. 4 lane + 3, the same for every head

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   // Sequences without positions: zeros, and the status of those out of range.
   for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
     if (seq_len(a, s) > 0) continue;
-    if (tid == 0 && __ldg(a.kv_len + s) != 0) atomicExch(a.status, (int)VP_ERR_SHAPE);
+    if (tid == 0 && __ldg(a.kv_len + s) != 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
     uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s * a.Hq * D);
     for (int i = tid; i < a.Hq * D / 8; i += kPaThreads) o[i] = make_uint4(0, 0, 0, 0);
     if (a.lse)
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
             bad |= 1 << j;
           }
         }
-        if (bad) atomicExch(a.status, (int)VP_ERR_SHAPE);
+        if (bad) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
         const int cnt = min(32, g.p1 - base);
         for (int i = 0; i < cnt; ++i, ++n) {
           int row[kMaxBoxes];

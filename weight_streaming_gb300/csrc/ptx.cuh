@@ -105,6 +105,17 @@ __device__ __forceinline__ void st_release_gpu(unsigned* p, unsigned v) {
   asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// Reports an argument error `code` in a status word, but never in the place of a timeout (`timeout`): a call that
+// timed out leaves counters behind, and its report is what tells the caller to zero-fill the workspace.
+__device__ __forceinline__ void report_unless(int* status, int code, int timeout) {
+  int seen = *(volatile int*)status;
+  while (seen != timeout && seen != code) {
+    const int was = atomicCAS(status, seen, code);
+    if (was == seen) return;
+    seen = was;
+  }
+}
+
 // ---------------------------------------------------------------- tensor memory
 // Tensor memory: allocation by one whole warp (cols a power of two, 32..512; the address lands in
 // shared memory), the fences around a thread synchronisation, and 32-bit columns of the warp's own
