@@ -100,6 +100,15 @@ def test_attention_out_of_range_context_is_reported(V):
     assert_close(out[8:], ref, a, "good lane")
 
 
+def test_attention_out_of_range_context_does_not_hide_a_timeout(V):
+    """A workspace that an earlier call's timeout has marked keeps the mark until it is zero-filled."""
+    c = case(6, 2, 6, 1, 100, [95, 10])
+    ws = workspace(V.vp_workspace_bytes(V.VP_OP_ATTN, 16, 1, 100))
+    ws[:4].view(torch.int32).fill_(V.VP_ERR_TIMEOUT)
+    out, _, _, st = run(V, c, ws)
+    assert st == V.VP_ERR_TIMEOUT and np.all(out[:8] == 0)
+
+
 def test_attention_values_over_bf16_range(V):
     """The cache is BF16: values far outside half precision's range (up to ~1e30 here, half's
     largest finite is 65504) and tiny ones (~1e-30, below half's smallest subnormal) must pass

@@ -33,6 +33,7 @@
 
 #include "attention.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace vp {
 
@@ -88,7 +89,7 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-constexpr int kStatusShape = 2;  // VP_ERR_SHAPE
+constexpr int kStatusShape = 2, kStatusTimeout = 6;  // VP_ERR_SHAPE, VP_ERR_TIMEOUT
 
 // A lane's cached length is usable when its 8 new positions fit the cache.
 __device__ __forceinline__ bool ctx_ok(int c, int cap) { return c >= 0 && c <= cap - 8; }
@@ -98,7 +99,7 @@ __global__ void attn_append(const uint16_t* __restrict__ k_new, const uint16_t* 
                             const int32_t* __restrict__ ctx, int Hkv, int cap, int* status) {
   const int r = blockIdx.x, g = blockIdx.y, l = r / 8, j = r % 8, t = threadIdx.x;  // 32 threads x 16 B
   if (!ctx_ok(ctx[l], cap)) {
-    if (t == 0) atomicExch(status, kStatusShape);
+    if (t == 0) report_unless(status, kStatusShape, kStatusTimeout);
     return;
   }
   const size_t src = ((size_t)r * Hkv + g) * kD + 8 * t;
