@@ -650,7 +650,8 @@ vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld
  * q, gate, out: bf16 [S][Hq][D]; kv_len: device int32 [S].  A sequence with kv_len 0 gives zeros and
  * lse -inf.  kv_len[s] < 0 or above max_pages * page_size does the same and sets the workspace's status
  * word to VP_ERR_SHAPE; so does a page outside 0 .. n_pages - 1 among the sequence's pages, whose
- * positions are left out.  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect;
+ * positions are left out.  VP_ERR_TIMEOUT there: a bounded wait gave up (out and lse are then not
+ * valid).  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect;
  * before it, an infinite value makes its column NaN.
  * Hq % Hkv == 0, Hq / Hkv <= 16, scale finite and below 2^127; 1 <= S <= 8192, S * Hkv <= 65536.  The cached positions
  * are cut into shares of about equal length, one per CTA, whatever the lengths (they are read on the

@@ -24,7 +24,8 @@
 // heads (1.18 GB) in 182 us, 6.5 TB/s; 4 sequences of up to 700 positions in 14.3 us: launch, lengths, first
 // copies, join.
 // Waits are bounded: a warp whose wait ran out reports VP_ERR_TIMEOUT and goes on without waiting, so the
-// CTA ends.
+// CTA ends; the warps that issue copies see them land first, whatever ran out, and no join copies start
+// once something has.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -211,6 +212,13 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
   float* join = reinterpret_cast<float*>(dyn + (ring - smem_addr(dyn)) + C::kStages * 2 * kPieceBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#ifdef VP_WAIT_TEST
+  // Wait-test hook (workspace word kWsTestSkip), for the first CTA: 1 leaves out the arrival that frees its first
+  // stage, 2 the copies of its first piece; 3, for every CTA that joins parts: a copy of theirs.
+  const int hook = ((const volatile int*)a.status)[kWsTestSkip / sizeof(int)];
+#else
+  constexpr int hook = 0;
+#endif
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -390,7 +398,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
             mbar_arrive_expect_tx(&full[st], gd * 2 * box_bytes);
 #pragma unroll
             for (int j = 0; j < kMaxBoxes; ++j) {
-              if (row[j] < 0) continue;
+              if (row[j] < 0 || (hook == 2 && blockIdx.x == 0 && n == 0)) continue;
               tma_load_3d(dst + j * box_bytes, &kmap, 0, row[j], 0, bar, pol);
               tma_load_3d(dst + kPieceBytes + j * box_bytes, &vmap, 0, row[j], 0, bar, pol);
             }
@@ -400,8 +408,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
         }
       }
     }
-    if (!ok)  // the copies in flight land before the shared memory goes
-      for (int i = 0; i < min(n, C::kStages); ++i) mbar_wait_bounded(&full[i], ((n - 1 - i) / C::kStages) & 1);
+    // Every copy lands before this warp leaves, and with it the shared memory: a consumer whose wait ran out may
+    // have left without them, after this warp's last wait.
+    for (int i = 0; i < min(n, C::kStages); ++i) mbar_wait_bounded(&full[i], ((n - 1 - i) / C::kStages) & 1);
     return;
   }
 
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       }
       if (masked) fence_proxy_async_smem();  // the zeros, before the stage's next copy
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[at]);
+      if (lane == 0 && !(hook == 1 && c == 0 && at == 0 && par == 0)) mbar_arrive(&empty[at]);
     }
     // ---- the warps' results of this (sequence, head)
 #pragma unroll
@@ -640,18 +649,27 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     const int first = pend_first[e], cnt = pend_last[e] - first + 1;
     const size_t qrow = ((size_t)pend_s[e] * a.Hq + (size_t)pend_h[e] * a.G) * D;
     // part x lies in its CTA's end slot when it is the first, else in the start slot
-    auto fetch = [&](int x0, int n, bool with_ml) {  // the first warp: parts x0 .. x0 + n - 1, and every part's maxima
+    // The first warp: parts x0 .. x0 + n - 1, and every part's maxima.  False, and nothing copied, once a wait of
+    // the CTA has run out: its ring may not be free, nor the barrier's last phase complete.
+    auto fetch = [&](int x0, int n, bool with_ml) -> bool {
+      if (__any_sync(0xFFFFFFFFu, *(volatile int*)&s_abort)) return false;
       const uint32_t bar = smem_addr(&s_join), ml_bytes = (2 * cnt - 1) * 128;
       asm volatile("fence.proxy.async;" ::: "memory");  // the other CTAs' stores, before these copies read them
       if (lane == 0) {
         mbar_arrive_expect_tx(&s_join, n * part_bytes + (with_ml ? ml_bytes : 0));
-        if (with_ml) bulk_load(ring + kRing, a.part_ml + ((size_t)first * 2 + 1) * 32, ml_bytes, bar);
+        if (with_ml && hook != 3) bulk_load(ring + kRing, a.part_ml + ((size_t)first * 2 + 1) * 32, ml_bytes, bar);
       }
       __syncwarp();
       for (int x = x0 + lane; x < x0 + n; x += 32)
         bulk_load(ring + (x - x0) * part_bytes, a.part_o + ((size_t)(first + x) * 2 + (x == 0)) * (16 * D), part_bytes, bar);
+      return true;
     };
-    if (warp == 0) fetch(0, min(room, cnt), true);
+    // The warp that copied does not leave before its copies have landed, even if the wait is called off.
+    auto landed = [&](bool copied) {
+      if (!wait(&s_join, jpar) && copied) mbar_wait_bounded(&s_join, jpar);
+      jpar ^= 1;
+    };
+    bool copied = warp == 0 && fetch(0, min(room, cnt), true);
     // the gate, while the parts are on their way
     uint2 gate[kItems];
 #pragma unroll
@@ -661,8 +679,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       if (a.gate && i < a.G * (D / 4))
         gate[k] = __ldg(reinterpret_cast<const uint2*>(a.gate + qrow + (size_t)(i / (D / 4)) * D + 4 * (i % (D / 4))));
     }
-    wait(&s_join, jpar);
-    jpar ^= 1;
+    landed(copied);
     // part 0's maxima and sums lie first, part x's at index 2 x - 1 (the slots in between are other tiles')
     for (int i = tid; i < a.G * cnt; i += kPaConsumers) {
       const int r = i / cnt, x = i - r * cnt;
@@ -682,9 +699,8 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
       const int n = min(room, cnt - x0);
       if (x0) {
         named_sync<kPaConsumers>();  // the ring is read
-        if (warp == 0) fetch(x0, n, false);
-        wait(&s_join, jpar);
-        jpar ^= 1;
+        copied = warp == 0 && fetch(x0, n, false);
+        landed(copied);
       }
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
