@@ -35,6 +35,32 @@ def attention(S, Hq, Hkv, D, P, n):
     return run, ws
 
 
+def linear(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    kb, nb = -(-K // 128), -(-N // 128)
+    xq, wq = (torch.randint(0, 120, s, generator=g, device="cuda").to(torch.uint8) for s in ((M, K), (N, K)))
+    xs, wsc = torch.rand((M, kb), generator=g, device="cuda"), torch.rand((nb, kb), generator=g, device="cuda")
+    packed = torch.empty(V.vp_packed_bytes_fp8_block(N, K), dtype=torch.uint8, device="cuda")
+    V.vp_pack_fp8_block(wq, N, K, packed)
+    y = torch.zeros((M, N), device="cuda")
+    ws = workspace(V.vp_linear_fp8_block_workspace_bytes(M, N, K))
+
+    def run():
+        V.vp_linear_fp8_block(packed, wsc, xq, xs, y, V.VP_F32, M, N, K, ws)
+        torch.cuda.synchronize()
+        return (y.clone(),)
+    return run, ws
+
+
+LINEAR = {
+    "parts in a cluster": (8, 5120, 17408),
+    "parts in a cluster, 32 columns": (24, 5120, 17408),
+    "parts in the workspace": (60, 5120, 17408),
+    "tokens on the lanes": (100, 5120, 17408),
+    "more tiles than CTAs": (8, 19600, 5136),
+    "pairs": (200, 16384, 5120),
+    "pairs, whole rounds and parts": (1024, 5120, 5120),
+}
 ATTENTION = {
     "one long sequence": (1, 6, 1, 256, 64, 16 * 152 * 20),
     "a group of 16": (1, 16, 1, 128, 16, 32 * 152 * 18),
@@ -47,6 +73,8 @@ def main():
     assert "waittest" in V.LIB_PATH, V.LIB_PATH
     cases = [(f"attention, {name}, hook {h}", attention, shape, h) for name, shape in ATTENTION.items()
              for h in ((1, 2) if name == "whole sequences" else (1, 2, 3))]
+    cases += [(f"linear, {name}, hook {h}", linear, shape, h) for name, shape in LINEAR.items()
+              for h in ((1, 2, 3, 4, 5) if "pairs" in name else (1, 2, 3, 4))]
     for what, make, shape, hook in cases:
         run, ws = make(*shape)
         want = run()

@@ -29,8 +29,8 @@
 // the tensor cycles.  A K block of a pair's tile is 512 cycles of MMAs and about 330 of reading and scaling its
 // sums; two tensor-memory buffers (all there is at 128 x 256 sums) leave 760 cycles a block of that chain.
 //
-// Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, drains its copies and MMAs and frees
-// its tensor memory.
+// Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, waits (again with a limit) for its copies and
+// MMAs and frees its tensor memory.  Timed out or not, the copying warp leaves last: see its end.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -154,15 +154,15 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-// Arrives on `bar` (in both CTAs of a pair, at the same offset) when every MMA issued so far by this thread
-// has completed.
+// Arrives on `bar` (in both CTAs of a pair, at the same offset; or in those of `mask`) when every MMA issued so
+// far by this thread has completed.
 template <bool kPair>
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint16_t mask = 3) {
   if constexpr (kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
@@ -342,6 +342,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t ring = (smem_addr(dyn) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kPair ? (int)cluster_rank() : 0;
+#ifdef VP_WAIT_TEST
+  // Wait-test hook (workspace word kWsTestSkip): the first CTA (5: the second) leaves out, of its first block,
+  // 1 the commit to the epilogue, 2 the commit that frees the stage, 3 an arrival that frees the tensor-memory
+  // buffer, 4 and 5 the copies.
+  const int hook = ((const volatile int*)a.status)[kWsTestSkip / sizeof(int)];
+  const bool hooked = blockIdx.x == (hook == 5 ? 1 : 0);
+#else
+  constexpr int hook = 0;
+  constexpr bool hooked = false;
+#endif
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -406,7 +416,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
 #pragma unroll
             for (int g = 0; g < C::kG; ++g) {
-              if (g >= cnt) break;
+              if (g >= cnt || (hooked && hook >= 4 && n == 0)) break;
               const int kb = kb0 + g;
               const uint32_t st = ring + s * C::kStage + g * C::kBlock;
               // lanes' operand first (16 KB), columns' operand behind it
@@ -427,16 +437,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (++s == C::kStages) s = 0, par ^= 1;
         }
       }
-      if (!ok && rank == 0)  // the copies in flight land before the shared memory goes
-        for (int s = 0; s < min(n, C::kStages); ++s) {
-          const int last = (n - 1 - s) / C::kStages;
-          mbar_wait_bounded(&full[s], last & 1);
+      // Nothing may be on its way to this CTA's shared memory, or from here to the pair's other CTA, when the CTA
+      // ends: each stage's last commit says that its copies have landed and been read, and it is itself the last
+      // arrival from the pair's first CTA.  Where the MMAs have stopped the wait takes its whole limit, a
+      // second, in which whatever was on its way arrives (the other CTA waits for this one at the end).
+      for (int i = 0; i < min(n, C::kStages); ++i)
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[i], ((n - 1 - i) / C::kStages) & 1))) {
+          *(volatile int*)&s_abort = 1;
+          atomicExch(a.status, (int)VP_ERR_TIMEOUT);
+          break;
         }
     }
     if (warp == 1 && rank == 0) {
       int s = 0, b = 0;
       uint32_t par = 0, tpar = 1;
-      bool ok = true;
+      bool ok = true, first = true;  // first: only the wait-test build asks
       while (ok && sched.next(a, it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
@@ -458,16 +473,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 mma_f8<kPair>(tmem + (b * C::kG + g) * kBC, da + g * (C::kBlock >> 4) + 2 * k,
                               db + g * (C::kBlock >> 4) + 2 * k, idesc, k > 0);
             }
-            mma_commit<kPair>(&tfull[b]);
-            mma_commit<kPair>(&empty[s]);
+            if (!(hooked && hook == 1 && first)) mma_commit<kPair>(&tfull[b]);
+            if (!(hooked && hook == 2 && first)) mma_commit<kPair>(&empty[s]);
           }
+          first = false;
           __syncwarp();
           if (++s == C::kStages) s = 0, par ^= 1;
           if (++b == C::kBufs) b = 0, tpar ^= 1;
         }
       }
       if (!ok) {
-        if (elect_one()) mma_commit<kPair>(&drain);
+        if (elect_one()) mma_commit<kPair>(&drain, 1);  // here alone
         __syncwarp();
         mbar_wait_bounded(&drain, 0);
       }
@@ -637,7 +653,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               for (int g = 0; g < C::kG; ++g) tmem_wait<kW>(r[g]);
               tmem_fence_before();
               __syncwarp();
-              if (elect_one()) mbar_arrive(tempty0 + 8 * b);
+              if (elect_one() && !(hooked && hook == 3 && warp == 4 && b == 0 && par == 0)) mbar_arrive(tempty0 + 8 * b);
 #pragma unroll
               for (int g = 0; g < C::kG; ++g) {
                 if (kb + g >= it.kb1) break;
@@ -676,7 +692,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           } else {  // the buffer is read: the next MMAs may have it
             tmem_fence_before();
             __syncwarp();
-            if (elect_one()) {
+            if (elect_one() && !(hooked && hook == 3 && warp == 4 && b == 0 && par == 0)) {
               if (kPair)
                 mbar_arrive_cluster(tempty0 + 8 * b);
               else
