@@ -6,7 +6,8 @@ import torch
 
 from helpers import workspace
 from oracle import served_layer as ref
-from test_served_layer_gpu import U, Paged, assert_within, attend, bf16, f32, f64, freqs, i32, linear
+from test_served_layer_gpu import (U, Paged, assert_within, attend, bf16, f32, f64, freqs, i32, linear, nearest_codes,
+                                   run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +41,52 @@ def test_a_bad_length_or_page_does_not_hide_a_timeout(V, before, after):
         V.vp_paged_append(p.desc(), None, 0, k, 2 * D, v, 2 * D, None, None, 0.0, None, start, i32([1, 1, -1]), 3, 3, 0, None,
                           None, status)
         assert int(status) == getattr(V, after)
+
+
+# ------------------------------------------------------------------ codes after the norm
+def exact_codes(h, w, K):
+    """Codes (without sign) of the exact quotients h w 448 / max of every group: the row's factor cancels; h w has 32
+    bits and 448 h w 35, so that the fp64 division rounds once and meets every tie."""
+    return nearest_codes(f64(h) * (1.0 if w is None else f64(w)), K)[0]
+
+
+WEIGHTS = {"none": lambda rng, K: None, "ones": lambda rng, K: np.ones(K), "tenths": lambda rng, K: np.full(K, 0.1),
+           "bf16": lambda rng, K: bf16(rng, K, 0.1).double().cpu().numpy() + 1.0, "random": lambda rng, K: rng.uniform(-2, 2, K)}
+
+
+def weights(rng, K, kind):
+    w = WEIGHTS[kind](rng, K)
+    if w is None:
+        return None
+    return f32(w) if kind != "bf16" else torch.from_numpy(w).to(torch.bfloat16).float().cuda()
+
+
+@pytest.mark.parametrize("M", [5, 700])
+@pytest.mark.parametrize("kind", ["none", "ones", "tenths", "bf16", "random"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_add_rmsnorm_codes_are_the_exact_quotients(V, M, kind, wide):
+    """Every code, ties and the codes below e4m3's smallest normal value among them."""
+    rng = np.random.default_rng(M)
+    K = 2064
+    x = rng.standard_normal((M, K)) * 2.0 ** -(rng.integers(0, 3, (M, K)) * rng.integers(0, 9, (M, K)))
+    x = f32(x) if wide else f32(x).to(torch.bfloat16)
+    w = weights(rng, K, kind)
+    h, q, _ = run_norm(V, x, None, w, 1e-6, K)
+    assert np.array_equal(q & 127, exact_codes(h, w, K))
+
+
+@pytest.mark.parametrize("kind", ["none", "ones", "tenths"])
+@pytest.mark.parametrize("rows", [1, 320])
+def test_add_rmsnorm_codes_of_every_pair_of_eight_bits(V, kind, rows):
+    """Group a: the largest value a, and 127 others over every power of two down to the smallest codes."""
+    K = 128 * 128
+    a, b, e = np.arange(128, 256)[:, None], np.arange(128, 255)[None, :], np.arange(0, 22)[:, None, None]
+    x = np.concatenate([np.broadcast_to(a * 1.0, (22, 128, 1)), b * 2.0 ** -(e + 1) * (1 - 2 * (b % 2)) * np.ones((1, 128, 1))], axis=2)
+    x = x.reshape(22, K)
+    x = torch.from_numpy(np.tile(x, (max(1, rows // 22), 1))).to(torch.bfloat16).cuda()
+    w = weights(None, K, kind)
+    h, q, _ = run_norm(V, x, None, w, 1e-6, K)
+    assert np.array_equal(q & 127, exact_codes(h, w, K))
 
 
 # ------------------------------------------------------------------ kernels of large calls

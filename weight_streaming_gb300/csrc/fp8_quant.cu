@@ -47,6 +47,11 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float min_abs(float a, float b, float c) {  // of magnitudes (a has no sign); NaN loses
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // of the magnitudes, NaN if either is; signs mean nothing
   uint32_t r;
   asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -173,10 +178,20 @@ __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, 
   }
 }
 
-// The codes of a group of values h w (eight per lane, weights at w; 0 past the row) in pairs of floats, for
-// the groups that fp32 does not decide: y = hi + lo and the maximum m + ml are exact, and t = hi 448 / m takes
-// back its remainder 448 y - t (m + ml) (both over 512, so that nothing overflows).  What is left of that after
-// its rounding makes t odd, so that e4m3's is the only rounding.
+// The border between two e4m3 codes that lies nearest above or below t >= 0 (to some steps of fp32): the middle
+// of the normal codes' interval is where the lower 20 bits read 0x80000.  The codes below 2^-6 lie 2^-9 apart, as
+// those from there to 2^-5 do, so adding 2^-6 makes them look alike.
+__device__ __forceinline__ float border_of(float t) {
+  const bool sub = t < 0.015625f;
+  const float s = sub ? fminf(t + 0.015625f, 0.031249998f) : t;  // below 2^-5
+  const float b = __uint_as_float((__float_as_uint(s) & 0xFFF00000u) | 0x80000u);
+  return sub ? b - 0.015625f : b;
+}
+// The codes of a group of values h w (eight per lane, weights at w; 0 past the row), for the groups that fp32 does
+// not decide.  y = hi + lo and the maximum m + ml are exact pairs, and 448 y is compared with (m + ml) times the
+// border at hand (both over 512, so that nothing overflows).  The values have 35 and 37 bits: where they differ
+// they do so by 2^-37 of themselves and more, and what the sum below rounds is under 2^-46 of them where they
+// agree; so the sign is the exact one, a tie is one, and e4m3's rounding the only one.
 __device__ __forceinline__ uint2 codes_pair(uint4 a, const float* w, bool valid) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
   float hi[8], lo[8], ml = 0.0f;
@@ -196,14 +211,13 @@ __device__ __forceinline__ uint2 codes_pair(uint4 a, const float* w, bool valid)
 #pragma unroll
   for (int o = 8; o; o >>= 1) ml = fmaxf(ml, __shfl_xor_sync(half, ml, o));
   m *= 0.001953125f, ml *= 0.001953125f;  // 1 / 512
-  const float c = r * 1.142857143f;  // 512 / 448
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = hi[e] * r, x = hi[e] * 0.875f, y = t * m;
-    const float rest = (x - y) + (fmaf(hi[e], 0.875f, -x) - fmaf(t, m, -y) + fmaf(lo[e], 0.875f, -t * ml));
-    const float u = fmaf(rest, c, t), d = fmaf(rest, c, t - u);
-    const int up = d == 0.0f || (__float_as_int(u) & 1) ? 0 : (d > 0.0f) == (u > 0.0f) ? 1 : -1;
-    hi[e] = u == 0.0f ? u : __int_as_float(__float_as_int(u) + up);
+    const float h = fabsf(hi[e]), b = border_of(h * r), x = h * 0.875f, y = b * m;  // 448 / 512
+    const float rest = (x - y) + ((fmaf(h, 0.875f, -x) - fmaf(b, m, -y)) +
+                                  fmaf(hi[e] < 0.0f ? -lo[e] : lo[e], 0.875f, -(b * ml)));
+    const int up = fabsf(rest) <= y * 2.27373675e-13f ? 0 : rest > 0.0f ? 1 : -1;  // 2^-42
+    hi[e] = copysignf(__int_as_float(__float_as_int(b) + up), hi[e]);
   }
   return codes_of(hi, 1.0f);
 }
@@ -310,12 +324,12 @@ __device__ __noinline__ void redo_row(const void* x, long long ld, const uint16_
 // stream is rounded to: one pass over the data, every load issued before the first use.  Many rows: four
 // chunks per thread, so that an SM holds several rows' CTAs and 100 KB and more of loads in flight while
 // others reduce; few rows: one chunk per thread, the shortest path through a row.  4099 rows of 5120 in bf16
-// with a residual (148 MB): 31 us from memory, 4.7 TB/s of the 6.8 that a copy reaches (5.1 in a row of calls; fp32
-// input 5.8; without weights 6.0): the bf16 form issues for most of the time.  With the rare paths inline, over
-// chunks held in registers, 33 us; two chunks per thread 33 us; a resident grid that copies a row ahead into shared
-// memory 37 us (fewer warps to hide a row's reductions).  Weights that are all one leave most groups open: 46 us
-// (NULL does not).  8 rows: 4.9 us, 1.4 more if one of them has an open
-// group; 4.2 us is a launch.
+// with a residual (148 MB) from memory, by the weights: random 24-bit ones 31.7 us, 4.7 TB/s of the 6.8 that a copy
+// reaches (fp32 input 35.3, 5.4 TB/s); none 26.8; bf16 ones (as checkpoints hold them), whose products with bf16
+// values meet e4m3's ties, 35 to 38; all one 51.  Looking at the borders below 2^-6 costs 0.7 us of these.  With
+// the rare paths inline, over chunks held in registers, 33 us; two chunks per thread 33 us; a resident grid that
+// copies a row ahead into shared memory 37 us (fewer warps to hide a row's reductions).  8 rows: 4.6 us, 1.4 more if
+// one of them has an open group; 4.2 us is a launch.
 template <bool kF32, int kC>
 __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld, const uint16_t* residual,
                                                     const float* __restrict__ weight, int vec, float eps, int K,
@@ -412,13 +426,22 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
         float s, r;
         const float most = group_max(v);
         scale_of(most, inv, s, r);
-        // Products within 5 steps of fp32 of a border of e4m3's (its normal ones, where the lower 20 bits begin):
-        // three fp32 roundings leave those open.
+        // Products within 5 steps of fp32 of a border of e4m3's (see border_of): three fp32 roundings leave those
+        // open.  The borders below 2^-6 are looked at only where a value lies there (normal values: 2 % of the warps).
         unsigned near = ~0u;
+        float least = 1.0f;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           v[e] *= r, v[e + 1] *= r;
           near = __vimin3_u32(near, (__float_as_uint(v[e]) << 12) - (0x7FFFBu << 12), (__float_as_uint(v[e + 1]) << 12) - (0x7FFFBu << 12));
+          least = min_abs(least, v[e], v[e + 1]);
+        }
+        if (least < 0.015625f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float t = fabsf(v[e]);
+            if (t < 0.015625f) near = min(near, (__float_as_uint(t + 0.015625f) << 12) - (0x7FFFBu << 12));
+          }
         }
         const uint2 c = codes_of(v, 1.0f);
         if (near <= 10u << 12) open |= 1u << i;
@@ -429,7 +452,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
     }
     open = __reduce_or_sync(0xFFFFFFFFu, open | far);
 #pragma unroll 1
-    for (int i = 0; open >> i; ++i) {  // 1 group in 900
+    for (int i = 0; open >> i; ++i) {  // 1 group in 760 with random 24-bit weights, 1 in 16 to 26 with bf16 ones
       const int k = k0 + i * step;
       if (!(open >> i & 1) || (k & ~127) >= K) continue;
       redo_chunk<kF32>(x, ld, residual, weight, m, k, K, h, inv, far >> i & 1, q, scales + (size_t)m * KB + k / kQBlock);
