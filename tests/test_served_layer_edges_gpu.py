@@ -6,8 +6,8 @@ import torch
 
 from helpers import workspace
 from oracle import served_layer as ref
-from test_served_layer_gpu import (U, Paged, assert_within, attend, bf16, f32, f64, freqs, i32, linear, nearest_codes,
-                                   run_norm)
+from test_served_layer_gpu import (U, Paged, assert_codes, assert_within, attend, bf16, f32, f64, freqs, i32, linear,
+                                   nearest_codes, run_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,6 +87,42 @@ def test_add_rmsnorm_codes_of_every_pair_of_eight_bits(V, kind, rows):
     w = weights(None, K, kind)
     h, q, _ = run_norm(V, x, None, w, 1e-6, K)
     assert np.array_equal(q & 127, exact_codes(h, w, K))
+
+
+# ------------------------------------------------------------------ outside fp32's range
+@pytest.mark.parametrize("M", [5, 400])
+@pytest.mark.parametrize("what", ["weights", "rows"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_add_rmsnorm_codes_outside_the_range_of_fp32(V, M, what, wide):
+    """Products of 2^-100 and of 2^110 (the row's factor is about 1), and rows whose squares fp32 does not hold (about
+    1e-21 and 1e21): codes of the exact quotients there, too."""
+    rng = np.random.default_rng(M)
+    K = 1040
+    x = rng.standard_normal((M, K)) * 2.0 ** -rng.integers(0, 16, (M, K))
+    w = np.ones(K)
+    if what == "weights":
+        w[:384], w[384:768] = 2.0 ** -100, 2.0 ** 110
+    else:
+        x *= np.where(np.arange(M) % 2, 2.0 ** -70, 2.0 ** 70)[:, None]
+        w[::3] = 1.0 + 2.0 ** -6
+    x = f32(x) if wide else f32(x).to(torch.bfloat16)
+    h, q, s = run_norm(V, x, None, f32(w), 1e-30, K)
+    assert np.array_equal(q & 127, exact_codes(h, f32(w), K))
+    _, y = ref.add_rmsnorm(f64(x), None, f64(f32(w)), 1e-30)
+    assert_codes(q, s, y, 40 * U, what)
+
+
+@pytest.mark.parametrize("M", [3, 400])
+def test_add_rmsnorm_values_above_fp32_have_finite_scales(V, M):
+    """y reaches sqrt(K) times the weight: beyond fp32, while max / 448 is not."""
+    K = 4096
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[:, 5], x[:, 6], x[:, 200] = 3.0, -1.0, 1.0
+    w = torch.full((K,), 3e38, device="cuda")
+    _, q, s = run_norm(V, x, None, w, 1e-6, K)
+    _, y = ref.add_rmsnorm(f64(x), None, f64(w), 1e-6)
+    assert np.abs(y).max() > 1e40
+    assert_codes(q, s, y, 40 * U, "above fp32")
 
 
 # ------------------------------------------------------------------ kernels of large calls

@@ -254,25 +254,59 @@ __device__ __forceinline__ uint4 reload(const void* x, long long at_x, const uin
   constexpr uint32_t kNone = 0x80008000u;  // -0: adding it leaves a zero's sign, too
   return residual_sum(v, residual ? *reinterpret_cast<const uint4*>(residual + at) : make_uint4(kNone, kNone, kNone, kNone));
 }
-// The group of this lane's chunk `a` with every product in fp64; w: the chunk's weights, or NULL.
+// The group of this lane's chunk `a` in fp64; w: the chunk's weights, or NULL.  h w has 32 bits, so it, 448 h w and
+// every tie of the quotient are exact; the quotient is cut to fp32 with a last bit for what was cut, so that
+// e4m3's rounding decides.  (At the scale's floor the values carry the row's factor and its rounding.)
 __device__ __noinline__ void group64(uint4 a, const float* w, double inv, bool valid, uint8_t* q, float* scale) {
-  float v[8];
+  const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
+  float v[8], s;
   uint2 c;
   unpack8(a, v);
   const bool some = ((a.x | a.y | a.z | a.w) & 0x7FFF7FFFu) != 0;
-  if (__any_sync(0xFFFFu << (threadIdx.x & 16), some) || !(fabs(inv) <= 1e300)) {
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {  // rotating, so that the loop stays one
-      const float y = (float)((double)v[0] * inv * (double)(valid && w ? __ldg(w + e) : 1.0f));
+  if (__any_sync(half, some) || !(fabs(inv) <= 1e300)) {
+    auto product = [&](int e) -> double {  // of v[0], the lane's value e; rotating, so that the loops stay loops
+      return (double)v[0] * (double)(valid && w ? __ldg(w + e) : 1.0f);
+    };
+    auto rotate = [&](float x) {
 #pragma unroll
       for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
-      v[7] = y;
+      v[7] = x;
+    };
+    double m = 0.0;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const double y = fabs(product(e));
+      m = y > m || y != y ? y : m;  // a NaN stays: nothing is above it
+      rotate(v[0]);
     }
-  } else if (valid && w) {  // zeros (a padding row's): theirs, or a NaN weight's
+#pragma unroll 1
+    for (int o = 8; o; o >>= 1) {
+      const double y = __shfl_xor_sync(half, m, o);
+      m = y > m || y != y ? y : m;
+    }
+    const double ym = m * inv, sd = ym / (double)kE4m3Max;
+    const bool least = !(sd > (double)kScaleFloor), inf = !(ym <= 1.7e308);  // inf: or no value
+    s = inf ? (float)ym : least ? kScaleFloor : (float)sd;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      double t = product(e);
+      if (inf)
+        t = t * (1.0 / ym);  // finite values over infinity: 0; NaN for the others
+      else if (least)
+        t = t * inv * 8.507059173023462e37;  // 2^126
+      else
+        t = t * (double)kE4m3Max / m;
+      float f = __double2float_rz(t);
+      if ((double)f != t) f = __int_as_float(__float_as_int(f) | 1);
+      rotate(f);
+    }
+    c = codes_of(v, 1.0f);
+  } else {  // zeros (a padding row's): theirs, or a NaN weight's
+    if (valid && w)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= __ldg(w + e);
+      for (int e = 0; e < 8; ++e) v[e] *= __ldg(w + e);
+    s = quant_group(v, c);
   }
-  const float s = quant_group(v, c);
   if (valid) *reinterpret_cast<uint2*>(q) = c;
   if ((threadIdx.x & 15) == 0) *scale = s;
 }
