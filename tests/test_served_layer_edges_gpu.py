@@ -125,6 +125,25 @@ def test_add_rmsnorm_values_above_fp32_have_finite_scales(V, M):
     assert_codes(q, s, y, 40 * U, "above fp32")
 
 
+# ------------------------------------------------------------------ the largest eps
+@pytest.mark.parametrize("eps", [1e38, 3.4e38])
+def test_norms_with_the_largest_eps(V, eps):
+    """mean + eps leaves fp32, its root does not."""
+    rng = np.random.default_rng(7)
+    x = bf16(rng, (3, 16), 4e18)
+    h, q, s = run_norm(V, x, None, None, eps, 16)
+    _, y = ref.add_rmsnorm(f64(x), None, None, eps)
+    assert np.abs(y).max() > 0.1
+    assert_codes(q, s, y, 40 * U, "norm")
+    D, P = 64, 16
+    p = Paged(V, 8, 3, 1, P, 1, D)
+    k, w = bf16(rng, (3, 1, D), 2e18), torch.ones(D, device="cuda")
+    V.vp_paged_append(p.desc(), None, 0, k, D, k, D, None, w, eps, None, None, i32([0, 0, 0]), 3, 3, 0, None)
+    want, mag = ref.norm_rope(f64(k), np.ones(D), eps, np.zeros(3), [], False)
+    assert np.abs(want).max() > 0.1
+    assert_within(f64(p.k[p.pages[:, 0].long(), :, 0]), want, 2.0 ** -8 * np.abs(want) + 32 * U * mag, "append")
+
+
 # ------------------------------------------------------------------ kernels of large calls
 def append_cases():  # (D, Hq, Hkv, norm)
     for D in (64, 128, 256):

@@ -366,7 +366,7 @@ __device__ __noinline__ void redo_row(const void* x, long long ld, const uint16_
 // one of them has an open group; 4.2 us is a launch.
 template <bool kF32, int kC>
 __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld, const uint16_t* residual,
-                                                    const float* __restrict__ weight, int vec, float eps, int K,
+                                                    const float* __restrict__ weight, int vec, float eps, float ss_max, int K,
                                                     uint16_t* h, uint8_t* __restrict__ q, float* __restrict__ scales) {
   __shared__ float red[32];
   __shared__ double redd[32];
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const void* x, long long ld,
   ss = 0.0f;
   for (int w = 0; w < warps; ++w) ss += red[w];
   const float* pw = weight + k0;
-  if (ss >= 1e-30f && ss <= 3.0e38f) {
+  if (ss >= 1e-30f && ss <= ss_max) {
     const float inv = 1.0f / sqrtf(ss / (float)K + eps);
     // The values at hand are h w: the row's factor cancels from the codes and enters the scales only.
     unsigned open = 0, far = 0;  // chunks of the thread that fp32 leaves open, or that leave its range
@@ -579,11 +579,12 @@ vp_status vp_add_rmsnorm_fp8(const void* x, int x_type, int64_t ld_x, const void
   const int per = M >= 2 * sms ? 4 : chunks > 1024 ? 2 : 1;
   const int threads = (chunks + 32 * per - 1) / (32 * per) * 32;
   const bool wide = x_type == VP_F32;
+  const float ss_max = eps <= 1e37f ? 3.0e38f : 0.0f;  // up to here the sum of squares, and the mean plus eps, are finite
   auto* kern = per == 4 ? (wide ? norm_kernel<true, 4> : norm_kernel<false, 4>)
                         : per == 2 ? (wide ? norm_kernel<true, 2> : norm_kernel<false, 2>)
                                    : (wide ? norm_kernel<true, 1> : norm_kernel<false, 1>);
   kern<<<(unsigned)M, threads, 0, (cudaStream_t)stream>>>(x, ld_x, static_cast<const uint16_t*>(residual), weight,
-                                                          al(weight, 16), eps, K, static_cast<uint16_t*>(h),
+                                                          al(weight, 16), eps, ss_max, K, static_cast<uint16_t*>(h),
                                                           static_cast<uint8_t*>(q), scales);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);

@@ -86,7 +86,7 @@ __device__ __forceinline__ void norm_head(float (&x)[8], const float* w0, const 
   for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
   for (int o = kL / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-  if (ss >= 1e-30f && ss <= 3.0e38f) {
+  if (ss >= 1e-30f && ss <= 3.0e38f && eps <= 1e37f) {  // the mean plus eps is finite
     const float inv = 1.0f / sqrtf(ss / (float)(8 * kL) + eps);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * __ldg(e < 4 ? w0 + e : w1 + e - 4);
