@@ -255,8 +255,10 @@ __device__ __forceinline__ uint4 reload(const void* x, long long at_x, const uin
   return residual_sum(v, residual ? *reinterpret_cast<const uint4*>(residual + at) : make_uint4(kNone, kNone, kNone, kNone));
 }
 // The group of this lane's chunk `a` in fp64; w: the chunk's weights, or NULL.  h w has 32 bits, so it, 448 h w and
-// every tie of the quotient are exact; the quotient is cut to fp32 with a last bit for what was cut, so that
-// e4m3's rounding decides.  (At the scale's floor the values carry the row's factor and its rounding.)
+// its maximum are exact; the product with 448 / m is off by less than 2^-51, ties lie in 5 bits and every other
+// quotient 2^-37 away from them, so rounding it to 41 bits gives each its side.  It is then cut to fp32 with a last
+// bit for what was cut, and e4m3's rounding decides.  (At the scale's floor the values carry the row's factor and
+// its rounding.)  Few fp64 operations, the rest on the bits: 4099 rows of 5120 that all come here take 0.67 ms.
 __device__ __noinline__ void group64(uint4 a, const float* w, double inv, bool valid, uint8_t* q, float* scale) {
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
   float v[8], s;
@@ -272,33 +274,25 @@ __device__ __noinline__ void group64(uint4 a, const float* w, double inv, bool v
       for (int i = 0; i < 7; ++i) v[i] = v[i + 1];
       v[7] = x;
     };
-    double m = 0.0;
+    unsigned long long top = 0;  // the largest magnitude's bits: NaN above infinity above the finite ones
 #pragma unroll 1
     for (int e = 0; e < 8; ++e) {
-      const double y = fabs(product(e));
-      m = y > m || y != y ? y : m;  // a NaN stays: nothing is above it
+      top = max(top, (unsigned long long)__double_as_longlong(product(e)) & ~(1ull << 63));
       rotate(v[0]);
     }
 #pragma unroll 1
-    for (int o = 8; o; o >>= 1) {
-      const double y = __shfl_xor_sync(half, m, o);
-      m = y > m || y != y ? y : m;
-    }
-    const double ym = m * inv, sd = ym / (double)kE4m3Max;
-    const bool least = !(sd > (double)kScaleFloor), inf = !(ym <= 1.7e308);  // inf: or no value
-    s = inf ? (float)ym : least ? kScaleFloor : (float)sd;
+    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
+    const double m = __longlong_as_double((long long)top), ym = m * inv, sd = ym / (double)kE4m3Max;
+    const bool least = !(sd > (double)kScaleFloor), none = !(ym <= 1.7e308);  // infinite, or no value
+    s = none ? (float)ym : least ? kScaleFloor : (float)sd;
+    const double r = none ? 1.0 / ym : least ? inv * 8.507059173023462e37 : (double)kE4m3Max / m;  // 2^126
 #pragma unroll 1
     for (int e = 0; e < 8; ++e) {
-      double t = product(e);
-      if (inf)
-        t = t * (1.0 / ym);  // finite values over infinity: 0; NaN for the others
-      else if (least)
-        t = t * inv * 8.507059173023462e37;  // 2^126
-      else
-        t = t * (double)kE4m3Max / m;
-      float f = __double2float_rz(t);
-      if ((double)f != t) f = __int_as_float(__float_as_int(f) | 1);
-      rotate(f);
+      const double t = product(e) * r;
+      const long long bits = (__double_as_longlong(t) + 0x800) & ~0xFFFll;
+      const float f = __double2float_rz(__longlong_as_double(bits));
+      // finite values over an infinity are 0, the others NaN
+      rotate(none ? (float)t : (bits & 0x1FFFFFFF) ? __int_as_float(__float_as_int(f) | 1) : f);
     }
     c = codes_of(v, 1.0f);
   } else {  // zeros (a padding row's): theirs, or a NaN weight's
