@@ -144,6 +144,26 @@ def test_norms_with_the_largest_eps(V, eps):
     assert_within(f64(p.k[p.pages[:, 0].long(), :, 0]), want, 2.0 ** -8 * np.abs(want) + 32 * U * mag, "append")
 
 
+# ------------------------------------------------------------------ attention: gates
+def test_attention_gates_near_the_end_of_the_exponents(V):
+    """sigmoid of -80 and below times values up to bf16's largest: a product that bf16 holds is not lost."""
+    S, Hq, Hkv, D, P = 2, 4, 2, 64, 16
+    rng = np.random.default_rng(3)
+    p = Paged(V, 4, S, 2, P, Hkv, D)
+    p.v[:] = torch.from_numpy(rng.choice([-1.0, 1.0], p.v.shape) * 2.0 ** rng.choice([0, 3, 60, 120], p.v.shape[:3])[..., None]).to(
+        torch.bfloat16).cuda()
+    q = bf16(rng, (S, Hq, D))
+    gate = torch.from_numpy(rng.uniform(-175, -80, (S, Hq, D))).to(torch.bfloat16).cuda()
+    gate[0, :, :4] = torch.tensor([0.0, 30.0, 200.0, -50.0], dtype=torch.bfloat16)
+    gate[1, 0, :2] = torch.tensor([float("-inf"), float("inf")], dtype=torch.bfloat16)
+    lens = [1, 1]  # one key: the output is its value times the gate's sigmoid
+    out, _ = attend(V, p, q, lens, D ** -0.5, gate)
+    want, mag, _, _ = ref.paged_attention(f64(q), f64(p.k), f64(p.v), p.table, lens, D ** -0.5, f64(gate))
+    assert (np.abs(want) > 1e-3).any() and ((np.abs(want) < 1e-37) & (np.abs(want) > 1e-40)).any()
+    # an exponential of half the gate, 2 ulp, used twice, three products: below 2^-19; bf16's half step, 2^-134 below its normal values
+    assert_within(f64(out), want, 2.0 ** -19 * mag + np.maximum(2.0 ** -8 * np.abs(want), 2.0 ** -134), "gate")
+
+
 # ------------------------------------------------------------------ kernels of large calls
 def append_cases():  # (D, Hq, Hkv, norm)
     for D in (64, 128, 256):

@@ -133,7 +133,12 @@ __device__ __forceinline__ void finish(const PagedArgs& a, size_t qrow, int r, i
   if (a.gate) {
     const float g[4] = {bfv(gate.x & 0xFFFF), bfv(gate.x >> 16), bfv(gate.y & 0xFFFF), bfv(gate.y >> 16)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __fdividef(v[e], 1.0f + expf(-g[e]));  // 2 ulp; 0 where the sum is above 2^126
+    for (int e = 0; e < 4; ++e) {
+      // 2 ulp, but 0 where the sum is above 2^126.  Far below that 1 + e^-g is e^-g, and half the gate twice keeps
+      // what a large value leaves of it.
+      const float half = expf(0.5f * g[e]);
+      v[e] = g[e] < -60.0f ? v[e] * half * half : __fdividef(v[e], 1.0f + expf(-g[e]));
+    }
   }
   const __nv_bfloat162 p0 = __floats2bfloat162_rn(v[0], v[1]), p1 = __floats2bfloat162_rn(v[2], v[3]);
   *reinterpret_cast<uint2*>(a.out + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
