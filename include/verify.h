@@ -549,12 +549,14 @@ vp_status vp_decode_steps_rows(const vp_model* model, int steps, int rows, const
 
 /* ------------------------------------------------------------------ a served attention layer
  *
- * The calls below run the attention layers of the same models outside the verify pass: prompts, and
- * single-token decode of many sequences, with the weights of a block-quantised FP8 checkpoint and a
- * KV cache in pages.  One layer of a step chains them:
+ * The calls below run the attention layers of the same models outside the verify pass: single-token
+ * decode of many sequences, with the weights of a block-quantised FP8 checkpoint and a KV cache in
+ * pages.  One layer of such a step chains them:
  *   vp_add_rmsnorm_fp8 -> vp_linear_fp8_block (q, k, v) -> vp_paged_append -> vp_paged_attention ->
  *   vp_quant_fp8 -> vp_linear_fp8_block (o).
- * All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph.  Outputs
+ * All but vp_paged_attention take a prompt's rows too; it takes one new token per sequence, so a
+ * prompt's own attention (several new rows per sequence) is the caller's.  The paged cache and the
+ * block-scaled weights are these calls' alone: the verify pass keeps its own formats.  All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph.  Outputs
  * must not overlap inputs except where a call says so.  One workspace, zero-filled once, serves
  * vp_linear_fp8_block and vp_paged_attention calls of any shapes in turn on one stream (of the
  * largest of their sizes); a workspace that another section's call has used, or whose status word
@@ -567,8 +569,10 @@ enum { VP_BF16 = 0, VP_F32 = 1 };
 /* Block-scaled e4m3 activations.  Per row m and group b of 128 columns (the last one shorter when
  * K % 128 != 0):
  *   scales[m][b] = max(max_k |x[m][k]| / 448, 2^-126),   q[m][k] = e4m3(x[m][k] * 448 / max_k |x[m][k]|),
- * to nearest even (of bf16 x the exact quotient's code, of fp32 x after three fp32 roundings); a NaN or infinity in a group makes the group's scale NaN or
- * infinite, and the elements that have no value NaN.  x: bf16 or fp32 (x_type VP_BF16 / VP_F32),
+ * or e4m3(x[m][k] * 2^126) where the scale is 2^-126 (a group of zeros: zeros), to nearest even: of bf16
+ * x the exact quotient's code, of fp32 x after three fp32 roundings.  (x over the fp32 scale, which is
+ * rounded, may have another code where x * 448 / max lies half way between two.)  A NaN or infinity in a
+ * group makes the group's scale NaN or infinite, and the elements that have no value NaN.  x: bf16 or fp32 (x_type VP_BF16 / VP_F32),
  * row stride ld_x elements; q: e4m3 bytes [M][K]; scales: fp32 [M][ceil(K / 128)].  1 <= M <= 2^24,
  * K % 16 == 0, 16 <= K <= 65536, ld_x >= K and rows 16-byte aligned (VP_ERR_SHAPE, VP_ERR_ALIGNMENT).
  * One launch, no workspace. */
@@ -577,7 +581,8 @@ vp_status vp_quant_fp8(const void* x, int x_type, int64_t ld_x, int M, int K, vo
 /* Residual addition, RMSNorm and the quantisation above in one pass over the rows:
  *   h = bf16(x + residual)   (the sum in fp32; bf16(x) when residual is NULL),
  *   y = h / sqrt(mean_k h^2 + eps) * weight   (weight 1 when NULL; not rounded),
- *   q, scales = the block quantisation of y (the codes rounded once, as of bf16 above).
+ *   q, scales = the block quantisation of y: the codes are the exact quotient's (the row's factor cancels
+ *   from it: h weight * 448 / max), but where the scale is 2^-126, whose codes carry y's own rounding.
  * The mean is taken over the rounded h, the residual stream that the next block reads.  It does not
  * overflow or vanish where h^2 leaves fp32's range.  x: bf16 or fp32, row stride ld_x; residual: bf16
  * [M][K] or NULL; weight: fp32 [K] or NULL; h: bf16 [M][K] or NULL (not written), may be `residual`
@@ -588,7 +593,8 @@ vp_status vp_add_rmsnorm_fp8(const void* x, int x_type, int64_t ld_x, const void
 
 /* Linear layer of a block-quantised FP8 checkpoint on block-quantised activations:
  *   y[m][n] = sum_b x_scales[m][b] * w_scales[n / 128][b] * sum_{k in block b} e4m3(xq[m][k]) * e4m3(w[n][k]),
- * the inner sums (128 products) on the tensor core with fp32 accumulation, the outer one in fp32.
+ * the inner sums (128 products) on the tensor core with fp32 accumulation, the outer one in fp32, as is
+ * the product of the two scales (within fp32's range: an infinite one gives no value even for sums of 0).
  * w_packed: the repacked weights (vp_pack_fp8_block, from [N][K] e4m3 bytes; 128 x 128 tiles, padded
  * with zeros); w_scales: fp32 [ceil(N / 128)][ceil(K / 128)]; xq: e4m3 bytes [M][K]; x_scales: fp32
  * [M][ceil(K / 128)]; y: bf16 (rounded once) or fp32 [M][N] (y_type).  Any M from 1 to 2^20; N % 16
@@ -652,7 +658,8 @@ vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld
  * word to VP_ERR_SHAPE; so does a page outside 0 .. n_pages - 1 among the sequence's pages, whose
  * positions are left out.  VP_ERR_TIMEOUT there: a bounded wait gave up (out and lse are then not
  * valid).  What lies in the cache behind kv_len[s] (NaN, infinities) has no effect;
- * before it, an infinite value makes its column NaN.
+ * before it, an infinite value makes its column NaN, and where every score of a head is -infinity the
+ * head's outputs are zeros and its lse -inf, as of a sequence without positions.
  * Hq % Hkv == 0, Hq / Hkv <= 16, scale finite and below 2^127; 1 <= S <= 8192, S * Hkv <= 65536.  The cached positions
  * are cut into shares of about equal length, one per CTA, whatever the lengths (they are read on the
  * device only); partial results are joined in a fixed order: bit-identical from run to run.  P V runs

@@ -2,10 +2,11 @@
 // (vp_quant_fp8), and the residual addition + RMSNorm with a quantised output (vp_add_rmsnorm_fp8).
 //
 // Mathematics: a group of 128 values shares s = max(max|x| / 448, 2^-126), so that |x / s| <= 448 up to
-// one rounding, and q = e4m3(x * 448 / max|x|).  Of bf16 values, and after a norm, the codes are those of the
-// exact quotient (e4m3's half step, 2^-4 of the value, is the only rounding); of fp32 values three fp32 roundings
-// come before, which move about 1 value in 2^18 across a border between two codes.  Infinities and NaN reach
-// the scale of their group, and nothing else.
+// one rounding, and q = e4m3(x * 448 / max|x|), or e4m3(x 2^126) where s is 2^-126.  Of bf16 values, and after a
+// norm, the codes are those of the exact quotient (e4m3's half step, 2^-4 of the value, is the only rounding; at
+// s = 2^-126 the norm's own rounding comes before); of fp32 values three fp32 roundings come before, which move
+// about 1 value in 2^18 across a border between two codes.  Infinities and NaN reach the scale of their group,
+// and nothing else.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
