@@ -64,7 +64,7 @@ struct LinArgs {
   void* y;
   int f32, M, N, KB;
   int vec_x, vec_w;           // the scales' rows can be read 16 bytes at a time
-  int tiles, tile_m, tile_n;  // output tiles: in all, along the tokens, along the weight rows
+  int tile_m, tile_n;         // output tiles along the tokens, along the weight rows
   int dp_rounds, cut_tiles;   // whole tiles per CTA (pair); the tiles after them, each cut into
   int split;                  // this many parts along K, one per CTA (pair), at multiples of
   int unit, units;            // this many K blocks; ceil(KB / unit)
@@ -327,7 +327,7 @@ __device__ __forceinline__ void tmem_wait(uint32_t* r) {
                  : "memory");
   }
 }
-// kBC: columns of a tile (token columns when kSwap, else weight rows).  kPair: two CTAs (a cluster) work
+// kBC: columns of a tile (token columns when kSwap, else weight rows: 128, or a pair's 256).  kPair: two CTAs (a cluster) work
 // on one tile of 256 tokens x 256 weight rows, 128 tokens' sums in each one's tensor memory; the first
 // CTA's MMA warp issues for both.
 template <int kBC, bool kSwap, bool kPair>
@@ -400,10 +400,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       while (ok && sched.next(a, it)) {
         int mt, nt;
         tile_at(a, it.tile, mt, nt);
-        // weight tiles of this output tile: one, or up to kBC / 128 (a pair's CTAs take one each; past the
-        // last row block the last one again, whose products are not stored)
-        const int nbs = kSwap || kPair ? 1 : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128));
-        const int nb = kSwap ? nt : kPair ? min(2 * nt + rank, qblocks(a.N) - 1) : nt * (kBC / 128);
+        // the weight tile of this output tile (a pair's CTAs take one each; past the last row block the last one
+        // again, whose products are not stored)
+        const int nb = kPair ? min(2 * nt + rank, qblocks(a.N) - 1) : nt;
         const int rows = kSwap ? kBC : 128, m0 = kPair ? mt * 256 + rank * 128 : mt * rows;
         for (int kb0 = it.kb0; kb0 < it.kb1; kb0 += C::kG, ++n) {
           if (!(ok = wait(smem_addr(&empty[s]), par))) break;
@@ -412,7 +411,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             if constexpr (kPair) {
               if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);  // both CTAs' copies
             } else {
-              mbar_arrive_expect_tx(&full[s], cnt * (rows * 128 + nbs * kQTileBytes));
+              mbar_arrive_expect_tx(&full[s], cnt * (rows * 128 + kQTileBytes));
             }
 #pragma unroll
             for (int g = 0; g < C::kG; ++g) {
@@ -428,8 +427,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
               } else {
                 const uint32_t bar = smem_addr(&full[s]);
                 tma_load_2d(dst_x, &xmap, kb * kQBlock, m0, bar);
-                for (int i = 0; i < nbs; ++i)
-                  bulk_load(dst_w + i * kQTileBytes, a.w + ((size_t)(nb + i) * a.KB + kb) * kQTileBytes, kQTileBytes, bar);
+                bulk_load(dst_w, a.w + ((size_t)nb * a.KB + kb) * kQTileBytes, kQTileBytes, bar);
               }
             }
           }
@@ -452,12 +450,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       int s = 0, b = 0;
       uint32_t par = 0, tpar = 1;
       bool ok = true, first = true;  // first: only the wait-test build asks
+      // e4m3 x e4m3 -> fp32, 128 rows (a pair's two CTAs: 256)
+      constexpr uint32_t idesc = 1u << 4 | (uint32_t)(kBC >> 3) << 17 | (kPair ? 16u : 8u) << 24;
       while (ok && sched.next(a, it)) {
-        int mt, nt;
-        tile_at(a, it.tile, mt, nt);
-        const int cols = kSwap || kPair ? kBC : min(kBC / 128, qblocks(a.N) - nt * (kBC / 128)) * 128;
-        // e4m3 x e4m3 -> fp32, 128 rows (a pair's two CTAs: 256)
-        const uint32_t idesc = 1u << 4 | (uint32_t)(cols >> 3) << 17 | (kPair ? 16u : 8u) << 24;
         for (int kb0 = it.kb0; kb0 < it.kb1; kb0 += C::kG) {
           const int cnt = min(C::kG, it.kb1 - kb0);
           const uint64_t da = smem_desc(ring) + (uint64_t)(s * (C::kStage >> 4)), db = da + (16384 >> 4);
@@ -514,7 +509,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       // the factor of this thread's row (tokens on the lanes) or of column c0 + lane (weights there); what is
       // past the last row or column is computed with another's factor and not stored
       const int m = kSwap ? next_mt * kBC + c0 + lane : kPair ? next_mt * 256 + rank * 128 + row : next_mt * 128 + row;
-      const int nb = kSwap ? next_nt : next_nt * (kBC / 128) + (kBC == 256 ? half : 0);
+      const int nb = kPair ? 2 * next_nt + half : next_nt;
       px = a.xs + (size_t)min(m, a.M - 1) * a.KB;
       pw = a.ws + (size_t)min(nb, qblocks(a.N) - 1) * a.KB;
       if constexpr (kSwap) {
@@ -936,7 +931,7 @@ vp_status vp_linear_fp8_block(const void* w_packed, const float* w_scales, const
   a.M = M, a.N = N, a.KB = qblocks(K);
   a.vec_x = a.KB % 4 == 0 && al(x_scales, 16);
   a.vec_w = a.KB % 4 == 0 && al(w_scales, 16);
-  a.tiles = p.tiles, a.tile_m = p.tile_m, a.tile_n = p.tile_n;
+  a.tile_m = p.tile_m, a.tile_n = p.tile_n;
   int grid = std::min(sms, kLinGrid) / (p.pair ? 2 : 1);  // CTAs, or pairs
   a.dp_rounds = p.tiles / grid;
   a.cut_tiles = p.tiles - a.dp_rounds * grid;
