@@ -1,6 +1,6 @@
 """Bounded waits of the served attention layer's kernels run out, and the library reports it.
 
-As test_wait_timeout_gpu.py, with the wait-test build: a workspace hook word leaves an arrival or a copy out."""
+As test_wait_timeout_gpu.py, with the wait-test build: a workspace hook word leaves an arrival or a copy out, or gives a wait up."""
 import importlib
 import os
 import subprocess
@@ -21,6 +21,6 @@ def test_waits_that_run_out_are_reported_and_leave_nothing_behind():
     assert out.returncode == 0, out.stdout[-2000:] + out.stderr[-3000:]
     from weight_streaming_gb300 import _lib as V
     lines = out.stdout.strip().splitlines()
-    assert len(lines) == 41, out.stdout
+    assert len(lines) == 52, out.stdout
     for line in lines:
         assert line.endswith(f": {V.VP_OK} {V.VP_ERR_TIMEOUT} {V.VP_OK} 1"), line

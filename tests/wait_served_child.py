@@ -1,10 +1,10 @@
 """Child process of test_wait_timeout_served_gpu.py (run with VP_LIBVERIFY naming the wait-test build of the
 library, whose bounded waits give up after milliseconds).
 
-Each case runs normally; then the workspace's test hook leaves an arrival or a copy out, so that a wait of the
-kernel runs out: the call must return and the status word read VP_ERR_TIMEOUT; then, after
-vp_workspace_init, the next call must give the first one's results.  Prints "case status status status equal"
-per case."""
+Each case runs normally; then the workspace's test hook leaves an arrival or a copy out, or gives a wait
+up, so that a wait of the kernel runs out: the call must return and the status word read VP_ERR_TIMEOUT;
+then, after vp_workspace_init, the next call must give the first one's results.  Prints "case: status status
+status equal" per case."""
 import os
 import sys
 
@@ -72,9 +72,9 @@ ATTENTION = {
 def main():
     assert "waittest" in V.LIB_PATH, V.LIB_PATH
     cases = [(f"attention, {name}, hook {h}", attention, shape, h) for name, shape in ATTENTION.items()
-             for h in ((1, 2) if name == "whole sequences" else (1, 2, 3))]
+             for h in ((1, 2, 4) if name == "whole sequences" else (1, 2, 3, 4))]
     cases += [(f"linear, {name}, hook {h}", linear, shape, h) for name, shape in LINEAR.items()
-              for h in ((1, 2, 3, 4, 5) if "pairs" in name else (1, 2, 3, 4))]
+              for h in ((1, 2, 3, 4, 5, 6) if "pairs" in name else (1, 2, 3, 4, 6))]
     for what, make, shape, hook in cases:
         run, ws = make(*shape)
         want = run()

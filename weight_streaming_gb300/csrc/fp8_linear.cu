@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #ifdef VP_WAIT_TEST
   // Wait-test hook (workspace word kWsTestSkip): the first CTA (5: the second) leaves out, of its first block,
   // 1 the commit to the epilogue, 2 the commit that frees the stage, 3 an arrival that frees the tensor-memory
-  // buffer, 4 and 5 the copies.
+  // buffer, 4 and 5 the copies; 6: its first epilogue warp's first wait runs out at once.
   const int hook = ((const volatile int*)a.status)[kWsTestSkip / sizeof(int)];
   const bool hooked = blockIdx.x == (hook == 5 ? 1 : 0);
 #else
@@ -382,6 +382,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   // A bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (hooked && hook == 6 && warp == 4) {
+      *(volatile int*)&s_abort = 1;
+      atomicExch(a.status, (int)VP_ERR_TIMEOUT);
+      return false;
+    }
     if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
     return wait_slow(bar, parity, &s_abort, a.status);
   };
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             }
 #pragma unroll
             for (int g = 0; g < C::kG; ++g) {
-              if (g >= cnt || (hooked && hook >= 4 && n == 0)) break;
+              if (g >= cnt || (hooked && (hook == 4 || hook == 5) && n == 0)) break;
               const int kb = kb0 + g;
               const uint32_t st = ring + s * C::kStage + g * C::kBlock;
               // lanes' operand first (16 KB), columns' operand behind it

@@ -23,8 +23,8 @@
 // TB/s while it streams; a copy reaches 6.8 of reads and writes); 61 sequences of 300 to 9,000 positions, 8 x 128
 // heads (1.18 GB) in 182 us, 6.5 TB/s; 4 sequences of up to 700 positions in 14.3 us: launch, lengths, first
 // copies, join.
-// Waits are bounded: a warp whose wait ran out reports VP_ERR_TIMEOUT and goes on without waiting, so the
-// CTA ends; the warps that issue copies see them land first, whatever ran out, and no join copies start
+// Waits are bounded: a warp whose wait ran out reports VP_ERR_TIMEOUT, takes no further stage and goes on to the
+// end, so the CTA ends; the warps that issue copies see them land first, whatever ran out, and no join copies start
 // once something has.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 #ifdef VP_WAIT_TEST
   // Wait-test hook (workspace word kWsTestSkip), for the first CTA: 1 leaves out the arrival that frees its first
-  // stage, 2 the copies of its first piece; 3, for every CTA that joins parts: a copy of theirs.
+  // stage, 2 the copies of its first piece; 3, for every CTA that joins parts: a copy of theirs; 4: its first
+  // consumer warp's first wait runs out at once.
   const int hook = ((const volatile int*)a.status)[kWsTestSkip / sizeof(int)];
 #else
   constexpr int hook = 0;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   Segment g;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {  // a converged warp
-    for (uint32_t i = 0; i < kMbarPolls; ++i) {
+    for (uint32_t i = hook == 4 && c == 0 && warp == 0 && bar == full ? kMbarPolls : 0; i < kMbarPolls; ++i) {
       if (__all_sync(0xFFFFFFFFu, mbar_try_wait_hint(bar, parity, 20000u))) return true;
       if (__any_sync(0xFFFFFFFFu, *(volatile int*)&s_abort)) return false;
     }
@@ -424,6 +425,9 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
   int n = 0;                       // the run's pieces before the segment
   int st = warp;                   // the warp's next stage (warp or warp + kWarps), and its phase
   uint32_t par = 0;
+  // A wait of this warp ran out: it takes and frees no more stages.  Its phases would be out of step (a parity two
+  // uses ahead of an unfinished phase reads as complete), and a stage freed so would be armed a second time.
+  bool dead = false;
   int pend_s[2] = {-1, -1}, pend_h[2] = {0, 0};
   int pend_first[2] = {0, 0}, pend_last[2] = {0, 0};
   const int sub = 128 << a.log_box;  // bytes between a box's 64-column groups
@@ -451,11 +455,13 @@ __global__ void __launch_bounds__(PaCfg<D, kWide>::kThreads, 1)
     const int skip = (warp - n % kPaWarps + kPaWarps) % kPaWarps;
     n += g.p1 - g.p0;
     for (int p = g.p0 + skip; p < g.p1; p += kPaWarps) {
-      const bool ok = wait(&full[st], par);
+      if (dead || !wait(&full[st], par)) {
+        dead = true;
+        break;
+      }
       const int at = st;
       st += kPaWarps;
       if (st >= C::kStages) st = warp, par ^= 1;
-      if (!ok) continue;
       const uint32_t kb = ring + at * 2 * kPieceBytes, vb = kb + kPieceBytes;
       const int valid = g.len - p * kR, bad = *(volatile int*)&s_bad[at];
       const bool masked = valid < kR || bad;
