@@ -25,9 +25,11 @@
 //
 // What bounds it, N x K: 8 tokens, 5120 x 17408 (89.5 MB of weights) take 20.8 us, 4.3 TB/s: the stream at about
 // 6.5 TB/s and 7 us of launch, first copies, last block and join.  200 tokens, 16384 x 5120: 26 us, 64 pairs
-// with a tile each.  4096 tokens, 17408 x 5120: 258 us, 2.8 PFLOP/s (cuBLAS' bf16 1.9), 292 us once at the power limit: 62 % of
-// the tensor cycles.  A K block of a pair's tile is 512 cycles of MMAs and about 330 of reading and scaling its
-// sums; two tensor-memory buffers (all there is at 128 x 256 sums) leave 760 cycles a block of that chain.
+// with a tile each.  100 tokens, 5120 x 17408: 28.7 us; 34816 x 5120, more tiles than CTAs: 29.6 us for 8 tokens
+// (6.0 TB/s), 38.8 for 100.  4096 tokens, 17408 x 5120: 283 to 291 us at the power limit, 2.5 PFLOP/s, 258 us in the
+// first calls (cuBLAS' bf16 1.9 PFLOP/s): 62 % of the tensor cycles.  A K block of a pair's tile is 512 cycles of
+// MMAs and about 330 of reading and scaling its sums, and takes 760; two tensor-memory buffers (all there is at 128 x
+// 256 sums) would allow 512, so about 680 cycles of a buffer's turn are commits, arrivals and waits.
 //
 // Waits are bounded: on a timeout the CTA reports VP_ERR_TIMEOUT, waits (again with a limit) for its copies and
 // MMAs and frees its tensor memory.  Timed out or not, the copying warp leaves last: see its end.

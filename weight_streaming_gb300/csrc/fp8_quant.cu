@@ -124,7 +124,7 @@ __device__ __forceinline__ float quant_group(uint4 w, float f, uint2& codes, flo
 // the pairs are consecutive in memory and need no row arithmetic.  2051 rows of 17408 in bf16 (108 MB): 21 us
 // from memory (5.2 TB/s, of 6.8 that a copy reaches), 19 us when L2 holds a part (23 and 21 with the maximum taken
 // over the magnitudes' bits as integers).  The integer pipe bounds it: product, cut and conversion of every value
-// are what is left.  One pair each: 29 us before the last steps.
+// are what is left.  One pair each: 29 us before the last steps.  fp32 input (179 MB): 27 us, 6.7 TB/s.
 // 4 rows of 6144: 4.2 us, a launch.
 template <bool kF32, int kU, bool kFlat>
 __global__ void __launch_bounds__(256) quant_kernel(const void* __restrict__ x, long long ld, int M, int K,
@@ -353,7 +353,7 @@ __device__ __noinline__ void redo_row(const void* x, long long ld, const uint16_
 // stream is rounded to: one pass over the data, every load issued before the first use.  Many rows: four
 // chunks per thread, so that an SM holds several rows' CTAs and 100 KB and more of loads in flight while
 // others reduce; few rows: one chunk per thread, the shortest path through a row.  4099 rows of 5120 in bf16
-// with a residual (148 MB) from memory, by the weights: random 24-bit ones 31.7 us, 4.7 TB/s of the 6.8 that a copy
+// with a residual (148 MB) from memory, by the weights: random 24-bit ones 31.6 us (32.8 between other work), 4.7 TB/s of the 6.8 that a copy
 // reaches (fp32 input 35.3, 5.4 TB/s); none 26.8; bf16 ones (as checkpoints hold them), whose products with bf16
 // values meet e4m3's ties, 35 to 38; all one 51.  Looking at the borders below 2^-6 costs 0.7 us of these.  With
 // the rare paths inline, over chunks held in registers, 33 us; two chunks per thread 33 us; a resident grid that

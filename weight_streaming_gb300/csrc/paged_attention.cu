@@ -19,7 +19,7 @@
 //  * A (sequence, head) that crosses CTAs goes through fp32 partials in the workspace (two per CTA at
 //    most: its first and its last one), announced after the CTA's last copy (a GPU-scope fence waits
 //    for the copies in flight); the last contributor joins them in order.
-// Measured, from memory: 131,071 positions of 4 x 256 heads (537 MB) in 92 us, 5.9 TB/s with start and join (7.1
+// Measured, from memory: 131,071 positions of 4 x 256 heads (537 MB) in 91 us, 5.9 TB/s with start and join (7.1
 // TB/s while it streams; a copy reaches 6.8 of reads and writes); 61 sequences of 300 to 9,000 positions, 8 x 128
 // heads (1.18 GB) in 182 us, 6.5 TB/s; 4 sequences of up to 700 positions in 14.3 us: launch, lengths, first
 // copies, join.
