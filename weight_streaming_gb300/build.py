@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libverify.so")
 BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(PKG, "libverify_trace.so")
 # The same library with tiny limits on every bounded device wait and a workspace hook that makes
-# one CTA skip its first grid-barrier arrival: the build in which a test makes a wait run out.
+# one CTA skip its first grid-barrier arrival (or, in the served layer's kernels, an arrival or a copy
+# of its ring): the build in which a test makes a wait run out.
 BUILD_WAIT = os.path.join(PKG, "_build_waittest")
 LIB_WAIT = os.path.join(PKG, "libverify_waittest.so")
 # A measurement build of the executor's unit loop alone (csrc/unit_bench.cu; unit_bench.py runs it).
