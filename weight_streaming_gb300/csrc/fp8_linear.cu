@@ -329,8 +329,8 @@ __device__ __forceinline__ void tmem_wait(uint32_t* r) {
                  : "memory");
   }
 }
-// kBC: columns of a tile (token columns when kSwap, else weight rows: 128, or a pair's 256).  kPair: two CTAs (a cluster) work
-// on one tile of 256 tokens x 256 weight rows, 128 tokens' sums in each one's tensor memory; the first
+// kBC: columns of a tile (token columns when kSwap, else weight rows: 128, or a pair's 256).  kPair: two CTAs (a
+// cluster) work on one tile of 256 tokens x 256 weight rows, 128 tokens' sums in each one's tensor memory; the first
 // CTA's MMA warp issues for both.
 template <int kBC, bool kSwap, bool kPair>
 __global__ void __launch_bounds__(kLinThreads, 1)

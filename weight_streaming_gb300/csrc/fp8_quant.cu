@@ -200,7 +200,7 @@ __device__ __forceinline__ uint2 codes_pair(uint4 a, const float* w, bool valid)
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float x = hi[e], g = valid ? __ldg(w + e) : 0.0f;
-    hi[e] = x * g;
+    hi[e] = __fmul_rn(x, g);
     lo[e] = fmaf(x, g, -hi[e]);
   }
   float m = group_max(hi);
@@ -214,9 +214,10 @@ __device__ __forceinline__ uint2 codes_pair(uint4 a, const float* w, bool valid)
   m *= 0.001953125f, ml *= 0.001953125f;  // 1 / 512
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float h = fabsf(hi[e]), b = border_of(h * r), x = h * 0.875f, y = b * m;  // 448 / 512
+    // 448 / 512; products that the compiler does not fuse with what follows
+    const float h = fabsf(hi[e]), b = border_of(h * r), x = __fmul_rn(h, 0.875f), y = __fmul_rn(b, m);
     const float rest = (x - y) + ((fmaf(h, 0.875f, -x) - fmaf(b, m, -y)) +
-                                  fmaf(hi[e] < 0.0f ? -lo[e] : lo[e], 0.875f, -(b * ml)));
+                                  fmaf(hi[e] < 0.0f ? -lo[e] : lo[e], 0.875f, -__fmul_rn(b, ml)));
     const int up = fabsf(rest) <= y * 2.27373675e-13f ? 0 : rest > 0.0f ? 1 : -1;  // 2^-42
     hi[e] = copysignf(__int_as_float(__float_as_int(b) + up), hi[e]);
   }
