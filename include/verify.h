@@ -670,6 +670,72 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
                              float scale, const void* gate, void* out, float* lse, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* ------------------------------------------------------------------ several new rows per sequence
+ *
+ * The attention of prompts, of a prompt's next chunk and of a few rows (drafts to verify) over the paged cache, and the
+ * cache in 8 bits.  A chunk runs vp_paged_append -> vp_paged_attention_rows, or vp_paged_append_fp8 ->
+ * vp_paged_attention_rows_fp8, which takes single tokens too; vp_prompt_attention takes whole prompts without a cache.
+ * The conventions of the section above hold; one workspace serves all its attention and linear calls in turn on one
+ * stream, of the largest of their sizes.
+ *
+ * Row r of sequence s is its new row i = r - row_start[s] (row_start: device int32 [S + 1], nondecreasing); q head h reads
+ * key-value head h / (Hq / Hkv).  With n = row_start[s + 1] - row_start[s] rows and L positions in all it sees t <= L - n + i:
+ *   out[r][h] = sum_t softmax_t(scale * q[r][h] . k_t) v_t,   lse[r][h] = log sum_t exp(scale * q[r][h] . k_t),
+ * out times sigmoid(gate[r][h]) elementwise when gate is not NULL, rounded once to bf16; lse: fp32 [M][Hq] or NULL.
+ * gate, out: bf16 [M][Hq][D].  Rows outside row_start[0] .. row_start[S] - 1 are left as they were.  A sequence whose rows
+ * or lengths do not fit (row_start decreasing, below 0 or above M; L < n, L above max_pages * page_size) gives zeros and
+ * lse -inf in the rows that it has, and VP_ERR_SHAPE in the workspace's status word; VP_ERR_TIMEOUT there: a bounded wait
+ * gave up (out and lse are then not valid).
+ * Keys and values that a row does not see have no effect on it, whatever they hold.  An infinite or NaN value that it sees
+ * leaves no finite value in its column; where every score of a head is -infinity the head's outputs are zeros and its lse
+ * -inf.  Products run on the tensor cores with fp32 sums; the probabilities enter the second one in bf16 (2^-9 relative
+ * each), the sums of the softmax in fp32.
+ * D 64, 128 or 256; Hkv <= 1024, Hq / Hkv <= 64; 1 <= S <= 65536, 1 <= M <= 2^24, M * Hkv <= 2^30; scale finite and below
+ * 2^127, of either sign.  Work is cut by keys, whatever the lengths (they are read on the device only), and parts are joined
+ * in a fixed order: bit-identical from run to run.  Two launches.  Workspace: the matching _workspace_bytes(), 256-byte
+ * aligned, zero-filled once; pointers 16-byte aligned (row_start, kv_len, pages, lse 4-byte). */
+
+/* Causal attention over whole prompts, packed one behind the other: L = n.  q, k, v: bf16 rows of Hq, Hkv, Hkv heads of D,
+ * strides ld_q, ld_k, ld_v elements (multiples of 8; the three may be parts of one fused projection). */
+size_t vp_prompt_attention_workspace_bytes(int S, int M, int Hq, int Hkv, int D); /* 0 if unsupported */
+vp_status vp_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                              const int32_t* row_start, int S, int M, int Hq, int Hkv, int D, float scale, const void* gate,
+                              void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* The same over the paged cache: L = kv_len[s] (device int32 [S]), the new rows' keys and values appended.  q: bf16
+ * [M][Hq][D].  row_start NULL: one row per sequence (M == S).  A page outside 0 .. n_pages - 1 among those that a row sees
+ * is left out and sets the status word to VP_ERR_SHAPE. */
+size_t vp_paged_attention_rows_workspace_bytes(int S, int M, int Hq, int Hkv, int D); /* 0 if unsupported */
+vp_status vp_paged_attention_rows(const vp_paged_cache* cache, const void* q, const int32_t* row_start, const int32_t* kv_len,
+                                  int S, int M, int Hq, float scale, const void* gate, void* out, float* lse, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* The paged cache in 8 bits: per position and head D e4m3 codes and one power of two, value = e4m3(code) * 2^(scale - 127)
+ * (scale 255, or code 0x7F: NaN).  k, v: bytes [n_pages][Hkv][page_size][D]; k_scales, v_scales: bytes
+ * [n_pages][Hkv][page_size]; all 16-byte aligned; the rest as vp_paged_cache.  2 (D + 1) bytes per position and head in
+ * place of 4 D. */
+typedef struct {
+  void *k, *v;
+  uint8_t *k_scales, *v_scales;
+  const int32_t* pages;
+  int n_pages, page_size, max_pages, Hkv, D;
+} vp_paged_cache_fp8;
+
+/* vp_paged_append into that cache: of every key (normed, rotated) and value head the exponent
+ *   e = max(ceil(log2(max |x| / 448)), -118),   scale = e + 127,   code = e4m3(x / 2^e) to nearest even,
+ * of the exact x, not of its bf16 rounding; q_out, kv_len, status and every argument as there.  A head with an infinite or
+ * NaN value, or whose norm or rotation leaves fp32's range, has scale 255 and codes 0x7F. */
+vp_status vp_paged_append_fp8(const vp_paged_cache_fp8* cache, const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                              const void* v, int64_t ld_v, const float* q_norm, const float* k_norm, float eps,
+                              const vp_rope* rope, const int32_t* row_start, const int32_t* ctx, int S, int M, int Hq,
+                              void* q_out, int32_t* kv_len, int* status, void* stream);
+
+/* vp_paged_attention_rows over that cache (workspace as there).  code * 2^(scale - 127) enters the products as a bf16 value:
+ * exact for scales 9 .. 247 (what the append writes) but values of 2^128 and above, which are infinite. */
+vp_status vp_paged_attention_rows_fp8(const vp_paged_cache_fp8* cache, const void* q, const int32_t* row_start,
+                                      const int32_t* kv_len, int S, int M, int Hq, float scale, const void* gate, void* out,
+                                      float* lse, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -80,6 +80,18 @@ class vp_paged_cache(ctypes.Structure):
         self._keep = (k, v, pages)
 
 
+class vp_paged_cache_fp8(ctypes.Structure):
+    """The 8-bit paged cache's descriptor; it keeps the tensors it was made from alive."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int)]
+
+    def __init__(self, k, v, k_scales, v_scales, pages, n_pages: int, page_size: int, max_pages: int, Hkv: int, D: int):
+        super().__init__(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), _ptr(pages), n_pages, page_size, max_pages,
+                         Hkv, D)
+        self._keep = (k, v, k_scales, v_scales, pages)
+
+
 class vp_rope(ctypes.Structure):
     """Rotary embedding: inv_freq is a host sequence of rot_dim / 2 floats (copied)."""
     _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int)]
@@ -154,6 +166,14 @@ def _load():
         "vp_linear_fp8_block": (I, [P, P, P, P, P, I, I, I, I, P, S, P]),
         "vp_paged_append": (I, [ctypes.POINTER(vp_paged_cache), P, ctypes.c_int64, P, ctypes.c_int64, P,
                                 ctypes.c_int64, P, P, F, ctypes.POINTER(vp_rope), P, P, I, I, I, P, P, P, P]),
+        "vp_paged_append_fp8": (I, [ctypes.POINTER(vp_paged_cache_fp8), P, ctypes.c_int64, P, ctypes.c_int64, P,
+                                    ctypes.c_int64, P, P, F, ctypes.POINTER(vp_rope), P, P, I, I, I, P, P, P, P]),
+        "vp_prompt_attention_workspace_bytes": (S, [I, I, I, I, I]),
+        "vp_prompt_attention": (I, [P, ctypes.c_int64, P, ctypes.c_int64, P, ctypes.c_int64, P, I, I, I, I, I, F, P, P, P,
+                                    P, S, P]),
+        "vp_paged_attention_rows_workspace_bytes": (S, [I, I, I, I, I]),
+        "vp_paged_attention_rows": (I, [ctypes.POINTER(vp_paged_cache), P, P, P, I, I, I, F, P, P, P, P, S, P]),
+        "vp_paged_attention_rows_fp8": (I, [ctypes.POINTER(vp_paged_cache_fp8), P, P, P, I, I, I, F, P, P, P, P, S, P]),
         "vp_paged_attention_workspace_bytes": (S, [I, I, I, I]),
         "vp_paged_attention": (I, [ctypes.POINTER(vp_paged_cache), P, P, I, I, F, P, P, P, P, S, P]),
     }
@@ -529,3 +549,43 @@ def vp_paged_attention(cache: vp_paged_cache, q, kv_len, S: int, Hq: int, scale:
     _check("vp_paged_attention",
            _L.vp_paged_attention(ctypes.byref(cache), _ptr(q), _ptr(kv_len), S, Hq, scale, _ptr(gate), _ptr(out),
                                  _ptr(lse), _ptr(ws), wb, _stream(stream)))
+
+
+def vp_prompt_attention_workspace_bytes(S: int, M: int, Hq: int, Hkv: int, D: int) -> int:
+    return _L.vp_prompt_attention_workspace_bytes(S, M, Hq, Hkv, D)
+
+
+def vp_prompt_attention(q, ld_q: int, k, ld_k: int, v, ld_v: int, row_start, S: int, M: int, Hq: int, Hkv: int, D: int,
+                        scale: float, gate, out, lse, ws, stream=None, ws_bytes=None):
+    wb = ws_bytes if ws_bytes is not None else _nbytes(ws)
+    _check("vp_prompt_attention",
+           _L.vp_prompt_attention(_ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(row_start), S, M, Hq, Hkv, D, scale,
+                                  _ptr(gate), _ptr(out), _ptr(lse), _ptr(ws), wb, _stream(stream)))
+
+
+def vp_paged_attention_rows_workspace_bytes(S: int, M: int, Hq: int, Hkv: int, D: int) -> int:
+    return _L.vp_paged_attention_rows_workspace_bytes(S, M, Hq, Hkv, D)
+
+
+def vp_paged_attention_rows(cache: vp_paged_cache, q, row_start, kv_len, S: int, M: int, Hq: int, scale: float, gate, out,
+                            lse, ws, stream=None, ws_bytes=None):
+    wb = ws_bytes if ws_bytes is not None else _nbytes(ws)
+    _check("vp_paged_attention_rows",
+           _L.vp_paged_attention_rows(ctypes.byref(cache), _ptr(q), _ptr(row_start), _ptr(kv_len), S, M, Hq, scale,
+                                      _ptr(gate), _ptr(out), _ptr(lse), _ptr(ws), wb, _stream(stream)))
+
+
+def vp_paged_append_fp8(cache: vp_paged_cache_fp8, q, ld_q: int, k, ld_k: int, v, ld_v: int, q_norm, k_norm, eps: float,
+                        rope, row_start, ctx, S: int, M: int, Hq: int, q_out, kv_len=None, status=None, stream=None):
+    _check("vp_paged_append_fp8",
+           _L.vp_paged_append_fp8(ctypes.byref(cache), _ptr(q), ld_q, _ptr(k), ld_k, _ptr(v), ld_v, _ptr(q_norm),
+                                  _ptr(k_norm), eps, ctypes.byref(rope) if rope is not None else None, _ptr(row_start),
+                                  _ptr(ctx), S, M, Hq, _ptr(q_out), _ptr(kv_len), _ptr(status), _stream(stream)))
+
+
+def vp_paged_attention_rows_fp8(cache: vp_paged_cache_fp8, q, row_start, kv_len, S: int, M: int, Hq: int, scale: float,
+                                gate, out, lse, ws, stream=None, ws_bytes=None):
+    wb = ws_bytes if ws_bytes is not None else _nbytes(ws)
+    _check("vp_paged_attention_rows_fp8",
+           _L.vp_paged_attention_rows_fp8(ctypes.byref(cache), _ptr(q), _ptr(row_start), _ptr(kv_len), S, M, Hq, scale,
+                                          _ptr(gate), _ptr(out), _ptr(lse), _ptr(ws), wb, _stream(stream)))

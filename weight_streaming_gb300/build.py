@@ -1,10 +1,10 @@
 """Builds libverify.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
-Fourteen translation units are compiled in parallel (host API + packers, the streaming executor for
+Eighteen translation units are compiled in parallel (host API + packers, the streaming executor for
 8/16 token columns, the executor for 24/32 token columns, the executor with the Q4 unit, the
 sampled acceptance, the verify attention, the Gated DeltaNet scan, the decode loop, the error
-bookkeeping, the mixer cores, the block-scaled FP8 producers and linear, the paged cache's append and
-attention) and linked against the shared CUDA runtime.
+bookkeeping, the mixer cores, the block-scaled FP8 producers and linear, the paged caches' append, the
+attention of single tokens, and of several rows per sequence for each head width) and linked against the shared CUDA runtime.
 """
 from __future__ import annotations
 
@@ -33,7 +33,8 @@ VARIANTS = {"": (LIB, BUILD, []), "trace": (LIB_TRACE, BUILD_TRACE, ["-DVP_PHASE
             "waittest": (LIB_WAIT, BUILD_WAIT, ["-DVP_WAIT_TEST"]), "unitbench": (LIB_UNIT, BUILD_UNIT, [])}
 UNIT_SOURCES = ["unit_bench.cu"]
 SOURCES = ["api.cu", "exec_nt12.cu", "exec_nt34.cu", "exec_q4.cu", "sample.cu", "attention.cu", "gdn.cu",
-           "loop.cu", "errors.cu", "mixer.cu", "fp8_quant.cu", "fp8_linear.cu", "paged.cu", "paged_attention.cu"]
+           "loop.cu", "errors.cu", "mixer.cu", "fp8_quant.cu", "fp8_linear.cu", "paged.cu", "paged_attention.cu",
+           "rows_attention.cu", "rows_attention_64.cu", "rows_attention_128.cu", "rows_attention_256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

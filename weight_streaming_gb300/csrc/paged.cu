@@ -41,7 +41,9 @@ struct AppendArgs {
   int rot, interleaved;
   const int32_t *row_start, *ctx, *pages;
   int S, M, Hq, Hkv, n_pages, log_page, max_pages;
-  uint16_t *k_cache, *v_cache, *q_out;
+  void *k_cache, *v_cache;
+  uint8_t *k_scales, *v_scales;  // 8-bit cache
+  uint16_t* q_out;
   int32_t* kv_len;
   int* status;
   unsigned long long turn[kMaxPairs];  // f_j / 2 pi mod 1, in units of 2^-64
@@ -108,9 +110,86 @@ __device__ __forceinline__ void turn(float& x0, float& x1, float c, float s) {
   x1 = fmaf(a, s, b * c);
 }
 
+// ------------------------------------------------------------------ the 8-bit cache
+// A head's codes are e4m3(x / 2^e), e the smallest exponent (from kMinExp on) with max |x| <= 448 2^e: the power of two
+// costs at most one of e4m3's 17 binades and no digit, and code * 2^e is a bf16 value, so that reading the cache back
+// rounds nothing.
+constexpr int kMinExp = -118;    // codes times 2^-118 are bf16 values down to e4m3's smallest, 2^-9
+constexpr float kOpen = 0x1p-19f;  // of a pair's length: twice what norm, sine, cosine and products may be off by
+
+// e of a maximum by its bits: max = f 2^E, 1/2 <= f < 1, against 448 = 7/8 2^9.
+__device__ __forceinline__ int scale_exp(uint32_t bits) {
+  return max((int)(bits >> 23) - 126 - 9 + ((bits & 0x7FFFFF) > 0x600000), kMinExp);
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The head again in fp64, for heads whose scale or a code fp32 leaves open (next to 448 2^e, or half way between two codes):
+// the exact value's codes and exponent.  rows: raw bf16; w0, w1: weights or NULL; turn0: the row's first turn for this
+// lane's pairs (NULL: not turned); split: pairs (j, j + 4) of the lane's eight, else neighbours.
+template <int kL>
+__device__ __noinline__ int quant64(uint4 raw, const float* w0, const float* w1, float eps, const unsigned long long* turns,
+                                    unsigned long long pos, bool split, uint32_t mask, uint2& codes) {
+  double x[8];
+  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[2 * k] = __uint_as_float(in[k] << 16), x[2 * k + 1] = __uint_as_float(in[k] & 0xFFFF0000u);
+  if (w0) {
+    double ss = 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss += x[k] * x[k];
+#pragma unroll
+    for (int o = kL / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+    const double inv = 1.0 / sqrt(ss / (8 * kL) + (double)eps);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = x[k] * inv * (double)__ldg(k < 4 ? w0 + k : w1 + k - 4);
+  }
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      double s, c;
+      sincospi((double)(long long)(pos * turns[j]) * 0x1p-63, &s, &c);
+      double &p = x[split ? j : 2 * j], &q = x[split ? j + 4 : 2 * j + 1];
+      const double u = p, v = q;
+      p = u * c - v * s;
+      q = u * s + v * c;
+    }
+  }
+  double top = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = fmax(top, fabs(x[k]));
+#pragma unroll
+  for (int o = kL / 2; o; o >>= 1) top = fmax(top, __shfl_xor_sync(mask, top, o));
+  const long long b = __double_as_longlong(top);
+  const int e = max((int)(b >> 52) - 1022 - 9 + ((b & 0xFFFFFFFFFFFFFLL) > 0xC000000000000LL), kMinExp);
+  const double inv = __longlong_as_double((long long)(1023 - e) << 52);
+  float y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {  // rounded once, to a multiple of the step at its size
+    const double v = x[k] * inv;
+    const int n = max((int)(__double_as_longlong(fabs(v)) >> 52) - 1023, -6) - 3;
+    y[k] = (float)(rint(v * __longlong_as_double((long long)(1023 - n) << 52)) * __longlong_as_double((long long)(1023 + n) << 52));
+  }
+  codes.x = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
+  codes.y = e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16;
+  return e;
+}
+
+// Eight codes of a lane and, by the head's first lane, the exponent (128: NaN).
+__device__ __forceinline__ void store8(const AppendArgs& a, void* cache, uint8_t* scales, int h, int page, long long pos, int off0,
+                                       int off1, int lane, int D, uint2 codes, int ex) {
+  const size_t at = (((size_t)page * a.Hkv + h) << a.log_page) + (pos & ((1 << a.log_page) - 1));
+  uint8_t* dst = static_cast<uint8_t*>(cache) + at * D;
+  *reinterpret_cast<uint32_t*>(dst + off0) = codes.x;
+  *reinterpret_cast<uint32_t*>(dst + off1) = codes.y;
+  if (lane == 0) scales[at] = (uint8_t)(ex + 127);
+}
+
 // kB: heads per group of lanes.  Every load of the block's heads is issued first: they depend on nothing
 // that the row's position has to be looked up for.
-template <int D, int kB, bool kNorm>
+template <int D, int kB, bool kNorm, bool kFp8>
 __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kL = D / 8;                    // lanes per head
   constexpr int kGroups = kThreadsP / kL;      // heads at a time
@@ -181,8 +260,8 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
   const int head_step = D << a.log_page;  // from one head's slot to the next one's in a page
   const ptrdiff_t slot = (((ptrdiff_t)page * a.Hkv << a.log_page) + (pos & ((1 << a.log_page) - 1))) * D;
   uint16_t* q_dst = a.q_out + (size_t)r * a.Hq * D;
-  uint16_t* k_dst = a.k_cache + (slot - (ptrdiff_t)nq * head_step);
-  uint16_t* v_dst = a.v_cache + (slot - (ptrdiff_t)(nq + a.Hkv) * head_step);
+  uint16_t* k_dst = static_cast<uint16_t*>(a.k_cache) + (slot - (ptrdiff_t)nq * head_step);
+  uint16_t* v_dst = static_cast<uint16_t*>(a.v_cache) + (slot - (ptrdiff_t)(nq + a.Hkv) * head_step);
   const uint32_t mask = kL == 32 ? 0xFFFFFFFFu : ((1u << (kL & 31)) - 1) << ((tid & 31) & ~(kL - 1));
 #pragma unroll
   for (int i = 0; i < kB; ++i) {
@@ -207,7 +286,59 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
         turn(x[4], x[5], cs.z, sn.z);
         turn(x[6], x[7], cs.w, sn.w);
       }
+      if (kFp8 && isk) {
+        // codes and exponent, and whether what fp32 may be off by could change one of them
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(mask, top);
+        int ex = scale_exp(top);
+        const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+        bool open = false;
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int p = split ? e : 2 * e, q = split ? e + 4 : 2 * e + 1;  // a pair
+          const float d = (fabsf(x[p]) + fabsf(x[q])) * kOpen;
+          lo[e] = e4m3x2((x[p] - d) * inv, (x[q] - d) * inv);
+          hi[e] = e4m3x2((x[p] + d) * inv, (x[q] + d) * inv);
+          open = open || lo[e] != hi[e];
+        }
+        // 64 fp32 steps are 2^-18 to 2^-17 of the maximum, more than its pair's kOpen (at most sqrt 2 of it)
+        open = open || scale_exp(top - min(top, 64u)) != scale_exp(top + 64u);
+        uint2 codes;
+        if (split) {
+          codes.x = __byte_perm(__byte_perm(lo[0], lo[1], 0x0040), __byte_perm(lo[2], lo[3], 0x0040), 0x5410);
+          codes.y = __byte_perm(__byte_perm(lo[0], lo[1], 0x0051), __byte_perm(lo[2], lo[3], 0x0051), 0x5410);
+        } else {
+          codes.x = lo[0] | lo[1] << 16, codes.y = lo[2] | lo[3] << 16;
+        }
+        if (top >= 0x7F800000u) {  // a value that is none: the head is none
+          codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), ex = 128;
+        } else if (__any_sync(mask, open)) {
+          ex = quant64<kL>(raw[i], w ? w + off0 : nullptr, w ? w + off1 : nullptr, a.eps, turns ? a.turn + 4 * lane : nullptr,
+                           (unsigned long long)pos, split, mask, codes);
+        }
+        store8(a, a.k_cache, a.k_scales, hh - nq, page, pos, off0, off1, lane, D, codes, ex);
+        continue;
+      }
       out = pack8(x);
+    }
+    if (kFp8 && !isq) {  // values, or keys as they came: exact in fp32
+      float x[8];
+      unpack8(raw[i], x);
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+      top = __reduce_max_sync(mask, top);
+      int ex = scale_exp(top);
+      const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+      uint2 codes = make_uint2(e4m3x2(x[0] * inv, x[1] * inv) | e4m3x2(x[2] * inv, x[3] * inv) << 16,
+                               e4m3x2(x[4] * inv, x[5] * inv) | e4m3x2(x[6] * inv, x[7] * inv) << 16);
+      if (top >= 0x7F800000u) codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu), ex = 128;
+      store8(a, isk ? a.k_cache : a.v_cache, isk ? a.k_scales : a.v_scales, isk ? hh - nq : hh - nq - a.Hkv, page, pos, off0,
+             off1, lane, D, codes, ex);
+      continue;
     }
     *reinterpret_cast<uint2*>(dst + off0) = make_uint2(out.x, out.y);
     *reinterpret_cast<uint2*>(dst + off1) = make_uint2(out.z, out.w);
@@ -233,16 +364,17 @@ vp_status check_cache(const vp_paged_cache* c) {
 
 using namespace vp;
 
-extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld_q, const void* k,
-                                     int64_t ld_k, const void* v, int64_t ld_v, const float* q_norm,
-                                     const float* k_norm, float eps, const vp_rope* rope, const int32_t* row_start,
-                                     const int32_t* ctx, int S, int M, int Hq, void* q_out, int32_t* kv_len,
-                                     int* status, void* stream) {
-  vp_status st = check_cache(cache);
-  if (st != VP_OK) return st;
+namespace {
+
+// Both appends; the cache is checked.
+template <bool kFp8>
+vp_status append(const vp_paged_cache& c, uint8_t* k_scales, uint8_t* v_scales, const void* q, int64_t ld_q, const void* k,
+                 int64_t ld_k, const void* v, int64_t ld_v, const float* q_norm, const float* k_norm, float eps,
+                 const vp_rope* rope, const int32_t* row_start, const int32_t* ctx, int S, int M, int Hq, void* q_out,
+                 int32_t* kv_len, int* status, void* stream) {
+  vp_status st;
   if (!k || !v || !ctx || (q && !q_out) || kv_len == ctx) return VP_ERR_INVALID_ARG;
   if ((q_norm || k_norm) && !(eps > 0.0f && std::isfinite(eps))) return VP_ERR_INVALID_ARG;
-  const vp_paged_cache& c = *cache;
   if (M < 1 || M > (1 << 24) || S < 1 || S > 65536 || (!row_start && M != S)) return VP_ERR_SHAPE;
   const long long kd = (long long)c.Hkv * c.D, qd = (long long)Hq * c.D;
   if (ld_k < kd || ld_v < kd || ld_k > (1LL << 40) || ld_v > (1LL << 40)) return VP_ERR_SHAPE;
@@ -279,8 +411,8 @@ extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q,
   a.S = S, a.M = M, a.Hq = Hq, a.Hkv = c.Hkv, a.n_pages = c.n_pages, a.max_pages = c.max_pages;
   a.log_page = 4;
   while ((1 << a.log_page) < c.page_size) ++a.log_page;
-  a.k_cache = static_cast<uint16_t*>(c.k);
-  a.v_cache = static_cast<uint16_t*>(c.v);
+  a.k_cache = c.k, a.v_cache = c.v;
+  a.k_scales = k_scales, a.v_scales = v_scales;
   a.q_out = static_cast<uint16_t*>(q_out);
   a.kv_len = kv_len, a.status = status;
   const int heads = (q ? Hq : 0) + 2 * c.Hkv, at_once = kThreadsP / (c.D / 8);
@@ -294,9 +426,9 @@ extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q,
   auto pick = [&](auto norm) -> Kernel {
     constexpr bool N = decltype(norm)::value;
     static const Kernel kernels[3][6] = {
-        {append_kernel<64, 1, N>, append_kernel<64, 2, N>, append_kernel<64, 3, N>, append_kernel<64, 4, N>, append_kernel<64, 5, N>, append_kernel<64, 6, N>},
-        {append_kernel<128, 1, N>, append_kernel<128, 2, N>, append_kernel<128, 3, N>, append_kernel<128, 4, N>, append_kernel<128, 5, N>, append_kernel<128, 6, N>},
-        {append_kernel<256, 1, N>, append_kernel<256, 2, N>, append_kernel<256, 3, N>, append_kernel<256, 4, N>, append_kernel<256, 5, N>, append_kernel<256, 6, N>}};
+        {append_kernel<64, 1, N, kFp8>, append_kernel<64, 2, N, kFp8>, append_kernel<64, 3, N, kFp8>, append_kernel<64, 4, N, kFp8>, append_kernel<64, 5, N, kFp8>, append_kernel<64, 6, N, kFp8>},
+        {append_kernel<128, 1, N, kFp8>, append_kernel<128, 2, N, kFp8>, append_kernel<128, 3, N, kFp8>, append_kernel<128, 4, N, kFp8>, append_kernel<128, 5, N, kFp8>, append_kernel<128, 6, N, kFp8>},
+        {append_kernel<256, 1, N, kFp8>, append_kernel<256, 2, N, kFp8>, append_kernel<256, 3, N, kFp8>, append_kernel<256, 4, N, kFp8>, append_kernel<256, 5, N, kFp8>, append_kernel<256, 6, N, kFp8>}};
     return kernels[c.D == 64 ? 0 : c.D == 128 ? 1 : 2][per - 1];
   };
   const Kernel kern = (q && q_norm) || k_norm ? pick(std::true_type()) : pick(std::false_type());
@@ -304,3 +436,31 @@ extern "C" vp_status vp_paged_append(const vp_paged_cache* cache, const void* q,
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? VP_OK : cuda_fail(e);
 }
+
+}  // namespace
+
+extern "C" {
+
+vp_status vp_paged_append(const vp_paged_cache* cache, const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                          int64_t ld_v, const float* q_norm, const float* k_norm, float eps, const vp_rope* rope,
+                          const int32_t* row_start, const int32_t* ctx, int S, int M, int Hq, void* q_out, int32_t* kv_len,
+                          int* status, void* stream) {
+  const vp_status st = check_cache(cache);
+  if (st != VP_OK) return st;
+  return append<false>(*cache, nullptr, nullptr, q, ld_q, k, ld_k, v, ld_v, q_norm, k_norm, eps, rope, row_start, ctx, S, M, Hq,
+                       q_out, kv_len, status, stream);
+}
+
+vp_status vp_paged_append_fp8(const vp_paged_cache_fp8* cache, const void* q, int64_t ld_q, const void* k, int64_t ld_k,
+                              const void* v, int64_t ld_v, const float* q_norm, const float* k_norm, float eps,
+                              const vp_rope* rope, const int32_t* row_start, const int32_t* ctx, int S, int M, int Hq,
+                              void* q_out, int32_t* kv_len, int* status, void* stream) {
+  const vp_status st = check_cache_fp8(cache);
+  if (st != VP_OK) return st;
+  const vp_paged_cache c = {cache->k, cache->v, cache->pages, cache->n_pages, cache->page_size, cache->max_pages, cache->Hkv,
+                            cache->D};
+  return append<true>(c, cache->k_scales, cache->v_scales, q, ld_q, k, ld_k, v, ld_v, q_norm, k_norm, eps, rope, row_start, ctx,
+                      S, M, Hq, q_out, kv_len, status, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,50 @@
+// Attention of several new rows per sequence (vp_prompt_attention, vp_paged_attention_rows and its form over an 8-bit
+// cache): what the host side (rows_attention.cu) and the kernel's instantiations (rows_attention_*.cu) share.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace vp {
+
+enum RowsSource : int { kDense = 0, kPaged = 1, kPagedFp8 = 2 };
+
+constexpr int kRowsGrid = 152;  // CTAs at most: one per SM
+
+struct RowsArgs {
+  const uint16_t *q, *gate;
+  uint16_t* out;
+  float* lse;
+  long long ld_q;
+  const int32_t *row_start, *kv_len, *pages;  // row_start NULL: one row per sequence; kv_len NULL: the rows themselves
+  const uint8_t *k_scales, *v_scales;         // 8-bit cache: one exponent byte per slot and head
+  int S, M, Hq, Hkv, G;
+  int n_pages, log_page, max_pages;
+  int tok_tile;                // tokens of an item: its rows / G
+  uint32_t q_and, q_flip;      // on the queries' bf16 pairs: the scale's zero and sign
+  float scale2;                // |scale| * log2(e), 1 for scale 0
+  int4* desc;                  // [grid][2]: s, h, first token (-1: no part), rows | ends << 16 (below)
+  float* part_ml;              // [grid][2][256][2]: maximum (log2 units), sum
+  float* part_o;               // [grid][2][D / 4][rows][4]
+  int* status;
+};
+
+// A part's descriptor word w: its rows, and whether the item ends with it.
+constexpr int kPartEnds = 1 << 16;
+
+template <int D, int kTiles>
+cudaError_t launch_rows(const RowsArgs& a, int source, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
+                        cudaStream_t s);
+
+extern template cudaError_t launch_rows<64, 1>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_rows<64, 2>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_rows<128, 1>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_rows<128, 2>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_rows<256, 1>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+
+// Key rows of a tile (the tensor map's box, too).
+constexpr int rows_block(int D) { return D == 256 ? 64 : 128; }
+
+}  // namespace vp

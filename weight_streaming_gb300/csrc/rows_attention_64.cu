@@ -1,0 +1,7 @@
+// Heads of 64 columns (see rows_attention.cu).
+#include "rows_attention.cuh"
+
+namespace vp {
+template cudaError_t launch_rows<64, 1>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+template cudaError_t launch_rows<64, 2>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+}  // namespace vp
