@@ -160,6 +160,8 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   // are on the device) one tile has a second score buffer instead.
   const int tiles = x.D == 256 || (long long)x.M * a.G <= 128LL * x.S ? 1 : 2;
   a.tok_tile = 128 * tiles / a.G;
+  a.g_inv = (65536 + a.G - 1) / a.G;
+  a.item_cost = 256;
   const int grid = std::min(sms, kRowsGrid);
   cudaError_t e;
   if (x.D == 256)

@@ -135,6 +135,11 @@ __device__ __forceinline__ float ra_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float ra_max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint64_t ra_pair(float lo, float hi) {
   uint64_t p;
   asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
@@ -163,6 +168,15 @@ __device__ __forceinline__ uint32_t ra_bmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// Two e4m3 codes (bytes 0, 1 with 0x9180, bytes 2, 3 with 0xB3A2: each and its sign, eight times) as bf16 bits of their values
+// times 2^-120: the sign, then exponent and digits three places below.  (0x7F is not told apart: 480.)
+template <uint32_t kSel>
+__device__ __forceinline__ uint32_t ra_code2(uint32_t w) {
+  uint32_t x;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(w), "n"(kSel));
+  return (x << 4) & 0x87F087F0u;
+}
+__device__ __forceinline__ void ra_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint4 ra_ldg128(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -195,6 +209,72 @@ __device__ __forceinline__ float ra_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// One tile of codes (rows of D bytes, then a scale byte per row) to a bf16 operand tile, by 128 threads.  Eight lanes take 64
+// codes of each of two rows, of neighbouring column groups where there are several: reads and writes then meet every bank
+// once.  kLook: rows from `left` on and those of `bad` groups of 16 become zeros (weights of zero times what lies there), and
+// where poison is given infinite and NaN values do, with their key noted there by column.
+template <int D, int BN, bool kLook>
+__device__ __forceinline__ void ra_expand(uint32_t src, uint32_t dst, int tid, int left, uint32_t bad, int key0, int* poison) {
+  constexpr int kChunks = D / 64, kUnits = BN * D / 16 / 128, kAtOnce = 4;
+  const int rsel = tid >> 2 & 1, i = tid & 3;
+#pragma unroll 1
+  for (int u0 = 0; u0 < kUnits; u0 += kAtOnce) {
+    uint4 w[kAtOnce];
+    uint32_t e[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int qd = (tid >> 3) + 16 * (u0 + k), row = 2 * (qd / kChunks) + rsel, ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
+      w[k] = lds128(src + row * D + ch * 64 + i * 16);
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[k]) : "r"(src + BN * D + row));
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int qd = (tid >> 3) + 16 * (u0 + k), row = 2 * (qd / kChunks) + rsel, ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
+      const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      // 2^(120 + scale - 127) at once where that is a bf16 value, else in two steps
+      const uint32_t f = e[k] > 134 ? 0x7B807B80u : (e[k] + 120) * 0x00800080u;
+      uint32_t o[8], nan = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        o[2 * x] = ra_bmul2(ra_code2<0x9180>(in[x]), f);
+        o[2 * x + 1] = ra_bmul2(ra_code2<0xB3A2>(in[x]), f);
+        nan |= (in[x] & 0x7F7F7F7Fu) + 0x01010101u;
+      }
+      if (e[k] > 134) {
+        const uint32_t f2 = e[k] == 255 ? 0x7FC07FC0u : e[k] * 0x00800080u;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[x] = ra_bmul2(o[x], f2);
+      }
+      if (nan & 0x80808080u) {  // codes 0x7F
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t two = in[x >> 1] >> (x & 1 ? 16 : 0);
+          if ((two & 0x7F) == 0x7F) o[x] |= 0x7FC0u;
+          if ((two & 0x7F00) == 0x7F00) o[x] |= 0x7FC00000u;
+        }
+      }
+      if (kLook) {
+        if (row >= left || (bad >> (row >> 4) & 1)) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) o[x] = 0;
+        }
+        if (poison) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint32_t z = ra_special(o[x]);
+            const int d = ch * 64 + i * 16 + 2 * x;
+            if (z & 0x8000u) atomicMin(poison + d, key0 + row), o[x] &= 0xFFFF0000u;
+            if (z & 0x80000000u) atomicMin(poison + d + 1, key0 + row), o[x] &= 0x0000FFFFu;
+          }
+        }
+      }
+      const uint32_t out = dst + ch * (BN * 128) + row * 128, sw = row & 7;
+      sts128(out + (((2 * i) ^ sw) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+      sts128(out + (((2 * i + 1) ^ sw) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+    }
+  }
+}
+
 // ------------------------------------------------------------------ work
 // A sequence: n new rows from row0 on, which see the L cached positions up to their own.  A bad one (lengths that do not
 // fit) has L = 0 and outputs of zero.
@@ -220,20 +300,19 @@ __device__ __forceinline__ RaSeq ra_seq(const RowsArgs& a, int s) {
   return q;
 }
 // The work is one line: for every sequence, key-value head and item (tok_tile tokens) in turn, the item's keys and
-// kItemCost.  Its blocks lie at multiples of kBlock keys from the item's start; a CTA owns the blocks that begin
+// item_cost.  Its blocks lie at multiples of kBlock keys from the item's start; a CTA owns the blocks that begin
 // in its part of the line.
-constexpr int kItemCost = 128;  // starting and ending an item, in keys
 constexpr int kMinKeys = 256;   // of the line per CTA at least
 
 // The line up to item t of one head.
 __device__ __forceinline__ long long ra_upto(const RowsArgs& a, const RaSeq& q, int t) {
-  if (q.bad) return (long long)t * kItemCost;
-  return (long long)t * (q.L - q.n + kItemCost) + (long long)a.tok_tile * ((long long)t * (t + 1) / 2);
+  if (q.bad) return (long long)t * a.item_cost;
+  return (long long)t * (q.L - q.n + a.item_cost) + (long long)a.tok_tile * ((long long)t * (t + 1) / 2);
 }
 __device__ __forceinline__ int ra_items(const RowsArgs& a, const RaSeq& q) { return (q.n + a.tok_tile - 1) / a.tok_tile; }
 __device__ __forceinline__ long long ra_line(const RowsArgs& a, const RaSeq& q) {
   if (q.n == 0) return 0;
-  return ra_upto(a, q, ra_items(a, q) - 1) + q.L + kItemCost;
+  return ra_upto(a, q, ra_items(a, q) - 1) + q.L + a.item_cost;
 }
 
 // One piece of work, in shared memory: blocks b0 .. b1 - 1 of an item.
@@ -267,7 +346,7 @@ struct RaCfg {
   static constexpr int kColO = 2 * kColS;
   static constexpr int kColQ = kColO + D;                            // one tile
   // registers: what issues or copies keeps few, the softmax warps take the rest of the launch's
-  static constexpr int kRegLow = kTiles == 2 ? 72 : 120, kRegHigh = kTiles == 2 ? 184 : 232;
+  static constexpr int kRegLow = kTiles == 2 ? 64 : 120, kRegHigh = kTiles == 2 ? 192 : 232;
   static_assert(kTiles == 2 ? 8 * kRegLow + 8 * kRegHigh <= 16 * 128 : 8 * kRegLow + 4 * kRegHigh <= 12 * 168, "");
   static_assert(kColO + kTiles * D <= 512 && (kTiles == 2 || kColQ + D / 2 <= 512), "");
 };
@@ -395,6 +474,11 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     if (__all_sync(0xFFFFFFFFu, ra_try(b, parity))) return true;
     return ra_wait_slow(b, parity, &sh.abort, a.status);
   };
+  auto wait2 = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) -> bool {
+    const bool one = ra_try(smem_addr(bar), parity), two = ra_try(smem_addr(bar2), parity2);
+    if (__all_sync(0xFFFFFFFFu, one && two)) return true;
+    return wait(bar, parity) && wait(bar2, parity2);
+  };
   // The it-th item, for every role but the scheduler; null when a wait ran out.
   auto get = [&](int it) -> const RaItem* {
     if (!wait(&sh.ifull[it % C::kRing], (it / C::kRing) & 1)) return nullptr;
@@ -481,7 +565,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           if (lane == 0 && !(hook == 5 && it == 0)) ra_arrive(smem_addr(&sh.ifull[slot]));
           ++it;
         }
-        at += keys + kItemCost;
+        at += keys + a.item_cost;
         if (++t == items) {
           t = 0;
           if (++h == a.Hkv) h = 0, ++s;
@@ -716,6 +800,12 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         if (!pi || pi->s < 0) break;
         const int b0 = pi->b0, b1 = pi->b1, edge = pi->edge, keys = pi->keys;
         int* const poison = sh.poison[it % C::kRing];
+        // The item's queries and gates on their way to L2, ahead of the warps that read them.
+        for (int u = tid; u < pi->toks * a.G * kChunks; u += 128) {
+          const int row = u / kChunks, t = row * a.g_inv >> 16, hd = pi->h * a.G + row - t * a.G;
+          if (it > 0) ra_prefetch(a.q + (size_t)(pi->row + t) * a.ld_q + (size_t)hd * D + u % kChunks * 64);
+          if (a.gate) ra_prefetch(a.gate + ((size_t)(pi->row + t) * a.Hq + hd) * D + u % kChunks * 64);
+        }
         for (int b = b0; ok && b < b1; ++b, ++g) {
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
@@ -726,64 +816,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               if (!(ok = wait(&sh.empty[st], wpar))) break;
               const uint32_t src = raw + rst * C::kRaw, dst = ring + st * C::kTile;
               const uint32_t bad = kv ? sh.bad[g & 15] : 0;
-#pragma unroll 2
-              for (int u = tid; u < BN * D / 16; u += 128) {
-                // eight lanes take 64 codes of each of two rows, of neighbouring column groups where there are several:
-                // reads and writes then meet every bank once
-                const int qd = u >> 3, rsel = u >> 2 & 1, i = u & 3;
-                const int pair = qd / kChunks, x = qd % kChunks, row = 2 * pair + rsel, ch = kChunks > 1 ? x ^ rsel : 0;
-                uint4 w = lds128(src + row * D + ch * 64 + i * 16);
-                uint32_t e;
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(src + BN * D + row));
-                // a code's bits as bf16 are the code's value times 2^-120
-                uint32_t f = e > 134 ? 0x7B807B80u : (e + 120) * 0x00800080u;
-                const uint32_t f2 = e == 255 ? 0x7FC07FC0u : e * 0x00800080u;
-                uint32_t in[4] = {w.x, w.y, w.z, w.w}, o[8];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t lo = __byte_perm(in[k], 0, 0x1404), hi = __byte_perm(in[k], 0, 0x3424);
-                  o[2 * k] = ra_bmul2((lo & 0x80008000u) | ((lo >> 4) & 0x07F007F0u), f);
-                  o[2 * k + 1] = ra_bmul2((hi & 0x80008000u) | ((hi >> 4) & 0x07F007F0u), f);
-                }
-                if (e > 134) {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) o[k] = ra_bmul2(o[k], f2);
-                }
-                uint32_t nan = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) nan |= ((in[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                if (nan) {  // codes 0x7F
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const uint32_t two = in[k >> 1] >> (k & 1 ? 16 : 0);
-                    if ((two & 0x7F) == 0x7F) o[k] |= 0x7FC0u;
-                    if ((two & 0x7F00) == 0x7F00) o[k] |= 0x7FC00000u;
-                  }
-                }
-                if (kv) {
-                  if (row >= left || (bad >> (row >> 4) & 1)) {  // weights of zero times what lies there
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = 0;
-                  }
-                  if (look) {
-                    uint32_t sp = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) sp |= ra_special(o[k]);
-                    if (sp) {
-#pragma unroll
-                      for (int k = 0; k < 8; ++k) {
-                        const uint32_t z = ra_special(o[k]);
-                        const int d = ch * 64 + i * 16 + 2 * k, key = b * BN + row;
-                        if (z & 0x8000u) atomicMin(poison + d, key), o[k] &= 0xFFFF0000u;
-                        if (z & 0x80000000u) atomicMin(poison + d + 1, key), o[k] &= 0x0000FFFFu;
-                      }
-                    }
-                  }
-                }
-                const uint32_t out = dst + ch * kGroup + row * 128, sw = row & 7;
-                sts128(out + (((2 * i) ^ sw) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-                sts128(out + (((2 * i + 1) ^ sw) << 4), make_uint4(o[4], o[5], o[6], o[7]));
-              }
+              if (look || bad)
+                ra_expand<D, BN, true>(src, dst, tid, left, bad, b * BN, look ? poison : nullptr);
+              else
+                ra_expand<D, BN, false>(src, dst, tid, left, bad, 0, nullptr);
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -844,34 +880,51 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     int g = 0, npv = 0;  // blocks (one tile: of the score buffers) and outputs so far
     bool ok = true;
 
+    const int first_tok = (w * 128 + quad * 32) / a.G;  // of the warp's rows; a warp without rows passes the scores through
     auto load_q = [&](const RaItem& i) {
-      const bool there = tok < i.toks;
-      const uint16_t* src = a.q + (size_t)(i.row + (there ? tok : 0)) * a.ld_q + (size_t)(i.h * a.G + head) * D;
-#pragma unroll 1
-      for (int ch = 0; ch < kChunks; ++ch) {
-        uint32_t x[32];
+      if (first_tok < i.toks) {
+        if constexpr (kTiles == 2) {  // a row's lanes together
+          constexpr int kLanes = D / 8, kAt = 32 / kLanes;
+          uint4 v[kLanes];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (there) v = ra_ldg128(src + ch * 64 + k * 8);
-          x[4 * k] = (v.x & a.q_and) ^ a.q_flip, x[4 * k + 1] = (v.y & a.q_and) ^ a.q_flip;
-          x[4 * k + 2] = (v.z & a.q_and) ^ a.q_flip, x[4 * k + 3] = (v.w & a.q_and) ^ a.q_flip;
-        }
-        __syncwarp();
-        if constexpr (kTiles == 2) {
-          const uint32_t dst = q_s + w * 128 * D * 2 + ch * 16384 + rr * 128;
+          for (int k = 0; k < kLanes; ++k) {
+            const int row = w * 128 + quad * 32 + k * kAt + lane / kLanes, t = row * a.g_inv >> 16, hd = row - t * a.G;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (t < i.toks)
+              v[k] = ra_ldg128(a.q + (size_t)(i.row + t) * a.ld_q + (size_t)(i.h * a.G + hd) * D + lane % kLanes * 8);
+          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            sts128(dst + ((k ^ (rr & 7)) << 4), make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+          for (int k = 0; k < kLanes; ++k) {
+            const int row = quad * 32 + k * kAt + lane / kLanes, piece = lane % kLanes;
+            v[k].x = (v[k].x & a.q_and) ^ a.q_flip, v[k].y = (v[k].y & a.q_and) ^ a.q_flip;
+            v[k].z = (v[k].z & a.q_and) ^ a.q_flip, v[k].w = (v[k].w & a.q_and) ^ a.q_flip;
+            sts128(q_s + w * 128 * D * 2 + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4), v[k]);
+          }
+          fence_proxy_async_smem();
         } else {
-          ra_st32(lanes + C::kColQ + ch * 32, x);
+          const bool there = tok < i.toks;
+          const uint16_t* src = a.q + (size_t)(i.row + (there ? tok : 0)) * a.ld_q + (size_t)(i.h * a.G + head) * D;
+          uint4 v[D / 8];
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) {
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (there) v[k] = ra_ldg128(src + k * 8);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int ch = 0; ch < kChunks; ++ch) {
+            uint32_t x[32];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint4 u = v[ch * 8 + k];
+              x[4 * k] = (u.x & a.q_and) ^ a.q_flip, x[4 * k + 1] = (u.y & a.q_and) ^ a.q_flip;
+              x[4 * k + 2] = (u.z & a.q_and) ^ a.q_flip, x[4 * k + 3] = (u.w & a.q_and) ^ a.q_flip;
+            }
+            ra_st32(lanes + C::kColQ + ch * 32, x);
+          }
+          tmem_wait_st();
+          tmem_fence_before();
         }
-      }
-      if constexpr (kTiles == 2) {
-        fence_proxy_async_smem();
-      } else {
-        tmem_wait_st();
-        tmem_fence_before();
       }
       __syncwarp();
       if (lane == 0) ra_arrive(smem_addr(&sh.qfull[w]));
@@ -888,15 +941,26 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       const int b0 = pi->b0, cnt = pi->cnt[w], nblk = pi->b1 - b0;
       const int lim = tok < pi->toks ? min(pi->lim0 + tok, pi->keys) : pi->keys;  // keys that this row sees
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
+      const bool idle = first_tok >= pi->toks;
       float m = -INFINITY, mc = 0.0f;  // reference of the exponents (log2 units), and what is subtracted
       uint64_t l2[2] = {0, 0};         // sums of the weights
       for (int j = 0; j < cnt; ++j) {
         const int buf = kTiles == 2 ? w : (g + j) & 1;
         const uint32_t sp = kTiles == 2 ? (uint32_t)(npv & 1) : (uint32_t)((g + j) >> 1 & 1);
-        if (!(ok = wait(&sh.sfull[buf], sp))) break;
-        // Every phase of the outputs' barriers is waited for in turn: a wait tells a phase from the one before it only.  These
-        // outputs (the last ones on their barrier) come before these scores: no time passes here.
-        if (j >= 3 - kTiles && !(ok = outputs_of(g + j - (3 - kTiles), npv - 1))) break;
+        // Every phase of the outputs' barriers is waited for in turn: a wait tells a phase from the one before it only.  The
+        // last outputs on the barrier come before these scores: no time passes for them.
+        if (j >= 3 - kTiles)
+          ok = kTiles == 1 ? wait2(&sh.sfull[buf], sp, &sh.ofull[buf], (g + j - 2) >> 1 & 1) : wait2(&sh.sfull[buf], sp, &sh.ofull[w], (npv - 1) & 1);
+        else
+          ok = wait(&sh.sfull[buf], sp);
+        if (!ok) break;
+        if (idle) {  // no row of the warp is there: whatever the products make of the scores is not read
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) ra_arrive(smem_addr(&sh.pfull[buf]));
+          ++npv;
+          continue;
+        }
         tmem_fence_after();
         const uint32_t ts = lanes + buf * C::kColS;
         uint32_t x[BN];
@@ -912,14 +976,12 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           for (int k = 0; k < BN; ++k)
             if (k >= sees || (bad >> (k >> 4) & 1)) x[k] = 0xFF800000u;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4];
 #pragma unroll
-        for (int k = 0; k < BN; k += 8) {
+        for (int e = 0; e < 4; ++e) mx[e] = ra_max3(__uint_as_float(x[3 * e]), __uint_as_float(x[3 * e + 1]), __uint_as_float(x[3 * e + 2]));
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[k + e]), __uint_as_float(x[k + 4 + e])));
-        }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+        for (int k = 12; k + 1 < BN; k += 2) mx[k / 2 % 4] = ra_max3(mx[k / 2 % 4], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        const float top = fmaxf(ra_max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale2;
         // The reference follows the maximum only where that has grown by 2^8: a weight may reach 2^8, which costs bf16
         // nothing, and the outputs are seldom scaled again.
         const bool grow = top > m + 8.0f || (m == -INFINITY && top > m);
@@ -971,6 +1033,16 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       if (!next) break;
       if (next->s >= 0 && next->cnt[w] > 0) load_q(*next);
       // ---- the item's outputs
+      const bool there = tok < pi->toks;
+      const int slot = pi->slot;
+      const bool special = pi->b1 > pi->edge;  // the piece has edge blocks
+      const int* const poison = sh.poison[it % C::kRing];
+      const size_t orow = (size_t)(pi->row + (there ? tok : 0)) * a.Hq + pi->h * a.G + head;
+      uint4 gt[4];  // the gates are loaded a step ahead
+      if (a.gate && there && slot < 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gt[k] = ra_ldg128(a.gate + orow * D + 8 * k);
+      }
       if (cnt > 0) {
         if (kTiles == 1 && cnt > 1 && !(ok = outputs_of(g - 2, 0))) break;
         if (!(ok = outputs_of(g - 1, npv - 1))) break;
@@ -980,16 +1052,11 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       ra_unpair(l2[0], s0, s1);
       ra_unpair(l2[1], s2, s3);
       const float l = (s0 + s1) + (s2 + s3);
-      const bool there = tok < pi->toks;
-      const int slot = pi->slot;
-      const bool special = pi->b1 > pi->edge;  // the piece has edge blocks
-      const int* const poison = sh.poison[it % C::kRing];
-      const size_t orow = (size_t)(pi->row + (there ? tok : 0)) * a.Hq + pi->h * a.G + head;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const uint32_t to_ = lanes + C::kColO + w * D;
       const size_t ps = (size_t)c * 2 + max(slot, 0);
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
+      for (int d = 0; d < D && !idle; d += 32) {
         uint32_t y[32];
         if (cnt > 0) {
           ra_ld32(to_ + d, y);
@@ -1016,7 +1083,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(y[8 * k + e]) * inv;
-            if (a.gate) ra_gate(v, ra_ldg128(a.gate + orow * D + d + 8 * k));
+            if (a.gate) {
+              ra_gate(v, gt[k]);
+              if (d + 32 < D) gt[k] = ra_ldg128(a.gate + orow * D + d + 32 + 8 * k);
+            }
             *reinterpret_cast<uint4*>(o + 8 * k) =
                 make_uint4(ra_bf16x2(v[0], v[1]), ra_bf16x2(v[2], v[3]), ra_bf16x2(v[4], v[5]), ra_bf16x2(v[6], v[7]));
           }
