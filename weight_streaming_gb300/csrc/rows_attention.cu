@@ -115,9 +115,17 @@ RowsWs rows_ws(int D) {
   w.desc = kServeData;
   w.part_ml = w.desc + sizeof(int4) * kRowsGrid * 2;
   w.part_o = w.part_ml + sizeof(float) * kRowsGrid * 2 * 256 * 2;
-  w.total = w.part_o + sizeof(float) * kRowsGrid * 2 * (size_t)(D == 256 ? 128 : 256) * D;
+  w.total = w.part_o + sizeof(float) * kRowsGrid * 2 * (size_t)(D == 256 ? 128 : 256) * D;  // a pair: 256 rows
   return w;
 }
+
+// Two tiles of 128 rows share every key and value that is read; where a sequence has fewer rows (on average: the lengths are
+// on the device) one tile does, with a second score buffer.
+int rows_tiles(int S, int M, int Hq, int Hkv) { return (long long)M * (Hq / Hkv) <= 128LL * S ? 1 : 2; }
+
+// Rows and columns of the key (0) and value (1) tiles.
+int tile_rows(int D, int tiles, int kv) { return kv ? rows_block(D, tiles) : rows_key_rows(D, tiles); }
+int tile_cols(int D, int tiles, int kv) { return kv ? rows_value_cols(D, tiles) : D; }
 
 // What the three calls share: the arguments that they have in common, checked, and the launches.
 struct Common {
@@ -156,22 +164,20 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   a.part_ml = reinterpret_cast<float*>(b + w.part_ml);
   a.part_o = reinterpret_cast<float*>(b + w.part_o);
   a.status = reinterpret_cast<int*>(b);
-  // Two tiles of 128 rows share every key and value that is read; where a sequence has fewer rows (on average: the lengths
-  // are on the device) one tile has a second score buffer instead.
-  const int tiles = x.D == 256 || (long long)x.M * a.G <= 128LL * x.S ? 1 : 2;
+  const int tiles = rows_tiles(x.S, x.M, x.Hq, x.Hkv);
   a.tok_tile = 128 * tiles / a.G;
   a.g_inv = (65536 + a.G - 1) / a.G;
   a.item_cost = 256;
   const int grid = std::min(sms, kRowsGrid);
   cudaError_t e;
   if (x.D == 256)
-    e = launch_rows<256, 1>(a, source, kmap, vmap, grid, s);
+    e = tiles == 2 ? launch_rows<256, 2>(a, source, kmap, vmap, grid, s) : launch_rows<256, 1>(a, source, kmap, vmap, grid, s);
   else if (x.D == 128)
     e = tiles == 2 ? launch_rows<128, 2>(a, source, kmap, vmap, grid, s) : launch_rows<128, 1>(a, source, kmap, vmap, grid, s);
   else
     e = tiles == 2 ? launch_rows<64, 2>(a, source, kmap, vmap, grid, s) : launch_rows<64, 1>(a, source, kmap, vmap, grid, s);
   if (e != cudaSuccess) return cuda_fail(e);
-  const dim3 jg((unsigned)grid, kJoinRows);
+  const dim3 jg((unsigned)(x.D == 256 && tiles == 2 ? grid / 2 : grid), kJoinRows);
   if (x.D == 256)
     join_kernel<256><<<jg, kJoinThreads, 0, s>>>(a, 128 * tiles);
   else if (x.D == 128)
@@ -224,10 +230,11 @@ vp_status vp_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_
   if ((st = tensor_map_encoder(&encode)) != VP_OK) return st;
   // rows of [Hkv D / 64][64]: a box is a block's rows of one head, its 64-column groups one behind the other
   CUtensorMap maps[2];
+  const int tiles = rows_tiles(S, M, Hq, Hkv);
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t dims[3] = {64, (cuuint64_t)M, (cuuint64_t)(kd / 64)};
     const cuuint64_t strides[2] = {(cuuint64_t)(i ? ld_v : ld_k) * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows_block(D), (cuuint32_t)D / 64}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)tile_rows(D, tiles, i), (cuuint32_t)tile_cols(D, tiles, i) / 64}, step[3] = {1, 1, 1};
     if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(i ? v : k), dims, strides, box, step,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -259,12 +266,13 @@ vp_status vp_paged_attention_rows(const vp_paged_cache* cache, const void* q, co
   if ((st = tensor_map_encoder(&encode)) != VP_OK) return st;
   // as [D / 64][rows of all pages and heads][64]: a box is a block's rows, or a page's where pages are shorter (one
   // 64-column group of it then: the next one lies a block's rows further on in shared memory)
-  const int rows = std::min(c.page_size, rows_block(c.D));
+  const int tiles = rows_tiles(S, M, Hq, c.Hkv);
   CUtensorMap maps[2];
   for (int i = 0; i < 2; ++i) {
+    const int all = tile_rows(c.D, tiles, i), rows = std::min(c.page_size, all);
     const cuuint64_t dims[3] = {64, (cuuint64_t)c.n_pages * c.Hkv * c.page_size, (cuuint64_t)c.D / 64};
     const cuuint64_t strides[2] = {(cuuint64_t)c.D * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows, rows == rows_block(c.D) ? (cuuint32_t)c.D / 64 : 1u}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, rows == all ? (cuuint32_t)tile_cols(c.D, tiles, i) / 64 : 1u}, step[3] = {1, 1, 1};
     if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i ? c.v : c.k, dims, strides, box, step,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -291,10 +299,11 @@ vp_status vp_paged_attention_rows_fp8(const vp_paged_cache_fp8* cache, const voi
   if ((st = device_sm_count(&sms)) != VP_OK) return st;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   if ((st = tensor_map_encoder(&encode)) != VP_OK) return st;
-  CUtensorMap maps[2];  // rows of D codes; a box is a block's rows, or a page's
+  const int tiles = rows_tiles(S, M, Hq, c.Hkv);
+  CUtensorMap maps[2];  // rows of D codes; a box is a tile's rows, or a page's
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t dims[2] = {(cuuint64_t)c.D, (cuuint64_t)c.n_pages * c.Hkv * c.page_size}, strides[1] = {(cuuint64_t)c.D};
-    const cuuint32_t box[2] = {(cuuint32_t)c.D, (cuuint32_t)std::min(c.page_size, rows_block(c.D))}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)tile_cols(c.D, tiles, i), (cuuint32_t)std::min(c.page_size, tile_rows(c.D, tiles, i))}, step[2] = {1, 1};
     if (encode(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, i ? c.v : c.k, dims, strides, box, step,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)

@@ -22,28 +22,66 @@ __device__ __forceinline__ bool ra_elect() {
 __device__ __forceinline__ void ra_arrive(uint32_t bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar) : "memory");
 }
+// An arrival at the barrier's copy in the pair's first CTA, after this thread's work.
+__device__ __forceinline__ void ra_arrive_first(uint32_t bar, uint32_t rank = 0) {
+  asm volatile(
+      "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, %1;\n mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a]; }" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+// One poll of at most 20 us.  kPair: the arrivals may come from the pair's other CTA.
+template <bool kPair>
 __device__ __forceinline__ bool ra_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-               : "=r"(ok)
-               : "r"(bar), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
-// The rest of a bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.
-__device__ __forceinline__ bool ra_wait_slow(uint32_t bar, uint32_t parity, int* abort, int* status) {
-  for (uint32_t i = 0; i < kMbarPolls; ++i) {
-    uint32_t ok;
+  if constexpr (kPair)
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+  else
     asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                  : "=r"(ok)
                  : "r"(bar), "r"(parity), "r"(20000u)
                  : "memory");
-    if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
+  return ok != 0;
+}
+// A bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.
+template <bool kPair>
+__device__ __forceinline__ bool ra_wait(uint32_t bar, uint32_t parity, int* abort, int* status) {
+  uint32_t left = kMbarPolls;
+  while (!__all_sync(0xFFFFFFFFu, ra_try<kPair>(bar, parity))) {
     if (__any_sync(0xFFFFFFFFu, *(volatile int*)abort)) return false;
+    if (--left == 0) {
+      *(volatile int*)abort = 1;
+      atomicExch(status, (int)VP_ERR_TIMEOUT);
+      return false;
+    }
   }
-  *(volatile int*)abort = 1;
-  atomicExch(status, (int)VP_ERR_TIMEOUT);
-  return false;
+  return true;
+}
+// The same without ordering this thread's memory accesses (what it announces lies in tensor memory, or is another's).
+__device__ __forceinline__ void ra_arrive_first_relaxed(uint32_t bar) {
+  asm volatile(
+      "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0;\n mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a]; }" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t ra_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void ra_pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of the shared memory of the pair's CTA `rank`, at this CTA's address.
+__device__ __forceinline__ int ra_ld_pair(const void* p, uint32_t rank) {
+  int v;
+  asm volatile("{ .reg .b32 a; mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.s32 %0, [a]; }"
+               : "=r"(v)
+               : "r"(smem_addr(p)), "r"(rank)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void ra_tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile(
@@ -57,6 +95,22 @@ __device__ __forceinline__ void ra_tma_3d(uint32_t dst, const CUtensorMap* map, 
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Into this CTA's shared memory, completing on a barrier of the pair's first CTA.
+__device__ __forceinline__ void ra_tma_3d_first(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{ .reg .b32 a; mapa.shared::cluster.u32 a, %5, 0;\n"
+      " cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
+      "[a]; }" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void ra_expect_first(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0;\n"
+      " mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [a], %1; }" ::"r"(bar),
+      "r"(bytes)
       : "memory");
 }
 __device__ __forceinline__ void ra_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -74,23 +128,50 @@ __device__ __forceinline__ uint64_t ra_desc_mn(uint32_t addr, uint32_t group) {
   return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(group >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
-// D(tensor memory) (+)= A B: A in shared memory, or in tensor memory.
+// D(tensor memory) (+)= A B: A in shared memory, or in tensor memory.  kPair: 256 rows, 128 in each CTA, which also holds half
+// of B; issued by the first CTA.
+template <bool kPair>
 __device__ __forceinline__ void ra_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
+template <bool kPair>
 __device__ __forceinline__ void ra_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
+// Arrives on `bar` (in both CTAs of a pair) when every product issued so far by this thread has ended.
+template <bool kPair>
 __device__ __forceinline__ void ra_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 // 32 columns of the warp's lanes: load, the wait that ties the loaded registers to it, and store.
 __device__ __forceinline__ void ra_ld32(uint32_t t, uint32_t* r) {
@@ -128,6 +209,15 @@ __device__ __forceinline__ void ra_st16(uint32_t t, const uint32_t* r) {
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
+      : "memory");
+}
+__device__ __forceinline__ void ra_ld16(uint32_t t, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(t)
       : "memory");
 }
 __device__ __forceinline__ float ra_ex2(float x) {
@@ -185,92 +275,117 @@ __device__ __forceinline__ uint4 ra_ldg128(const void* p) {
 // Whether one of a pair's bf16 values is infinite or NaN: the exponent's ones carry into the sign.
 __device__ __forceinline__ uint32_t ra_special(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
-// v *= sigmoid(g) for eight bf16 gates.  Below zero by half the exponential twice: e^g itself leaves fp32's range long
-// before the product does.
+// v *= sigmoid(g) for two bf16 gates.
 __device__ __forceinline__ void ra_gate2(float& v0, float& v1, uint32_t w) {
   constexpr float kLog2e = 1.4426950408889634f;
-  const float g[2] = {__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
-  float* const v[2] = {&v0, &v1};
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const float h = ra_ex2(-0.5f * kLog2e * fabsf(g[e]));  // NaN stays NaN
-    const float den = fmaf(h, h, 1.0f);
-    *v[e] = __fdividef(g[e] < 0.0f ? *v[e] * h * h : *v[e], den);
+  const float g0 = __uint_as_float(w << 16), g1 = __uint_as_float(w & 0xFFFF0000u);
+  if (fminf(g0, g1) > -60.0f) {
+    v0 = __fdividef(v0, 1.0f + ra_ex2(-kLog2e * g0));
+    v1 = __fdividef(v1, 1.0f + ra_ex2(-kLog2e * g1));
+  } else {  // by half the exponential twice: e^g itself leaves fp32's range long before the product does (NaN stays NaN)
+    const float h0 = ra_ex2(-0.5f * kLog2e * fabsf(g0)), h1 = ra_ex2(-0.5f * kLog2e * fabsf(g1));
+    v0 = (g0 < 0.0f ? v0 * h0 * h0 : v0) / fmaf(h0, h0, 1.0f);
+    v1 = (g1 < 0.0f ? v1 * h1 * h1 : v1) / fmaf(h1, h1, 1.0f);
   }
-}
-__device__ __forceinline__ void ra_gate(float (&v)[8], uint4 w) {
-  ra_gate2(v[0], v[1], w.x);
-  ra_gate2(v[2], v[3], w.y);
-  ra_gate2(v[4], v[5], w.z);
-  ra_gate2(v[6], v[7], w.w);
 }
 // log sum exp from the reference in log2 units and the sum of 2^(t - m).
 __device__ __forceinline__ float ra_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// One tile of codes (rows of D bytes, then a scale byte per row) to a bf16 operand tile, by 128 threads.  Eight lanes take 64
-// codes of each of two rows, of neighbouring column groups where there are several: reads and writes then meet every bank
-// once.  kLook: rows from `left` on and those of `bad` groups of 16 become zeros (weights of zero times what lies there), and
-// where poison is given infinite and NaN values do, with their key noted there by column.
-template <int D, int BN, bool kLook>
-__device__ __forceinline__ void ra_expand(uint32_t src, uint32_t dst, int tid, int left, uint32_t bad, int key0, int* poison) {
-  constexpr int kChunks = D / 64, kUnits = BN * D / 16 / 128, kAtOnce = 4;
-  const int rsel = tid >> 2 & 1, i = tid & 3;
+// Codes to bf16: a tile of kRowsT rows of kCols codes, then a scale byte per row, to an operand tile, by 128 threads.  Eight
+// lanes take 64 codes of each of two rows, of neighbouring column groups where there are several: reads and writes then meet
+// every bank once.  Scales from 2^8 on (the factor leaves bf16's range) and codes 0x7F are left to ra_expand_rare, for which
+// this says whether there are any.
+template <int kCols, int kRowsT>
+struct RaUnit {  // unit u (of kRowsT * kCols / 16) of thread tid: 16 codes
+  int row, ch, i;
+  __device__ RaUnit(int tid, int u) {
+    constexpr int kChunks = kCols / 64;
+    const int qd = (tid >> 3) + 16 * u, rsel = tid >> 2 & 1;
+    row = 2 * (qd / kChunks) + rsel;
+    ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
+    i = tid & 3;
+  }
+  __device__ uint32_t in(uint32_t src) const { return src + row * kCols + ch * 64 + i * 16; }
+  __device__ uint32_t scale(uint32_t src) const { return src + kRowsT * kCols + row; }
+  __device__ uint32_t out(uint32_t dst, int k) const {  // of the k-th eight values
+    return dst + ch * (kRowsT * 128) + row * 128 + (((2 * i + k) ^ (row & 7)) << 4);
+  }
+};
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+template <int kCols, int kRowsT>
+__device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
+  constexpr int kUnits = kRowsT * kCols / 16 / 128, kAtOnce = 4;
+  uint32_t rare = 0;
 #pragma unroll 1
   for (int u0 = 0; u0 < kUnits; u0 += kAtOnce) {
     uint4 w[kAtOnce];
     uint32_t e[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int qd = (tid >> 3) + 16 * (u0 + k), row = 2 * (qd / kChunks) + rsel, ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
-      w[k] = lds128(src + row * D + ch * 64 + i * 16);
-      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[k]) : "r"(src + BN * D + row));
+      const RaUnit<kCols, kRowsT> u(tid, u0 + k);
+      w[k] = lds128(u.in(src));
+      e[k] = lds8(u.scale(src));
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int qd = (tid >> 3) + 16 * (u0 + k), row = 2 * (qd / kChunks) + rsel, ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
-      const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-      // 2^(120 + scale - 127) at once where that is a bf16 value, else in two steps
-      const uint32_t f = e[k] > 134 ? 0x7B807B80u : (e[k] + 120) * 0x00800080u;
-      uint32_t o[8], nan = 0;
+      const RaUnit<kCols, kRowsT> u(tid, u0 + k);
+      const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w}, f = (e[k] + 120) * 0x00800080u;  // 2^(120 + scale - 127)
+      uint32_t o[8];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         o[2 * x] = ra_bmul2(ra_code2<0x9180>(in[x]), f);
         o[2 * x + 1] = ra_bmul2(ra_code2<0xB3A2>(in[x]), f);
-        nan |= (in[x] & 0x7F7F7F7Fu) + 0x01010101u;
+        rare |= (in[x] & 0x7F7F7F7Fu) + 0x01010101u;
       }
-      if (e[k] > 134) {
-        const uint32_t f2 = e[k] == 255 ? 0x7FC07FC0u : e[k] * 0x00800080u;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) o[x] = ra_bmul2(o[x], f2);
-      }
-      if (nan & 0x80808080u) {  // codes 0x7F
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint32_t two = in[x >> 1] >> (x & 1 ? 16 : 0);
-          if ((two & 0x7F) == 0x7F) o[x] |= 0x7FC0u;
-          if ((two & 0x7F00) == 0x7F00) o[x] |= 0x7FC00000u;
-        }
-      }
-      if (kLook) {
-        if (row >= left || (bad >> (row >> 4) & 1)) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) o[x] = 0;
-        }
-        if (poison) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const uint32_t z = ra_special(o[x]);
-            const int d = ch * 64 + i * 16 + 2 * x;
-            if (z & 0x8000u) atomicMin(poison + d, key0 + row), o[x] &= 0xFFFF0000u;
-            if (z & 0x80000000u) atomicMin(poison + d + 1, key0 + row), o[x] &= 0x0000FFFFu;
-          }
-        }
-      }
-      const uint32_t out = dst + ch * (BN * 128) + row * 128, sw = row & 7;
-      sts128(out + (((2 * i) ^ sw) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-      sts128(out + (((2 * i + 1) ^ sw) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+      if (e[k] > 134) rare = 0x80u;
+      sts128(u.out(dst, 0), make_uint4(o[0], o[1], o[2], o[3]));
+      sts128(u.out(dst, 1), make_uint4(o[4], o[5], o[6], o[7]));
+    }
+  }
+  return rare & 0x80808080u;
+}
+template <int kCols, int kRowsT>
+__device__ __forceinline__ void ra_expand_rare(uint32_t src, uint32_t dst, int tid) {
+#pragma unroll 1
+  for (int k = 0; k < kRowsT * kCols / 128; ++k) {
+    const RaUnit<kCols, kRowsT> u(tid, k >> 4);
+    const uint32_t code = lds8(u.in(src) + (k & 15)), e = lds8(u.scale(src));
+    const uint32_t bits = (code & 0x80) << 8 | (code & 0x7F) << 4, one = e == 0 ? 0x40u : e << 7;
+    uint32_t v = ra_bmul2(ra_bmul2(bits, 0x7B80u), one) & 0xFFFFu;
+    if ((code & 0x7F) == 0x7F || e == 255) v = 0x7FFFu;
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(u.out(dst, k >> 3 & 1) + (k & 7) * 2), "h"((uint16_t)v) : "memory");
+  }
+}
+// A value tile with keys that some row does not see, or without keys in part (rows from `left` on, `bad` groups of 16 rows):
+// what lies in those becomes zeros (weights of zero times what lies there), and, where the block is an edge block, so do
+// infinite and NaN values, whose key is noted by column.
+template <int kCols, int kRowsT>
+__device__ __forceinline__ void ra_look(uint32_t tile, int tid, int left, uint32_t bad, bool edge, int key0, int* poison, int* special) {
+#pragma unroll 1
+  for (int u = tid; u < kRowsT * kCols / 8; u += 128) {
+    const int ch = u / (kRowsT * 8), row = (u >> 3) % kRowsT, d = ch * 64 + (((u & 7) ^ (row & 7)) << 3);
+    const uint32_t at = tile + u * 16;
+    if (row >= left || (bad >> (row >> 4) & 1)) {
+      sts128(at, make_uint4(0, 0, 0, 0));
+      continue;
+    }
+    if (!edge) continue;
+    const uint4 w = lds128(at);
+    if (!(ra_special(w.x) | ra_special(w.y) | ra_special(w.z) | ra_special(w.w))) continue;
+    *(volatile int*)special = 1;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at + 2 * k));
+      if ((v & 0x7F80) != 0x7F80) continue;
+      atomicMin(poison + d + k, key0 + row);
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2 * k), "h"((uint16_t)0) : "memory");
     }
   }
 }
@@ -300,8 +415,8 @@ __device__ __forceinline__ RaSeq ra_seq(const RowsArgs& a, int s) {
   return q;
 }
 // The work is one line: for every sequence, key-value head and item (tok_tile tokens) in turn, the item's keys and
-// item_cost.  Its blocks lie at multiples of kBlock keys from the item's start; a CTA owns the blocks that begin
-// in its part of the line.
+// item_cost.  Its blocks lie at multiples of kBlock keys from the item's start; a CTA (a pair) owns the blocks that begin in
+// its part of the line.
 constexpr int kMinKeys = 256;   // of the line per CTA at least
 
 // The line up to item t of one head.
@@ -329,37 +444,46 @@ struct RaItem {
   int slot;            // -1: the whole item; 0, 1: the CTA's first, last part
 };
 
+// kTiles: tiles of 128 rows per item.  Two lie in one CTA, or, with 256 columns, in the two CTAs of a pair, each of which
+// holds half of every key and value block.
 template <int D, int kTiles, int kSrc>
 struct RaCfg {
-  static constexpr bool kFp8 = kSrc == kPagedFp8;
-  static constexpr int kBlock = rows_block(D);
+  static constexpr bool kFp8 = kSrc == kPagedFp8, kPair = D == 256 && kTiles == 2;
+  static constexpr int kSub = kPair ? 1 : kTiles;                    // tiles in a CTA
+  static constexpr int kSoft = 4 * kSub, kThreads = 32 * (8 + kSoft);  // softmax warps
+  static constexpr int kBlock = rows_block(D, kTiles);
   static constexpr int kRows = 128 * kTiles;
-  static constexpr int kThreads = kTiles == 2 ? 512 : 384;
-  static constexpr int kTile = kBlock * D * 2;                       // bytes of a block's keys, or values
-  static constexpr int kRaw = kBlock * D + 128;                      // the same in codes, and the scales' bytes
-  static constexpr int kQ = kTiles == 2 ? kRows * D * 2 : 0;         // one tile's queries lie in tensor memory
-  static constexpr int kStages = kFp8 ? (D == 64 ? 6 : 4) : D == 64 ? (kTiles == 2 ? 8 : 10) : kTiles == 2 ? 5 : 6;
-  static constexpr int kRawStages = !kFp8 ? 0 : kTiles == 2 ? (D == 64 ? 6 : 2) : D == 64 ? 8 : 5;
-  static constexpr int kRing = 3;                                    // items
-  // tensor memory: scores (two tiles, or two buffers of the one), outputs, queries
-  static constexpr int kColS = kTiles == 2 ? 128 : kBlock;           // from one score buffer to the next
+  // operand tiles in a CTA: key rows and columns; a pair's CTA holds half of the keys, and half of the values' columns
+  static constexpr int kKRows = kPair ? kBlock / 2 : kBlock, kVCols = kPair ? D / 2 : D;
+  static constexpr int kTile = kKRows * D * 2;                       // bytes, of either
+  static_assert(kTile == kBlock * kVCols * 2, "");
+  static constexpr int kRaw = kTile / 2 + 128;                       // the same in codes, and the scales' bytes
+  static constexpr bool kQSmem = kTiles == 2;                        // else the queries lie in tensor memory
+  static constexpr int kQ = kQSmem ? kSub * 128 * D * 2 : 0;
+  static constexpr int kStages = kFp8 ? (D == 64 ? 6 : kPair ? 3 : 4) : D == 64 ? 8 : kTiles == 2 ? 5 : 6;
+  static constexpr int kRawStages = !kFp8 ? 0 : kPair ? 3 : kTiles == 2 ? (D == 64 ? 6 : 2) : D == 64 ? 8 : 5;
+  static constexpr int kRing = kPair ? 2 : 3;                        // items
+  static constexpr int kParts = kBlock / 64;                         // of a block's weights: the products take the first ones early
+  // tensor memory: scores (two tiles, or two buffers of one), outputs, queries
+  static constexpr int kColS = kBlock;                               // from one score buffer to the next
   static constexpr int kColO = 2 * kColS;
-  static constexpr int kColQ = kColO + D;                            // one tile
-  // registers: what issues or copies keeps few, the softmax warps take the rest of the launch's
-  static constexpr int kRegLow = kTiles == 2 ? 64 : 120, kRegHigh = kTiles == 2 ? 192 : 232;
-  static_assert(kTiles == 2 ? 8 * kRegLow + 8 * kRegHigh <= 16 * 128 : 8 * kRegLow + 4 * kRegHigh <= 12 * 168, "");
-  static_assert(kColO + kTiles * D <= 512 && (kTiles == 2 || kColQ + D / 2 <= 512), "");
+  static constexpr int kColQ = kColO + D;
+  // registers: what issues keeps few, what prepares operands some, the softmax warps take the rest of the launch's
+  static constexpr int kRegIssue = kSub == 2 ? 64 : 104, kRegPrep = kSub == 2 ? 64 : 168, kRegSoft = kSub == 2 ? 192 : 232;
+  static_assert(4 * kRegIssue + 4 * kRegPrep + kSoft * kRegSoft <= kThreads / 32 * (65536 / kThreads / 8 * 8), "");
+  static_assert(kColO + kSub * D <= 512 && (kQSmem || kColQ + D / 2 <= 512), "");
 };
 template <int D, int kTiles, int kSrc>
 struct RaShared {
   using C = RaCfg<D, kTiles, kSrc>;
   uint64_t full[C::kStages], ready[C::kStages], empty[C::kStages];
   uint64_t rfull[8], rempty[8];
-  uint64_t sfull[2], pfull[2], ofull[2], qfull[2];
+  uint64_t sfull[2], pfull[2][2], ofull[2], qfull[2], qfree[2];
   uint64_t ifull[C::kRing], iempty[C::kRing], drain;
-  unsigned long long scan[16];
+  unsigned long long scan[C::kThreads / 32];
   unsigned long long x0, x1, base;
   RaItem item[C::kRing];
+  int special[C::kRing];    // whether poison has an entry
   int poison[C::kRing][D];  // per column: the first key of the item's edge blocks whose value is infinite or NaN
   uint32_t bad[16];         // per block: the groups of 16 keys whose page does not exist
   int s0;
@@ -377,9 +501,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
   using C = RaCfg<D, kTiles, kSrc>;
-  constexpr int BN = C::kBlock;
-  constexpr int kChunks = D / 64;                 // 128-byte column groups of a tile
-  constexpr uint32_t kGroup = BN * 128;           // bytes from one to the next
+  constexpr bool kPair = C::kPair;
+  constexpr int BN = C::kBlock, kSub = C::kSub;
+  constexpr int kChunks = D / 64, kVChunks = C::kVCols / 64;                    // 128-byte column groups of keys, of values
+  constexpr uint32_t kKGroup = C::kKRows * 128, kVGroup = BN * 128;             // bytes from one to the next
   extern __shared__ __align__(1024) uint8_t dyn[];
   uint8_t* const q_p = dyn;
   uint8_t* const ring_p = q_p + C::kQ;
@@ -387,18 +512,21 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   auto& sh = *reinterpret_cast<RaShared<D, kTiles, kSrc>*>(raw_p + C::kRawStages * C::kRaw);
   const uint32_t q_s = smem_addr(q_p), ring = smem_addr(ring_p), raw = smem_addr(raw_p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x;
+  const int rank = kPair ? (int)ra_rank() : 0;
+  const int c = kPair ? blockIdx.x >> 1 : blockIdx.x, workers = kPair ? gridDim.x >> 1 : gridDim.x;  // CTAs or pairs
 #ifdef VP_WAIT_TEST
-  // Wait-test hook (workspace word kWsTestSkip): the first CTA leaves out 1 its first scores' commit, 2 a softmax warp's
-  // first arrival, 3 its first copies, 4 the first arrival of the warps that prepare values, 5 its first item.
-  const int hook = c == 0 ? ((const volatile int*)a.status)[kWsTestSkip / sizeof(int)] : 0;
+  // Wait-test hook (workspace word kWsTestSkip): the first CTA (a pair's second one with 6, 7 in place of 2, 4) leaves out
+  // 1 its first scores' commit, 2 a softmax warp's first arrival, 3 its first copies, 4 the first arrival of the warps
+  // that prepare operands, 5 its first item.
+  const int word = ((const volatile int*)a.status)[kWsTestSkip / sizeof(int)];
+  const int hook = blockIdx.x == 0 && word < 6 ? word : blockIdx.x == 1 && word == 6 ? 2 : blockIdx.x == 1 && word == 7 ? 4 : 0;
 #else
   constexpr int hook = 0;
 #endif
 
-  // -------------------------------------------------------------- the CTA's part of the line
+  // -------------------------------------------------------------- the CTA's (pair's) part of the line
   if (threadIdx.x == 0) {
-    a.desc[2 * c] = a.desc[2 * c + 1] = make_int4(0, 0, -1, 0);
+    if (rank == 0) a.desc[2 * c] = a.desc[2 * c + 1] = make_int4(0, 0, -1, 0);
     sh.abort = 0;
   }
   {
@@ -406,7 +534,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     unsigned long long mine = 0;
     for (int s = s0; s < s1; ++s) {
       const RaSeq q = ra_seq<kSrc>(a, s);
-      if (q.bad && c == 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
+      if (q.bad && blockIdx.x == 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
       mine += (unsigned long long)ra_line(a, q) * a.Hkv;
     }
     unsigned long long upto = mine;
@@ -418,16 +546,16 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     if (lane == 31) sh.scan[warp] = upto;
     __syncthreads();
     unsigned long long total = 0, before = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < C::kThreads / 32; ++w) {
       if (w == warp) before = total;
       total += sh.scan[w];
     }
     const unsigned long long most = total / kMinKeys;
-    const int ctas = most < 1 ? 1 : most < gridDim.x ? (int)most : (int)gridDim.x;
-    if (total == 0 || c >= ctas) return;
-    const unsigned long long each = total / ctas, more = total % ctas;
-    const unsigned long long x0 = each * c + more * c / ctas, x1 = each * (c + 1) + more * (c + 1) / ctas;
+    const int parts = most < 1 ? 1 : most < workers ? (int)most : workers;
+    if (total == 0 || c >= parts) return;
+    const unsigned long long each = total / parts, more = total % parts;
+    const unsigned long long x0 = each * c + more * c / parts, x1 = each * (c + 1) + more * (c + 1) / parts;
     before += upto - mine;
     if (x0 >= before && x0 < before + mine) {  // the sequence that holds the part's start
       unsigned long long at = before;
@@ -440,10 +568,11 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       sh.s0 = s, sh.base = at, sh.x0 = x0, sh.x1 = x1;
     }
   }
+  constexpr int kBoth = kPair ? 2 : 1;  // CTAs that arrive at the first one's barriers
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.ready[i], 4);
+      mbar_init(&sh.ready[i], (C::kFp8 ? 4 : 5) * kBoth);  // the preparing warps and the copying one, or that one in their place
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 8; ++i) {
@@ -452,32 +581,49 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pfull[i], 4);
+      for (int k = 0; k < 2; ++k) mbar_init(&sh.pfull[i][k], 4 * kBoth);
       mbar_init(&sh.ofull[i], 1);
-      mbar_init(&sh.qfull[i], 4);
+      mbar_init(&sh.qfull[i], 4 * kBoth);
+      mbar_init(&sh.qfree[i], 4);
     }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&sh.ifull[i], 1);
-      mbar_init(&sh.iempty[i], 2 + 4 + 4 * kTiles);  // copying, issuing, value and softmax warps
+      mbar_init(&sh.iempty[i], 2 + 4 + C::kSoft * kBoth);  // copying, issuing, preparing and softmax warps (a pair's: of both)
     }
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(&sh.tmem, 512);
+  if (warp == 1) {
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(&sh.tmem, 512);
+    }
+  }
   tmem_fence_before();
   __syncthreads();
+  if (kPair) ra_pair_sync();  // the other CTA's barriers exist
   tmem_fence_after();
   const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
 
+  // Bounded waits of a converged warp; false when one ran out here or elsewhere in the CTA.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    const uint32_t b = smem_addr(bar);
-    if (__all_sync(0xFFFFFFFFu, ra_try(b, parity))) return true;
-    return ra_wait_slow(b, parity, &sh.abort, a.status);
+    return ra_wait<kPair>(smem_addr(bar), parity, &sh.abort, a.status);
   };
-  auto wait2 = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) -> bool {
-    const bool one = ra_try(smem_addr(bar), parity), two = ra_try(smem_addr(bar2), parity2);
-    if (__all_sync(0xFFFFFFFFu, one && two)) return true;
-    return wait(bar, parity) && wait(bar2, parity2);
+  // One lane's arrival for its warp, here, or where the products are issued.
+  auto arrive = [&](uint64_t* bar) { ra_arrive(smem_addr(bar)); };
+  auto arrive_first = [&](uint64_t* bar) {
+    if constexpr (kPair)
+      ra_arrive_first(smem_addr(bar));
+    else
+      ra_arrive(smem_addr(bar));
+  };
+  auto arrive_first_relaxed = [&](uint64_t* bar) {
+    if constexpr (kPair)
+      ra_arrive_first_relaxed(smem_addr(bar));
+    else
+      ra_arrive(smem_addr(bar));
   };
   // The it-th item, for every role but the scheduler; null when a wait ran out.
   auto get = [&](int it) -> const RaItem* {
@@ -486,13 +632,13 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   };
   auto release = [&](int it) {
     __syncwarp();
-    if (lane == 0) ra_arrive(smem_addr(&sh.iempty[it % C::kRing]));
+    if (lane == 0) arrive(&sh.iempty[it % C::kRing]);
   };
 
-  if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegLow));
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegIssue));
     if (warp == 3) {
-      // ---------------------------------------------------------- scheduler: the pieces in turn
+      // ---------------------------------------------------------- scheduler: the pieces in turn (a pair's CTAs: the same ones)
       const long long x0 = (long long)sh.x0, x1 = (long long)sh.x1;
       long long at = (long long)sh.base;       // the line at the current sequence's (head's, item's) start
       int s = sh.s0, h = 0, t = 0, cached = -1, it = 0;
@@ -536,14 +682,15 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         const int tok0 = t * a.tok_tile, toks = min(a.tok_tile, q.n - tok0);
         const int keys = q.bad ? 0 : q.L - q.n + tok0 + toks, nb = (keys + BN - 1) / BN;
         // blocks whose place on the line lies in [x0, x1); a bad sequence's item by its start
-        long long f = x0 - at, e = x1 - at;
-        int b0 = f <= 0 ? 0 : (int)min((f + BN - 1) / BN, (long long)nb), b1 = (int)min((e + BN - 1) / BN, (long long)nb);
+        const long long f = x0 - at, e = x1 - at;
+        const int b0 = f <= 0 ? 0 : (int)min((f + BN - 1) / BN, (long long)nb), b1 = (int)min((e + BN - 1) / BN, (long long)nb);
         const bool mine = nb ? b0 < b1 : f <= 0;
         if (mine) {
           const int slot = it % C::kRing;
           if (it >= C::kRing && !(ok = wait(&sh.iempty[slot], (it / C::kRing - 1) & 1))) break;
           for (int d = lane; d < D; d += 32) sh.poison[slot][d] = 0x7FFFFFFF;
           if (lane == 0) {
+            sh.special[slot] = 0;
             RaItem& i = sh.item[slot];
             i.s = s, i.h = h;
             i.row = q.row0 + tok0;
@@ -552,17 +699,18 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             i.lim0 = q.bad ? 0 : q.L - q.n + tok0 + 1;
             i.keys = keys;
             i.b0 = b0, i.b1 = b1;
-            // the first 128 rows see no further than their last token; the others are there only if there are more
+            // Of two tiles in a CTA the first sees no further than its last token, and the second is there only if there
+            // are more than 128 rows.
             const int rows = toks * a.G, k0 = q.bad ? 0 : i.lim0 + min(toks - 1, 127 / a.G);
-            i.cnt[0] = max(min(b1, (k0 + BN - 1) / BN) - b0, 0);
-            i.cnt[1] = kTiles == 2 && rows > 128 ? b1 - b0 : 0;
+            i.cnt[0] = kSub == 1 ? b1 - b0 : max(min(b1, (k0 + BN - 1) / BN) - b0, 0);
+            i.cnt[1] = kSub == 2 && rows > 128 ? b1 - b0 : 0;
             i.edge = i.lim0 / BN;
             const bool starts = b0 == 0, ends = b1 == nb;
             i.slot = starts && ends ? -1 : starts ? 1 : 0;
-            if (i.slot >= 0) a.desc[2 * c + i.slot] = make_int4(s, h, q.row0 + tok0, rows | (ends ? kPartEnds : 0));
+            if (i.slot >= 0 && rank == 0) a.desc[2 * c + i.slot] = make_int4(s, h, q.row0 + tok0, rows | (ends ? kPartEnds : 0));
           }
           __syncwarp();
-          if (lane == 0 && !(hook == 5 && it == 0)) ra_arrive(smem_addr(&sh.ifull[slot]));
+          if (lane == 0 && !(hook == 5 && it == 0)) arrive(&sh.ifull[slot]);
           ++it;
         }
         at += keys + a.item_cost;
@@ -575,85 +723,108 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       if (ok && (it < C::kRing || wait(&sh.iempty[slot], (it / C::kRing - 1) & 1))) {
         if (lane == 0) {
           sh.item[slot].s = -1;
-          ra_arrive(smem_addr(&sh.ifull[slot]));
+          arrive(&sh.ifull[slot]);
         }
       }
       __syncwarp();
     } else if (warp == 0) {
       // ---------------------------------------------------------- copies
       constexpr int kSt = C::kFp8 ? C::kRawStages : C::kStages;
-      uint64_t *const full = C::kFp8 ? sh.rfull : sh.full, *const empty = C::kFp8 ? sh.rempty : sh.empty;
-      const int P = 1 << a.log_page, box = min(P, BN), npg = BN / box;  // pages of a block, rows of each
-      int cur = 0, nxt = 0, cur_s = -1, cur_w = -1, nxt_w = -1;         // lane l: page table entry cur_w + l
+      uint64_t* const empty = C::kFp8 ? sh.rempty : sh.empty;
+      const int P = 1 << a.log_page;
+      int cur = 0, nxt = 0, cur_s = -1, cur_w = -1, nxt_w = -1;  // lane l: page table entry cur_w + l
       int n = 0, st = 0, g = 0;
       uint32_t par = 1;
       bool ok = true;
       for (int it = 0; ok; ++it) {
         const RaItem* pi = get(it);
         if (!pi || pi->s < 0) break;
-        const RaItem i = *pi;
-        for (int b = i.b0; ok && b < i.b1; ++b, ++g) {
-          const int key0 = b * BN;
-          int pg = 0;          // of this lane's copy (paged)
-          uint32_t bad = 0;    // pages of the block that do not exist, and those with keys to copy
-          int have = npg;
+        const int i_s = pi->s, i_h = pi->h, i_kv = pi->kv_row, i_keys = pi->keys, i_b0 = pi->b0, i_b1 = pi->b1, i_edge = pi->edge;
+        for (int b = i_b0; ok && b < i_b1; ++b, ++g) {
+          const int key0 = b * BN, last = (i_keys - 1) >> a.log_page;
+          uint32_t wrong = 0;  // the block's pages that do not exist
           if (kSrc != kDense) {
-            const int p0 = key0 >> a.log_page, last = (i.keys - 1) >> a.log_page, w = p0 & ~31;
-            if (i.s != cur_s || w != cur_w) {
-              const int32_t* tab = a.pages + (size_t)i.s * a.max_pages;
-              cur = i.s == cur_s && w == nxt_w ? nxt : w + lane < a.max_pages ? __ldg(tab + w + lane) : 0;
-              cur_s = i.s, cur_w = w, nxt_w = w + 32;
+            const int p0 = key0 >> a.log_page, w = p0 & ~31;
+            if (i_s != cur_s || w != cur_w) {
+              const int32_t* tab = a.pages + (size_t)i_s * a.max_pages;
+              cur = i_s == cur_s && w == nxt_w ? nxt : w + lane < a.max_pages ? __ldg(tab + w + lane) : 0;
+              cur_s = i_s, cur_w = w, nxt_w = w + 32;
               nxt = nxt_w + lane < a.max_pages ? __ldg(tab + nxt_w + lane) : 0;
             }
-            const int mine = C::kFp8 || box == BN ? lane : lane / kChunks;
-            pg = __shfl_sync(0xFFFFFFFFu, cur, (p0 - w + mine) & 31);
-            have = min(npg, last - p0 + 1);
+            const int box = min(P, BN), have = min(BN / box, last - p0 + 1);
             const int page = __shfl_sync(0xFFFFFFFFu, cur, (p0 - w + lane) & 31);
-            const uint32_t wrong = __ballot_sync(0xFFFFFFFFu, lane < have && (page < 0 || page >= a.n_pages));
-            const int per = box / 16;  // groups of 16 keys of a page
+            wrong = __ballot_sync(0xFFFFFFFFu, lane < have && (page < 0 || page >= a.n_pages));
+            uint32_t bad = 0;
             if (wrong) {
+              const int per = box / 16;  // groups of 16 keys of a page
               for (int k = 0; k < have; ++k)
                 if (wrong >> k & 1) bad |= ((1u << per) - 1) << (k * per);
               if (lane == 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
             }
             if (lane == 0) sh.bad[g & 15] = bad;
-            if (C::kFp8) have = __popc(((1u << have) - 1) & ~wrong);  // copies
           }
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n) {
             if (!(ok = wait(&empty[st], par))) break;
-            const uint32_t bar = smem_addr(&full[st]);
             const bool skip = hook == 3 && n == 0;
+            // Values that some row does not see whole go by the preparing warps; what else is copied as it is announces itself
+            // where the products are issued.
+            const bool look = kv && b >= i_edge;
+            auto announce = [&](uint32_t bytes) {
+              if (look) {
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], bytes);
+                if (lane == 1) arrive_first_relaxed(&sh.ready[st]);
+              } else if (lane == 0) {
+                if constexpr (kPair)
+                  ra_expect_first(smem_addr(&sh.ready[st]), bytes);
+                else
+                  mbar_arrive_expect_tx(&sh.ready[st], bytes);
+              } else if (lane < 5) {
+                arrive_first_relaxed(&sh.ready[st]);
+              }
+              __syncwarp();
+            };
+            auto copy3d = [&](uint32_t dst, int y, int z) {
+              const CUtensorMap* map = kv ? &vmap : &kmap;
+              if (!kPair || look)
+                ra_tma_3d(dst, map, 0, y, z, smem_addr(look ? &sh.full[st] : &sh.ready[st]));
+              else
+                ra_tma_3d_first(dst, map, 0, y, z, smem_addr(&sh.ready[st]));
+            };
+            // this CTA's rows and columns of the block
+            const int rows = kv ? BN : C::kKRows, key = key0 + (kPair && !kv ? rank * C::kKRows : 0);
+            const int chunks = kv ? kVChunks : kChunks, chunk0 = kPair && kv ? rank * kVChunks : 0;
             if constexpr (kSrc == kDense) {
-              if (ra_elect()) {
-                mbar_arrive_expect_tx(&full[st], C::kTile);
-                if (!skip) ra_tma_3d(ring + st * C::kTile, kv ? &vmap : &kmap, 0, i.kv_row + key0, i.h * kChunks, bar);
-              }
-            } else if constexpr (kSrc == kPaged) {
-              const uint32_t dst = ring + st * C::kTile;
-              const int in_page = key0 & (P - 1), none = a.n_pages * a.Hkv << a.log_page;  // behind the cache: zeros
-              const bool real = pg >= 0 && pg < a.n_pages;
-              const int y = real ? ((pg * a.Hkv + i.h) << a.log_page) + in_page : none;
-              if (lane == 0) mbar_arrive_expect_tx(&full[st], have * box * D * 2);
-              __syncwarp();
-              if (!skip) {
-                if (box == BN) {
-                  if (lane == 0) ra_tma_3d(dst, kv ? &vmap : &kmap, 0, y, 0, bar);
-                } else if (lane < have * kChunks) {  // a page's column groups apart
-                  ra_tma_3d(dst + (lane % kChunks) * kGroup + (lane / kChunks) * box * 128, kv ? &vmap : &kmap, 0, y,
-                            lane % kChunks, bar);
-                }
-              }
+              announce(C::kTile);
+              if (lane == 0 && !skip) copy3d(ring + st * C::kTile, i_kv + key, i_h * kChunks + chunk0);
             } else {
-              const uint32_t dst = raw + st * C::kRaw;
-              const int in_page = key0 & (P - 1);
-              if (lane == 0) mbar_arrive_expect_tx(&full[st], have * box * (D + 1));
-              __syncwarp();
-              const int last = (i.keys - 1) >> a.log_page, p0 = key0 >> a.log_page;
-              if (!skip && lane < npg && p0 + lane <= last && pg >= 0 && pg < a.n_pages) {
-                const int y = ((pg * a.Hkv + i.h) << a.log_page) + in_page;
-                ra_tma_2d(dst + lane * box * D, kv ? &vmap : &kmap, 0, y, bar);
-                ra_bulk(dst + BN * D + lane * box, (kv ? a.v_scales : a.k_scales) + y, box, bar);
+              const int box = min(P, rows), p0 = key >> a.log_page, in_page = key & (P - 1);
+              const int have = max(min(rows / box, last - p0 + 1), 0);  // pages with keys
+              // lane -> page, and column group where a page's rows are not the whole tile's
+              const bool apart = !C::kFp8 && box < rows;
+              const int of = apart ? lane / chunks : lane;
+              const int page = __shfl_sync(0xFFFFFFFFu, cur, (p0 - cur_w + of) & 31);
+              const bool real = page >= 0 && page < a.n_pages;
+              const int y = ((page * a.Hkv + i_h) << a.log_page) + in_page;
+              if constexpr (kSrc == kPaged) {
+                const uint32_t dst = ring + st * C::kTile;
+                const int none = a.n_pages * a.Hkv << a.log_page;  // behind the cache: zeros
+                announce(have * box * chunks * 128);
+                if (!skip && (apart ? lane < have * chunks : lane < have)) {
+                  const int ch = apart ? lane % chunks : 0;
+                  copy3d(dst + (ch * rows + of * box) * 128, real ? y : none, chunk0 + ch);
+                }
+              } else {
+                const uint32_t dst = raw + st * C::kRaw;
+                const bool copy = lane < have && real;
+                const int copies = __popc(__ballot_sync(0xFFFFFFFFu, copy));
+                const uint32_t bar = smem_addr(&sh.rfull[st]);
+                if (lane == 0) mbar_arrive_expect_tx(&sh.rfull[st], copies * box * (chunks * 64 + 1));
+                __syncwarp();
+                if (!skip && copy) {
+                  ra_tma_2d(dst + lane * box * chunks * 64, kv ? &vmap : &kmap, chunk0 * 64, y, bar);
+                  ra_bulk(dst + rows * chunks * 64 + lane * box, (kv ? a.v_scales : a.k_scales) + y, box, bar);
+                }
               }
             }
             __syncwarp();
@@ -662,42 +833,60 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
         if (ok) release(it);
       }
-      // Nothing may be on its way to this CTA's shared memory when it ends: what was issued has landed, whatever ran out.
+      // Nothing may be on its way to this CTA's shared memory when it ends.  Copies of codes: they have landed, whatever ran
+      // out.  Others: a stage's last commit says that its copies have been read, and is itself the last arrival; where the
+      // products have stopped this takes the wait's whole limit, in which whatever was on its way arrives.
       for (int i = 0; i < min(n, kSt); ++i) {
         const int e = n - 1 - (n - 1 - i) % kSt;  // the last copy into stage i
-        mbar_wait_bounded(&full[e % kSt], (e / kSt) & 1);
-      }
-      // ... and no commit: a stage's last one frees it
-      if (!C::kFp8 && ok)
-        for (int i = 0; i < min(n, kSt); ++i) {
-          const int e = n - 1 - (n - 1 - i) % kSt;
-          if (!wait(&empty[e % kSt], (e / kSt) & 1)) break;
+        uint64_t* const bar = C::kFp8 ? &sh.rfull[e % kSt] : &sh.empty[e % kSt];
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, (e / kSt) & 1))) {
+          *(volatile int*)&sh.abort = 1;
+          atomicExch(a.status, (int)VP_ERR_TIMEOUT);
+          break;
         }
+      }
     } else if (warp == 1) {
       // ---------------------------------------------------------- matrix products
-      constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | 8u << 24;  // bf16 x bf16 -> fp32, 128 rows
+      constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (kPair ? 16u : 8u) << 24;  // bf16 x bf16 -> fp32, rows
       constexpr uint32_t kIdS = kIdesc | (uint32_t)(BN >> 3) << 17, kIdO = kIdesc | 1u << 16 | (uint32_t)(D >> 3) << 17;
       int st = 0, g = 0;                       // stage; blocks so far (one tile: of the score buffers)
-      uint32_t par = 0;
-      uint32_t qpar[2] = {0, 0}, ppar[2] = {0, 0};
+      uint32_t par = 0, qpar = 0, ppar = 0;    // of the stages, queries, weights (a bit per tile or buffer)
       bool ok = true, first = true;
       auto scores = [&](int i, int stage) {  // tile i, or buffer i of the one tile
-        const uint64_t db = ra_desc_k(ring + stage * C::kTile);
+        const uint64_t db = ra_desc_k(ring + stage * C::kTile), da = ra_desc_k(q_s + (kSub == 2 ? i * 128 * D * 2 : 0));
         const uint32_t d = tmem + i * C::kColS;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint64_t kb = db + (uint64_t)((k / 4) * (kGroup >> 4) + (k % 4) * 2);
-          if constexpr (kTiles == 2)
-            ra_mma_ss(d, ra_desc_k(q_s + i * 128 * D * 2) + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2), kb, kIdS, k > 0);
+          const uint64_t kb = db + (uint64_t)((k / 4) * (kKGroup >> 4) + (k % 4) * 2);
+          if constexpr (C::kQSmem)
+            ra_mma_ss<kPair>(d, da + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2), kb, kIdS, k > 0);
           else
-            ra_mma_ts(d, tmem + C::kColQ + 8 * k, kb, kIdS, k > 0);
+            ra_mma_ts<kPair>(d, tmem + C::kColQ + 8 * k, kb, kIdS, k > 0);
         }
       };
-      auto outputs = [&](int i, int o, int stage, bool accumulate) {  // P of score buffer i into output o
-        const uint64_t db = ra_desc_mn(ring + stage * C::kTile, kGroup);
-        const uint32_t p = tmem + i * C::kColS, d = tmem + C::kColO + o * D;
+      // weights of score buffer i, from block part on, into output o
+      auto outputs = [&](int i, int o, int stage, int part, bool accumulate) {
+        const uint64_t db = ra_desc_mn(ring + stage * C::kTile, kVGroup) + (uint64_t)(part * 4 * (2048 >> 4));
+        const uint32_t p = tmem + i * C::kColS + part * 32, d = tmem + C::kColO + o * D;
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k) ra_mma_ts(d, p + 8 * k, db + (uint64_t)(k * (2048 >> 4)), kIdO, accumulate || k > 0);
+        for (int k = 0; k < 4; ++k) ra_mma_ts<kPair>(d, p + 8 * k, db + (uint64_t)(k * (2048 >> 4)), kIdO, accumulate || k > 0);
+      };
+      auto q_ready = [&](int i) -> bool {
+        const bool there = wait(&sh.qfull[i], qpar >> i & 1);
+        qpar ^= 1u << i;
+        return there;
+      };
+      // Outputs of block j from buffer i as its weights come, a part at a time.
+      auto weigh = [&](int i, int o, int stage, bool accumulate) -> bool {
+#pragma unroll
+        for (int part = 0; part < C::kParts; ++part) {
+          if (!wait(&sh.pfull[i][part], ppar >> i & 1)) return false;
+          tmem_fence_after();
+          if (ra_elect()) outputs(i, o, stage, part, accumulate || part > 0);
+          __syncwarp();
+        }
+        ppar ^= 1u << i;
+        return true;
       };
       auto step = [&]() {
         if (++st == C::kStages) st = 0, par ^= 1;
@@ -705,12 +894,13 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       for (int it = 0; ok; ++it) {
         const RaItem* pi = get(it);
         if (!pi || pi->s < 0) break;
+        if (kPair && rank) {  // the first CTA issues
+          release(it);
+          continue;
+        }
         const int nblk = pi->b1 - pi->b0, cnt0 = pi->cnt[0], cnt1 = pi->cnt[1];
-        for (int i = 0; i < kTiles && ok; ++i)
-          if ((i ? cnt1 : cnt0) > 0) {
-            ok = wait(&sh.qfull[i], qpar[i]);
-            qpar[i] ^= 1;
-          }
+        if (cnt0 > 0) ok = q_ready(0);
+        if (kSub == 2 && ok && cnt1 > 0) ok = q_ready(1);
         // Scores of block j + 1 and outputs of block j (the ring's order: keys 0, values 0, keys 1, ...).  With two tiles
         // one's softmax runs beside the other's products, with one its next scores lie in a second buffer.
         for (int j = -1; ok && j < nblk; ++j) {
@@ -718,46 +908,37 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           const uint32_t vpar = par;
           if (j >= 0) step();
           const int ks = st;
-          bool have_v = false, have_k = false;
-          if constexpr (kTiles == 1) {
+          if constexpr (kSub == 1) {
             if (j + 1 < nblk) {
               if (!(ok = wait(&sh.ready[ks], par))) break;
               step();
               tmem_fence_after();
               if (ra_elect()) {
                 scores((g + j + 1) & 1, ks);
-                if (!(hook == 1 && first)) ra_commit(&sh.sfull[(g + j + 1) & 1]);
-                ra_commit(&sh.empty[ks]);
+                if (!(hook == 1 && first)) ra_commit<kPair>(&sh.sfull[(g + j + 1) & 1]);
+                ra_commit<kPair>(&sh.empty[ks]);
               }
               first = false;
               __syncwarp();
             }
             if (j >= 0) {
               const int buf = (g + j) & 1;
-              if (!(ok = wait(&sh.ready[vs], vpar))) break;
-              if (!(ok = wait(&sh.pfull[buf], ppar[buf]))) break;
-              ppar[buf] ^= 1;
-              tmem_fence_after();
+              if (!(ok = wait(&sh.ready[vs], vpar) && weigh(buf, 0, vs, j > 0))) break;
               if (ra_elect()) {
-                outputs(buf, 0, vs, j > 0);
-                ra_commit(&sh.ofull[buf]);
-                ra_commit(&sh.empty[vs]);
+                ra_commit<kPair>(&sh.ofull[buf]);
+                ra_commit<kPair>(&sh.empty[vs]);
               }
               __syncwarp();
             }
           } else {
-#pragma unroll
+            bool have_v = false, have_k = false;
+#pragma unroll 1
             for (int i = 0; i < 2; ++i) {
               const int cnt = i ? cnt1 : cnt0;
               if (ok && j >= 0 && j < cnt) {
                 if (!have_v) ok = have_v = wait(&sh.ready[vs], vpar);
-                ok = ok && wait(&sh.pfull[i], ppar[i]);
-                ppar[i] ^= 1;
-                tmem_fence_after();
-                if (ok && ra_elect()) {
-                  outputs(i, i, vs, j > 0);
-                  ra_commit(&sh.ofull[i]);
-                }
+                ok = ok && weigh(i, i, vs, j > 0);
+                if (ok && ra_elect()) ra_commit<kPair>(&sh.ofull[i]);
                 __syncwarp();
               }
               if (ok && j + 1 < cnt) {
@@ -765,7 +946,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                 tmem_fence_after();
                 if (ok && ra_elect()) {
                   scores(i, ks);
-                  if (!(hook == 1 && first)) ra_commit(&sh.sfull[i]);
+                  if (!(hook == 1 && first)) ra_commit<kPair>(&sh.sfull[i]);
                 }
                 first = false;
                 __syncwarp();
@@ -774,8 +955,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             if (!ok) break;
             // every block is some tile's: the second's where there are more than 128 rows, else the first's
             if (ra_elect()) {
-              if (j >= 0) ra_commit(&sh.empty[vs]);
-              if (j + 1 < nblk) ra_commit(&sh.empty[ks]);
+              if (j >= 0) ra_commit<kPair>(&sh.empty[vs]);
+              if (j + 1 < nblk) ra_commit<kPair>(&sh.empty[ks]);
             }
             __syncwarp();
             if (j + 1 < nblk) step();
@@ -786,274 +967,314 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         release(it);
       }
       // every product has ended before the tensor memory goes
-      if (ra_elect()) ra_commit(&sh.drain);
-      __syncwarp();
-      mbar_wait_bounded(&sh.drain, 0);
-    } else if (warp >= 4) {
-      // ---------------------------------------------------------- values that need a look, 8-bit tiles
-      const int tid = threadIdx.x - 128;
-      int st = 0, g = 0, rst = 0, done = 0;
-      uint32_t par = 0, wpar = 1, rpar = 0;
-      bool ok = true;
-      for (int it = 0; ok; ++it) {
-        const RaItem* pi = get(it);
-        if (!pi || pi->s < 0) break;
-        const int b0 = pi->b0, b1 = pi->b1, edge = pi->edge, keys = pi->keys;
-        int* const poison = sh.poison[it % C::kRing];
-        // The item's queries and gates on their way to L2, ahead of the warps that read them.
-        for (int u = tid; u < pi->toks * a.G * kChunks; u += 128) {
-          const int row = u / kChunks, t = row * a.g_inv >> 16, hd = pi->h * a.G + row - t * a.G;
-          if (it > 0) ra_prefetch(a.q + (size_t)(pi->row + t) * a.ld_q + (size_t)hd * D + u % kChunks * 64);
-          if (a.gate) ra_prefetch(a.gate + ((size_t)(pi->row + t) * a.Hq + hd) * D + u % kChunks * 64);
-        }
-        for (int b = b0; ok && b < b1; ++b, ++g) {
+      if (!kPair || rank == 0) {
+        if (ra_elect()) ra_commit<kPair>(&sh.drain);
+        __syncwarp();
+        mbar_wait_bounded(&sh.drain, 0);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ queries, values that need a look, 8-bit tiles
+    if constexpr (C::kRegPrep < 65536 / C::kThreads / 8 * 8)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegPrep));
+    const int tid = threadIdx.x - 128, quad = warp & 3;
+    int st = 0, g = 0, rst = 0, done = 0;
+    int nq0 = 0, nq1 = 0;  // query tiles so far
+    uint32_t fpar = 0, wpar = 1, rpar = 0;  // of the full barriers (a bit each: their phases are the looks'), the stages, the codes
+    bool ok = true;
+    // This warp's 32 rows of the CTA's tile w; rows that are not there read as zeros, warps without rows load nothing.
+    auto load_q = [&](const RaItem& i, int w) {
+      const int row0 = (kPair ? rank : w) * 128 + quad * 32;  // of the item
+      if (row0 * a.g_inv >> 16 < i.toks) {
+        if constexpr (C::kQSmem) {  // into shared memory, a row's lanes together
+          constexpr int kLanes = D / 8, kAt = 32 / kLanes, kAtOnce = kSub == 2 ? 4 : 16;
+          const int piece = lane % kLanes;
+          const uint32_t dst = q_s + w * 128 * D * 2 + (piece >> 3) * 16384;
+          const uint16_t* src = a.q + (size_t)i.row * a.ld_q + (size_t)i.h * a.G * D + piece * 8;
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv) {
-            const bool look = kv == 1 && b >= edge;
-            const int left = keys - b * BN;  // rows of the tile that hold keys
-            if constexpr (C::kFp8) {
-              if (!(ok = wait(&sh.rfull[rst], rpar))) break;
-              if (!(ok = wait(&sh.empty[st], wpar))) break;
-              const uint32_t src = raw + rst * C::kRaw, dst = ring + st * C::kTile;
-              const uint32_t bad = kv ? sh.bad[g & 15] : 0;
-              if (look || bad)
-                ra_expand<D, BN, true>(src, dst, tid, left, bad, b * BN, look ? poison : nullptr);
-              else
-                ra_expand<D, BN, false>(src, dst, tid, left, bad, 0, nullptr);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (!(hook == 4 && done == 0 && warp == 4)) ra_arrive(smem_addr(&sh.ready[st]));
-                ra_arrive(smem_addr(&sh.rempty[rst]));
-              }
-              ++done;
-              if (++rst == C::kRawStages) rst = 0, rpar ^= 1;
-              if (++st == C::kStages) st = 0, wpar ^= 1;
-            } else {
-              if (!(ok = wait(&sh.full[st], par))) break;
-              if (look) {
-                // (pages that do not exist were filled with zeros)
-                for (int u = tid; u < BN * D / 8; u += 128) {
-                  const int ch = u / (BN * 8), row = (u >> 3) % BN, at = u & 7;
-                  const uint32_t addr = ring + st * C::kTile + u * 16;
-                  if (row >= left) {
-                    sts128(addr, make_uint4(0, 0, 0, 0));
-                    continue;
-                  }
-                  const uint4 w = lds128(addr);
-                  uint32_t o[4] = {w.x, w.y, w.z, w.w};
-                  if (ra_special(o[0]) | ra_special(o[1]) | ra_special(o[2]) | ra_special(o[3])) {
+          for (int k0 = 0; k0 < kLanes; k0 += kAtOnce) {
+            uint4 v[kAtOnce];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      const uint32_t z = ra_special(o[k]);
-                      const int d = ch * 64 + ((at ^ (row & 7)) << 3) + 2 * k, key = b * BN + row;
-                      if (z & 0x8000u) atomicMin(poison + d, key), o[k] &= 0xFFFF0000u;
-                      if (z & 0x80000000u) atomicMin(poison + d + 1, key), o[k] &= 0x0000FFFFu;
-                    }
-                    sts128(addr, make_uint4(o[0], o[1], o[2], o[3]));
-                  }
-                }
-                fence_proxy_async_smem();
-              }
-              __syncwarp();
-              if (lane == 0 && !(hook == 4 && done == 0 && warp == 4)) ra_arrive(smem_addr(&sh.ready[st]));
-              ++done;
-              if (++st == C::kStages) st = 0, par ^= 1;
+            for (int k = 0; k < kAtOnce; ++k) {
+              const int r = row0 + (k0 + k) * kAt + lane / kLanes, t = r * a.g_inv >> 16;
+              v[k] = make_uint4(0, 0, 0, 0);
+              if (t < i.toks) v[k] = ra_ldg128(src + t * a.ld_q + (r - t * a.G) * D);
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+              const int row = quad * 32 + (k0 + k) * kAt + lane / kLanes;
+              sts128(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
+                     make_uint4((v[k].x & a.q_and) ^ a.q_flip, (v[k].y & a.q_and) ^ a.q_flip, (v[k].z & a.q_and) ^ a.q_flip,
+                                (v[k].w & a.q_and) ^ a.q_flip));
             }
           }
-        }
-        if (ok) release(it);
-      }
-      if (C::kFp8 && ok)  // the stages' last commits have arrived
-        for (int i = 0; i < min(done, C::kStages); ++i) {
-          const int e = done - 1 - (done - 1 - i) % C::kStages;
-          if (!wait(&sh.empty[e % C::kStages], (e / C::kStages) & 1)) break;
-        }
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegHigh));
-    // ------------------------------------------------------------ softmax: a thread per row of tile w
-    const int w = (warp - 8) >> 2, quad = warp & 3, rr = quad * 32 + lane, r = w * 128 + rr;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int tok = r / a.G, head = r - tok * a.G;
-    const uint64_t scale_2 = ra_pair(a.scale2, a.scale2);
-    int g = 0, npv = 0;  // blocks (one tile: of the score buffers) and outputs so far
-    bool ok = true;
-
-    const int first_tok = (w * 128 + quad * 32) / a.G;  // of the warp's rows; a warp without rows passes the scores through
-    auto load_q = [&](const RaItem& i) {
-      if (first_tok < i.toks) {
-        if constexpr (kTiles == 2) {  // a row's lanes together
-          constexpr int kLanes = D / 8, kAt = 32 / kLanes;
-          uint4 v[kLanes];
-#pragma unroll
-          for (int k = 0; k < kLanes; ++k) {
-            const int row = w * 128 + quad * 32 + k * kAt + lane / kLanes, t = row * a.g_inv >> 16, hd = row - t * a.G;
-            v[k] = make_uint4(0, 0, 0, 0);
-            if (t < i.toks)
-              v[k] = ra_ldg128(a.q + (size_t)(i.row + t) * a.ld_q + (size_t)(i.h * a.G + hd) * D + lane % kLanes * 8);
-          }
-#pragma unroll
-          for (int k = 0; k < kLanes; ++k) {
-            const int row = quad * 32 + k * kAt + lane / kLanes, piece = lane % kLanes;
-            v[k].x = (v[k].x & a.q_and) ^ a.q_flip, v[k].y = (v[k].y & a.q_and) ^ a.q_flip;
-            v[k].z = (v[k].z & a.q_and) ^ a.q_flip, v[k].w = (v[k].w & a.q_and) ^ a.q_flip;
-            sts128(q_s + w * 128 * D * 2 + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4), v[k]);
-          }
           fence_proxy_async_smem();
-        } else {
-          const bool there = tok < i.toks;
-          const uint16_t* src = a.q + (size_t)(i.row + (there ? tok : 0)) * a.ld_q + (size_t)(i.h * a.G + head) * D;
-          uint4 v[D / 8];
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k) {
-            v[k] = make_uint4(0, 0, 0, 0);
-            if (there) v[k] = ra_ldg128(src + k * 8);
-          }
-          __syncwarp();
-#pragma unroll
+        } else {  // into tensor memory, a row per lane
+          const int r = row0 + lane, t = r * a.g_inv >> 16;
+          const bool there = t < i.toks;
+          const uint16_t* src = a.q + (size_t)(i.row + (there ? t : 0)) * a.ld_q + (size_t)(i.h * a.G + r - t * a.G) * D;
+#pragma unroll 2
           for (int ch = 0; ch < kChunks; ++ch) {
             uint32_t x[32];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const uint4 u = v[ch * 8 + k];
+              uint4 u = make_uint4(0, 0, 0, 0);
+              if (there) u = ra_ldg128(src + ch * 64 + k * 8);
               x[4 * k] = (u.x & a.q_and) ^ a.q_flip, x[4 * k + 1] = (u.y & a.q_and) ^ a.q_flip;
               x[4 * k + 2] = (u.z & a.q_and) ^ a.q_flip, x[4 * k + 3] = (u.w & a.q_and) ^ a.q_flip;
             }
-            ra_st32(lanes + C::kColQ + ch * 32, x);
+            __syncwarp();
+            ra_st32(tmem + ((uint32_t)(quad * 32) << 16) + C::kColQ + ch * 32, x);
           }
           tmem_wait_st();
           tmem_fence_before();
         }
       }
       __syncwarp();
-      if (lane == 0) ra_arrive(smem_addr(&sh.qfull[w]));
+      if (lane == 0) arrive_first(&sh.qfull[w]);
     };
-
+    for (int it = 0; ok; ++it) {
+      const RaItem* pi = get(it);
+      if (!pi || pi->s < 0) break;
+      const int b0 = pi->b0, b1 = pi->b1, edge = pi->edge, keys = pi->keys;
+      int* const poison = sh.poison[it % C::kRing] + (kPair ? rank * C::kVCols : 0);
+      int* const special = &sh.special[it % C::kRing];
+      // the queries and gates on their way to L2, ahead of those who read them
+      for (int u = tid; u < min(pi->toks * a.G - (kPair ? rank * 128 : 0), kSub * 128) * kChunks; u += 128) {
+        const int row = u / kChunks + (kPair ? rank * 128 : 0), t = row * a.g_inv >> 16, hd = pi->h * a.G + row - t * a.G;
+        if (it > 0) ra_prefetch(a.q + (size_t)(pi->row + t) * a.ld_q + (size_t)hd * D + u % kChunks * 64);
+        if (a.gate) ra_prefetch(a.gate + ((size_t)(pi->row + t) * a.Hq + hd) * D + u % kChunks * 64);
+      }
+      // the queries, once the last item's scores are done with theirs
+      if (pi->cnt[0] > 0) {
+        if (nq0 > 0 && !(ok = wait(&sh.qfree[0], (nq0 - 1) & 1))) break;
+        ++nq0;
+        tmem_fence_after();
+        load_q(*pi, 0);
+      }
+      if (kSub == 2 && pi->cnt[1] > 0) {
+        if (nq1 > 0 && !(ok = wait(&sh.qfree[1], (nq1 - 1) & 1))) break;
+        ++nq1;
+        load_q(*pi, 1);
+      }
+      for (int b = b0; ok && b < b1; ++b, ++g) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++done) {
+          const uint32_t tile = ring + st * C::kTile;
+          if (!C::kFp8 && !(kv && b >= edge)) {  // nothing to do
+            if (++st == C::kStages) st = 0;
+            continue;
+          }
+          if constexpr (C::kFp8) {
+            if (!(ok = wait(&sh.rfull[rst], rpar) && wait(&sh.empty[st], wpar))) break;
+            const uint32_t src = raw + rst * C::kRaw;
+            if (C::kKRows == BN || kv) {
+              if (ra_expand<C::kVCols, BN>(src, tile, tid)) ra_expand_rare<C::kVCols, BN>(src, tile, tid);
+            } else {
+              if (ra_expand<D, C::kKRows>(src, tile, tid)) ra_expand_rare<D, C::kKRows>(src, tile, tid);
+            }
+            // (a unit's values may be another thread's to look at)
+            asm volatile("bar.sync 15, 128;" ::: "memory");
+          } else {
+            if (!(ok = wait(&sh.full[st], fpar >> st & 1))) break;
+            fpar ^= 1u << st;
+          }
+          const uint32_t bad = C::kFp8 ? *(volatile uint32_t*)&sh.bad[g & 15] : 0;  // (else filled with zeros)
+          const bool look = kv && (b >= edge || bad);
+          if (look) ra_look<C::kVCols, BN>(tile, tid, keys - b * BN, bad, b >= edge, b * BN, poison, special);
+          if (C::kFp8 || look) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (!(hook == 4 && done == 0 && warp == 4)) arrive_first(&sh.ready[st]);
+            if (C::kFp8) arrive(&sh.rempty[rst]);
+          }
+          if (C::kFp8 && ++rst == C::kRawStages) rst = 0, rpar ^= 1;
+          if (++st == C::kStages) st = 0, wpar ^= 1;
+        }
+      }
+      if (ok) release(it);
+    }
+    if (C::kFp8)  // no commit is on its way when the CTA ends: a stage's last one frees it
+      for (int i = 0; i < min(done, C::kStages); ++i) {
+        const int e = done - 1 - (done - 1 - i) % C::kStages;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.empty[e % C::kStages], (e / C::kStages) & 1))) break;
+      }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
+    // ------------------------------------------------------------ softmax: rows of the CTA's tile w, a thread per row
+    const int sm = warp - 8, w = sm >> 2, quad = warp & 3;
+    const int row0 = (kPair ? rank : w) * 128 + quad * 32, r = row0 + lane;  // of the item
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int tok = r * a.g_inv >> 16, first_tok = row0 * a.g_inv >> 16;
+    const uint64_t scale_2 = ra_pair(a.scale2, a.scale2);
+    int g = 0, npv = 0;  // blocks (one tile: of the score buffers) and outputs so far
+    bool ok = true;
     // The outputs of block n (one tile), or of this tile's block v, are there.
     auto outputs_of = [&](int n, int v) -> bool {
-      return kTiles == 1 ? wait(&sh.ofull[n & 1], n >> 1 & 1) : wait(&sh.ofull[w], v & 1);
+      return kSub == 1 ? wait(&sh.ofull[n & 1], n >> 1 & 1) : wait(&sh.ofull[w], v & 1);
     };
-
-    const RaItem* pi = get(0);
-    if (pi && pi->s >= 0 && pi->cnt[w] > 0) load_q(*pi);
-    for (int it = 0; pi && pi->s >= 0; ++it) {
-      const int b0 = pi->b0, cnt = pi->cnt[w], nblk = pi->b1 - b0;
-      const int lim = tok < pi->toks ? min(pi->lim0 + tok, pi->keys) : pi->keys;  // keys that this row sees
+    for (int it = 0; ok; ++it) {
+      const RaItem* pi = get(it);
+      if (!pi || pi->s < 0) break;
+      const int b0 = pi->b0, cnt = pi->cnt[w], nblk = pi->b1 - b0, toks = pi->toks;
+      const int lim = tok < toks ? min(pi->lim0 + tok, pi->keys) : pi->keys;  // keys that this row sees
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
-      const bool idle = first_tok >= pi->toks;
-      float m = -INFINITY, mc = 0.0f;  // reference of the exponents (log2 units), and what is subtracted
-      uint64_t l2[2] = {0, 0};         // sums of the weights
+      const bool idle = first_tok >= toks;  // no row of the warp is there
+      float m = -INFINITY;                  // reference of the exponents (log2 units)
+      uint64_t l2[2] = {0, 0};              // sums of the weights
       for (int j = 0; j < cnt; ++j) {
-        const int buf = kTiles == 2 ? w : (g + j) & 1;
-        const uint32_t sp = kTiles == 2 ? (uint32_t)(npv & 1) : (uint32_t)((g + j) >> 1 & 1);
+        const int buf = kSub == 2 ? w : (g + j) & 1;
+        const uint32_t sp = kSub == 2 ? (uint32_t)(npv & 1) : (uint32_t)((g + j) >> 1 & 1);
         // Every phase of the outputs' barriers is waited for in turn: a wait tells a phase from the one before it only.  The
         // last outputs on the barrier come before these scores: no time passes for them.
-        if (j >= 3 - kTiles)
-          ok = kTiles == 1 ? wait2(&sh.sfull[buf], sp, &sh.ofull[buf], (g + j - 2) >> 1 & 1) : wait2(&sh.sfull[buf], sp, &sh.ofull[w], (npv - 1) & 1);
-        else
-          ok = wait(&sh.sfull[buf], sp);
+        ok = wait(&sh.sfull[buf], sp);
+        if (ok && j >= 3 - kSub) ok = outputs_of(g + j - 2, npv - 1);
         if (!ok) break;
-        if (idle) {  // no row of the warp is there: whatever the products make of the scores is not read
+        if (j == cnt - 1) {  // the queries have been read
           tmem_fence_before();
           __syncwarp();
-          if (lane == 0) ra_arrive(smem_addr(&sh.pfull[buf]));
+          if (lane == 0) arrive(&sh.qfree[w]);
+        }
+        if (idle) {  // whatever the products make of the scores is not read
+          tmem_fence_before();
+          __syncwarp();
+          if (lane < C::kParts) arrive_first_relaxed(&sh.pfull[buf][lane]);
           ++npv;
           continue;
         }
         tmem_fence_after();
         const uint32_t ts = lanes + buf * C::kColS;
-        uint32_t x[BN];
-#pragma unroll
-        for (int k = 0; k < BN; k += 32) ra_ld32(ts + k, x + k);
         const int key0 = (b0 + j) * BN;
         const uint32_t bad = kSrc == kDense ? 0 : *(volatile uint32_t*)&sh.bad[(g + j) & 15];
+        if (key0 + BN > lim_min || bad) {  // keys that a row does not see
+#pragma unroll 1
+          for (int k0 = 0; k0 < BN; k0 += 32) {
+            const int sees = lim - key0 - k0;
+            const uint32_t groups = bad >> (k0 / 16);
+            uint32_t x[32];
+            ra_ld32(ts + k0, x);
+            ra_wait32(x);
 #pragma unroll
-        for (int k = 0; k < BN; k += 32) ra_wait32(x + k);
-        if (key0 + BN > lim_min || bad) {
-          const int sees = lim - key0;
-#pragma unroll
-          for (int k = 0; k < BN; ++k)
-            if (k >= sees || (bad >> (k >> 4) & 1)) x[k] = 0xFF800000u;
+            for (int k = 0; k < 32; ++k)
+              if (k >= sees || (groups >> (k >> 4) & 1)) x[k] = 0xFF800000u;
+            ra_st32(ts + k0, x);
+          }
+          tmem_wait_st();
         }
-        float mx[4];
+        // The scores are read twice, 32 at a time: unrolled over all of them the loop is too long for the instruction caches.
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        {
+          uint32_t x[2][32];
+          ra_ld32(ts, x[0]);
+#pragma unroll 1
+          for (int k0 = 0; k0 < BN; k0 += 64) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = ra_max3(__uint_as_float(x[3 * e]), __uint_as_float(x[3 * e + 1]), __uint_as_float(x[3 * e + 2]));
+            for (int h = 0; h < 2; ++h) {
+              ra_wait32(x[h]);
+              if (h == 0 || k0 + 64 < BN) ra_ld32(ts + k0 + 32 * (h + 1), x[h ^ 1]);
 #pragma unroll
-        for (int k = 12; k + 1 < BN; k += 2) mx[k / 2 % 4] = ra_max3(mx[k / 2 % 4], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        const float top = fmaxf(ra_max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale2;
+              for (int k = 0; k < 32; k += 2)
+                mx[k / 2 % 4] = ra_max3(mx[k / 2 % 4], __uint_as_float(x[h][k]), __uint_as_float(x[h][k + 1]));
+            }
+          }
+        }
+        uint32_t x[2][32];
+        ra_ld32(ts, x[0]);  // again, while the reference is found
+        float top = fmaxf(ra_max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale2;
         // The reference follows the maximum only where that has grown by 2^8: a weight may reach 2^8, which costs bf16
         // nothing, and the outputs are seldom scaled again.
-        const bool grow = top > m + 8.0f || (m == -INFINITY && top > m);
-        if (j == 0) {
-          if (grow) m = top;
-        } else if (__any_sync(0xFFFFFFFFu, grow)) {
+        bool grow = top > m + 8.0f || (m == -INFINITY && top > m);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
           const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
           m = to;
-          const uint64_t ff = ra_pair(f, f), zero = 0;
-          l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
-          if (kTiles == 1 && !(ok = outputs_of(g + j - 1, 0))) break;
-          tmem_fence_after();
-          const uint32_t to_ = lanes + C::kColO + w * D;
+          if (j > 0) {
+            const uint64_t ff = ra_pair(f, f), zero = 0;
+            l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
+            if (kSub == 1 && !(ok = outputs_of(g + j - 1, 0))) break;
+            tmem_fence_after();
+            const uint32_t to_ = lanes + C::kColO + w * D;
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            uint32_t y[32];
-            ra_ld32(to_ + d, y);
-            ra_wait32(y);
+            for (int d = 0; d < D; d += 16) {
+              uint32_t y[16];
+              ra_ld16(to_ + d, y);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-            ra_st32(to_ + d, y);
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+              ra_st16(to_ + d, y);
+            }
           }
         }
-        mc = m == -INFINITY ? 0.0f : m;
+        const float mc = m == -INFINITY ? 0.0f : m;
         const uint64_t mc2 = ra_pair(-mc, -mc);
+        // the weights go over the scores, 32 over the first 16 columns and so on: behind what is still read
+#pragma unroll 1
+        for (int k0 = 0; k0 < BN; k0 += 64) {
 #pragma unroll
-        for (int k = 0; k < BN; k += 32) {
-          uint32_t p[16];
+          for (int h = 0; h < 2; ++h) {
+            ra_wait32(x[h]);
+            if (h == 0 || k0 + 64 < BN) ra_ld32(ts + k0 + 32 * (h + 1), x[h ^ 1]);
+            uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float lo, hi;
-            ra_unpair(ra_fma2(ra_pair(__uint_as_float(x[k + 2 * e]), __uint_as_float(x[k + 2 * e + 1])), scale_2, mc2), lo, hi);
-            lo = ra_ex2(lo), hi = ra_ex2(hi);
-            l2[e & 1] = ra_add2(l2[e & 1], ra_pair(lo, hi));
-            p[e] = ra_bf16x2(lo, hi);
+            for (int e = 0; e < 16; ++e) {
+              float lo, hi;
+              ra_unpair(ra_fma2(ra_pair(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])), scale_2, mc2), lo, hi);
+              lo = ra_ex2(lo), hi = ra_ex2(hi);
+              l2[e & 1] = ra_add2(l2[e & 1], ra_pair(lo, hi));
+              p[e] = ra_bf16x2(lo, hi);
+            }
+            ra_st16(ts + (k0 + 32 * h) / 2, p);
           }
-          ra_st16(ts + k / 2, p);
+          tmem_wait_st();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0 && !(hook == 2 && it == 0 && j == 0 && warp == 8)) arrive_first_relaxed(&sh.pfull[buf][k0 / 64]);
         }
-        tmem_wait_st();
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0 && !(hook == 2 && it == 0 && j == 0 && warp == 8)) ra_arrive(smem_addr(&sh.pfull[buf]));
         ++npv;
       }
       if (!ok) break;
       g += nblk;
-      // the next item's queries, while the last products run
-      const RaItem* next = get(it + 1);
-      if (!next) break;
-      if (next->s >= 0 && next->cnt[w] > 0) load_q(*next);
       // ---- the item's outputs
-      const bool there = tok < pi->toks;
-      const int slot = pi->slot;
-      const bool special = pi->b1 > pi->edge;  // the piece has edge blocks
-      const int* const poison = sh.poison[it % C::kRing];
-      const size_t orow = (size_t)(pi->row + (there ? tok : 0)) * a.Hq + pi->h * a.G + head;
-      uint4 gt[4];  // the gates are loaded a step ahead
-      if (a.gate && there && slot < 0) {
+      const int slot = pi->slot, rows = min(32, toks * a.G - row0);  // the warp's rows
+      float l;
+      {
+        float s0, s1, s2, s3;
+        ra_unpair(l2[0], s0, s1);
+        ra_unpair(l2[1], s2, s3);
+        l = (s0 + s1) + (s2 + s3);
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const uint32_t to_ = lanes + C::kColO + w * D;
+      const bool there = lane < rows;
+      const size_t at = (((size_t)pi->row + (there ? tok : 0)) * a.Hq + pi->h * a.G + r - tok * a.G) * D;  // the row's outputs
+      // 32 columns at a time; gates are loaded two steps ahead: behind the ring's copies a load takes long.
+      uint4 gt[2][4];
+      const bool gated = a.gate && slot < 0 && there;
+      auto gates = [&](uint4 (&to)[4], int d) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) gt[k] = ra_ldg128(a.gate + orow * D + 8 * k);
+        for (int k = 0; k < 4; ++k) to[k] = ra_ldg128(a.gate + at + d + 8 * k);
+      };
+      if (gated) {
+        gates(gt[0], 0);
+        gates(gt[1], 32);
       }
       if (cnt > 0) {
-        if (kTiles == 1 && cnt > 1 && !(ok = outputs_of(g - 2, 0))) break;
+        if (kSub == 1 && cnt > 1 && !(ok = outputs_of(g - 2, 0))) break;
         if (!(ok = outputs_of(g - 1, npv - 1))) break;
         tmem_fence_after();
       }
-      float s0, s1, s2, s3;
-      ra_unpair(l2[0], s0, s1);
-      ra_unpair(l2[1], s2, s3);
-      const float l = (s0 + s1) + (s2 + s3);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const uint32_t to_ = lanes + C::kColO + w * D;
+      if (pi->b1 > pi->edge) {  // values that were none, of edge blocks (a pair's CTAs note their own columns)
+        bool special = *(volatile int*)&sh.special[it % C::kRing];
+        if (kPair) special = special || ra_ld_pair(&sh.special[it % C::kRing], rank ^ 1);
+#pragma unroll 1
+        for (int d = 0; d < D && special && cnt > 0; ++d) {
+          const int* p = &sh.poison[it % C::kRing][d];
+          const int from = kPair && d / C::kVCols != rank ? ra_ld_pair(p, rank ^ 1) : *(const volatile int*)p;
+          if (!__any_sync(0xFFFFFFFFu, lim > from)) continue;
+          uint32_t y;
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(y) : "r"(to_ + d) : "memory");
+          if (lim > from) y = 0x7FFFFFFFu;
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\ntcgen05.wait::st.sync.aligned;" ::"r"(to_ + d), "r"(y) : "memory");
+        }
+      }
       const size_t ps = (size_t)c * 2 + max(slot, 0);
 #pragma unroll 1
       for (int d = 0; d < D && !idle; d += 32) {
@@ -1065,30 +1286,32 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 32; ++k) y[k] = 0;
         }
-        if (special) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (lim > poison[d + k]) y[k] = 0x7FFFFFFFu;
-        }
-        if (!there) {
-        } else if (slot >= 0) {
+        if (slot >= 0) {
           float* o = a.part_o + (ps * (D / 4) + d / 4) * (C::kRows * 4) + r * 4;
+          if (there) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            __stcg(reinterpret_cast<uint4*>(o + k * (C::kRows * 4)), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
-        } else {
-          uint16_t* o = a.out + orow * D + d;
+            for (int k = 0; k < 8; ++k)
+              __stcg(reinterpret_cast<uint4*>(o + k * (C::kRows * 4)), make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]));
+          }
+        } else if (there) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(y[8 * k + e]) * inv;
-            if (a.gate) {
-              ra_gate(v, gt[k]);
-              if (d + 32 < D) gt[k] = ra_ldg128(a.gate + orow * D + d + 32 + 8 * k);
+            if (gated) {
+              ra_gate2(v[0], v[1], gt[0][k].x);
+              ra_gate2(v[2], v[3], gt[0][k].y);
+              ra_gate2(v[4], v[5], gt[0][k].z);
+              ra_gate2(v[6], v[7], gt[0][k].w);
             }
-            *reinterpret_cast<uint4*>(o + 8 * k) =
+            *reinterpret_cast<uint4*>(a.out + at + d + 8 * k) =
                 make_uint4(ra_bf16x2(v[0], v[1]), ra_bf16x2(v[2], v[3]), ra_bf16x2(v[4], v[5]), ra_bf16x2(v[6], v[7]));
+          }
+          if (gated) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) gt[0][k] = gt[1][k];
+            if (d + 64 < D) gates(gt[1], d + 64);
           }
         }
         __syncwarp();
@@ -1097,34 +1320,55 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         if (slot >= 0)
           __stcg(reinterpret_cast<float2*>(a.part_ml + (ps * 256 + r) * 2), make_float2(m, l));
         else if (a.lse)
-          a.lse[orow] = ra_lse(m, l);
+          a.lse[at / D] = ra_lse(m, l);
       }
-      if (cnt > 0) tmem_fence_before();
+      tmem_fence_before();
+      if (kPair) {  // the other CTA reads this one's poison
+        __syncwarp();
+        if (lane == 0) ra_arrive_first(smem_addr(&sh.iempty[it % C::kRing]), rank ^ 1);
+      }
       release(it);
-      pi = next;
     }
   }
   tmem_fence_before();
   __syncthreads();
+  if (kPair) ra_pair_sync();  // nothing of the other CTA's is on its way here
   tmem_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else
+      tmem_dealloc(tmem, 512);
+  }
 }
 
 template <int D, int kTiles, int kSrc>
 cudaError_t launch_one(const RowsArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  using C = RaCfg<D, kTiles, kSrc>;
   constexpr int kSmem = ra_smem<D, kTiles, kSrc>();
   static_assert(kSmem <= kSmemBytes, "shared memory");
+  auto* kern = rows_kernel<D, kTiles, kSrc>;
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !done[dev].load()) {
-    e = cudaFuncSetAttribute(rows_kernel<D, kTiles, kSrc>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(true);
   }
-  rows_kernel<D, kTiles, kSrc><<<grid, (RaCfg<D, kTiles, kSrc>::kThreads), kSmem, s>>>(a, kmap, vmap);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(C::kPair ? grid / 2 * 2 : grid));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = C::kPair ? 2 : 1;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, kmap, vmap);
 }
 
 }  // namespace

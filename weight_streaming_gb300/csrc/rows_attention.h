@@ -29,7 +29,7 @@ struct RowsArgs {
   float scale2;                // |scale| * log2(e), 1 for scale 0
   int4* desc;                  // [grid][2]: s, h, first token (-1: no part), rows | ends << 16 (below)
   float* part_ml;              // [grid][2][256][2]: maximum (log2 units), sum
-  float* part_o;               // [grid][2][D / 4][rows][4]
+  float* part_o;               // [grid or pairs][2][D / 4][rows][4]
   int* status;
 };
 
@@ -44,9 +44,13 @@ extern template cudaError_t launch_rows<64, 1>(const RowsArgs&, int, const CUten
 extern template cudaError_t launch_rows<64, 2>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 extern template cudaError_t launch_rows<128, 1>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 extern template cudaError_t launch_rows<128, 2>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+extern template cudaError_t launch_rows<256, 2>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 extern template cudaError_t launch_rows<256, 1>(const RowsArgs&, int, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 
-// Key rows of a tile (the tensor map's box, too).
-constexpr int rows_block(int D) { return D == 256 ? 64 : 128; }
+// Keys of a block, and this CTA's rows and columns of its key and value tiles (the tensor maps' boxes, too): with 256
+// columns an item's two tiles lie in a pair of CTAs, which hold half of the keys and half of the values' columns each.
+constexpr int rows_block(int D, int tiles) { return D == 256 && tiles == 1 ? 64 : 128; }
+constexpr int rows_key_rows(int D, int tiles) { return D == 256 ? 64 : 128; }
+constexpr int rows_value_cols(int D, int tiles) { return D == 256 && tiles == 2 ? 128 : D; }
 
 }  // namespace vp
