@@ -710,8 +710,8 @@ vp_status vp_paged_attention_rows(const vp_paged_cache* cache, const void* q, co
                                   int S, int M, int Hq, float scale, const void* gate, void* out, float* lse, void* ws,
                                   size_t ws_bytes, void* stream);
 
-/* The paged cache in 8 bits: per position and head D e4m3 codes and one power of two, value = e4m3(code) * 2^(scale - 127)
- * (scale 255, or code 0x7F: NaN).  k, v: bytes [n_pages][Hkv][page_size][D]; k_scales, v_scales: bytes
+/* The paged cache in 8 bits: per position and head D e4m3 codes and one power of two, value = e4m3(code) * 2^(scale - 127),
+ * NaN where the scale is 255 (and there alone: a code 0x7F under another scale, which the append does not write, reads as 480).  k, v: bytes [n_pages][Hkv][page_size][D]; k_scales, v_scales: bytes
  * [n_pages][Hkv][page_size]; all 16-byte aligned; the rest as vp_paged_cache.  2 (D + 1) bytes per position and head in
  * place of 4 D. */
 typedef struct {

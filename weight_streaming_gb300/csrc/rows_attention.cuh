@@ -275,34 +275,31 @@ __device__ __forceinline__ uint4 ra_ldg128(const void* p) {
 // Whether one of a pair's bf16 values is infinite or NaN: the exponent's ones carry into the sign.
 __device__ __forceinline__ uint32_t ra_special(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
 
-// v *= sigmoid(g) for two bf16 gates.
+// v *= sigmoid(g) for two bf16 gates.  By half the exponential twice: e^g itself leaves fp32's range long before the product
+// does (NaN stays NaN).
 __device__ __forceinline__ void ra_gate2(float& v0, float& v1, uint32_t w) {
-  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kHalfLog2e = 0.7213475204444817f;
   const float g0 = __uint_as_float(w << 16), g1 = __uint_as_float(w & 0xFFFF0000u);
-  if (fminf(g0, g1) > -60.0f) {
-    v0 = __fdividef(v0, 1.0f + ra_ex2(-kLog2e * g0));
-    v1 = __fdividef(v1, 1.0f + ra_ex2(-kLog2e * g1));
-  } else {  // by half the exponential twice: e^g itself leaves fp32's range long before the product does (NaN stays NaN)
-    const float h0 = ra_ex2(-0.5f * kLog2e * fabsf(g0)), h1 = ra_ex2(-0.5f * kLog2e * fabsf(g1));
-    v0 = (g0 < 0.0f ? v0 * h0 * h0 : v0) / fmaf(h0, h0, 1.0f);
-    v1 = (g1 < 0.0f ? v1 * h1 * h1 : v1) / fmaf(h1, h1, 1.0f);
-  }
+  const float h0 = ra_ex2(-kHalfLog2e * fabsf(g0)), h1 = ra_ex2(-kHalfLog2e * fabsf(g1));
+  const float n0 = g0 < 0.0f ? h0 : 1.0f, n1 = g1 < 0.0f ? h1 : 1.0f;
+  v0 = __fdividef(v0 * n0 * n0, fmaf(h0, h0, 1.0f));
+  v1 = __fdividef(v1 * n1 * n1, fmaf(h1, h1, 1.0f));
 }
 // log sum exp from the reference in log2 units and the sum of 2^(t - m).
 __device__ __forceinline__ float ra_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Codes to bf16: a tile of kRowsT rows of kCols codes, then a scale byte per row, to an operand tile, by 128 threads.  Eight
+// Codes to bf16: a tile of kRowsT rows of kCols codes, then a scale byte per row, to an operand tile, by kThreads threads.  Eight
 // lanes take 64 codes of each of two rows, of neighbouring column groups where there are several: reads and writes then meet
-// every bank once.  Scales from 2^8 on (the factor leaves bf16's range) and codes 0x7F are left to ra_expand_rare, for which
-// this says whether there are any.
-template <int kCols, int kRowsT>
+// every bank once.  Scales from 2^8 on (the factor leaves bf16's range; 255 is NaN) are left to ra_expand_rare, for which this
+// says whether there are any.  (A code 0x7F under another scale, which the append does not write, comes out as 480.)
+template <int kCols, int kRowsT, int kThreads>
 struct RaUnit {  // unit u (of kRowsT * kCols / 16) of thread tid: 16 codes
   int row, ch, i;
   __device__ RaUnit(int tid, int u) {
     constexpr int kChunks = kCols / 64;
-    const int qd = (tid >> 3) + 16 * u, rsel = tid >> 2 & 1;
+    const int qd = (tid >> 3) + kThreads / 8 * u, rsel = tid >> 2 & 1;
     row = 2 * (qd / kChunks) + rsel;
     ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
     i = tid & 3;
@@ -318,57 +315,56 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-template <int kCols, int kRowsT>
+template <int kCols, int kRowsT, int kThreads>
 __device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
-  constexpr int kUnits = kRowsT * kCols / 16 / 128, kAtOnce = 4;
-  uint32_t rare = 0;
+  constexpr int kUnits = kRowsT * kCols / 16 / kThreads, kAtOnce = kUnits < 4 ? kUnits : 4;
+  bool rare = false;
 #pragma unroll 1
   for (int u0 = 0; u0 < kUnits; u0 += kAtOnce) {
     uint4 w[kAtOnce];
     uint32_t e[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const RaUnit<kCols, kRowsT> u(tid, u0 + k);
+      const RaUnit<kCols, kRowsT, kThreads> u(tid, u0 + k);
       w[k] = lds128(u.in(src));
       e[k] = lds8(u.scale(src));
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const RaUnit<kCols, kRowsT> u(tid, u0 + k);
+      const RaUnit<kCols, kRowsT, kThreads> u(tid, u0 + k);
       const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w}, f = (e[k] + 120) * 0x00800080u;  // 2^(120 + scale - 127)
       uint32_t o[8];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         o[2 * x] = ra_bmul2(ra_code2<0x9180>(in[x]), f);
         o[2 * x + 1] = ra_bmul2(ra_code2<0xB3A2>(in[x]), f);
-        rare |= (in[x] & 0x7F7F7F7Fu) + 0x01010101u;
       }
-      if (e[k] > 134) rare = 0x80u;
+      rare = rare || e[k] > 134;
       sts128(u.out(dst, 0), make_uint4(o[0], o[1], o[2], o[3]));
       sts128(u.out(dst, 1), make_uint4(o[4], o[5], o[6], o[7]));
     }
   }
-  return rare & 0x80808080u;
+  return rare;
 }
-template <int kCols, int kRowsT>
+template <int kCols, int kRowsT, int kThreads>
 __device__ __forceinline__ void ra_expand_rare(uint32_t src, uint32_t dst, int tid) {
 #pragma unroll 1
-  for (int k = 0; k < kRowsT * kCols / 128; ++k) {
-    const RaUnit<kCols, kRowsT> u(tid, k >> 4);
+  for (int k = 0; k < kRowsT * kCols / kThreads; ++k) {
+    const RaUnit<kCols, kRowsT, kThreads> u(tid, k >> 4);
     const uint32_t code = lds8(u.in(src) + (k & 15)), e = lds8(u.scale(src));
     const uint32_t bits = (code & 0x80) << 8 | (code & 0x7F) << 4, one = e == 0 ? 0x40u : e << 7;
     uint32_t v = ra_bmul2(ra_bmul2(bits, 0x7B80u), one) & 0xFFFFu;
-    if ((code & 0x7F) == 0x7F || e == 255) v = 0x7FFFu;
+    if (e == 255) v = 0x7FFFu;
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(u.out(dst, k >> 3 & 1) + (k & 7) * 2), "h"((uint16_t)v) : "memory");
   }
 }
 // A value tile with keys that some row does not see, or without keys in part (rows from `left` on, `bad` groups of 16 rows):
 // what lies in those becomes zeros (weights of zero times what lies there), and, where the block is an edge block, so do
 // infinite and NaN values, whose key is noted by column.
-template <int kCols, int kRowsT>
+template <int kCols, int kRowsT, int kThreads>
 __device__ __forceinline__ void ra_look(uint32_t tile, int tid, int left, uint32_t bad, bool edge, int key0, int* poison, int* special) {
 #pragma unroll 1
-  for (int u = tid; u < kRowsT * kCols / 8; u += 128) {
+  for (int u = tid; u < kRowsT * kCols / 8; u += kThreads) {
     const int ch = u / (kRowsT * 8), row = (u >> 3) % kRowsT, d = ch * 64 + (((u & 7) ^ (row & 7)) << 3);
     const uint32_t at = tile + u * 16;
     if (row >= left || (bad >> (row >> 4) & 1)) {
@@ -450,7 +446,8 @@ template <int D, int kTiles, int kSrc>
 struct RaCfg {
   static constexpr bool kFp8 = kSrc == kPagedFp8, kPair = D == 256 && kTiles == 2;
   static constexpr int kSub = kPair ? 1 : kTiles;                    // tiles in a CTA
-  static constexpr int kSoft = 4 * kSub, kThreads = 32 * (8 + kSoft);  // softmax warps
+  // warps that prepare operands (expanding codes is most of the work where few rows use them), softmax warps
+  static constexpr int kPrep = kFp8 && kTiles == 1 ? 8 : 4, kSoft = 4 * kSub, kThreads = 32 * (4 + kPrep + kSoft);
   static constexpr int kBlock = rows_block(D, kTiles);
   static constexpr int kRows = 128 * kTiles;
   // operand tiles in a CTA: key rows and columns; a pair's CTA holds half of the keys, and half of the values' columns
@@ -469,8 +466,10 @@ struct RaCfg {
   static constexpr int kColO = 2 * kColS;
   static constexpr int kColQ = kColO + D;
   // registers: what issues keeps few, what prepares operands some, the softmax warps take the rest of the launch's
-  static constexpr int kRegIssue = kSub == 2 ? 64 : 104, kRegPrep = kSub == 2 ? 64 : 168, kRegSoft = kSub == 2 ? 192 : 232;
-  static_assert(4 * kRegIssue + 4 * kRegPrep + kSoft * kRegSoft <= kThreads / 32 * (65536 / kThreads / 8 * 8), "");
+  static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegIssue = kLaunch == 128 ? 64 : 104, kRegPrep = kSub == 2 ? 64 : kPrep == 8 ? 96 : 168,
+                       kRegSoft = kSub == 2 ? 192 : 232;
+  static_assert(4 * kRegIssue + kPrep * kRegPrep + kSoft * kRegSoft <= kThreads / 32 * kLaunch, "");
   static_assert(kColO + kSub * D <= 512 && (kQSmem || kColQ + D / 2 <= 512), "");
 };
 template <int D, int kTiles, int kSrc>
@@ -478,7 +477,7 @@ struct RaShared {
   using C = RaCfg<D, kTiles, kSrc>;
   uint64_t full[C::kStages], ready[C::kStages], empty[C::kStages];
   uint64_t rfull[8], rempty[8];
-  uint64_t sfull[2], pfull[2][2], ofull[2], qfull[2], qfree[2];
+  uint64_t sfull[2], pfull[2][2], ofull[2], opart[2], qfull[2], qfree[2];
   uint64_t ifull[C::kRing], iempty[C::kRing], drain;
   unsigned long long scan[C::kThreads / 32];
   unsigned long long x0, x1, base;
@@ -572,23 +571,24 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.ready[i], (C::kFp8 ? 4 : 5) * kBoth);  // the preparing warps and the copying one, or that one in their place
+      mbar_init(&sh.ready[i], (C::kFp8 ? C::kPrep : 5) * kBoth);  // the preparing warps and the copying one, or that one in their place
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.rfull[i], 1);
-      mbar_init(&sh.rempty[i], 4);
+      mbar_init(&sh.rempty[i], C::kPrep);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sfull[i], 1);
       for (int k = 0; k < 2; ++k) mbar_init(&sh.pfull[i][k], 4 * kBoth);
       mbar_init(&sh.ofull[i], 1);
+      mbar_init(&sh.opart[i], 1);
       mbar_init(&sh.qfull[i], 4 * kBoth);
       mbar_init(&sh.qfree[i], 4);
     }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&sh.ifull[i], 1);
-      mbar_init(&sh.iempty[i], 2 + 4 + C::kSoft * kBoth);  // copying, issuing, preparing and softmax warps (a pair's: of both)
+      mbar_init(&sh.iempty[i], 2 + C::kPrep + C::kSoft * kBoth);  // copying, issuing, preparing and softmax warps (a pair's: of both)
     }
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
@@ -882,7 +882,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         for (int part = 0; part < C::kParts; ++part) {
           if (!wait(&sh.pfull[i][part], ppar >> i & 1)) return false;
           tmem_fence_after();
-          if (ra_elect()) outputs(i, o, stage, part, accumulate || part > 0);
+          if (ra_elect()) {
+            outputs(i, o, stage, part, accumulate || part > 0);
+            if (part + 1 < C::kParts) ra_commit<kPair>(&sh.opart[i]);
+          }
           __syncwarp();
         }
         ppar ^= 1u << i;
@@ -973,10 +976,11 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         mbar_wait_bounded(&sh.drain, 0);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 4 + C::kPrep) {
     // ------------------------------------------------------------ queries, values that need a look, 8-bit tiles
-    if constexpr (C::kRegPrep < 65536 / C::kThreads / 8 * 8)
+    if constexpr (C::kRegPrep < C::kLaunch)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegPrep));
+    constexpr int kPrepT = 32 * C::kPrep;
     const int tid = threadIdx.x - 128, quad = warp & 3;
     int st = 0, g = 0, rst = 0, done = 0;
     int nq0 = 0, nq1 = 0;  // query tiles so far
@@ -1040,7 +1044,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       int* const poison = sh.poison[it % C::kRing] + (kPair ? rank * C::kVCols : 0);
       int* const special = &sh.special[it % C::kRing];
       // the queries and gates on their way to L2, ahead of those who read them
-      for (int u = tid; u < min(pi->toks * a.G - (kPair ? rank * 128 : 0), kSub * 128) * kChunks; u += 128) {
+      for (int u = tid; u < min(pi->toks * a.G - (kPair ? rank * 128 : 0), kSub * 128) * kChunks; u += 32 * C::kPrep) {
         const int row = u / kChunks + (kPair ? rank * 128 : 0), t = row * a.g_inv >> 16, hd = pi->h * a.G + row - t * a.G;
         if (it > 0) ra_prefetch(a.q + (size_t)(pi->row + t) * a.ld_q + (size_t)hd * D + u % kChunks * 64);
         if (a.gate) ra_prefetch(a.gate + ((size_t)(pi->row + t) * a.Hq + hd) * D + u % kChunks * 64);
@@ -1050,7 +1054,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         if (nq0 > 0 && !(ok = wait(&sh.qfree[0], (nq0 - 1) & 1))) break;
         ++nq0;
         tmem_fence_after();
-        load_q(*pi, 0);
+        if (warp < 8) load_q(*pi, 0);
       }
       if (kSub == 2 && pi->cnt[1] > 0) {
         if (nq1 > 0 && !(ok = wait(&sh.qfree[1], (nq1 - 1) & 1))) break;
@@ -1069,19 +1073,19 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             if (!(ok = wait(&sh.rfull[rst], rpar) && wait(&sh.empty[st], wpar))) break;
             const uint32_t src = raw + rst * C::kRaw;
             if (C::kKRows == BN || kv) {
-              if (ra_expand<C::kVCols, BN>(src, tile, tid)) ra_expand_rare<C::kVCols, BN>(src, tile, tid);
+              if (ra_expand<C::kVCols, BN, kPrepT>(src, tile, tid)) ra_expand_rare<C::kVCols, BN, kPrepT>(src, tile, tid);
             } else {
-              if (ra_expand<D, C::kKRows>(src, tile, tid)) ra_expand_rare<D, C::kKRows>(src, tile, tid);
+              if (ra_expand<D, C::kKRows, kPrepT>(src, tile, tid)) ra_expand_rare<D, C::kKRows, kPrepT>(src, tile, tid);
             }
             // (a unit's values may be another thread's to look at)
-            asm volatile("bar.sync 15, 128;" ::: "memory");
+            asm volatile("bar.sync 15, %0;" ::"n"(kPrepT) : "memory");
           } else {
             if (!(ok = wait(&sh.full[st], fpar >> st & 1))) break;
             fpar ^= 1u << st;
           }
           const uint32_t bad = C::kFp8 ? *(volatile uint32_t*)&sh.bad[g & 15] : 0;  // (else filled with zeros)
           const bool look = kv && (b >= edge || bad);
-          if (look) ra_look<C::kVCols, BN>(tile, tid, keys - b * BN, bad, b >= edge, b * BN, poison, special);
+          if (look) ra_look<C::kVCols, BN, kPrepT>(tile, tid, keys - b * BN, bad, b >= edge, b * BN, poison, special);
           if (C::kFp8 || look) fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -1102,7 +1106,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ------------------------------------------------------------ softmax: rows of the CTA's tile w, a thread per row
-    const int sm = warp - 8, w = sm >> 2, quad = warp & 3;
+    const int w = (warp - 4 - C::kPrep) >> 2, quad = warp & 3;
     const int row0 = (kPair ? rank : w) * 128 + quad * 32, r = row0 + lane;  // of the item
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const int tok = r * a.g_inv >> 16, first_tok = row0 * a.g_inv >> 16;
@@ -1120,16 +1124,15 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       const int lim = tok < toks ? min(pi->lim0 + tok, pi->keys) : pi->keys;  // keys that this row sees
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
       const bool idle = first_tok >= toks;  // no row of the warp is there
-      float m = -INFINITY;                  // reference of the exponents (log2 units)
+      float m = -INFINITY, mc = 0.0f;       // reference of the exponents (log2 units), and what is subtracted
       uint64_t l2[2] = {0, 0};              // sums of the weights
-      for (int j = 0; j < cnt; ++j) {
-        const int buf = kSub == 2 ? w : (g + j) & 1;
-        const uint32_t sp = kSub == 2 ? (uint32_t)(npv & 1) : (uint32_t)((g + j) >> 1 & 1);
+      for (int j = 0; ok && j < cnt; ++j) {
+        const int n = g + j, buf = kSub == 2 ? w : n & 1;
         // Every phase of the outputs' barriers is waited for in turn: a wait tells a phase from the one before it only.  The
-        // last outputs on the barrier come before these scores: no time passes for them.
-        ok = wait(&sh.sfull[buf], sp);
-        if (ok && j >= 3 - kSub) ok = outputs_of(g + j - 2, npv - 1);
-        if (!ok) break;
+        // last outputs on the barriers end before these scores do: no time passes for them.
+        if (j >= 3 - kSub && !(ok = outputs_of(n - 2, npv - 1))) break;
+        if (kSub == 1 && C::kParts > 1 && n >= 2 && !(ok = wait(&sh.opart[buf], (n >> 1) - 1 & 1))) break;
+        if (!(ok = wait(&sh.sfull[buf], kSub == 2 ? npv & 1 : n >> 1 & 1))) break;
         if (j == cnt - 1) {  // the queries have been read
           tmem_fence_before();
           __syncwarp();
@@ -1139,95 +1142,86 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           tmem_fence_before();
           __syncwarp();
           if (lane < C::kParts) arrive_first_relaxed(&sh.pfull[buf][lane]);
-          ++npv;
-          continue;
-        }
-        tmem_fence_after();
-        const uint32_t ts = lanes + buf * C::kColS;
-        const int key0 = (b0 + j) * BN;
-        const uint32_t bad = kSrc == kDense ? 0 : *(volatile uint32_t*)&sh.bad[(g + j) & 15];
-        if (key0 + BN > lim_min || bad) {  // keys that a row does not see
+        } else {
+          tmem_fence_after();
+          const uint32_t ts = lanes + buf * C::kColS;
+          const uint32_t bad = kSrc == kDense ? 0 : *(volatile uint32_t*)&sh.bad[n & 15];
+          uint32_t x[64];
+          ra_ld32(ts, x);
+          ra_ld32(ts + 32, x + 32);
+          // 64 keys at a time, whose weights the products can start with
 #pragma unroll 1
-          for (int k0 = 0; k0 < BN; k0 += 32) {
-            const int sees = lim - key0 - k0;
-            const uint32_t groups = bad >> (k0 / 16);
-            uint32_t x[32];
-            ra_ld32(ts + k0, x);
+          for (int part = 0; part < C::kParts; ++part) {
+            const int key0 = (b0 + j) * BN + part * 64;
             ra_wait32(x);
+            ra_wait32(x + 32);
+            const uint32_t groups = bad >> (part * 4);
+            if (key0 + 64 > lim_min || (groups & 15)) {  // keys that a row does not see
+              const int sees = lim - key0;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (k >= sees || (groups >> (k >> 4) & 1)) x[k] = 0xFF800000u;
-            ra_st32(ts + k0, x);
-          }
-          tmem_wait_st();
-        }
-        // The scores are read twice, 32 at a time: unrolled over all of them the loop is too long for the instruction caches.
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        {
-          uint32_t x[2][32];
-          ra_ld32(ts, x[0]);
+              for (int k = 0; k < 64; ++k)
+                if (k >= sees || (groups >> (k >> 4) & 1)) x[k] = 0xFF800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = ra_max3(__uint_as_float(x[3 * e]), __uint_as_float(x[3 * e + 1]), __uint_as_float(x[3 * e + 2]));
+#pragma unroll
+            for (int k = 12; k < 64; k += 2)
+              mx[k / 2 % 4] = ra_max3(mx[k / 2 % 4], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+            const float top = fmaxf(ra_max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale2;
+            // The reference follows the maximum only where that has grown by 2^8: a weight may reach 2^8, which costs bf16
+            // nothing, and the outputs are seldom scaled again.
+            const bool grow = top > m + 8.0f || (m == -INFINITY && top > m);
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+              const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
+              m = to;
+              mc = m == -INFINITY ? 0.0f : m;
+              if (j + part > 0) {
+                const uint64_t ff = ra_pair(f, f), zero = 0;
+                l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
+                // the last block's outputs, and those of this block's first weights
+                if (kSub == 1 && j > 0 && !(ok = outputs_of(n - 1, 0))) break;
+                if (part > 0 && !(ok = wait(&sh.opart[buf], kSub == 2 ? npv & 1 : n >> 1 & 1))) break;
+                tmem_fence_after();
+                const uint32_t to_ = lanes + C::kColO + w * D;
 #pragma unroll 1
-          for (int k0 = 0; k0 < BN; k0 += 64) {
+                for (int d = 0; d < D; d += 16) {
+                  uint32_t y[16];
+                  ra_ld16(to_ + d, y);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                  ra_st16(to_ + d, y);
+                }
+              }
+            }
+            const uint64_t mc2 = ra_pair(-mc, -mc);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              ra_wait32(x[h]);
-              if (h == 0 || k0 + 64 < BN) ra_ld32(ts + k0 + 32 * (h + 1), x[h ^ 1]);
+              uint32_t p[16];
 #pragma unroll
-              for (int k = 0; k < 32; k += 2)
-                mx[k / 2 % 4] = ra_max3(mx[k / 2 % 4], __uint_as_float(x[h][k]), __uint_as_float(x[h][k + 1]));
+              for (int e = 0; e < 16; ++e) {
+                float lo, hi;
+                ra_unpair(ra_fma2(ra_pair(__uint_as_float(x[32 * h + 2 * e]), __uint_as_float(x[32 * h + 2 * e + 1])), scale_2, mc2),
+                          lo, hi);
+                lo = ra_ex2(lo), hi = ra_ex2(hi);
+                l2[e & 1] = ra_add2(l2[e & 1], ra_pair(lo, hi));
+                p[e] = ra_bf16x2(lo, hi);
+              }
+              ra_st16(ts + part * 32 + h * 16, p);  // over the scores, behind what is still read
             }
-          }
-        }
-        uint32_t x[2][32];
-        ra_ld32(ts, x[0]);  // again, while the reference is found
-        float top = fmaxf(ra_max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale2;
-        // The reference follows the maximum only where that has grown by 2^8: a weight may reach 2^8, which costs bf16
-        // nothing, and the outputs are seldom scaled again.
-        bool grow = top > m + 8.0f || (m == -INFINITY && top > m);
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
-          m = to;
-          if (j > 0) {
-            const uint64_t ff = ra_pair(f, f), zero = 0;
-            l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
-            if (kSub == 1 && !(ok = outputs_of(g + j - 1, 0))) break;
-            tmem_fence_after();
-            const uint32_t to_ = lanes + C::kColO + w * D;
-#pragma unroll 1
-            for (int d = 0; d < D; d += 16) {
-              uint32_t y[16];
-              ra_ld16(to_ + d, y);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-              ra_st16(to_ + d, y);
+            if (part + 1 < C::kParts) {
+              ra_ld32(ts + (part + 1) * 64, x);
+              ra_ld32(ts + (part + 1) * 64 + 32, x + 32);
             }
+            tmem_wait_st();
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0 && !(hook == 2 && it == 0 && j == 0 && warp == 4 + C::kPrep)) arrive_first_relaxed(&sh.pfull[buf][part]);
           }
+          if (!ok) break;
         }
-        const float mc = m == -INFINITY ? 0.0f : m;
-        const uint64_t mc2 = ra_pair(-mc, -mc);
-        // the weights go over the scores, 32 over the first 16 columns and so on: behind what is still read
-#pragma unroll 1
-        for (int k0 = 0; k0 < BN; k0 += 64) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ra_wait32(x[h]);
-            if (h == 0 || k0 + 64 < BN) ra_ld32(ts + k0 + 32 * (h + 1), x[h ^ 1]);
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float lo, hi;
-              ra_unpair(ra_fma2(ra_pair(__uint_as_float(x[h][2 * e]), __uint_as_float(x[h][2 * e + 1])), scale_2, mc2), lo, hi);
-              lo = ra_ex2(lo), hi = ra_ex2(hi);
-              l2[e & 1] = ra_add2(l2[e & 1], ra_pair(lo, hi));
-              p[e] = ra_bf16x2(lo, hi);
-            }
-            ra_st16(ts + (k0 + 32 * h) / 2, p);
-          }
-          tmem_wait_st();
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0 && !(hook == 2 && it == 0 && j == 0 && warp == 8)) arrive_first_relaxed(&sh.pfull[buf][k0 / 64]);
-        }
+        if (kSub == 2 && !(ok = wait(&sh.opart[w], npv & 1))) break;
         ++npv;
       }
       if (!ok) break;
