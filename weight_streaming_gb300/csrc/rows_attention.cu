@@ -167,7 +167,7 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   const int tiles = rows_tiles(x.S, x.M, x.Hq, x.Hkv);
   a.tok_tile = 128 * tiles / a.G;
   a.g_inv = (65536 + a.G - 1) / a.G;
-  a.item_cost = 256;
+  a.item_cost = 384;
   const int grid = std::min(sms, kRowsGrid);
   cudaError_t e;
   if (x.D == 256)

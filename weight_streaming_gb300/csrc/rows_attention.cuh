@@ -19,6 +19,9 @@ __device__ __forceinline__ bool ra_elect() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
   return p != 0;
 }
+// A value that is the same in the whole warp, as one that the compiler knows to be: the products' operands are uniform
+// registers, and moving others there costs more than a product takes.
+__device__ __forceinline__ int ra_uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ void ra_arrive(uint32_t bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar) : "memory");
 }
@@ -290,16 +293,16 @@ __device__ __forceinline__ float ra_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Codes to bf16: a tile of kRowsT rows of kCols codes, then a scale byte per row, to an operand tile, by kThreads threads.  Eight
+// Codes to bf16: a tile of kRowsT rows of kCols codes, then a scale byte per row, to an operand tile, by 128 threads.  Eight
 // lanes take 64 codes of each of two rows, of neighbouring column groups where there are several: reads and writes then meet
 // every bank once.  Scales from 2^8 on (the factor leaves bf16's range; 255 is NaN) are left to ra_expand_rare, for which this
 // says whether there are any.  (A code 0x7F under another scale, which the append does not write, comes out as 480.)
-template <int kCols, int kRowsT, int kThreads>
+template <int kCols, int kRowsT>
 struct RaUnit {  // unit u (of kRowsT * kCols / 16) of thread tid: 16 codes
   int row, ch, i;
   __device__ RaUnit(int tid, int u) {
     constexpr int kChunks = kCols / 64;
-    const int qd = (tid >> 3) + kThreads / 8 * u, rsel = tid >> 2 & 1;
+    const int qd = (tid >> 3) + 16 * u, rsel = tid >> 2 & 1;
     row = 2 * (qd / kChunks) + rsel;
     ch = kChunks > 1 ? (qd % kChunks) ^ rsel : 0;
     i = tid & 3;
@@ -315,9 +318,9 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
-template <int kCols, int kRowsT, int kThreads>
+template <int kCols, int kRowsT>
 __device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
-  constexpr int kUnits = kRowsT * kCols / 16 / kThreads, kAtOnce = kUnits < 4 ? kUnits : 4;
+  constexpr int kUnits = kRowsT * kCols / 16 / 128, kAtOnce = 4;
   bool rare = false;
 #pragma unroll 1
   for (int u0 = 0; u0 < kUnits; u0 += kAtOnce) {
@@ -325,13 +328,13 @@ __device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
     uint32_t e[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const RaUnit<kCols, kRowsT, kThreads> u(tid, u0 + k);
+      const RaUnit<kCols, kRowsT> u(tid, u0 + k);
       w[k] = lds128(u.in(src));
       e[k] = lds8(u.scale(src));
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const RaUnit<kCols, kRowsT, kThreads> u(tid, u0 + k);
+      const RaUnit<kCols, kRowsT> u(tid, u0 + k);
       const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w}, f = (e[k] + 120) * 0x00800080u;  // 2^(120 + scale - 127)
       uint32_t o[8];
 #pragma unroll
@@ -346,11 +349,11 @@ __device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
   }
   return rare;
 }
-template <int kCols, int kRowsT, int kThreads>
+template <int kCols, int kRowsT>
 __device__ __forceinline__ void ra_expand_rare(uint32_t src, uint32_t dst, int tid) {
 #pragma unroll 1
-  for (int k = 0; k < kRowsT * kCols / kThreads; ++k) {
-    const RaUnit<kCols, kRowsT, kThreads> u(tid, k >> 4);
+  for (int k = 0; k < kRowsT * kCols / 128; ++k) {
+    const RaUnit<kCols, kRowsT> u(tid, k >> 4);
     const uint32_t code = lds8(u.in(src) + (k & 15)), e = lds8(u.scale(src));
     const uint32_t bits = (code & 0x80) << 8 | (code & 0x7F) << 4, one = e == 0 ? 0x40u : e << 7;
     uint32_t v = ra_bmul2(ra_bmul2(bits, 0x7B80u), one) & 0xFFFFu;
@@ -361,10 +364,10 @@ __device__ __forceinline__ void ra_expand_rare(uint32_t src, uint32_t dst, int t
 // A value tile with keys that some row does not see, or without keys in part (rows from `left` on, `bad` groups of 16 rows):
 // what lies in those becomes zeros (weights of zero times what lies there), and, where the block is an edge block, so do
 // infinite and NaN values, whose key is noted by column.
-template <int kCols, int kRowsT, int kThreads>
+template <int kCols, int kRowsT>
 __device__ __forceinline__ void ra_look(uint32_t tile, int tid, int left, uint32_t bad, bool edge, int key0, int* poison, int* special) {
 #pragma unroll 1
-  for (int u = tid; u < kRowsT * kCols / 8; u += kThreads) {
+  for (int u = tid; u < kRowsT * kCols / 8; u += 128) {
     const int ch = u / (kRowsT * 8), row = (u >> 3) % kRowsT, d = ch * 64 + (((u & 7) ^ (row & 7)) << 3);
     const uint32_t at = tile + u * 16;
     if (row >= left || (bad >> (row >> 4) & 1)) {
@@ -446,8 +449,8 @@ template <int D, int kTiles, int kSrc>
 struct RaCfg {
   static constexpr bool kFp8 = kSrc == kPagedFp8, kPair = D == 256 && kTiles == 2;
   static constexpr int kSub = kPair ? 1 : kTiles;                    // tiles in a CTA
-  // warps that prepare operands (expanding codes is most of the work where few rows use them), softmax warps
-  static constexpr int kPrep = kFp8 && kTiles == 1 ? 8 : 4, kSoft = 4 * kSub, kThreads = 32 * (4 + kPrep + kSoft);
+  // warps that prepare operands (with codes, four expand keys and four values), softmax warps
+  static constexpr int kPrep = kFp8 ? 8 : 4, kSoft = 4 * kSub, kThreads = 32 * (4 + kPrep + kSoft);
   static constexpr int kBlock = rows_block(D, kTiles);
   static constexpr int kRows = 128 * kTiles;
   // operand tiles in a CTA: key rows and columns; a pair's CTA holds half of the keys, and half of the values' columns
@@ -467,8 +470,9 @@ struct RaCfg {
   static constexpr int kColQ = kColO + D;
   // registers: what issues keeps few, what prepares operands some, the softmax warps take the rest of the launch's
   static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
-  static constexpr int kRegIssue = kLaunch == 128 ? 64 : 104, kRegPrep = kSub == 2 ? 64 : kPrep == 8 ? 96 : 168,
-                       kRegSoft = kSub == 2 ? 192 : 232;
+  static constexpr int kRegIssue = kThreads == 640 ? 48 : kSub == 2 || kFp8 ? 64 : 104,
+                       kRegPrep = kThreads == 640 ? 56 : kSub == 2 ? 64 : kFp8 ? 96 : 168,
+                       kRegSoft = kThreads == 640 ? 160 : kSub == 2 ? 192 : 232;
   static_assert(4 * kRegIssue + kPrep * kRegPrep + kSoft * kRegSoft <= kThreads / 32 * kLaunch, "");
   static_assert(kColO + kSub * D <= 512 && (kQSmem || kColQ + D / 2 <= 512), "");
 };
@@ -571,12 +575,12 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.ready[i], (C::kFp8 ? C::kPrep : 5) * kBoth);  // the preparing warps and the copying one, or that one in their place
+      mbar_init(&sh.ready[i], (C::kFp8 ? 4 : 5) * kBoth);  // four preparing warps and the copying one, or that one in their place
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.rfull[i], 1);
-      mbar_init(&sh.rempty[i], C::kPrep);
+      mbar_init(&sh.rempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.sfull[i], 1);
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   __syncthreads();
   if (kPair) ra_pair_sync();  // the other CTA's barriers exist
   tmem_fence_after();
-  const uint32_t tmem = *(volatile uint32_t*)&sh.tmem;
+  const uint32_t tmem = ra_uniform(*(volatile uint32_t*)&sh.tmem);
 
   // Bounded waits of a converged warp; false when one ran out here or elsewhere in the CTA.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -852,16 +856,21 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       int st = 0, g = 0;                       // stage; blocks so far (one tile: of the score buffers)
       uint32_t par = 0, qpar = 0, ppar = 0;    // of the stages, queries, weights (a bit per tile or buffer)
       bool ok = true, first = true;
+      // Four products at a time in a loop: the warps of a scheduler share its instruction cache, and products unrolled all the
+      // way are fetched anew each time, which takes longer than they do (one block's 32 products of 64 cycles: 4,800 cycles).
       auto scores = [&](int i, int stage) {  // tile i, or buffer i of the one tile
-        const uint64_t db = ra_desc_k(ring + stage * C::kTile), da = ra_desc_k(q_s + (kSub == 2 ? i * 128 * D * 2 : 0));
-        const uint32_t d = tmem + i * C::kColS;
+        uint64_t db = ra_desc_k(ring + stage * C::kTile), da = ra_desc_k(q_s + (kSub == 2 ? i * 128 * D * 2 : 0));
+        uint32_t d = tmem + i * C::kColS, qa = tmem + C::kColQ;
+#pragma unroll 1
+        for (int ch = 0; ch < kChunks; ++ch) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t kb = db + (uint64_t)((k / 4) * (kKGroup >> 4) + (k % 4) * 2);
-          if constexpr (C::kQSmem)
-            ra_mma_ss<kPair>(d, da + (uint64_t)((k / 4) * (16384 >> 4) + (k % 4) * 2), kb, kIdS, k > 0);
-          else
-            ra_mma_ts<kPair>(d, tmem + C::kColQ + 8 * k, kb, kIdS, k > 0);
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (C::kQSmem)
+              ra_mma_ss<kPair>(d, da + 2 * k, db + 2 * k, kIdS, ch + k > 0);
+            else
+              ra_mma_ts<kPair>(d, qa + 8 * k, db + 2 * k, kIdS, ch + k > 0);
+          }
+          db += kKGroup >> 4, da += 16384 >> 4, qa += 32;
         }
       };
       // weights of score buffer i, from block part on, into output o
@@ -878,7 +887,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       };
       // Outputs of block j from buffer i as its weights come, a part at a time.
       auto weigh = [&](int i, int o, int stage, bool accumulate) -> bool {
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < C::kParts; ++part) {
           if (!wait(&sh.pfull[i][part], ppar >> i & 1)) return false;
           tmem_fence_after();
@@ -896,12 +905,12 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       };
       for (int it = 0; ok; ++it) {
         const RaItem* pi = get(it);
-        if (!pi || pi->s < 0) break;
+        if (!pi || ra_uniform(pi->s) < 0) break;
         if (kPair && rank) {  // the first CTA issues
           release(it);
           continue;
         }
-        const int nblk = pi->b1 - pi->b0, cnt0 = pi->cnt[0], cnt1 = pi->cnt[1];
+        const int nblk = ra_uniform(pi->b1 - pi->b0), cnt0 = ra_uniform(pi->cnt[0]), cnt1 = ra_uniform(pi->cnt[1]);
         if (cnt0 > 0) ok = q_ready(0);
         if (kSub == 2 && ok && cnt1 > 0) ok = q_ready(1);
         // Scores of block j + 1 and outputs of block j (the ring's order: keys 0, values 0, keys 1, ...).  With two tiles
@@ -980,18 +989,19 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     // ------------------------------------------------------------ queries, values that need a look, 8-bit tiles
     if constexpr (C::kRegPrep < C::kLaunch)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegPrep));
-    constexpr int kPrepT = 32 * C::kPrep;
-    const int tid = threadIdx.x - 128, quad = warp & 3;
-    int st = 0, g = 0, rst = 0, done = 0;
+    const int group = warp >> 3, tid = threadIdx.x - 128 - 128 * group, quad = warp & 3;  // group 1: values of codes
+    int st = group, g = 0, rst = group, done = 0;
     int nq0 = 0, nq1 = 0;  // query tiles so far
     uint32_t fpar = 0, wpar = 1, rpar = 0;  // of the full barriers (a bit each: their phases are the looks'), the stages, the codes
     bool ok = true;
     // This warp's 32 rows of the CTA's tile w; rows that are not there read as zeros, warps without rows load nothing.
-    auto load_q = [&](const RaItem& i, int w) {
+    auto load_q = [&](const RaItem& i, int w, int before) -> bool {
+      auto free = [&]() -> bool { return before == 0 || wait(&sh.qfree[w], (before - 1) & 1); };
+      bool waited = false;
       const int row0 = (kPair ? rank : w) * 128 + quad * 32;  // of the item
       if (row0 * a.g_inv >> 16 < i.toks) {
         if constexpr (C::kQSmem) {  // into shared memory, a row's lanes together
-          constexpr int kLanes = D / 8, kAt = 32 / kLanes, kAtOnce = kSub == 2 ? 4 : 16;
+          constexpr int kLanes = D / 8, kAt = 32 / kLanes, kAtOnce = kSub == 2 ? 8 : 16;
           const int piece = lane % kLanes;
           const uint32_t dst = q_s + w * 128 * D * 2 + (piece >> 3) * 16384;
           const uint16_t* src = a.q + (size_t)i.row * a.ld_q + (size_t)i.h * a.G * D + piece * 8;
@@ -1004,6 +1014,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               v[k] = make_uint4(0, 0, 0, 0);
               if (t < i.toks) v[k] = ra_ldg128(src + t * a.ld_q + (r - t * a.G) * D);
             }
+            if (!waited && !free()) return false;  // the first ones are on their way meanwhile
+            waited = true;
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
               const int row = quad * 32 + (k0 + k) * kAt + lane / kLanes;
@@ -1028,6 +1040,9 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               x[4 * k + 2] = (u.z & a.q_and) ^ a.q_flip, x[4 * k + 3] = (u.w & a.q_and) ^ a.q_flip;
             }
             __syncwarp();
+            if (!waited && !free()) return false;
+            if (!waited) tmem_fence_after();
+            waited = true;
             ra_st32(tmem + ((uint32_t)(quad * 32) << 16) + C::kColQ + ch * 32, x);
           }
           tmem_wait_st();
@@ -1035,7 +1050,9 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
       }
       __syncwarp();
+      if (!waited && !free()) return false;  // (every phase is waited for)
       if (lane == 0) arrive_first(&sh.qfull[w]);
+      return true;
     };
     for (int it = 0; ok; ++it) {
       const RaItem* pi = get(it);
@@ -1044,65 +1061,63 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       int* const poison = sh.poison[it % C::kRing] + (kPair ? rank * C::kVCols : 0);
       int* const special = &sh.special[it % C::kRing];
       // the queries and gates on their way to L2, ahead of those who read them
-      for (int u = tid; u < min(pi->toks * a.G - (kPair ? rank * 128 : 0), kSub * 128) * kChunks; u += 32 * C::kPrep) {
+      for (int u = tid; u < min(pi->toks * a.G - (kPair ? rank * 128 : 0), kSub * 128) * kChunks && group == 0; u += 128) {
         const int row = u / kChunks + (kPair ? rank * 128 : 0), t = row * a.g_inv >> 16, hd = pi->h * a.G + row - t * a.G;
         if (it > 0) ra_prefetch(a.q + (size_t)(pi->row + t) * a.ld_q + (size_t)hd * D + u % kChunks * 64);
         if (a.gate) ra_prefetch(a.gate + ((size_t)(pi->row + t) * a.Hq + hd) * D + u % kChunks * 64);
       }
       // the queries, once the last item's scores are done with theirs
-      if (pi->cnt[0] > 0) {
-        if (nq0 > 0 && !(ok = wait(&sh.qfree[0], (nq0 - 1) & 1))) break;
-        ++nq0;
-        tmem_fence_after();
-        if (warp < 8) load_q(*pi, 0);
-      }
-      if (kSub == 2 && pi->cnt[1] > 0) {
-        if (nq1 > 0 && !(ok = wait(&sh.qfree[1], (nq1 - 1) & 1))) break;
-        ++nq1;
-        load_q(*pi, 1);
+      if (group == 0) {
+        if (pi->cnt[0] > 0) ok = load_q(*pi, 0, nq0++);
+        if (kSub == 2 && ok && pi->cnt[1] > 0) ok = load_q(*pi, 1, nq1++);
+        if (!ok) break;
       }
       for (int b = b0; ok && b < b1; ++b, ++g) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++done) {
-          const uint32_t tile = ring + st * C::kTile;
-          if (!C::kFp8 && !(kv && b >= edge)) {  // nothing to do
-            if (++st == C::kStages) st = 0;
-            continue;
-          }
-          if constexpr (C::kFp8) {
-            if (!(ok = wait(&sh.rfull[rst], rpar) && wait(&sh.empty[st], wpar))) break;
-            const uint32_t src = raw + rst * C::kRaw;
-            if (C::kKRows == BN || kv) {
-              if (ra_expand<C::kVCols, BN, kPrepT>(src, tile, tid)) ra_expand_rare<C::kVCols, BN, kPrepT>(src, tile, tid);
-            } else {
-              if (ra_expand<D, C::kKRows, kPrepT>(src, tile, tid)) ra_expand_rare<D, C::kKRows, kPrepT>(src, tile, tid);
-            }
-            // (a unit's values may be another thread's to look at)
-            asm volatile("bar.sync 15, %0;" ::"n"(kPrepT) : "memory");
+        if constexpr (C::kFp8) {  // every tile: this group's keys, or values
+          const uint32_t tile = ring + st * C::kTile, src = raw + rst * C::kRaw;
+          if (!(ok = wait(&sh.rfull[rst], rpar) && wait(&sh.empty[st], wpar))) break;
+          if (C::kKRows == BN || group) {
+            if (ra_expand<C::kVCols, BN>(src, tile, tid)) ra_expand_rare<C::kVCols, BN>(src, tile, tid);
           } else {
-            if (!(ok = wait(&sh.full[st], fpar >> st & 1))) break;
-            fpar ^= 1u << st;
+            if (ra_expand<D, C::kKRows>(src, tile, tid)) ra_expand_rare<D, C::kKRows>(src, tile, tid);
           }
-          const uint32_t bad = C::kFp8 ? *(volatile uint32_t*)&sh.bad[g & 15] : 0;  // (else filled with zeros)
-          const bool look = kv && (b >= edge || bad);
-          if (look) ra_look<C::kVCols, BN, kPrepT>(tile, tid, keys - b * BN, bad, b >= edge, b * BN, poison, special);
-          if (C::kFp8 || look) fence_proxy_async_smem();
+          const uint32_t bad = *(volatile uint32_t*)&sh.bad[g & 15];
+          if (group && (b >= edge || bad)) {
+            asm volatile("bar.sync 15, 128;" ::: "memory");  // other threads' values are looked at
+            ra_look<C::kVCols, BN>(tile, tid, keys - b * BN, bad, b >= edge, b * BN, poison, special);
+          }
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (!(hook == 4 && done == 0 && warp == 4)) arrive_first(&sh.ready[st]);
-            if (C::kFp8) arrive(&sh.rempty[rst]);
+            arrive(&sh.rempty[rst]);
           }
-          if (C::kFp8 && ++rst == C::kRawStages) rst = 0, rpar ^= 1;
-          if (++st == C::kStages) st = 0, wpar ^= 1;
+          ++done;
+          if ((rst += 2) >= C::kRawStages) rst -= C::kRawStages, rpar ^= 1;
+          if ((st += 2) >= C::kStages) st -= C::kStages, wpar ^= 1;
+        } else {  // values of edge blocks
+          if (++st == C::kStages) st = 0;
+          if (b >= edge) {
+            if (!(ok = wait(&sh.full[st], fpar >> st & 1))) break;
+            fpar ^= 1u << st;
+            ra_look<C::kVCols, BN>(ring + st * C::kTile, tid, keys - b * BN, 0, true, b * BN, poison, special);  // (no pages: zeros)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && !(hook == 4 && done == 0 && warp == 4)) arrive_first(&sh.ready[st]);
+            ++done;
+          }
+          if (++st == C::kStages) st = 0;
         }
       }
       if (ok) release(it);
     }
-    if (C::kFp8)  // no commit is on its way when the CTA ends: a stage's last one frees it
-      for (int i = 0; i < min(done, C::kStages); ++i) {
-        const int e = done - 1 - (done - 1 - i) % C::kStages;
+    if (C::kFp8 && group == 0) {  // no commit is on its way when the CTA ends: a stage's last one frees it
+      const int n = 2 * g;
+      for (int i = 0; i < min(n, C::kStages); ++i) {
+        const int e = n - 1 - (n - 1 - i) % C::kStages;
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.empty[e % C::kStages], (e / C::kStages) & 1))) break;
       }
+    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ------------------------------------------------------------ softmax: rows of the CTA's tile w, a thread per row
