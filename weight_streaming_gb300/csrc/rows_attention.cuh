@@ -116,10 +116,12 @@ __device__ __forceinline__ void ra_expect_first(uint32_t bar, uint32_t bytes) {
       "r"(bytes)
       : "memory");
 }
-__device__ __forceinline__ void ra_bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// 16 bytes by this lane, and its arrival once all of them have landed.
+__device__ __forceinline__ void ra_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ra_copy16_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // Shared-memory operands with the 128-byte swizzle.  K-major (queries, keys): rows 128 bytes apart, groups of 8 rows
 // 1024.  MN-major (values: 64 columns of 16 bits are the 128 bytes, keys the rows): 64-column groups `group` bytes apart.
@@ -460,8 +462,10 @@ struct RaCfg {
   static constexpr int kRaw = kTile / 2 + 128;                       // the same in codes, and the scales' bytes
   static constexpr bool kQSmem = kTiles == 2;                        // else the queries lie in tensor memory
   static constexpr int kQ = kQSmem ? kSub * 128 * D * 2 : 0;
-  static constexpr int kStages = kFp8 ? (D == 64 ? 6 : kPair ? 3 : 4) : D == 64 ? 8 : kTiles == 2 ? 5 : 6;
-  static constexpr int kRawStages = !kFp8 ? 0 : kPair ? 3 : kTiles == 2 ? (D == 64 ? 6 : 2) : D == 64 ? 8 : 5;
+  // stages of keys and of values, rings of their own (with codes: of bf16 tiles, and of codes)
+  static constexpr int kKSt = kFp8 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 3, kVSt = !kFp8 && D > 64 && kTiles == 2 ? 2 : kKSt;
+  static constexpr int kStages = kKSt + kVSt;
+  static constexpr int kRawSt = !kFp8 ? 0 : D == 64 ? 4 : kTiles == 2 ? 1 : 2, kRawStages = 2 * kRawSt;
   static constexpr int kRing = kPair ? 2 : 3;                        // items
   static constexpr int kParts = kBlock / 64;                         // of a block's weights: the products take the first ones early
   // tensor memory: scores (two tiles, or two buffers of one), outputs, queries
@@ -480,7 +484,7 @@ template <int D, int kTiles, int kSrc>
 struct RaShared {
   using C = RaCfg<D, kTiles, kSrc>;
   uint64_t full[C::kStages], ready[C::kStages], empty[C::kStages];
-  uint64_t rfull[8], rempty[8];
+  uint64_t rfull[C::kRawStages + 1], rempty[C::kRawStages + 1];
   uint64_t sfull[2], pfull[2][2], ofull[2], opart[2], qfull[2], qfree[2];
   uint64_t ifull[C::kRing], iempty[C::kRing], drain;
   unsigned long long scan[C::kThreads / 32];
@@ -578,8 +582,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       mbar_init(&sh.ready[i], (C::kFp8 ? 4 : 5) * kBoth);  // four preparing warps and the copying one, or that one in their place
       mbar_init(&sh.empty[i], 1);
     }
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&sh.rfull[i], 1);
+    for (int i = 0; i < C::kRawStages; ++i) {
+      mbar_init(&sh.rfull[i], 33);  // the copies of codes, and every lane's of scales
       mbar_init(&sh.rempty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&sh.ifull[i], 1);
-      mbar_init(&sh.iempty[i], 2 + C::kPrep + C::kSoft * kBoth);  // copying, issuing, preparing and softmax warps (a pair's: of both)
+      mbar_init(&sh.iempty[i], 3 + C::kPrep + C::kSoft * kBoth);  // copying (two), issuing, preparing and softmax warps (a pair's: of both)
     }
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
@@ -731,13 +735,15 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 0) {
-      // ---------------------------------------------------------- copies
-      constexpr int kSt = C::kFp8 ? C::kRawStages : C::kStages;
+    } else if (warp == 0 || warp == 2) {
+      // ---------------------------------------------------------- copies: a warp for keys, one for values (starting a copy takes
+      // about 130 cycles, and a block of pages of 16 has up to 32 of them)
+      const int kv = warp >> 1;
+      const int base = !kv ? 0 : C::kFp8 ? C::kRawSt : C::kKSt, stages = C::kFp8 ? C::kRawSt : kv ? C::kVSt : C::kKSt;
       uint64_t* const empty = C::kFp8 ? sh.rempty : sh.empty;
       const int P = 1 << a.log_page;
       int cur = 0, nxt = 0, cur_s = -1, cur_w = -1, nxt_w = -1;  // lane l: page table entry cur_w + l
-      int n = 0, st = 0, g = 0;
+      int st = base, g = 0;
       uint32_t par = 1;
       bool ok = true;
       for (int it = 0; ok; ++it) {
@@ -765,12 +771,11 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                 if (wrong >> k & 1) bad |= ((1u << per) - 1) << (k * per);
               if (lane == 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
             }
-            if (lane == 0) sh.bad[g & 15] = bad;
+            if (lane == 0) sh.bad[g & 15] = bad;  // (by both warps, the same)
           }
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++n) {
+          {
             if (!(ok = wait(&empty[st], par))) break;
-            const bool skip = hook == 3 && n == 0;
+            const bool skip = hook == 3 && g + kv == 0;
             // Values that some row does not see whole go by the preparing warps; what else is copied as it is announces itself
             // where the products are issued.
             const bool look = kv && b >= i_edge;
@@ -819,20 +824,22 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                   copy3d(dst + (ch * rows + of * box) * 128, real ? y : none, chunk0 + ch);
                 }
               } else {
-                const uint32_t dst = raw + st * C::kRaw;
+                const uint32_t dst = raw + st * C::kRaw, bar = smem_addr(&sh.rfull[st]);
                 const bool copy = lane < have && real;
                 const int copies = __popc(__ballot_sync(0xFFFFFFFFu, copy));
-                const uint32_t bar = smem_addr(&sh.rfull[st]);
-                if (lane == 0) mbar_arrive_expect_tx(&sh.rfull[st], copies * box * (chunks * 64 + 1));
+                if (lane == 0) mbar_arrive_expect_tx(&sh.rfull[st], copies * box * chunks * 64);
                 __syncwarp();
-                if (!skip && copy) {
-                  ra_tma_2d(dst + lane * box * chunks * 64, kv ? &vmap : &kmap, chunk0 * 64, y, bar);
-                  ra_bulk(dst + rows * chunks * 64 + lane * box, (kv ? a.v_scales : a.k_scales) + y, box, bar);
-                }
+                if (!skip && copy) ra_tma_2d(dst + lane * box * chunks * 64, kv ? &vmap : &kmap, chunk0 * 64, y, bar);
+                // the scales, 16 a lane: lane l those of the tile's rows 16 l ..
+                const int sp = lane / (box / 16), spage = __shfl_sync(0xFFFFFFFFu, cur, (p0 - cur_w + sp) & 31);
+                if (sp < have && spage >= 0 && spage < a.n_pages)
+                  ra_copy16(dst + rows * chunks * 64 + lane * 16,
+                            (kv ? a.v_scales : a.k_scales) + ((size_t)(spage * a.Hkv + i_h) << a.log_page) + in_page + lane % (box / 16) * 16);
+                ra_copy16_arrive(bar);
               }
             }
             __syncwarp();
-            if (++st == kSt) st = 0, par ^= 1;
+            if (++st == base + stages) st = base, par ^= 1;
           }
         }
         if (ok) release(it);
@@ -840,10 +847,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       // Nothing may be on its way to this CTA's shared memory when it ends.  Copies of codes: they have landed, whatever ran
       // out.  Others: a stage's last commit says that its copies have been read, and is itself the last arrival; where the
       // products have stopped this takes the wait's whole limit, in which whatever was on its way arrives.
-      for (int i = 0; i < min(n, kSt); ++i) {
-        const int e = n - 1 - (n - 1 - i) % kSt;  // the last copy into stage i
-        uint64_t* const bar = C::kFp8 ? &sh.rfull[e % kSt] : &sh.empty[e % kSt];
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, (e / kSt) & 1))) {
+      for (int i = 0; i < min(g, stages); ++i) {
+        const int e = g - 1 - (g - 1 - i) % stages;  // the last copy into the ring's stage i
+        uint64_t* const bar = (C::kFp8 ? sh.rfull : sh.empty) + base + i;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, (e / stages) & 1))) {
           *(volatile int*)&sh.abort = 1;
           atomicExch(a.status, (int)VP_ERR_TIMEOUT);
           break;
@@ -853,8 +860,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       // ---------------------------------------------------------- matrix products
       constexpr uint32_t kIdesc = 1u << 4 | 1u << 7 | 1u << 10 | (kPair ? 16u : 8u) << 24;  // bf16 x bf16 -> fp32, rows
       constexpr uint32_t kIdS = kIdesc | (uint32_t)(BN >> 3) << 17, kIdO = kIdesc | 1u << 16 | (uint32_t)(D >> 3) << 17;
-      int st = 0, g = 0;                       // stage; blocks so far (one tile: of the score buffers)
-      uint32_t par = 0, qpar = 0, ppar = 0;    // of the stages, queries, weights (a bit per tile or buffer)
+      int ks = 0, vs = C::kKSt, g = 0;         // stages; blocks so far (one tile: of the score buffers)
+      uint32_t kpar = 0, vpar = 0, qpar = 0, ppar = 0;  // of the stages, queries, weights (a bit per tile or buffer)
       bool ok = true, first = true;
       // Four products at a time in a loop: the warps of a scheduler share its instruction cache, and products unrolled all the
       // way are fetched anew each time, which takes longer than they do (one block's 32 products of 64 cycles: 4,800 cycles).
@@ -900,8 +907,11 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         ppar ^= 1u << i;
         return true;
       };
-      auto step = [&]() {
-        if (++st == C::kStages) st = 0, par ^= 1;
+      auto next_k = [&]() {
+        if (++ks == C::kKSt) ks = 0, kpar ^= 1;
+      };
+      auto next_v = [&]() {
+        if (++vs == C::kStages) vs = C::kKSt, vpar ^= 1;
       };
       for (int it = 0; ok; ++it) {
         const RaItem* pi = get(it);
@@ -913,17 +923,12 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         const int nblk = ra_uniform(pi->b1 - pi->b0), cnt0 = ra_uniform(pi->cnt[0]), cnt1 = ra_uniform(pi->cnt[1]);
         if (cnt0 > 0) ok = q_ready(0);
         if (kSub == 2 && ok && cnt1 > 0) ok = q_ready(1);
-        // Scores of block j + 1 and outputs of block j (the ring's order: keys 0, values 0, keys 1, ...).  With two tiles
-        // one's softmax runs beside the other's products, with one its next scores lie in a second buffer.
+        // Scores of block j + 1 and outputs of block j.  With two tiles one's softmax runs beside the other's products, with one
+        // its next scores lie in a second buffer.
         for (int j = -1; ok && j < nblk; ++j) {
-          const int vs = st;
-          const uint32_t vpar = par;
-          if (j >= 0) step();
-          const int ks = st;
           if constexpr (kSub == 1) {
             if (j + 1 < nblk) {
-              if (!(ok = wait(&sh.ready[ks], par))) break;
-              step();
+              if (!(ok = wait(&sh.ready[ks], kpar))) break;
               tmem_fence_after();
               if (ra_elect()) {
                 scores((g + j + 1) & 1, ks);
@@ -932,6 +937,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               }
               first = false;
               __syncwarp();
+              next_k();
             }
             if (j >= 0) {
               const int buf = (g + j) & 1;
@@ -941,6 +947,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                 ra_commit<kPair>(&sh.empty[vs]);
               }
               __syncwarp();
+              next_v();
             }
           } else {
             bool have_v = false, have_k = false;
@@ -954,7 +961,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                 __syncwarp();
               }
               if (ok && j + 1 < cnt) {
-                if (!have_k) ok = have_k = wait(&sh.ready[ks], par);
+                if (!have_k) ok = have_k = wait(&sh.ready[ks], kpar);
                 tmem_fence_after();
                 if (ok && ra_elect()) {
                   scores(i, ks);
@@ -971,7 +978,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               if (j + 1 < nblk) ra_commit<kPair>(&sh.empty[ks]);
             }
             __syncwarp();
-            if (j + 1 < nblk) step();
+            if (j >= 0) next_v();
+            if (j + 1 < nblk) next_k();
           }
         }
         if (!ok) break;
@@ -990,7 +998,9 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     if constexpr (C::kRegPrep < C::kLaunch)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegPrep));
     const int group = warp >> 3, tid = threadIdx.x - 128 - 128 * group, quad = warp & 3;  // group 1: values of codes
-    int st = group, g = 0, rst = group, done = 0;
+    // rings: with codes this group's, else the values'
+    const int base = C::kFp8 && !group ? 0 : C::kKSt, stages = C::kFp8 && !group ? C::kKSt : C::kVSt, rbase = group * C::kRawSt;
+    int st = base, g = 0, rst = rbase, done = 0;
     int nq0 = 0, nq1 = 0;  // query tiles so far
     uint32_t fpar = 0, wpar = 1, rpar = 0;  // of the full barriers (a bit each: their phases are the looks'), the stages, the codes
     bool ok = true;
@@ -1093,10 +1103,9 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             arrive(&sh.rempty[rst]);
           }
           ++done;
-          if ((rst += 2) >= C::kRawStages) rst -= C::kRawStages, rpar ^= 1;
-          if ((st += 2) >= C::kStages) st -= C::kStages, wpar ^= 1;
+          if (++rst == rbase + C::kRawSt) rst = rbase, rpar ^= 1;
+          if (++st == base + stages) st = base, wpar ^= 1;
         } else {  // values of edge blocks
-          if (++st == C::kStages) st = 0;
           if (b >= edge) {
             if (!(ok = wait(&sh.full[st], fpar >> st & 1))) break;
             fpar ^= 1u << st;
@@ -1106,18 +1115,16 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             if (lane == 0 && !(hook == 4 && done == 0 && warp == 4)) arrive_first(&sh.ready[st]);
             ++done;
           }
-          if (++st == C::kStages) st = 0;
+          if (++st == base + stages) st = base;
         }
       }
       if (ok) release(it);
     }
-    if (C::kFp8 && group == 0) {  // no commit is on its way when the CTA ends: a stage's last one frees it
-      const int n = 2 * g;
-      for (int i = 0; i < min(n, C::kStages); ++i) {
-        const int e = n - 1 - (n - 1 - i) % C::kStages;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.empty[e % C::kStages], (e / C::kStages) & 1))) break;
+    if (C::kFp8)  // no commit is on its way when the CTA ends: a stage's last one frees it
+      for (int i = 0; i < min(done, stages); ++i) {
+        const int e = done - 1 - (done - 1 - i) % stages;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&sh.empty[base + i], (e / stages) & 1))) break;
       }
-    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ------------------------------------------------------------ softmax: rows of the CTA's tile w, a thread per row
