@@ -460,6 +460,9 @@ struct RaCfg {
   static constexpr int kTile = kKRows * D * 2;                       // bytes, of either
   static_assert(kTile == kBlock * kVCols * 2, "");
   static constexpr int kRaw = kTile / 2 + 128;                       // the same in codes, and the scales' bytes
+  // One tile with at most 32 rows: every softmax warp takes all of them and a quarter of each block's keys (else three of the
+  // four would have nothing to do, and the fourth would take longer than codes take to arrive); the quarters are joined here.
+  static constexpr int kJoin = kTiles == 1 ? 4 * 4096 : 0;
   static constexpr bool kQSmem = kTiles == 2;                        // else the queries lie in tensor memory
   static constexpr int kQ = kQSmem ? kSub * 128 * D * 2 : 0;
   // stages of keys and of values, rings of their own (with codes: of bf16 tiles, and of codes)
@@ -493,6 +496,7 @@ struct RaShared {
   int special[C::kRing];    // whether poison has an entry
   int poison[C::kRing][D];  // per column: the first key of the item's edge blocks whose value is infinite or NaN
   uint32_t bad[16];         // per block: the groups of 16 keys whose page does not exist
+  float quarter[kTiles == 1 ? 4 : 1][kTiles == 1 ? 32 : 1][2];  // maxima and sums of the quarters
   int s0;
   uint32_t tmem;
   int abort;
@@ -500,7 +504,7 @@ struct RaShared {
 template <int D, int kTiles, int kSrc>
 constexpr int ra_smem() {
   using C = RaCfg<D, kTiles, kSrc>;
-  return C::kQ + C::kStages * C::kTile + C::kRawStages * C::kRaw + (int)sizeof(RaShared<D, kTiles, kSrc>);
+  return C::kQ + C::kStages * C::kTile + C::kJoin + C::kRawStages * C::kRaw + (int)sizeof(RaShared<D, kTiles, kSrc>);
 }
 
 template <int D, int kTiles, int kSrc>
@@ -515,7 +519,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t dyn[];
   uint8_t* const q_p = dyn;
   uint8_t* const ring_p = q_p + C::kQ;
-  uint8_t* const raw_p = ring_p + C::kStages * C::kTile;
+  uint8_t* const join_p = ring_p + C::kStages * C::kTile;
+  uint8_t* const raw_p = join_p + C::kJoin;
   auto& sh = *reinterpret_cast<RaShared<D, kTiles, kSrc>*>(raw_p + C::kRawStages * C::kRaw);
   const uint32_t q_s = smem_addr(q_p), ring = smem_addr(ring_p), raw = smem_addr(raw_p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1008,7 +1013,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     auto load_q = [&](const RaItem& i, int w, int before) -> bool {
       auto free = [&]() -> bool { return before == 0 || wait(&sh.qfree[w], (before - 1) & 1); };
       bool waited = false;
-      const int row0 = (kPair ? rank : w) * 128 + quad * 32;  // of the item
+      const int row0 = kTiles == 1 && i.toks * a.G <= 32 ? 0 : (kPair ? rank : w) * 128 + quad * 32;  // of the item
       if (row0 * a.g_inv >> 16 < i.toks) {
         if constexpr (C::kQSmem) {  // into shared memory, a row's lanes together
           constexpr int kLanes = D / 8, kAt = 32 / kLanes, kAtOnce = kSub == 2 ? 8 : 16;
@@ -1129,9 +1134,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegSoft));
     // ------------------------------------------------------------ softmax: rows of the CTA's tile w, a thread per row
     const int w = (warp - 4 - C::kPrep) >> 2, quad = warp & 3;
-    const int row0 = (kPair ? rank : w) * 128 + quad * 32, r = row0 + lane;  // of the item
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int tok = r * a.g_inv >> 16, first_tok = row0 * a.g_inv >> 16;
     const uint64_t scale_2 = ra_pair(a.scale2, a.scale2);
     int g = 0, npv = 0;  // blocks (one tile: of the score buffers) and outputs so far
     bool ok = true;
@@ -1143,6 +1146,9 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       const RaItem* pi = get(it);
       if (!pi || pi->s < 0) break;
       const int b0 = pi->b0, cnt = pi->cnt[w], nblk = pi->b1 - b0, toks = pi->toks;
+      const bool few = kTiles == 1 && toks * a.G <= 32;  // every warp has the rows, for a quarter of the keys
+      const int row0 = few ? 0 : (kPair ? rank : w) * 128 + quad * 32, r = row0 + lane;  // of the item
+      const int tok = r * a.g_inv >> 16, first_tok = row0 * a.g_inv >> 16;
       const int lim = tok < toks ? min(pi->lim0 + tok, pi->keys) : pi->keys;  // keys that this row sees
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
       const bool idle = first_tok >= toks;  // no row of the warp is there
@@ -1164,6 +1170,72 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           tmem_fence_before();
           __syncwarp();
           if (lane < C::kParts) arrive_first_relaxed(&sh.pfull[buf][lane]);
+        } else if (kTiles == 1 && few) {
+          constexpr int kQ = BN / 4;
+          tmem_fence_after();
+          const uint32_t ts = lanes + buf * C::kColS;
+          const uint32_t groups = kSrc == kDense ? 0 : *(volatile uint32_t*)&sh.bad[n & 15] >> (quad * (kQ / 16));
+          const int sees = lim - (b0 + j) * BN - quad * kQ;
+          uint32_t x[kQ];
+#pragma unroll
+          for (int k = 0; k < kQ; k += 16) ra_ld16(ts + quad * kQ + k, x + k);
+          if (sees < kQ || groups) {
+#pragma unroll
+            for (int k = 0; k < kQ; ++k)
+              if (k >= sees || (groups >> (k >> 4) & 1)) x[k] = 0xFF800000u;
+          }
+          __syncwarp();
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < kQ; k += 2) mx[k / 2 % 2] = ra_max3(mx[k / 2 % 2], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+          const float top = fmaxf(mx[0], mx[1]) * a.scale2;
+          const bool grow = top > m + 8.0f || (m == -INFINITY && top > m);
+          if (__any_sync(0xFFFFFFFFu, grow)) {  // as below
+            const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
+            m = to;
+            mc = m == -INFINITY ? 0.0f : m;
+            if (j > 0) {
+              const uint64_t ff = ra_pair(f, f), zero = 0;
+              l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
+              if (!(ok = outputs_of(n - 1, 0))) break;
+              tmem_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < D; d += 16) {
+                uint32_t y[16];
+                ra_ld16(lanes + C::kColO + d, y);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                ra_st16(lanes + C::kColO + d, y);
+              }
+            }
+          }
+          const uint64_t mc2 = ra_pair(-mc, -mc);
+          uint32_t p[16], none[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p[e] = none[e] = 0;
+#pragma unroll
+          for (int e = 0; e < kQ / 2; ++e) {
+            float lo, hi;
+            ra_unpair(ra_fma2(ra_pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale_2, mc2), lo, hi);
+            lo = ra_ex2(lo), hi = ra_ex2(hi);
+            l2[e & 1] = ra_add2(l2[e & 1], ra_pair(lo, hi));
+            p[e] = ra_bf16x2(lo, hi);
+          }
+          if (kQ == 16 && (quad & 1)) {  // the second half of 16 columns
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e + 8] = p[e], p[e] = 0;
+          }
+#pragma unroll
+          for (int k = 0; k < BN / 32; ++k) {  // weights of zero for the other warps' keys
+            if (k == quad * kQ / 32)
+              ra_st16(ts + k * 16, p);
+            else
+              ra_st16(ts + k * 16, none);
+          }
+          tmem_wait_st();
+          tmem_fence_before();
+          __syncwarp();
+          if (lane < C::kParts && !(hook == 2 && it == 0 && j == 0 && warp == 4 + C::kPrep)) arrive_first_relaxed(&sh.pfull[buf][lane]);
         } else {
           tmem_fence_after();
           const uint32_t ts = lanes + buf * C::kColS;
@@ -1268,7 +1340,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) to[k] = ra_ldg128(a.gate + at + d + 8 * k);
       };
-      if (gated) {
+      if (gated && !few) {
         gates(gt[0], 0);
         gates(gt[1], 32);
       }
@@ -1292,8 +1364,80 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
       }
       const size_t ps = (size_t)c * 2 + max(slot, 0);
+      if (kTiles == 1 && few) {  // the quarters' sums: eight rows a warp
+        const uint32_t mine = smem_addr(join_p) + quad * 4096;
+        const int row = quad * 8 + (lane >> 2), col = (lane & 3) * 8, t = row * a.g_inv >> 16;
+        const bool real = row < rows;
+        const size_t to = (((size_t)pi->row + (real ? t : 0)) * a.Hq + pi->h * a.G + (real ? row - t * a.G : 0)) * D + col;
+        uint4 gt[2];
+        if (a.gate && slot < 0 && real) gt[0] = ra_ldg128(a.gate + to), gt[1] = ra_ldg128(a.gate + to + 32);
+        float(*const quarter)[32][2] = reinterpret_cast<float(*)[32][2]>(sh.quarter);
+        quarter[quad][lane][0] = m, quarter[quad][lane][1] = l;
+        asm volatile("bar.sync 13, 128;" ::: "memory");
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = fmaxf(top, quarter[x][lane][0]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float mx = quarter[x][lane][0];
+          sum += (mx == -INFINITY ? 0.0f : ra_ex2(mx - top)) * quarter[x][lane][1];
+        }
+        const float f = (m == -INFINITY ? 0.0f : ra_ex2(m - top)) * (slot >= 0 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum);
+        m = top, l = sum;
 #pragma unroll 1
-      for (int d = 0; d < D && !idle; d += 32) {
+        for (int d = 0; d < D; d += 32) {
+          uint32_t y[32];
+          if (cnt > 0) {
+            ra_ld32(to_ + d, y);
+            ra_wait32(y);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = 0;
+          }
+          __syncwarp();
+          asm volatile("bar.sync 13, 128;" ::: "memory");  // the last columns have been read
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(y[4 * k + e]) * f;
+            sts128(mine + lane * 128 + ((k ^ (lane & 7)) << 4),
+                   make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+          }
+          asm volatile("bar.sync 13, 128;" ::: "memory");
+          float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint4 u = lds128(smem_addr(join_p) + x * 4096 + row * 128 + ((((lane & 3) * 2 + k) ^ (row & 7)) << 4));
+              v[4 * k] += __uint_as_float(u.x), v[4 * k + 1] += __uint_as_float(u.y);
+              v[4 * k + 2] += __uint_as_float(u.z), v[4 * k + 3] += __uint_as_float(u.w);
+            }
+          }
+          if (!real) continue;
+          if (slot >= 0) {
+            float* o = a.part_o + (ps * (D / 4) + (d + col) / 4) * (C::kRows * 4) + row * 4;
+            __stcg(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
+            __stcg(reinterpret_cast<float4*>(o + C::kRows * 4), make_float4(v[4], v[5], v[6], v[7]));
+            continue;
+          }
+          if (a.gate) {
+            ra_gate2(v[0], v[1], gt[0].x);
+            ra_gate2(v[2], v[3], gt[0].y);
+            ra_gate2(v[4], v[5], gt[0].z);
+            ra_gate2(v[6], v[7], gt[0].w);
+            gt[0] = gt[1];
+            if (d + 64 < D) gt[1] = ra_ldg128(a.gate + to + d + 64);
+          }
+          *reinterpret_cast<uint4*>(a.out + to + d) =
+              make_uint4(ra_bf16x2(v[0], v[1]), ra_bf16x2(v[2], v[3]), ra_bf16x2(v[4], v[5]), ra_bf16x2(v[6], v[7]));
+        }
+        __syncwarp();
+        asm volatile("bar.sync 13, 128;" ::: "memory");  // before the next item's
+      }
+#pragma unroll 1
+      for (int d = 0; d < D && !idle && !few; d += 32) {
         uint32_t y[32];
         if (cnt > 0) {
           ra_ld32(to_ + d, y);
@@ -1332,7 +1476,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
         __syncwarp();
       }
-      if (there) {
+      if (there && (!few || quad == 0)) {
         if (slot >= 0)
           __stcg(reinterpret_cast<float2*>(a.part_ml + (ps * 256 + r) * 2), make_float2(m, l));
         else if (a.lse)
