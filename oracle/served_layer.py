@@ -111,3 +111,44 @@ def paged_attention(q, k_cache, v_cache, pages, kv_len, scale, gate=None):
         sg = 1.0 / (1.0 + np.exp(-gate))
         out, mag = out * sg, mag * sg
     return out, mag, lse, dot
+
+
+def rows_attention(q, start, keys, values, seen, scale, gate=None):
+    """q: fp64 [M][Hq][D]; start [S + 1]; keys, values: per sequence fp64 [L][Hkv][D]; seen: per sequence bool [n][L], the
+    positions that each new row sees.  Returns (out, sum p |v| times the gate, lse, max over t of sum |q k| scale, the largest
+    number of positions); rows of no sequence are zero, those that see nothing zero with lse -inf."""
+    M, Hq, D = q.shape
+    out, mag = np.zeros((M, Hq, D)), np.zeros((M, Hq, D))
+    lse, dot = np.full((M, Hq), -np.inf), np.zeros((M, Hq))
+    for s in range(len(start) - 1):
+        a, b = int(start[s]), int(start[s + 1])
+        if a == b or keys[s] is None or len(keys[s]) == 0:
+            continue
+        G = Hq // keys[s].shape[1]
+        for h in range(Hq):
+            k, v = keys[s][:, h // G], values[s][:, h // G]
+            sc = np.where(seen[s], scale * (q[a:b, h] @ k.T), -np.inf)
+            m = sc.max(axis=1, keepdims=True)
+            some = np.isfinite(m)
+            e = np.exp(sc - np.where(some, m, 0.0))
+            z = e.sum(axis=1, keepdims=True)
+            w = np.where(some, e / np.where(some, z, 1.0), 0.0)
+            out[a:b, h], mag[a:b, h] = w @ v, w @ np.abs(v)
+            with np.errstate(divide="ignore"):
+                lse[a:b, h] = np.where(some, m + np.log(z), -np.inf)[:, 0]
+            dot[a:b, h] = abs(scale) * (np.abs(q[a:b, h]) @ np.abs(k).T).max(axis=1)
+    if gate is not None:
+        sg = 1.0 / (1.0 + np.exp(-gate))
+        out, mag = out * sg, mag * sg
+    return out, mag, lse, dot
+
+
+def pow2_codes(x: np.ndarray):
+    """fp64 [...][D] -> (e4m3 values of x / 2^e rounded to nearest even, e): e the smallest exponent >= -118 with
+    max |x| <= 448 * 2^e."""
+    top = np.abs(x).max(axis=-1)
+    m, n = np.frexp(top)  # 448 = 0.875 * 2^9
+    e = np.where(top > 0, np.maximum(n - 9 + (m > 0.875), -118), -118)
+    y = np.ldexp(x, -e[..., None])
+    step = np.ldexp(1.0, np.maximum(np.frexp(y)[1] - 1, -6) - 3)
+    return np.rint(y / step) * step, e

@@ -115,7 +115,9 @@ __device__ __forceinline__ void turn(float& x0, float& x1, float c, float s) {
 // costs at most one of e4m3's 17 binades and no digit, and code * 2^e is a bf16 value, so that reading the cache back
 // rounds nothing.
 constexpr int kMinExp = -118;    // codes times 2^-118 are bf16 values down to e4m3's smallest, 2^-9
-constexpr float kOpen = 0x1p-19f;  // of a pair's length: twice what norm, sine, cosine and products may be off by
+// What fp32 may be off by, of a pair's length: the angle as a fraction of a half turn pi u / 2, sine and cosine 2 u each, products
+// and sum 2 u (u = 2^-24): below 8 u; the norm 20 u more.
+constexpr float kOpenTurn = 0x1p-21f, kOpenNorm = 0x1p-19f;
 
 // e of a maximum by its bits: max = f 2^E, 1/2 <= f < 1, against 448 = 7/8 2^9.
 __device__ __forceinline__ int scale_exp(uint32_t bits) {
@@ -299,12 +301,12 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int p = split ? e : 2 * e, q = split ? e + 4 : 2 * e + 1;  // a pair
-          const float d = (fabsf(x[p]) + fabsf(x[q])) * kOpen;
+          const float d = (fabsf(x[p]) + fabsf(x[q])) * (kNorm ? kOpenNorm : kOpenTurn);
           lo[e] = e4m3x2((x[p] - d) * inv, (x[q] - d) * inv);
           hi[e] = e4m3x2((x[p] + d) * inv, (x[q] + d) * inv);
           open = open || lo[e] != hi[e];
         }
-        // 64 fp32 steps are 2^-18 to 2^-17 of the maximum, more than its pair's kOpen (at most sqrt 2 of it)
+        // 64 fp32 steps are 2^-18 to 2^-17 of the maximum, more than it may be off by (a pair's length is at most sqrt 2 of it)
         open = open || scale_exp(top - min(top, 64u)) != scale_exp(top + 64u);
         uint2 codes;
         if (split) {

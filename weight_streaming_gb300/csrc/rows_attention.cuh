@@ -488,7 +488,7 @@ struct RaShared {
   using C = RaCfg<D, kTiles, kSrc>;
   uint64_t full[C::kStages], ready[C::kStages], empty[C::kStages];
   uint64_t rfull[C::kRawStages + 1], rempty[C::kRawStages + 1];
-  uint64_t sfull[2], pfull[2][2], ofull[2], opart[2], qfull[2], qfree[2];
+  uint64_t sfull[2], pfull[2][2], ofull[2], opart[2], qfull[2], qfree[2], meet[2];
   uint64_t ifull[C::kRing], iempty[C::kRing], drain;
   unsigned long long scan[C::kThreads / 32];
   unsigned long long x0, x1, base;
@@ -598,6 +598,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       mbar_init(&sh.opart[i], 1);
       mbar_init(&sh.qfull[i], 4 * kBoth);
       mbar_init(&sh.qfree[i], 4);
+      mbar_init(&sh.meet[i], 4);
     }
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(&sh.ifull[i], 1);
@@ -637,6 +638,14 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       ra_arrive_first_relaxed(smem_addr(bar));
     else
       ra_arrive(smem_addr(bar));
+  };
+  // Four warps meet (a bounded wait, unlike a hardware barrier: another warp may have given up).
+  auto meet = [&](int i, uint32_t& parity) -> bool {
+    __syncwarp();
+    if (lane == 0) arrive(&sh.meet[i]);
+    const bool there = wait(&sh.meet[i], parity);
+    parity ^= 1;
+    return there;
   };
   // The it-th item, for every role but the scheduler; null when a wait ran out.
   auto get = [&](int it) -> const RaItem* {
@@ -1007,7 +1016,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     const int base = C::kFp8 && !group ? 0 : C::kKSt, stages = C::kFp8 && !group ? C::kKSt : C::kVSt, rbase = group * C::kRawSt;
     int st = base, g = 0, rst = rbase, done = 0;
     int nq0 = 0, nq1 = 0;  // query tiles so far
-    uint32_t fpar = 0, wpar = 1, rpar = 0;  // of the full barriers (a bit each: their phases are the looks'), the stages, the codes
+    uint32_t mpar = 0, fpar = 0, wpar = 1, rpar = 0;  // of the meetings, the full barriers (a bit each: their phases are the looks'), the stages, the codes
     bool ok = true;
     // This warp's 32 rows of the CTA's tile w; rows that are not there read as zeros, warps without rows load nothing.
     auto load_q = [&](const RaItem& i, int w, int before) -> bool {
@@ -1098,7 +1107,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           }
           const uint32_t bad = *(volatile uint32_t*)&sh.bad[g & 15];
           if (group && (b >= edge || bad)) {
-            asm volatile("bar.sync 15, 128;" ::: "memory");  // other threads' values are looked at
+            if (!(ok = meet(1, mpar))) break;  // other threads' values are looked at
             ra_look<C::kVCols, BN>(tile, tid, keys - b * BN, bad, b >= edge, b * BN, poison, special);
           }
           fence_proxy_async_smem();
@@ -1137,6 +1146,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const uint64_t scale_2 = ra_pair(a.scale2, a.scale2);
     int g = 0, npv = 0;  // blocks (one tile: of the score buffers) and outputs so far
+    uint32_t mpar = 0;   // of the meetings
     bool ok = true;
     // The outputs of block n (one tile), or of this tile's block v, are there.
     auto outputs_of = [&](int n, int v) -> bool {
@@ -1373,7 +1383,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         if (a.gate && slot < 0 && real) gt[0] = ra_ldg128(a.gate + to), gt[1] = ra_ldg128(a.gate + to + 32);
         float(*const quarter)[32][2] = reinterpret_cast<float(*)[32][2]>(sh.quarter);
         quarter[quad][lane][0] = m, quarter[quad][lane][1] = l;
-        asm volatile("bar.sync 13, 128;" ::: "memory");
+        if (!(ok = meet(0, mpar))) break;
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
         for (int x = 0; x < 4; ++x) top = fmaxf(top, quarter[x][lane][0]);
@@ -1394,8 +1404,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) y[k] = 0;
           }
-          __syncwarp();
-          asm volatile("bar.sync 13, 128;" ::: "memory");  // the last columns have been read
+          if (!(ok = meet(0, mpar))) break;  // the last columns have been read
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float v[4];
@@ -1404,7 +1413,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             sts128(mine + lane * 128 + ((k ^ (lane & 7)) << 4),
                    make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
           }
-          asm volatile("bar.sync 13, 128;" ::: "memory");
+          if (!(ok = meet(0, mpar))) break;
           float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -1433,8 +1442,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           *reinterpret_cast<uint4*>(a.out + to + d) =
               make_uint4(ra_bf16x2(v[0], v[1]), ra_bf16x2(v[2], v[3]), ra_bf16x2(v[4], v[5]), ra_bf16x2(v[6], v[7]));
         }
-        __syncwarp();
-        asm volatile("bar.sync 13, 128;" ::: "memory");  // before the next item's
+        if (!ok || !(ok = meet(0, mpar))) break;  // before the next item's
       }
 #pragma unroll 1
       for (int d = 0; d < D && !idle && !few; d += 32) {
