@@ -554,8 +554,8 @@ vp_status vp_decode_steps_rows(const vp_model* model, int steps, int rows, const
  * pages.  One layer of such a step chains them:
  *   vp_add_rmsnorm_fp8 -> vp_linear_fp8_block (q, k, v) -> vp_paged_append -> vp_paged_attention ->
  *   vp_quant_fp8 -> vp_linear_fp8_block (o).
- * All but vp_paged_attention take a prompt's rows too; it takes one new token per sequence, so a
- * prompt's own attention (several new rows per sequence) is the caller's.  The paged cache and the
+ * All but vp_paged_attention take a prompt's rows too; it takes one new token per sequence, and the
+ * next section's calls several.  The paged cache and the
  * block-scaled weights are these calls' alone: the verify pass keeps its own formats.  All are asynchronous on `stream`, synchronise nothing and can be captured into a CUDA graph.  Outputs
  * must not overlap inputs except where a call says so.  One workspace, zero-filled once, serves
  * vp_linear_fp8_block and vp_paged_attention calls of any shapes in turn on one stream (of the

@@ -35,6 +35,8 @@ EXPORTS = [
     "vp_quant_fp8", "vp_add_rmsnorm_fp8", "vp_packed_bytes_fp8_block", "vp_pack_fp8_block",
     "vp_linear_fp8_block_workspace_bytes", "vp_linear_fp8_block", "vp_paged_append",
     "vp_paged_attention_workspace_bytes", "vp_paged_attention",
+    "vp_prompt_attention_workspace_bytes", "vp_prompt_attention", "vp_paged_attention_rows_workspace_bytes",
+    "vp_paged_attention_rows", "vp_paged_append_fp8", "vp_paged_attention_rows_fp8",
 ]
 
 

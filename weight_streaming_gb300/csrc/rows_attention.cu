@@ -1,5 +1,39 @@
 // Attention of several new rows per sequence: whole prompts (vp_prompt_attention), chunks over a paged cache
-// (vp_paged_attention_rows) and over an 8-bit one (vp_paged_attention_rows_fp8).
+// (vp_paged_attention_rows) and over an 8-bit one (vp_paged_attention_rows_fp8).  The kernel stands in rows_attention.cuh.
+//
+// Mathematics: as for single tokens (paged_attention.cu): one pass over the keys keeps a reference m, l = sum 2^(t - m) and o =
+// sum 2^(t - m) v of t = scale log2(e) q . k; two parts join as m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), o alike.  m is
+// the running maximum of some earlier block: it follows only where the maximum has grown by 2^8, so o is seldom scaled.
+//
+// Design: 4 D flops a key, row and query head on the tensor cores (bf16, fp32 sums in tensor memory).
+//  * Rows: the G query heads of a key-value head are rows of their own (row = token * G + head), so that the keys are read
+//    once for all of them and a few tokens fill a tile.  An item is 128 or 256 rows of one sequence and key-value head.
+//  * Two tiles of 128 rows share the keys.  With 64 or 128 columns both lie in one CTA (scores and outputs fill the tensor
+//    memory; one tile's softmax runs beside the other's products).  With 256 columns a CTA pair (cta_group::2) takes a
+//    tile each, holds half of every key and value block, and has two score buffers.  A single CTA would take 64 bytes of L2 a
+//    cycle there and stay at half the rate (12,289 rows of 24 / 4 x 256 heads: 2.0 ms, in pairs 1.5).
+//  * One tile (sequences with few rows): queries in tensor memory, two score buffers; with at most 32 rows every softmax warp
+//    takes all rows and a quarter of the keys (61 single tokens over an 8-bit cache: 299 us without, 198 with).
+//  * Warps: a scheduler, two that start copies (TMA, 128-byte swizzle; a block's pages), one that issues products, four or
+//    eight that prepare operands, a softmax warp per 32 rows of a tile.  Weights go back into tensor memory over the scores, 64
+//    keys at a time, and the products start with the first 64.
+//  * Values that a row of the item does not see have a weight of zero, which times infinity or NaN is not zero: in blocks that
+//    some row does not see whole (its own diagonal, the sequence's end) the preparing warps look at the values first, make
+//    those zeros and note their columns and first keys; the rows that see them get NaN at the end.
+//  * 8-bit cache: the preparing warps expand codes to bf16 operand tiles.  A code's bits three places lower are its value times
+//    2^-120 as bf16; one product with 2^(120 + scale - 127) gives the exact value.
+//  * Work: the items of all sequences and heads form one line of keys plus a fixed cost each, cut into equal parts, one per CTA or
+//    pair (the lengths are read on the device: each CTA sums the line up and finds its part).  At most two items of a CTA are
+//    cut; their parts lie in the workspace and a second launch joins them.  No counters: nothing to reset.
+//
+// What bounds it (2,048 rows behind 30,000 positions): 24 / 4 x 256 heads 957 us, 1.63 PFLOP/s, 84 % of the measured bf16 rate: the
+// tensor cores, 2,050 of about 2,280 cycles a block of 128 keys.  32 / 8 x 128 heads 921 us, 1.13 PFLOP/s: a tile's chain of softmax
+// (two warps of a scheduler share its instruction slots and caches) and products, about 2,900 cycles a block against 2,048 of
+// products.  64 columns: 0.71 PFLOP/s, the exponentials and the same chain.  Few rows: the cache's bytes in bf16 (64 x 8,000 positions of
+// 8 x 128 heads 6.5 TB/s); in 8 bits the expansion and the softmax of 128 keys take longer than their bytes (3.5 to 3.9 TB/s, so that
+// a token takes 0.8 to 0.9 of the bf16 cache's time).
+// Loops are kept short on purpose: a scheduler's warps share its instruction cache.  With the softmax unrolled over 128 keys and
+// copies of the waits' slow halves 61 single tokens took 566 us in place of 290.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
