@@ -429,7 +429,8 @@ def codes_equal(got, want):
 
 @pytest.mark.parametrize("D,Hq,Hkv,P,rot,inter,norm", [
     (256, 24, 4, 64, 256, True, True), (256, 6, 1, 16, 64, False, True), (128, 32, 8, 16, 128, False, False),
-    (128, 5, 5, 32, 96, False, True), (64, 8, 2, 128, 64, True, False), (64, 3, 1, 64, 16, False, True), (128, 4, 2, 64, 0, True, False)])
+    (128, 5, 5, 32, 96, False, True), (64, 8, 2, 128, 64, True, False), (64, 3, 1, 64, 16, False, True), (128, 4, 2, 64, 0, True, False),
+    (256, 6, 2, 32, 64, False, False), (128, 4, 4, 16, 32, True, False), (64, 1, 3, 16, 16, False, False)])  # a part rotates, no norm
 def test_append_fp8(V, D, Hq, Hkv, P, rot, inter, norm):
     rng = np.random.default_rng(D + rot)
     rows, ctx = [1, 0, P + 3, 2, 400], [0, 5, P - 2, 3 * P - 1, 2 * P]

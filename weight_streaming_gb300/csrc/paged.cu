@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
     uint16_t* dst = isq ? q_dst + hh * D : (isk ? k_dst : v_dst) + (ptrdiff_t)hh * head_step;
     uint4 out = raw[i];
     const float* w = !kNorm ? nullptr : isq ? a.q_norm : isk ? a.k_norm : nullptr;
-    if ((isq || isk) && (w || turns)) {
+    // (8-bit keys: all lanes of a head together, as they share its maximum)
+    if ((isq || isk) && (w || turns || (kFp8 && isk && a.rot))) {
       float x[8];
       unpack8(raw[i], x);
       if (kNorm && w) norm_head<kL>(x, w + off0, w + off1, a.eps, mask);
@@ -299,12 +300,13 @@ __global__ void __launch_bounds__(kThreadsP) append_kernel(const __grid_constant
         top = __reduce_max_sync(mask, top);
         int ex = scale_exp(top);
         const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+        const float off = kNorm ? kOpenNorm : turns ? kOpenTurn : 0.0f;
         bool open = false;
         uint32_t lo[4], hi[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int p = split ? e : 2 * e, q = split ? e + 4 : 2 * e + 1;  // a pair
-          const float d = (fabsf(x[p]) + fabsf(x[q])) * (kNorm ? kOpenNorm : kOpenTurn);
+          const float d = (fabsf(x[p]) + fabsf(x[q])) * off;
           lo[e] = e4m3x2((x[p] - d) * inv, (x[q] - d) * inv);
           hi[e] = e4m3x2((x[p] + d) * inv, (x[q] + d) * inv);
           open = open || lo[e] != hi[e];

@@ -201,7 +201,9 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   const int tiles = rows_tiles(x.S, x.M, x.Hq, x.Hkv);
   a.tok_tile = 128 * tiles / a.G;
   a.g_inv = (65536 + a.G - 1) / a.G;
-  a.item_cost = 384;
+  // Starting and ending an item, in keys (12,289 rows of 24 / 4 x 256 heads at 256, 384, 640: 1.62, 1.54, 1.44 ms; 9 prompts of
+  // 12,001 rows, 32 / 8 x 128: 407, 354, 369 us)
+  a.item_cost = x.D == 256 && tiles == 2 ? 640 : 448;
   const int grid = std::min(sms, kRowsGrid);
   cudaError_t e;
   if (x.D == 256)

@@ -32,30 +32,33 @@ __device__ __forceinline__ void ra_arrive_first(uint32_t bar, uint32_t rank = 0)
       "r"(rank)
       : "memory");
 }
-// One poll of at most 20 us.  kPair: the arrivals may come from the pair's other CTA.
+// One poll of at most `ns`.  kPair: the arrivals may come from the pair's other CTA.
 template <bool kPair>
-__device__ __forceinline__ bool ra_try(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool ra_try(uint32_t bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
   if constexpr (kPair)
     asm volatile(
         "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
+        : "r"(bar), "r"(parity), "r"(ns)
         : "memory");
   else
     asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                  : "=r"(ok)
-                 : "r"(bar), "r"(parity), "r"(20000u)
+                 : "r"(bar), "r"(parity), "r"(ns)
                  : "memory");
   return ok != 0;
 }
+constexpr uint32_t kRaShort = 64;
 // A bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.
 template <bool kPair>
 __device__ __forceinline__ bool ra_wait(uint32_t bar, uint32_t parity, int* abort, int* status) {
-  uint32_t left = kMbarPolls;
-  while (!__all_sync(0xFFFFFFFFu, ra_try<kPair>(bar, parity))) {
+  uint32_t left = kMbarPolls + kRaShort;  // short polls first, then of 20 us
+  while (!__all_sync(0xFFFFFFFFu, ra_try<kPair>(bar, parity, left > kMbarPolls ? 0 : 20000))) {
+    --left;
+    if (left > kMbarPolls) continue;
     if (__any_sync(0xFFFFFFFFu, *(volatile int*)abort)) return false;
-    if (--left == 0) {
+    if (left == 0) {
       *(volatile int*)abort = 1;
       atomicExch(status, (int)VP_ERR_TIMEOUT);
       return false;
@@ -466,7 +469,7 @@ struct RaCfg {
   static constexpr bool kQSmem = kTiles == 2;                        // else the queries lie in tensor memory
   static constexpr int kQ = kQSmem ? kSub * 128 * D * 2 : 0;
   // stages of keys and of values, rings of their own (with codes: of bf16 tiles, and of codes)
-  static constexpr int kKSt = kFp8 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 3, kVSt = !kFp8 && D > 64 && kTiles == 2 ? 2 : kKSt;
+  static constexpr int kKSt = kFp8 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : kTiles == 2 ? 2 : 3, kVSt = !kFp8 && D > 64 && kTiles == 2 ? 3 : kKSt;
   static constexpr int kStages = kKSt + kVSt;
   static constexpr int kRawSt = !kFp8 ? 0 : D == 64 ? 4 : kTiles == 2 ? 1 : 2, kRawStages = 2 * kRawSt;
   static constexpr int kRing = kPair ? 2 : 3;                        // items
