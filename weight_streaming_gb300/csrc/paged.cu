@@ -14,8 +14,8 @@
 // the norm's code stands in the same kernel: its instructions outgrow their cache), 37 us with Q/K norms; of 32 x
 // 256 heads with Q/K norms (197 MB) 65 us; 48 rows of 32 x 256 heads: 6.2 us.
 //
-// Into 8 bits 6001 rows of 32 + 16 x 128 heads (135 MB) take 55 to 59 us, 2.3 to 2.4 TB/s: instructions (92 registers, 1,300 of them
-// a warp), and the one head in a few hundred that is formed again in fp64 for an open code.
+// Into 8 bits 6001 rows of 32 + 16 x 128 heads (135 MB) take 60 us, 2.3 TB/s: instructions, at 88 registers a quarter of the warp
+// slots (one to three heads per group of lanes: 75, 67, 62 us), and the heads that are formed again in fp64 for an open code.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

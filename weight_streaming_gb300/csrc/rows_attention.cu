@@ -11,9 +11,9 @@
 //  * Two tiles of 128 rows share the keys.  With 64 or 128 columns both lie in one CTA (scores and outputs fill the tensor
 //    memory; one tile's softmax runs beside the other's products).  With 256 columns a CTA pair (cta_group::2) takes a
 //    tile each, holds half of every key and value block, and has two score buffers.  A single CTA would take 64 bytes of L2 a
-//    cycle there and stay at half the rate (12,289 rows of 24 / 4 x 256 heads: 2.0 ms, in pairs 1.5).
+//    cycle there and stay at half the rate (12,289 rows of 24 / 4 x 256 heads: 2.0 ms, in pairs 1.8 at first, 1.36 now).
 //  * One tile (sequences with few rows): queries in tensor memory, two score buffers; with at most 32 rows every softmax warp
-//    takes all rows and a quarter of the keys (61 single tokens over an 8-bit cache: 299 us without, 198 with).
+//    takes all rows and a quarter of the keys (61 single tokens over an 8-bit cache: 299 us without, 198 with, at that time).
 //  * Warps: a scheduler, two that start copies (TMA, 128-byte swizzle; a block's pages), one that issues products, four or
 //    eight that prepare operands, a softmax warp per 32 rows of a tile.  Weights go back into tensor memory over the scores, 64
 //    keys at a time, and the products start with the first 64.
@@ -26,14 +26,13 @@
 //    pair (the lengths are read on the device: each CTA sums the line up and finds its part).  At most two items of a CTA are
 //    cut; their parts lie in the workspace and a second launch joins them.  No counters: nothing to reset.
 //
-// What bounds it (2,048 rows behind 30,000 positions): 24 / 4 x 256 heads 957 us, 1.63 PFLOP/s, 84 % of the measured bf16 rate: the
-// tensor cores, 2,050 of about 2,280 cycles a block of 128 keys.  32 / 8 x 128 heads 921 us, 1.13 PFLOP/s: a tile's chain of softmax
-// (two warps of a scheduler share its instruction slots and caches) and products, about 2,900 cycles a block against 2,048 of
-// products.  64 columns: 0.71 PFLOP/s, the exponentials and the same chain.  Few rows: the cache's bytes in bf16 (64 x 8,000 positions of
-// 8 x 128 heads 6.5 TB/s); in 8 bits the expansion and the softmax of 128 keys take longer than their bytes (3.5 to 3.9 TB/s, so that
-// a token takes 0.8 to 0.9 of the bf16 cache's time).
+// What bounds it (2,048 rows behind 30,000 positions): 24 / 4 x 256 heads 913 us, 1.71 PFLOP/s, 88 % of the measured bf16 rate: the
+// tensor cores.  32 / 8 x 128 heads 949 us, 1.10 PFLOP/s: a tile's chain of softmax (two warps of a scheduler share its instruction
+// slots and caches) and products, about 2,900 cycles a block against 2,048 of products.  64 columns: 0.70 PFLOP/s, the
+// exponentials and the same chain.  Few rows: the cache's bytes in bf16 (64 x 8,001 positions of 8 x 128 heads 328 us, 6.4
+// TB/s); in 8 bits the expansion and the softmax of 128 keys take longer than their bytes (286 us, 3.7 TB/s).
 // Loops are kept short on purpose: a scheduler's warps share its instruction cache.  With the softmax unrolled over 128 keys and
-// copies of the waits' slow halves 61 single tokens took 566 us in place of 290.
+// copies of the waits' slow halves 61 single tokens over an 8-bit cache took 566 us in place of 290 (now 188).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

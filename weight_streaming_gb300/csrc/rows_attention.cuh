@@ -19,8 +19,8 @@ __device__ __forceinline__ bool ra_elect() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
   return p != 0;
 }
-// A value that is the same in the whole warp, as one that the compiler knows to be: the products' operands are uniform
-// registers, and moving others there costs more than a product takes.
+// A value that is the same in the whole warp, as one that the compiler knows to be (the products' operands are uniform
+// registers).
 __device__ __forceinline__ int ra_uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ void ra_arrive(uint32_t bar) {
   asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar) : "memory");
@@ -880,8 +880,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       int ks = 0, vs = C::kKSt, g = 0;         // stages; blocks so far (one tile: of the score buffers)
       uint32_t kpar = 0, vpar = 0, qpar = 0, ppar = 0;  // of the stages, queries, weights (a bit per tile or buffer)
       bool ok = true, first = true;
-      // Four products at a time in a loop: the warps of a scheduler share its instruction cache, and products unrolled all the
-      // way are fetched anew each time, which takes longer than they do (one block's 32 products of 64 cycles: 4,800 cycles).
+      // Four products at a time in a loop (the warps of a scheduler share its instruction cache).
       auto scores = [&](int i, int stage) {  // tile i, or buffer i of the one tile
         uint64_t db = ra_desc_k(ring + stage * C::kTile), da = ra_desc_k(q_s + (kSub == 2 ? i * 128 * D * 2 : 0));
         uint32_t d = tmem + i * C::kColS, qa = tmem + C::kColQ;
