@@ -28,7 +28,7 @@
 //
 // What bounds it (2,048 rows behind 30,000 positions): 24 / 4 x 256 heads 913 us, 1.71 PFLOP/s, 88 % of the measured bf16 rate: the
 // tensor cores.  32 / 8 x 128 heads 949 us, 1.10 PFLOP/s: a tile's chain of softmax (two warps of a scheduler share its instruction
-// slots and caches) and products, about 2,900 cycles a block against 2,048 of products.  64 columns: 0.70 PFLOP/s, the
+// slots and caches) and products, an estimated 2,900 cycles a block against 2,048 of products.  64 columns: 0.70 PFLOP/s, the
 // exponentials and the same chain.  Few rows: the cache's bytes in bf16 (64 x 8,001 positions of 8 x 128 heads 328 us, 6.4
 // TB/s); in 8 bits the expansion and the softmax of 128 keys take longer than their bytes (286 us, 3.7 TB/s).
 // Loops are kept short on purpose: a scheduler's warps share its instruction cache.  With the softmax unrolled over 128 keys and
