@@ -1,0 +1,47 @@
+"""GPU tests of the attention of several new rows and of the 8-bit cache at their edges.  Tolerances as in
+test_rows_attention_gpu.py, unless a test derives its own."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import workspace
+from oracle import served_layer as ref  # noqa: F401
+from test_rows_attention_gpu import Cache, buffers, check, want_of
+from test_served_layer_gpu import bf16, f64, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def V():
+    from weight_streaming_gb300 import _lib
+    return _lib
+
+
+# ------------------------------------------------------------------ few rows: warps some of whose lanes have nothing to write
+@pytest.mark.parametrize("D,G,n", [(64, 1, 1), (64, 4, 1), (128, 4, 1), (256, 4, 1), (256, 3, 1), (128, 9, 1), (64, 5, 5), (128, 31, 1),
+                                   (256, 6, 5), (128, 1, 13), (256, 32, 1)])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("gate", [False, True])
+def test_rows_that_fill_a_warp_in_part(V, D, G, n, fp8, gate):
+    """1 to 32 rows per key head: a warp writes eight of them, four lanes each, and the others of its lanes nothing."""
+    S, P, Hkv, L = 5, 32, 2, [n + 70, n, n + 600, n + 128, 2500]
+    c, M, Hq = Cache(V, D + G, S, -(-2500 // P), P, Hkv, D, fp8), S * n, G * Hkv
+    q, start = bf16(np.random.default_rng(G), (M, Hq, D), 1.5), np.arange(S + 1) * n
+    out, lse, g = buffers(M, Hq, D, gate)
+    ws = workspace(V.vp_paged_attention_rows_workspace_bytes(S, M, Hq, Hkv, D))
+    c.attend(q, i32(start), i32(L), M, Hq, D ** -0.5, g, out, lse, ws)
+    torch.cuda.synchronize()
+    assert V.vp_read_status(ws) == V.VP_OK
+    kv = [c.values(s, L[s]) for s in range(S)]
+    want, m = want_of(q, start, [x[0] for x in kv], [x[1] for x in kv], [a - n for a in L], None, D ** -0.5, g)
+    check(out, lse, want, m, D, f"{D} {G} {n}")
+    # one row at a time, whatever lies beside it in the warp: the same keys in the same order, but for where the work is cut
+    one = torch.empty_like(out)
+    for i in range(n):
+        part = torch.empty((S, Hq, D), dtype=torch.bfloat16, device="cuda")
+        rows = torch.arange(S, device="cuda") * n + i
+        c.attend(q[rows].contiguous(), None, i32([a - n + i + 1 for a in L]), S, Hq, D ** -0.5, None if g is None else g[rows].contiguous(),
+                 part, None, ws)
+        one[rows] = part
+    check(one, None, want, m, D, f"one by one {D} {G} {n}")

@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
+  __syncwarp();  // the sequence's finder comes back: the allocation is a whole warp's
   if (warp == 1) {
     if constexpr (kPair) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem)) : "memory");
@@ -1177,6 +1178,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           tmem_fence_before();
           __syncwarp();
           if (lane == 0) arrive(&sh.qfree[w]);
+          __syncwarp();
         }
         if (idle) {  // whatever the products make of the scores is not read
           tmem_fence_before();
@@ -1206,6 +1208,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
             m = to;
             mc = m == -INFINITY ? 0.0f : m;
+            __syncwarp();
             if (j > 0) {
               const uint64_t ff = ra_pair(f, f), zero = 0;
               l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
@@ -1259,6 +1262,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 #pragma unroll 1
           for (int part = 0; part < C::kParts; ++part) {
             const int key0 = (b0 + j) * BN + part * 64;
+            __syncwarp();
             ra_wait32(x);
             ra_wait32(x + 32);
             const uint32_t groups = bad >> (part * 4);
@@ -1283,6 +1287,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
               m = to;
               mc = m == -INFINITY ? 0.0f : m;
+              __syncwarp();
               if (j + part > 0) {
                 const uint64_t ff = ra_pair(f, f), zero = 0;
                 l2[0] = ra_fma2(l2[0], ff, zero), l2[1] = ra_fma2(l2[1], ff, zero);
@@ -1372,6 +1377,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           uint32_t y;
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;" : "=r"(y) : "r"(to_ + d) : "memory");
           if (lim > from) y = 0x7FFFFFFFu;
+          __syncwarp();
           asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\ntcgen05.wait::st.sync.aligned;" ::"r"(to_ + d), "r"(y) : "memory");
         }
       }
@@ -1399,6 +1405,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           uint32_t y[32];
+          __syncwarp();  // the lanes with rows to write come back: the load is the whole warp's
           if (cnt > 0) {
             ra_ld32(to_ + d, y);
             ra_wait32(y);
@@ -1426,29 +1433,29 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
               v[4 * k + 2] += __uint_as_float(u.z), v[4 * k + 3] += __uint_as_float(u.w);
             }
           }
-          if (!real) continue;
-          if (slot >= 0) {
+          if (real && slot >= 0) {
             float* o = a.part_o + (ps * (D / 4) + (d + col) / 4) * (C::kRows * 4) + row * 4;
             __stcg(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
             __stcg(reinterpret_cast<float4*>(o + C::kRows * 4), make_float4(v[4], v[5], v[6], v[7]));
-            continue;
+          } else if (real) {
+            if (a.gate) {
+              ra_gate2(v[0], v[1], gt[0].x);
+              ra_gate2(v[2], v[3], gt[0].y);
+              ra_gate2(v[4], v[5], gt[0].z);
+              ra_gate2(v[6], v[7], gt[0].w);
+              gt[0] = gt[1];
+              if (d + 64 < D) gt[1] = ra_ldg128(a.gate + to + d + 64);
+            }
+            *reinterpret_cast<uint4*>(a.out + to + d) =
+                make_uint4(ra_bf16x2(v[0], v[1]), ra_bf16x2(v[2], v[3]), ra_bf16x2(v[4], v[5]), ra_bf16x2(v[6], v[7]));
           }
-          if (a.gate) {
-            ra_gate2(v[0], v[1], gt[0].x);
-            ra_gate2(v[2], v[3], gt[0].y);
-            ra_gate2(v[4], v[5], gt[0].z);
-            ra_gate2(v[6], v[7], gt[0].w);
-            gt[0] = gt[1];
-            if (d + 64 < D) gt[1] = ra_ldg128(a.gate + to + d + 64);
-          }
-          *reinterpret_cast<uint4*>(a.out + to + d) =
-              make_uint4(ra_bf16x2(v[0], v[1]), ra_bf16x2(v[2], v[3]), ra_bf16x2(v[4], v[5]), ra_bf16x2(v[6], v[7]));
         }
         if (!ok || !(ok = meet(0, mpar))) break;  // before the next item's
       }
 #pragma unroll 1
       for (int d = 0; d < D && !idle && !few; d += 32) {
         uint32_t y[32];
+        __syncwarp();  // as above
         if (cnt > 0) {
           ra_ld32(to_ + d, y);
           ra_wait32(y);
@@ -1484,7 +1491,6 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             if (d + 64 < D) gates(gt[1], d + 64);
           }
         }
-        __syncwarp();
       }
       if (there && (!few || quad == 0)) {
         if (slot >= 0)
