@@ -1262,7 +1262,6 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 #pragma unroll 1
           for (int part = 0; part < C::kParts; ++part) {
             const int key0 = (b0 + j) * BN + part * 64;
-            __syncwarp();
             ra_wait32(x);
             ra_wait32(x + 32);
             const uint32_t groups = bad >> (part * 4);
@@ -1329,6 +1328,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             tmem_fence_before();
             __syncwarp();
             if (lane == 0 && !(hook == 2 && it == 0 && j == 0 && warp == 4 + C::kPrep)) arrive_first_relaxed(&sh.pfull[buf][part]);
+            __syncwarp();
           }
           if (!ok) break;
         }
