@@ -45,3 +45,27 @@ def test_rows_that_fill_a_warp_in_part(V, D, G, n, fp8, gate):
                  part, None, ws)
         one[rows] = part
     check(one, None, want, m, D, f"one by one {D} {G} {n}")
+
+
+# ------------------------------------------------------------------ missing pages
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,G,n,P", [(256, 6, 60, 16), (256, 4, 150, 128), (256, 2, 260, 64), (128, 8, 40, 32), (64, 3, 100, 16), (256, 4, 3, 16)])
+def test_missing_pages_block_by_block(V, D, G, n, P, fp8):
+    """Pages that are missing here and there among 50 blocks of keys, so that every note of them is used again for a block with
+    other ones: in CTA pairs (256 columns, more than 128 rows), single CTAs, and with few rows."""
+    Hkv, S, L = 1, 2, [n + 6000, n + 3210]
+    c = Cache(V, D + P, S, -(-max(L) // P), P, Hkv, D, fp8)
+    rng = np.random.default_rng(P)
+    gone = rng.random(c.table.shape) < 0.3
+    c.table[gone] = rng.choice([-1, c.n, c.n + 77, 2 ** 31 - 1, -2 ** 31], gone.sum())
+    c.pages = i32(c.table)
+    M, Hq, start = S * n, G * Hkv, np.arange(S + 1) * n
+    q = bf16(rng, (M, Hq, D), 1.5)
+    out, lse, _ = buffers(M, Hq, D, False)
+    ws = workspace(V.vp_paged_attention_rows_workspace_bytes(S, M, Hq, Hkv, D))
+    c.attend(q, i32(start), i32(L), M, Hq, D ** -0.5, None, out, lse, ws)
+    torch.cuda.synchronize()
+    assert V.vp_read_status(ws) == V.VP_ERR_SHAPE
+    kv = [c.values(s, L[s]) for s in range(S)]
+    want, m = want_of(q, start, [x[0] for x in kv], [x[1] for x in kv], [a - n for a in L], [x[2] for x in kv], D ** -0.5, None)
+    check(out, lse, want, m, D, f"missing {D} {fp8}")

@@ -112,12 +112,21 @@ __device__ __forceinline__ void ra_tma_3d_first(uint32_t dst, const CUtensorMap*
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// kRelease: with what this thread has written for those who wait behind the products.
+template <bool kRelease>
 __device__ __forceinline__ void ra_expect_first(uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0;\n"
-      " mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [a], %1; }" ::"r"(bar),
-      "r"(bytes)
-      : "memory");
+  if constexpr (kRelease)
+    asm volatile(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0;\n"
+        " mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [a], %1; }" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0;\n"
+        " mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [a], %1; }" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
 }
 // 16 bytes by this lane, and its arrival once all of them have landed.
 __device__ __forceinline__ void ra_copy16(uint32_t dst, const void* src) {
@@ -789,7 +798,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                 if (wrong >> k & 1) bad |= ((1u << per) - 1) << (k * per);
               if (lane == 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
             }
-            if (lane == 0) sh.bad[g & 15] = bad;  // (by both warps, the same)
+            if (lane == 0) sh.bad[g & 15] = bad;  // (by both warps, the same; its announcement below releases it)
           }
           {
             if (!(ok = wait(&empty[st], par))) break;
@@ -803,7 +812,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
                 if (lane == 1) arrive_first_relaxed(&sh.ready[st]);
               } else if (lane == 0) {
                 if constexpr (kPair)
-                  ra_expect_first(smem_addr(&sh.ready[st]), bytes);
+                  ra_expect_first<kSrc != kDense>(smem_addr(&sh.ready[st]), bytes);  // pages: lane 0 has noted the missing ones
                 else
                   mbar_arrive_expect_tx(&sh.ready[st], bytes);
               } else if (lane < 5) {
