@@ -69,3 +69,42 @@ def test_missing_pages_block_by_block(V, D, G, n, P, fp8):
     kv = [c.values(s, L[s]) for s in range(S)]
     want, m = want_of(q, start, [x[0] for x in kv], [x[1] for x in kv], [a - n for a in L], [x[2] for x in kv], D ** -0.5, None)
     check(out, lse, want, m, D, f"missing {D} {fp8}")
+
+
+# ------------------------------------------------------------------ the longest sequences
+def longest(V, D, G, n, P, fp8):
+    """Just below 2^31 positions, nearly all of them the same few pages over and over, with scores 64 below those of the last
+    positions (less what the other columns add: 5 sigma of 4 at most): together below 2^31 e^-40 = 1e-8 of the weight, 2^-26."""
+    mp, low, hi = (2 ** 31 - 1) // P, 37, 640 // P
+    L = mp * P
+    c = Cache(V, 4, 1, 1, P, 1, D, fp8, spare=low + hi - 1)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn((low + hi, 1, P, D), generator=g, device="cuda") for _ in "kv")
+    k[..., 0] = 0.0
+    k[:low, ..., 0] = -8.0
+    if fp8:
+        c.k, c.v = (x.mul(32.0).to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v))
+        c.ks, c.vs = (torch.full((low + hi, 1, P), 122, dtype=torch.uint8, device="cuda") for _ in "kv")
+    else:
+        c.k, c.v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    c.n, c.max_pages = low + hi, mp
+    c.pages = torch.randint(0, low, (mp,), generator=g, device="cuda", dtype=torch.int32)
+    c.pages[mp - hi:] = torch.arange(low, low + hi, device="cuda", dtype=torch.int32)
+    q = (0.25 * torch.randn((n, G, D), generator=g, device="cuda")).to(torch.bfloat16)
+    q[..., 0] = 8.0
+    out, lse, _ = buffers(n, G, D, False)
+    ws = workspace(V.vp_paged_attention_rows_workspace_bytes(1, n, G, 1, D))
+    c.attend(q, i32([0, n]), i32([L]), n, G, 1.0, None, out, lse, ws)
+    torch.cuda.synchronize()
+    assert V.vp_read_status(ws) == V.VP_OK
+    tail = hi * P  # the positions on pages of their own
+    c.table = c.pages[mp - hi:].cpu().numpy().reshape(1, -1)
+    kk, vv, _ = c.values(0, tail)
+    want, m = want_of(q, [0, n], [kk], [vv], [tail - n], None, 1.0, None)
+    check(out, lse, want, m, D, f"longest {D} {G}")
+
+
+@pytest.mark.parametrize("D,G,n,fp8", [(256, 64, 3, False), (256, 64, 3, True), (128, 64, 3, False), (64, 30, 4, True), (128, 8, 1, False)])
+def test_items_that_take_long(V, D, G, n, fp8):
+    """Warps that have nothing to do in an item wait for as long as it takes the others: 0.3 s for 192 rows here."""
+    longest(V, D, G, n, 128, fp8)

@@ -204,6 +204,13 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   // 12,001 rows, 32 / 8 x 128: 407, 354, 369 us)
   a.item_cost = x.D == 256 && tiles == 2 ? 640 : 448;
   const int grid = std::min(sms, kRowsGrid);
+  // Polls after which a wait for an item gives up: kMbarPolls and one per 32 keys of a CTA's part of the line, were every sequence as long as it
+  // can be.  A role that has nothing to do in an item (a tile without rows, queries loaded ahead, the issuing warp of a pair's second
+  // CTA) waits for as long as the others work on it, up to the CTA's whole time.  A poll takes 4 us (measured, whatever the
+  // hint), 32 keys 0.6 us at most: kMbarPolls alone, 0.26 s, ran out where 192 rows saw 2^31 positions (0.35 s an item).
+  const long long longest = source == kDense ? x.M : (long long)a.max_pages << a.log_page;
+  const long long line = ((long long)x.S + x.M / a.tok_tile) * (longest + a.item_cost) * x.Hkv;
+  a.polls = kMbarPolls + (uint32_t)std::min((line / (x.D == 256 && tiles == 2 ? grid / 2 : grid) + 2 * kMinKeys) / 32, 1LL << 31);
   cudaError_t e;
   if (x.D == 256)
     e = tiles == 2 ? launch_rows<256, 2>(a, source, kmap, vmap, grid, s) : launch_rows<256, 1>(a, source, kmap, vmap, grid, s);

@@ -50,13 +50,14 @@ __device__ __forceinline__ bool ra_try(uint32_t bar, uint32_t parity, uint32_t n
   return ok != 0;
 }
 constexpr uint32_t kRaShort = 64;
-// A bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.
+// A bounded wait of a converged warp; false when it ran out here or elsewhere in the CTA.  polls: kMbarPolls where the others
+// are at work on the same block, RowsArgs::polls where they may be at work on a whole item.
 template <bool kPair>
-__device__ __forceinline__ bool ra_wait(uint32_t bar, uint32_t parity, int* abort, int* status) {
-  uint32_t left = kMbarPolls + kRaShort;  // short polls first, then of 20 us
-  while (!__all_sync(0xFFFFFFFFu, ra_try<kPair>(bar, parity, left > kMbarPolls ? 0 : 20000))) {
+__device__ __forceinline__ bool ra_wait(uint32_t bar, uint32_t parity, uint32_t polls, int* abort, int* status) {
+  uint32_t left = polls + kRaShort;  // short polls first, then of at most 20 us
+  while (!__all_sync(0xFFFFFFFFu, ra_try<kPair>(bar, parity, left > polls ? 0 : 20000))) {
     --left;
-    if (left > kMbarPolls) continue;
+    if (left > polls) continue;
     if (__any_sync(0xFFFFFFFFu, *(volatile int*)abort)) return false;
     if (left == 0) {
       *(volatile int*)abort = 1;
@@ -636,7 +637,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
 
   // Bounded waits of a converged warp; false when one ran out here or elsewhere in the CTA.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return ra_wait<kPair>(smem_addr(bar), parity, &sh.abort, a.status);
+    return ra_wait<kPair>(smem_addr(bar), parity, kMbarPolls, &sh.abort, a.status);
+  };
+  auto wait_item = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return ra_wait<kPair>(smem_addr(bar), parity, a.polls, &sh.abort, a.status);
   };
   // One lane's arrival for its warp, here, or where the products are issued.
   auto arrive = [&](uint64_t* bar) { ra_arrive(smem_addr(bar)); };
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   };
   // The it-th item, for every role but the scheduler; null when a wait ran out.
   auto get = [&](int it) -> const RaItem* {
-    if (!wait(&sh.ifull[it % C::kRing], (it / C::kRing) & 1)) return nullptr;
+    if (!wait_item(&sh.ifull[it % C::kRing], (it / C::kRing) & 1)) return nullptr;
     return &sh.item[it % C::kRing];
   };
   auto release = [&](int it) {
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         const bool mine = nb ? b0 < b1 : f <= 0;
         if (mine) {
           const int slot = it % C::kRing;
-          if (it >= C::kRing && !(ok = wait(&sh.iempty[slot], (it / C::kRing - 1) & 1))) break;
+          if (it >= C::kRing && !(ok = wait_item(&sh.iempty[slot], (it / C::kRing - 1) & 1))) break;
           for (int d = lane; d < D; d += 32) sh.poison[slot][d] = 0x7FFFFFFF;
           if (lane == 0) {
             sh.special[slot] = 0;
@@ -755,7 +759,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
       }
       const int slot = it % C::kRing;
-      if (ok && (it < C::kRing || wait(&sh.iempty[slot], (it / C::kRing - 1) & 1))) {
+      if (ok && (it < C::kRing || wait_item(&sh.iempty[slot], (it / C::kRing - 1) & 1))) {
         if (lane == 0) {
           sh.item[slot].s = -1;
           arrive(&sh.ifull[slot]);
@@ -1032,7 +1036,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
     bool ok = true;
     // This warp's 32 rows of the CTA's tile w; rows that are not there read as zeros, warps without rows load nothing.
     auto load_q = [&](const RaItem& i, int w, int before) -> bool {
-      auto free = [&]() -> bool { return before == 0 || wait(&sh.qfree[w], (before - 1) & 1); };
+      auto free = [&]() -> bool { return before == 0 || wait_item(&sh.qfree[w], (before - 1) & 1); };
       bool waited = false;
       const int row0 = kTiles == 1 && i.toks * a.G <= 32 ? 0 : (kPair ? rank : w) * 128 + quad * 32;  // of the item
       if (row0 * a.g_inv >> 16 < i.toks) {
@@ -1133,7 +1137,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           if (++st == base + stages) st = base, wpar ^= 1;
         } else {  // values of edge blocks
           if (b >= edge) {
-            if (!(ok = wait(&sh.full[st], fpar >> st & 1))) break;
+            if (!(ok = wait_item(&sh.full[st], fpar >> st & 1))) break;
             fpar ^= 1u << st;
             ra_look<C::kVCols, BN>(ring + st * C::kTile, tid, keys - b * BN, 0, true, b * BN, poison, special);  // (no pages: zeros)
             fence_proxy_async_smem();
@@ -1176,6 +1180,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       const bool idle = first_tok >= toks;  // no row of the warp is there
       float m = -INFINITY, mc = 0.0f;       // reference of the exponents (log2 units), and what is subtracted
       uint64_t l2[2] = {0, 0};              // sums of the weights
+      // (a second tile may have had no rows in the items before)
+      if (kSub == 2 && cnt > 0 && !(ok = wait_item(&sh.sfull[w], npv & 1))) break;
       for (int j = 0; ok && j < cnt; ++j) {
         const int n = g + j, buf = kSub == 2 ? w : n & 1;
         // Every phase of the outputs' barriers is waited for in turn: a wait tells a phase from the one before it only.  The

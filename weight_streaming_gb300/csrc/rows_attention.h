@@ -25,6 +25,7 @@ struct RowsArgs {
   int tok_tile;                // tokens of an item: its rows / G
   int g_inv;                   // 65536 / G, rounded up: r * g_inv >> 16 is r / G for r < 256
   int item_cost;               // what starting and ending an item costs, in keys
+  uint32_t polls;              // after which a wait for others' work on an item gives up
   uint32_t q_and, q_flip;      // on the queries' bf16 pairs: the scale's zero and sign
   float scale2;                // |scale| * log2(e), 1 for scale 0
   int4* desc;                  // [grid][2]: s, h, first token (-1: no part), rows | ends << 16 (below)
