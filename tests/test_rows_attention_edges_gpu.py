@@ -108,3 +108,11 @@ def longest(V, D, G, n, P, fp8):
 def test_items_that_take_long(V, D, G, n, fp8):
     """Warps that have nothing to do in an item wait for as long as it takes the others: 0.3 s for 192 rows here."""
     longest(V, D, G, n, 128, fp8)
+
+
+@pytest.mark.parametrize("D,G,n,P,fp8", [(64, 1, 1, 16, False), (64, 64, 3, 16, True), (128, 8, 1, 32, True), (256, 64, 3, 64, False),
+                                         (256, 64, 3, 16, True), (64, 40, 13, 64, False)])
+def test_lengths_whose_last_block_ends_beyond_2_31(V, D, G, n, P, fp8):
+    """Pages shorter than a block: up to 2^31 - 16 positions, so that the length rounded up to blocks has 32 bits; 13 rows of 40
+    heads are three items."""
+    longest(V, D, G, n, P, fp8)

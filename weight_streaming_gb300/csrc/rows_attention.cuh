@@ -436,8 +436,11 @@ constexpr int kMinKeys = 256;   // of the line per CTA at least
 // The line up to item t of one head.
 __device__ __forceinline__ long long ra_upto(const RowsArgs& a, const RaSeq& q, int t) {
   if (q.bad) return (long long)t * a.item_cost;
-  return (long long)t * (q.L - q.n + a.item_cost) + (long long)a.tok_tile * ((long long)t * (t + 1) / 2);
+  return (long long)t * ((long long)(q.L - q.n) + a.item_cost) + (long long)a.tok_tile * ((long long)t * (t + 1) / 2);
 }
+// Blocks of B keys; keys may be any int from 0 on.
+template <int B>
+__device__ __forceinline__ int ra_blocks(int keys) { return (int)(((uint32_t)keys + (B - 1)) / B); }
 __device__ __forceinline__ int ra_items(const RowsArgs& a, const RaSeq& q) { return (q.n + a.tok_tile - 1) / a.tok_tile; }
 __device__ __forceinline__ long long ra_line(const RowsArgs& a, const RaSeq& q) {
   if (q.n == 0) return 0;
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           }
         }
         const int tok0 = t * a.tok_tile, toks = min(a.tok_tile, q.n - tok0);
-        const int keys = q.bad ? 0 : q.L - q.n + tok0 + toks, nb = (keys + BN - 1) / BN;
+        const int keys = q.bad ? 0 : q.L - q.n + tok0 + toks, nb = ra_blocks<BN>(keys);
         // blocks whose place on the line lies in [x0, x1); a bad sequence's item by its start
         const long long f = x0 - at, e = x1 - at;
         const int b0 = f <= 0 ? 0 : (int)min((f + BN - 1) / BN, (long long)nb), b1 = (int)min((e + BN - 1) / BN, (long long)nb);
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             // Of two tiles in a CTA the first sees no further than its last token, and the second is there only if there
             // are more than 128 rows.
             const int rows = toks * a.G, k0 = q.bad ? 0 : i.lim0 + min(toks - 1, 127 / a.G);
-            i.cnt[0] = kSub == 1 ? b1 - b0 : max(min(b1, (k0 + BN - 1) / BN) - b0, 0);
+            i.cnt[0] = kSub == 1 ? b1 - b0 : max(min(b1, ra_blocks<BN>(k0)) - b0, 0);
             i.cnt[1] = kSub == 2 && rows > 128 ? b1 - b0 : 0;
             i.edge = i.lim0 / BN;
             const bool starts = b0 == 0, ends = b1 == nb;
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           if (lane == 0 && !(hook == 5 && it == 0)) arrive(&sh.ifull[slot]);
           ++it;
         }
-        at += keys + a.item_cost;
+        at += (long long)keys + a.item_cost;
         if (++t == items) {
           t = 0;
           if (++h == a.Hkv) h = 0, ++s;
@@ -1280,7 +1283,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             ra_wait32(x);
             ra_wait32(x + 32);
             const uint32_t groups = bad >> (part * 4);
-            if (key0 + 64 > lim_min || (groups & 15)) {  // keys that a row does not see
+            if (lim_min - key0 < 64 || (groups & 15)) {  // keys that a row does not see
               const int sees = lim - key0;
 #pragma unroll
               for (int k = 0; k < 64; ++k)
