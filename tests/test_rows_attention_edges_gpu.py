@@ -116,3 +116,26 @@ def test_lengths_whose_last_block_ends_beyond_2_31(V, D, G, n, P, fp8):
     """Pages shorter than a block: up to 2^31 - 16 positions, so that the length rounded up to blocks has 32 bits; 13 rows of 40
     heads are three items."""
     longest(V, D, G, n, P, fp8)
+
+
+# ------------------------------------------------------------------ sequences that see nothing
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,G,rows", [(64, 2, [1, 2, 1]), (128, 8, [40, 3, 60]), (256, 4, [1, 1, 1]), (256, 6, [50, 30, 200])])
+def test_zeros_of_bad_sequences_whatever_the_gate_holds(V, D, G, rows, fp8):
+    c = Cache(V, 1, 3, 8, 64, 1, D, fp8)
+    start = np.cumsum([0] + rows)
+    M = int(start[-1])
+    q = bf16(np.random.default_rng(1), (M, G, D))
+    out, lse, g = buffers(M, G, D, True)
+    g[start[1]:start[2]] = float("nan")
+    ws = workspace(V.vp_paged_attention_rows_workspace_bytes(3, M, G, 1, D))
+    L = [300, 513, 400]  # the second is behind its table
+    c.attend(q, i32(start), i32(L), M, G, 0.1, g, out, lse, ws)
+    torch.cuda.synchronize()
+    assert V.vp_read_status(ws) == V.VP_ERR_SHAPE
+    bad = slice(start[1], start[2])
+    assert not bool(out[bad].any()) and bool(torch.isneginf(lse[bad]).all())
+    kv = [c.values(s, 0 if s == 1 else L[s]) for s in range(3)]
+    g[bad] = 0.0
+    want, m = want_of(q, start, [x[0] for x in kv], [x[1] for x in kv], [L[s] - rows[s] for s in range(3)], None, 0.1, g)
+    check(out, lse, want, m, D, "beside a bad one")

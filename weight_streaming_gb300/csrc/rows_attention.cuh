@@ -1370,7 +1370,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       const size_t at = (((size_t)pi->row + (there ? tok : 0)) * a.Hq + pi->h * a.G + r - tok * a.G) * D;  // the row's outputs
       // 32 columns at a time; gates are loaded two steps ahead: behind the ring's copies a load takes long.
       uint4 gt[2][4];
-      const bool gated = a.gate && slot < 0 && there;
+      // (rows of a sequence without keys are zeros, whatever their gates hold)
+      const bool gate = a.gate && pi->keys > 0, gated = gate && slot < 0 && there;
       auto gates = [&](uint4 (&to)[4], int d) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) to[k] = ra_ldg128(a.gate + at + d + 8 * k);
@@ -1406,7 +1407,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         const bool real = row < rows;
         const size_t to = (((size_t)pi->row + (real ? t : 0)) * a.Hq + pi->h * a.G + (real ? row - t * a.G : 0)) * D + col;
         uint4 gt[2];
-        if (a.gate && slot < 0 && real) gt[0] = ra_ldg128(a.gate + to), gt[1] = ra_ldg128(a.gate + to + 32);
+        if (gate && slot < 0 && real) gt[0] = ra_ldg128(a.gate + to), gt[1] = ra_ldg128(a.gate + to + 32);
         float(*const quarter)[32][2] = reinterpret_cast<float(*)[32][2]>(sh.quarter);
         quarter[quad][lane][0] = m, quarter[quad][lane][1] = l;
         if (!(ok = meet(0, mpar))) break;
@@ -1456,7 +1457,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             __stcg(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
             __stcg(reinterpret_cast<float4*>(o + C::kRows * 4), make_float4(v[4], v[5], v[6], v[7]));
           } else if (real) {
-            if (a.gate) {
+            if (gate) {
               ra_gate2(v[0], v[1], gt[0].x);
               ra_gate2(v[2], v[3], gt[0].y);
               ra_gate2(v[4], v[5], gt[0].z);
