@@ -703,7 +703,8 @@ vp_status vp_prompt_attention(const void* q, int64_t ld_q, const void* k, int64_
                               void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* The same over the paged cache: L = kv_len[s] (device int32 [S]), the new rows' keys and values appended.  q: bf16
- * [M][Hq][D].  row_start NULL: one row per sequence (M == S).  A page outside 0 .. n_pages - 1 among those that a row sees
+ * [M][Hq][D].  row_start NULL: one row per sequence (M == S), and a sequence with kv_len 0 is an empty slot: zeros and lse -inf, the
+ * status word as it was.  A page outside 0 .. n_pages - 1 among those that a row sees
  * is left out and sets the status word to VP_ERR_SHAPE. */
 size_t vp_paged_attention_rows_workspace_bytes(int S, int M, int Hq, int Hkv, int D); /* 0 if unsupported */
 vp_status vp_paged_attention_rows(const vp_paged_cache* cache, const void* q, const int32_t* row_start, const int32_t* kv_len,

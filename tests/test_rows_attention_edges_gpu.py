@@ -139,3 +139,34 @@ def test_zeros_of_bad_sequences_whatever_the_gate_holds(V, D, G, rows, fp8):
     g[bad] = 0.0
     want, m = want_of(q, start, [x[0] for x in kv], [x[1] for x in kv], [L[s] - rows[s] for s in range(3)], None, 0.1, g)
     check(out, lse, want, m, D, "beside a bad one")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D,G,lens", [(64, 2, [0, 100, 0, 1, 3000, 0]), (128, 4, [0] * 40), (256, 4, [7, 0, 0, 2000]),
+                                      (128, 64, [0, 0, 65]), (256, 64, [0] * 3), (64, 1, [0] * 700 + [50] + [0] * 900)])
+def test_empty_slots_are_no_error(V, D, G, lens, fp8):
+    """Single tokens of a batch with idle slots, as the call for single tokens alone takes them: kv_len 0 gives zeros, lse -inf
+    and VP_OK."""
+    S, P = len(lens), 64
+    c = Cache(V, 1, 1, 64, P, 1, D, fp8)
+    c.S, c.max_pages, n = S, 64, max(max(lens), 1)
+    c.table = np.repeat(c.table, S, 0)  # the same pages for all
+    c.pages = i32(c.table)
+    q = bf16(np.random.default_rng(1), (S, G, D), 1.5)
+    out, lse, g = buffers(S, G, D, True)
+    ws = workspace(V.vp_paged_attention_rows_workspace_bytes(S, S, G, 1, D))
+    c.attend(q, None, i32(lens), S, G, D ** -0.5, g, out, lse, ws)
+    torch.cuda.synchronize()
+    assert V.vp_read_status(ws) == V.VP_OK
+    idle = torch.tensor([x == 0 for x in lens], device="cuda")
+    assert not bool(out[idle].any()) and bool(torch.isneginf(lse[idle]).all())
+    kv = [c.values(s, lens[s]) for s in range(S)]
+    want, m = want_of(q, np.arange(S + 1), [x[0] for x in kv], [x[1] for x in kv], [x - 1 for x in lens], None, D ** -0.5, g)
+    check(out, lse, want, m, D, f"idle {D}")
+    # with row_start the same lengths do not fit, and a negative one never does
+    for start, ls in ((np.arange(S + 1), lens), (None, [-1] + lens[1:])):
+        c.attend(q, None if start is None else i32(start), i32(ls), S, G, D ** -0.5, g, out, lse, ws)
+        torch.cuda.synchronize()
+        assert V.vp_read_status(ws) == V.VP_ERR_SHAPE
+        V.vp_workspace_init(ws)
+    check(out[1:], lse[1:], [w[1:] for w in want], m, D, f"negative {D}")

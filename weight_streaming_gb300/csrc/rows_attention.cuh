@@ -405,11 +405,11 @@ __device__ __forceinline__ void ra_look(uint32_t tile, int tid, int left, uint32
 }
 
 // ------------------------------------------------------------------ work
-// A sequence: n new rows from row0 on, which see the L cached positions up to their own.  A bad one (lengths that do not
-// fit) has L = 0 and outputs of zero.
+// A sequence: n new rows from row0 on, which see the L cached positions up to their own.  A blank one has L = 0 and outputs of zero:
+// an empty slot (no row_start, no positions), or a bad one, whose lengths do not fit.
 struct RaSeq {
   int row0, n, L;
-  bool bad;
+  bool blank, bad;
 };
 template <int kSrc>
 __device__ __forceinline__ RaSeq ra_seq(const RowsArgs& a, int s) {
@@ -421,11 +421,14 @@ __device__ __forceinline__ RaSeq ra_seq(const RowsArgs& a, int s) {
   q.row0 = r0;
   q.n = max(r1 - r0, 0);
   q.L = q.n;
+  bool empty = false;
   if (kSrc != kDense) {
     q.L = __ldg(a.kv_len + s);
-    q.bad = q.bad || q.L < q.n || q.L > (long long)a.max_pages << a.log_page;
+    empty = !a.row_start && q.L == 0;
+    q.bad = !empty && (q.bad || q.L < q.n || q.L > (long long)a.max_pages << a.log_page);
   }
-  if (q.bad) q.L = 0;
+  q.blank = q.bad || empty;
+  if (q.blank) q.L = 0;
   return q;
 }
 // The work is one line: for every sequence, key-value head and item (tok_tile tokens) in turn, the item's keys and
@@ -435,7 +438,7 @@ constexpr int kMinKeys = 256;   // of the line per CTA at least
 
 // The line up to item t of one head.
 __device__ __forceinline__ long long ra_upto(const RowsArgs& a, const RaSeq& q, int t) {
-  if (q.bad) return (long long)t * a.item_cost;
+  if (q.blank) return (long long)t * a.item_cost;
   return (long long)t * ((long long)(q.L - q.n) + a.item_cost) + (long long)a.tok_tile * ((long long)t * (t + 1) / 2);
 }
 // Blocks of B keys; keys may be any int from 0 on.
@@ -454,7 +457,7 @@ struct RaItem {
   int kv_row;          // global row of the sequence's first key (dense)
   int toks;
   int lim0;            // keys that the first token sees; each further token one more
-  int keys;            // that the last one sees (0: a bad sequence)
+  int keys;            // that the last one sees (0: a blank sequence)
   int b0, b1;
   int cnt[2];          // blocks of each tile of 128 rows in this piece
   int edge;            // first block that some token does not see whole
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       const long long x0 = (long long)sh.x0, x1 = (long long)sh.x1;
       long long at = (long long)sh.base;       // the line at the current sequence's (head's, item's) start
       int s = sh.s0, h = 0, t = 0, cached = -1, it = 0;
-      int c_row = 0, c_n = 0, c_L = 0, c_bad = 0;  // lane l: sequence cached + l
+      int c_row = 0, c_n = 0, c_L = 0, c_blank = 0;  // lane l: sequence cached + l
       bool ok = true, jump = true;
       while (ok && s < a.S && at < x1) {
         if ((s & ~31) != cached) {
@@ -692,7 +695,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           c_n = 0;
           if (cached + lane < a.S) {
             const RaSeq q = ra_seq<kSrc>(a, cached + lane);
-            c_row = q.row0, c_n = q.n, c_L = q.L, c_bad = q.bad;
+            c_row = q.row0, c_n = q.n, c_L = q.L, c_blank = q.blank;
           }
         }
         RaSeq q;
@@ -704,7 +707,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
         }
         q.row0 = __shfl_sync(0xFFFFFFFFu, c_row, s & 31);
         q.L = __shfl_sync(0xFFFFFFFFu, c_L, s & 31);
-        q.bad = __shfl_sync(0xFFFFFFFFu, c_bad, s & 31);
+        q.blank = __shfl_sync(0xFFFFFFFFu, c_blank, s & 31);
         const int items = ra_items(a, q);
         if (jump) {  // to the item that holds x0
           jump = false;
@@ -722,8 +725,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           }
         }
         const int tok0 = t * a.tok_tile, toks = min(a.tok_tile, q.n - tok0);
-        const int keys = q.bad ? 0 : q.L - q.n + tok0 + toks, nb = ra_blocks<BN>(keys);
-        // blocks whose place on the line lies in [x0, x1); a bad sequence's item by its start
+        const int keys = q.blank ? 0 : q.L - q.n + tok0 + toks, nb = ra_blocks<BN>(keys);
+        // blocks whose place on the line lies in [x0, x1); a blank sequence's item by its start
         const long long f = x0 - at, e = x1 - at;
         const int b0 = f <= 0 ? 0 : (int)min((f + BN - 1) / BN, (long long)nb), b1 = (int)min((e + BN - 1) / BN, (long long)nb);
         const bool mine = nb ? b0 < b1 : f <= 0;
@@ -738,12 +741,12 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             i.row = q.row0 + tok0;
             i.kv_row = q.row0;
             i.toks = toks;
-            i.lim0 = q.bad ? 0 : q.L - q.n + tok0 + 1;
+            i.lim0 = q.blank ? 0 : q.L - q.n + tok0 + 1;
             i.keys = keys;
             i.b0 = b0, i.b1 = b1;
             // Of two tiles in a CTA the first sees no further than its last token, and the second is there only if there
             // are more than 128 rows.
-            const int rows = toks * a.G, k0 = q.bad ? 0 : i.lim0 + min(toks - 1, 127 / a.G);
+            const int rows = toks * a.G, k0 = q.blank ? 0 : i.lim0 + min(toks - 1, 127 / a.G);
             i.cnt[0] = kSub == 1 ? b1 - b0 : max(min(b1, ra_blocks<BN>(k0)) - b0, 0);
             i.cnt[1] = kSub == 2 && rows > 128 ? b1 - b0 : 0;
             i.edge = i.lim0 / BN;
