@@ -683,9 +683,10 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
  *   out[r][h] = sum_t softmax_t(scale * q[r][h] . k_t) v_t,   lse[r][h] = log sum_t exp(scale * q[r][h] . k_t),
  * out times sigmoid(gate[r][h]) elementwise when gate is not NULL, rounded once to bf16; lse: fp32 [M][Hq] or NULL.
  * gate, out: bf16 [M][Hq][D].  Rows outside row_start[0] .. row_start[S] - 1 are left as they were.  A sequence whose rows
- * or lengths do not fit (row_start decreasing, below 0 or above M; L < n, L above max_pages * page_size) gives zeros and
- * lse -inf in the rows that it has, and VP_ERR_SHAPE in the workspace's status word; VP_ERR_TIMEOUT there: a bounded wait
- * gave up (out and lse are then not valid).
+ * or lengths do not fit (row_start below 0 or above M; L < n, L above max_pages * page_size) gives zeros and
+ * lse -inf in the rows that it has, and VP_ERR_SHAPE in the workspace's status word; a row_start that decreases anywhere sets it too,
+ * and no row is then written (its sequences would overlap).  VP_ERR_TIMEOUT there: a bounded wait gave up (out and lse are then
+ * not valid).
  * Keys and values that a row does not see have no effect on it, whatever they hold.  An infinite or NaN value that it sees
  * leaves no finite value in its column; where every score of a head is -infinity the head's outputs are zeros and its lse
  * -inf.  Products run on the tensor cores with fp32 sums; the probabilities enter the second one in bf16 (at most 2^-8

@@ -170,3 +170,24 @@ def test_empty_slots_are_no_error(V, D, G, lens, fp8):
         assert V.vp_read_status(ws) == V.VP_ERR_SHAPE
         V.vp_workspace_init(ws)
     check(out[1:], lse[1:], [w[1:] for w in want], m, D, f"negative {D}")
+
+
+@pytest.mark.parametrize("source", ["prompt", "rows", "rows8"])
+@pytest.mark.parametrize("start", [[0, 60, 0, 60, 0, 60], [5, 4], [0, 20, 40, 39, 60], list(range(50)) + [48, 60], [0, 2 ** 31 - 1, 0, 60],
+                                   [30, -2 ** 31, 60], [0] * 1000 + [60] + [59] * 900 + [60]])
+def test_a_row_start_that_decreases_writes_no_row(V, source, start):
+    """Overlapping sequences would multiply the work without limit, and write the same rows twice."""
+    D, Hq, Hkv, n, S = 128, 4, 2, 60, len(start) - 1
+    rng = np.random.default_rng(1)
+    q, k, v = bf16(rng, (n, Hq, D)), bf16(rng, (n, Hkv, D)), bf16(rng, (n, Hkv, D))
+    out, lse, _ = buffers(n, Hq, D, False)
+    ws = workspace(V.vp_paged_attention_rows_workspace_bytes(S, n, Hq, Hkv, D))
+    if source == "prompt":
+        V.vp_prompt_attention(q, Hq * D, k, Hkv * D, v, Hkv * D, i32(start), S, n, Hq, Hkv, D, 0.1, None, out, lse, ws)
+    else:
+        c = Cache(V, 1, 1, 10, 16, Hkv, D, source == "rows8")
+        c.S, c.pages = S, i32(np.repeat(c.table, S, 0))
+        c.attend(q, i32(start), i32([100] * S), n, Hq, 0.1, None, out, lse, ws)
+    torch.cuda.synchronize()
+    assert V.vp_read_status(ws) == V.VP_ERR_SHAPE
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())

@@ -419,7 +419,7 @@ __device__ __forceinline__ RaSeq ra_seq(const RowsArgs& a, int s) {
   q.bad = r0 < 0 || r1 > a.M || r1 < r0;
   r0 = max(r0, 0), r1 = min(r1, a.M);
   q.row0 = r0;
-  q.n = max(r1 - r0, 0);
+  q.n = r1 > r0 ? r1 - r0 : 0;
   q.L = q.n;
   bool empty = false;
   if (kSrc != kDense) {
@@ -563,8 +563,10 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
   {
     const int per = (a.S + C::kThreads - 1) / C::kThreads, s0 = min((int)threadIdx.x * per, a.S), s1 = min(s0 + per, a.S);
     unsigned long long mine = 0;
+    bool falls = false;
     for (int s = s0; s < s1; ++s) {
       const RaSeq q = ra_seq<kSrc>(a, s);
+      falls = falls || (a.row_start && __ldg(a.row_start + s + 1) < __ldg(a.row_start + s));
       if (q.bad && blockIdx.x == 0) report_unless(a.status, VP_ERR_SHAPE, VP_ERR_TIMEOUT);
       mine += (unsigned long long)ra_line(a, q) * a.Hkv;
     }
@@ -575,7 +577,8 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
       if (lane >= o) upto += v;
     }
     if (lane == 31) sh.scan[warp] = upto;
-    __syncthreads();
+    // Sequences that overlap could have any number of rows: no work is begun.
+    if (__syncthreads_or(falls)) return;
     unsigned long long total = 0, before = 0;
 #pragma unroll 1
     for (int w = 0; w < C::kThreads / 32; ++w) {
