@@ -689,7 +689,8 @@ vp_status vp_paged_attention(const vp_paged_cache* cache, const void* q, const i
  * not valid).
  * Keys and values that a row does not see have no effect on it, whatever they hold.  An infinite or NaN value that it sees
  * leaves no finite value in its column; where every score of a head is -infinity the head's outputs are zeros and its lse
- * -inf.  Products run on the tensor cores with fp32 sums; the probabilities enter the second one in bf16 (at most 2^-8
+ * -inf.  A score times log2 e that leaves fp32's range counts as infinite: below it has no weight, above it makes its row NaN,
+ * lse included.  Products run on the tensor cores with fp32 sums; the probabilities enter the second one in bf16 (at most 2^-8
  * relative each), the sums of the softmax in fp32.
  * D 64, 128 or 256; Hkv <= 1024, Hq / Hkv <= 64; 1 <= S <= 65536, 1 <= M <= 2^24, M * Hkv <= 2^30; scale finite and below
  * 2^127, of either sign.  Work is cut by keys, whatever the lengths (they are read on the device only), and parts are joined

@@ -191,3 +191,52 @@ def test_a_row_start_that_decreases_writes_no_row(V, source, start):
     torch.cuda.synchronize()
     assert V.vp_read_status(ws) == V.VP_ERR_SHAPE
     assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
+# ------------------------------------------------------------------ scores beyond fp32's range
+@pytest.mark.parametrize("D,G,n,long", [(64, 1, 1, 0), (128, 4, 2, 0), (128, 8, 90, 0), (256, 4, 70, 0), (256, 1, 3, 1), (128, 64, 5, 1)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scores_beyond_the_range_are_no_zeros(V, D, G, n, long, fp8):
+    """One key with a score of 2^130 makes the rows that see it NaN, one with -2^130 has no weight, and so do all of a row."""
+    P, L = 64, 200 + 30_000 * long
+    c = Cache(V, 1, 1, -(-L // P), P, 1, D, fp8)
+    q = bf16(np.random.default_rng(1), (n, G, D))
+    q[..., 0] = 2.0 ** 60
+    pg = lambda t: (int(c.table[0, t // P]), 0, t % P)  # noqa: E731
+    if fp8:
+        c.k[..., 0] = 0  # no part in the other scores
+    else:
+        c.k[..., 0] = 0.0
+    t = L - n + n // 2  # the rows from n // 2 on see it
+
+    def put(t, sign):  # a key of 2^62 sign, alone in its column
+        if fp8:
+            c.k[pg(t)] = 0
+            c.k[pg(t)][0] = 0x38 | (0x80 if sign < 0 else 0)
+            c.ks[pg(t)] = 127 + 62
+        else:
+            c.k[pg(t)] = 0.0
+            c.k[pg(t)][0] = sign * 2.0 ** 62
+
+    def run():
+        out, lse, _ = buffers(n, G, D, False)
+        ws = workspace(V.vp_paged_attention_rows_workspace_bytes(1, n, G, 1, D))
+        c.attend(q, i32([0, n]), i32([L]), n, G, 2.0 ** 8, None, out, lse, ws)
+        torch.cuda.synchronize()
+        assert V.vp_read_status(ws) == V.VP_OK
+        return out, lse
+
+    good, l0 = run()
+    put(t, 1)
+    out, lse = run()
+    assert torch.equal(out[:n // 2], good[:n // 2]) and torch.equal(lse[:n // 2], l0[:n // 2])
+    assert bool(torch.isnan(out[n // 2:]).all()) and bool(torch.isnan(lse[n // 2:]).all())
+    put(t, -1)
+    out, lse = run()
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    c.k.zero_()
+    c.k[..., 0] = 0xB8 if fp8 else -2.0 ** 62
+    if fp8:
+        c.ks.fill_(127 + 62)
+    out, lse = run()
+    assert not bool(out.any()) and bool(torch.isneginf(lse).all())

@@ -303,6 +303,11 @@ __device__ __forceinline__ void ra_gate2(float& v0, float& v1, uint32_t w) {
   v0 = __fdividef(v0 * n0 * n0, fmaf(h0, h0, 1.0f));
   v1 = __fdividef(v1 * n1 * n1, fmaf(h1, h1, 1.0f));
 }
+// What is subtracted from the scores for a reference: nothing where there is none yet; NaN, which every weight of the row then is,
+// where a score is infinite or beyond fp32's range (finite scores less infinity would be weights of zero).
+__device__ __forceinline__ float ra_less(float m) {
+  return m == -INFINITY ? 0.0f : m == INFINITY ? __int_as_float(0x7FFFFFFF) : m;
+}
 // log sum exp from the reference in log2 units and the sum of 2^(t - m).
 __device__ __forceinline__ float ra_lse(float m, float l) {
   return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -1231,7 +1236,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           if (__any_sync(0xFFFFFFFFu, grow)) {  // as below
             const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
             m = to;
-            mc = m == -INFINITY ? 0.0f : m;
+            mc = ra_less(m);
             __syncwarp();
             if (j > 0) {
               const uint64_t ff = ra_pair(f, f), zero = 0;
@@ -1309,7 +1314,7 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
             if (__any_sync(0xFFFFFFFFu, grow)) {
               const float to = grow ? top : m, f = grow ? ra_ex2(m - to) : 1.0f;
               m = to;
-              mc = m == -INFINITY ? 0.0f : m;
+              mc = ra_less(m);
               __syncwarp();
               if (j + part > 0) {
                 const uint64_t ff = ra_pair(f, f), zero = 0;
