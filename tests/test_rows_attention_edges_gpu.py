@@ -240,3 +240,50 @@ def test_scores_beyond_the_range_are_no_zeros(V, D, G, n, long, fp8):
         c.ks.fill_(127 + 62)
     out, lse = run()
     assert not bool(out.any()) and bool(torch.isneginf(lse).all())
+
+
+# ------------------------------------------------------------------ scale bytes behind the end
+@pytest.mark.parametrize("D,G,n,L", [(128, 4, 1, 130), (256, 6, 1, 65), (64, 2, 3, 300), (128, 8, 40, 1000), (256, 4, 60, 201), (256, 4, 60, 190)])
+def test_scale_bytes_behind_the_end_have_no_effect(V, D, G, n, L):
+    """Any byte may lie there; large ones before the end are scales like others, beside whatever lies behind it."""
+    S, P, M = 3, 128, 3 * n
+    c = Cache(V, D, S, -(-L // P), P, 2, D, True)
+    for s in range(S):
+        c.vs[int(c.table[s, 0]), :, 3::7] = 140 + s
+    q = bf16(np.random.default_rng(1), (M, 2 * G, D), 1.5)
+    ws, outs = workspace(V.vp_paged_attention_rows_workspace_bytes(S, M, 2 * G, 2, D)), []
+    for byte in (120, 0, 134, 135, 254, 255):
+        for t in (c.ks, c.vs):
+            for s in range(S):
+                if L % P:
+                    t[int(c.table[s, (L - 1) // P]), :, L % P:] = byte
+        out, lse, _ = buffers(M, 2 * G, D, False)
+        c.attend(q, i32(np.arange(S + 1) * n), i32([L] * S), M, 2 * G, D ** -0.5, None, out, lse, ws)
+        outs.append(out)
+    assert all(torch.equal(outs[0], o) for o in outs)
+    kv = [c.values(s, L) for s in range(S)]
+    want, m = want_of(q, np.arange(S + 1) * n, [x[0] for x in kv], [x[1] for x in kv], [L - n] * S, None, D ** -0.5, None)
+    check(out, lse, want, m, D, "scales behind the end")
+
+
+def test_scale_bytes_behind_the_end_cost_nothing(V):
+    """64 single tokens of 130 positions, 126 unused slots each: 41 us whatever lies there (77 where every large byte made its tile
+    go the slow way).  The best of 20 runs; half as much again is allowed."""
+    S, L, P, Hkv, D, Hq = 64, 130, 128, 8, 128, 32
+    c = Cache(V, 1, S, 2, P, Hkv, D, True)
+    q, ln = bf16(np.random.default_rng(1), (S, Hq, D)), i32([L] * S)
+    out, ws, best = torch.empty_like(q), workspace(V.vp_paged_attention_rows_workspace_bytes(S, S, Hq, Hkv, D)), []
+    for byte in (120, 255):
+        for t in (c.ks, c.vs):
+            t[torch.from_numpy(c.table[:, 1]).cuda().long(), :, L % P:] = byte
+        times = []
+        for _ in range(20):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+            a.record()
+            for _ in range(5):
+                c.attend(q, None, ln, S, Hq, 0.1, None, out, None, ws)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        best.append(min(times))
+    assert best[1] < 1.5 * best[0], best

@@ -316,7 +316,8 @@ __device__ __forceinline__ float ra_lse(float m, float l) {
 // Codes to bf16: a tile of kRowsT rows of kCols codes, then a scale byte per row, to an operand tile, by 128 threads.  Eight
 // lanes take 64 codes of each of two rows, of neighbouring column groups where there are several: reads and writes then meet
 // every bank once.  Scales from 2^8 on (the factor leaves bf16's range; 255 is NaN) are left to ra_expand_rare, for which this
-// says whether there are any.  (A code 0x7F under another scale, which the append does not write, comes out as 480.)
+// says whether there are any among the first `left` rows (behind them lies what nobody sees: a scale there may be anything, and costs
+// nothing).  (A code 0x7F under another scale, which the append does not write, comes out as 480.)
 template <int kCols, int kRowsT>
 struct RaUnit {  // unit u (of kRowsT * kCols / 16) of thread tid: 16 codes
   int row, ch, i;
@@ -339,7 +340,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return v;
 }
 template <int kCols, int kRowsT>
-__device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
+__device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid, int left) {
   constexpr int kUnits = kRowsT * kCols / 16 / 128, kAtOnce = 4;
   bool rare = false;
 #pragma unroll 1
@@ -362,7 +363,7 @@ __device__ __forceinline__ bool ra_expand(uint32_t src, uint32_t dst, int tid) {
         o[2 * x] = ra_bmul2(ra_code2<0x9180>(in[x]), f);
         o[2 * x + 1] = ra_bmul2(ra_code2<0xB3A2>(in[x]), f);
       }
-      rare = rare || e[k] > 134;
+      rare = rare || (e[k] > 134 && u.row < left);
       sts128(u.out(dst, 0), make_uint4(o[0], o[1], o[2], o[3]));
       sts128(u.out(dst, 1), make_uint4(o[4], o[5], o[6], o[7]));
     }
@@ -1131,9 +1132,9 @@ __global__ void __launch_bounds__(RaCfg<D, kTiles, kSrc>::kThreads, 1)
           const uint32_t tile = ring + st * C::kTile, src = raw + rst * C::kRaw;
           if (!(ok = wait(&sh.rfull[rst], rpar) && wait(&sh.empty[st], wpar))) break;
           if (C::kKRows == BN || group) {
-            if (ra_expand<C::kVCols, BN>(src, tile, tid)) ra_expand_rare<C::kVCols, BN>(src, tile, tid);
+            if (ra_expand<C::kVCols, BN>(src, tile, tid, keys - b * BN)) ra_expand_rare<C::kVCols, BN>(src, tile, tid);
           } else {
-            if (ra_expand<D, C::kKRows>(src, tile, tid)) ra_expand_rare<D, C::kKRows>(src, tile, tid);
+            if (ra_expand<D, C::kKRows>(src, tile, tid, keys - b * BN - rank * C::kKRows)) ra_expand_rare<D, C::kKRows>(src, tile, tid);
           }
           const uint32_t bad = *(volatile uint32_t*)&sh.bad[g & 15];
           if (group && (b >= edge || bad)) {
