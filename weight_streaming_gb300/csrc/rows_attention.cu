@@ -200,9 +200,13 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   const int tiles = rows_tiles(x.S, x.M, x.Hq, x.Hkv);
   a.tok_tile = 128 * tiles / a.G;
   a.g_inv = (65536 + a.G - 1) / a.G;
-  // Starting and ending an item, in keys (12,289 rows of 24 / 4 x 256 heads at 256, 384, 640: 1.62, 1.54, 1.44 ms; 9 prompts of
-  // 12,001 rows, 32 / 8 x 128: 407, 354, 369 us)
-  a.item_cost = x.D == 256 && tiles == 2 ? 640 : 448;
+  // Starting and ending an item, in keys: 64 to 2,560 tried over 16 calls of each width (prompts of 2,000 to 16,384 rows, one to 40 a
+  // call, chunks, drafts, single tokens), without and with gates, which are read at an item's end.  40 prompts of 16,000 rows:
+  // pairs 512, 640, 768: 309, 299, 310 us, with gates 640, 1,024, 1,280: 441, 397, 409; 64 columns (two tiles) 128, 256, 448: 228, 195,
+  // 221, with gates 268, 213, 225; 128 columns 256, 448, 640: 313, 276, 301, with gates 373, 307, 316.  60 single tokens in 8 bits of
+  // 128 columns 256, 448, 640: 193, 178, 174.  The other calls come within 4 % of their best at these values.
+  const bool pair = x.D == 256 && tiles == 2;
+  a.item_cost = pair ? (x.gate ? 1024 : 640) : x.D == 64 && tiles == 2 ? 256 : 448;
   const int grid = std::min(sms, kRowsGrid);
   // Polls after which a wait for an item gives up: kMbarPolls and one per 32 keys of a CTA's part of the line, were every sequence as long as it
   // can be.  A role that has nothing to do in an item (a tile without rows, queries loaded ahead, the issuing warp of a pair's second
@@ -210,7 +214,7 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   // hint), 32 keys 0.6 us at most: kMbarPolls alone, 0.26 s, ran out where 192 rows saw 2^31 positions (0.35 s an item).
   const long long longest = source == kDense ? x.M : (long long)a.max_pages << a.log_page;
   const long long line = ((long long)x.S + x.M / a.tok_tile) * (longest + a.item_cost) * x.Hkv;
-  a.polls = kMbarPolls + (uint32_t)std::min((line / (x.D == 256 && tiles == 2 ? grid / 2 : grid) + 2 * kMinKeys) / 32, 1LL << 31);
+  a.polls = kMbarPolls + (uint32_t)std::min((line / (pair ? grid / 2 : grid) + 2 * kMinKeys) / 32, 1LL << 31);
   cudaError_t e;
   if (x.D == 256)
     e = tiles == 2 ? launch_rows<256, 2>(a, source, kmap, vmap, grid, s) : launch_rows<256, 1>(a, source, kmap, vmap, grid, s);
@@ -219,7 +223,7 @@ vp_status run_rows(const Common& x, RowsArgs a, int source, const CUtensorMap& k
   else
     e = tiles == 2 ? launch_rows<64, 2>(a, source, kmap, vmap, grid, s) : launch_rows<64, 1>(a, source, kmap, vmap, grid, s);
   if (e != cudaSuccess) return cuda_fail(e);
-  const dim3 jg((unsigned)(x.D == 256 && tiles == 2 ? grid / 2 : grid), kJoinRows);
+  const dim3 jg((unsigned)(pair ? grid / 2 : grid), kJoinRows);
   if (x.D == 256)
     join_kernel<256><<<jg, kJoinThreads, 0, s>>>(a, 128 * tiles);
   else if (x.D == 128)
