@@ -4,6 +4,10 @@
 // Mathematics: as for single tokens (paged_attention.cu): one pass over the keys keeps a reference m, l = sum 2^(t - m) and o =
 // sum 2^(t - m) v of t = scale log2(e) q . k; two parts join as m = max(m1, m2), l = l1 2^(m1 - m) + l2 2^(m2 - m), o alike.  m is
 // the running maximum of some earlier block: it follows only where the maximum has grown by 2^8, so o is seldom scaled.
+// l sums the weights in fp32; the tensor cores take them in bf16, one rounding of at most 2^-8 each (the values are bf16, and both
+// operands of a product have one type).  Outputs are 1.1 to 1.4 times as far from the definition as with weights in 32 bits.  A second
+// bf16 part, as single tokens have it in paged_attention.cu, would mean these products twice, half as much tensor work again where
+// that is the bound.
 //
 // Design: 4 D flops a key, row and query head on the tensor cores (bf16, fp32 sums in tensor memory).
 //  * Rows: the G query heads of a key-value head are rows of their own (row = token * G + head), so that the keys are read
@@ -11,7 +15,7 @@
 //  * Two tiles of 128 rows share the keys.  With 64 or 128 columns both lie in one CTA (scores and outputs fill the tensor
 //    memory; one tile's softmax runs beside the other's products).  With 256 columns a CTA pair (cta_group::2) takes a
 //    tile each, holds half of every key and value block, and has two score buffers.  A single CTA would take 64 bytes of L2 a
-//    cycle there and stay at half the rate (12,289 rows of 24 / 4 x 256 heads: 2.0 ms, in pairs 1.8 at first, 1.36 now).
+//    cycle there and stay at half the rate (12,289 rows of 24 / 4 x 256 heads: 2.0 ms, in pairs 1.8 at first, 1.29 now).
 //  * One tile (sequences with few rows): queries in tensor memory, two score buffers; with at most 32 rows every softmax warp
 //    takes all rows and a quarter of the keys (61 single tokens over an 8-bit cache: 299 us without, 198 with, at that time).
 //  * Warps: a scheduler, two that start copies (TMA, 128-byte swizzle; a block's pages), one that issues products, four or
@@ -26,13 +30,13 @@
 //    pair (the lengths are read on the device: each CTA sums the line up and finds its part).  At most two items of a CTA are
 //    cut; their parts lie in the workspace and a second launch joins them.  No counters: nothing to reset.
 //
-// What bounds it (2,048 rows behind 30,000 positions): 24 / 4 x 256 heads 913 us, 1.71 PFLOP/s, 88 % of the measured bf16 rate: the
-// tensor cores.  32 / 8 x 128 heads 949 us, 1.10 PFLOP/s: a tile's chain of softmax (two warps of a scheduler share its instruction
-// slots and caches) and products, an estimated 2,900 cycles a block against 2,048 of products.  64 columns: 0.70 PFLOP/s, the
-// exponentials and the same chain.  Few rows: the cache's bytes in bf16 (64 x 8,001 positions of 8 x 128 heads 328 us, 6.4
-// TB/s); in 8 bits the expansion and the softmax of 128 keys take longer than their bytes (286 us, 3.7 TB/s).
+// What bounds it (2,048 rows behind 30,000 positions): 24 / 4 x 256 heads 938 us, 1.67 PFLOP/s, 86 % of the measured bf16 rate: the
+// tensor cores.  32 / 8 x 128 heads 880 us, 1.18 PFLOP/s: a tile's chain of softmax (two warps of a scheduler share its instruction
+// slots and caches) and products, an estimated 2,900 cycles a block against 2,048 of products.  64 columns: 754 us, 0.69 PFLOP/s, the
+// exponentials and the same chain.  Few rows: the cache's bytes in bf16 (64 x 8,001 positions of 8 x 128 heads 327 us, 6.4
+// TB/s); in 8 bits the expansion and the softmax of 128 keys take longer than their bytes (291 us, 3.6 TB/s).
 // Loops are kept short on purpose: a scheduler's warps share its instruction cache.  With the softmax unrolled over 128 keys and
-// copies of the waits' slow halves 61 single tokens over an 8-bit cache took 566 us in place of 290 (now 188).
+// copies of the waits' slow halves 61 single tokens over an 8-bit cache took 566 us in place of 290 (now 192).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -153,7 +157,11 @@ RowsWs rows_ws(int D) {
 }
 
 // Two tiles of 128 rows share every key and value that is read; where a sequence has fewer rows (on average: the lengths are
-// on the device) one tile does, with a second score buffer.
+// on the device) one tile does, with a second score buffer.  16 sequences of 4,000 positions, one / two tiles in us: of 128 columns
+// (32 / 8 heads) with 4, 32, 128, 160, 256 rows per key head 62 / 72, 70 / 79, 76 / 83, 113 / 98, 115 / 104, in 8 bits 61 / 85, 68 / 91, 82 / 97,
+// 123 / 108, 130 / 115; of 64 the same way, 65 / 72 at 128 and 91 / 78 at 160; of 256 (24 / 4 heads) 64 / 72 at 6, 75 / 81 at 96, 96 / 86 at 144,
+// 107 / 93 at 240.  Against the rule: 256 columns in 8 bits, where one tile stays ahead (107 / 122 at 240, 266 / 323 at 768), and batches
+// whose sequences differ (39 single tokens and 2,001 rows, by the average two tiles: 223 / 271 of 128 columns, 208 / 230 of 256).
 int rows_tiles(int S, int M, int Hq, int Hkv) { return (long long)M * (Hq / Hkv) <= 128LL * S ? 1 : 2; }
 
 // Rows and columns of the key (0) and value (1) tiles.

@@ -54,7 +54,7 @@ constexpr uint32_t kRaShort = 64;
 // are at work on the same block, RowsArgs::polls where they may be at work on a whole item.
 template <bool kPair>
 __device__ __forceinline__ bool ra_wait(uint32_t bar, uint32_t parity, uint32_t polls, int* abort, int* status) {
-  uint32_t left = polls + kRaShort;  // short polls first, then of at most 20 us
+  uint32_t left = polls + kRaShort;  // short polls first, then of 4 us (the hint's 20 are cut)
   while (!__all_sync(0xFFFFFFFFu, ra_try<kPair>(bar, parity, left > polls ? 0 : 20000))) {
     --left;
     if (left > polls) continue;
